@@ -106,7 +106,8 @@ typedef enum {
     SC_I32 = 0, SC_U32 = 1, SC_F32 = 2,
     SC_AFFINE_U32 = 3,   /* uint32 pairs (a, b), 8 bytes: the map h -> a*h + b */
     SC_I64 = 4, SC_U64 = 5, SC_F64 = 6,
-    SC_MAXCOUNT_I32 = 7  /* pairs (int32 value, uint32 count), 8 bytes */
+    SC_MAXCOUNT_I32 = 7, /* pairs (int32 value, uint32 count), 8 bytes */
+    SC_F16 = 8, SC_BF16 = 9  /* the sequence operators of sc_seq.h only; no scan takes them */
 } sc_dtype;
 typedef enum {
     SC_SUM = 0, SC_MAX = 1,

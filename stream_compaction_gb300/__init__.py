@@ -6,8 +6,9 @@ Thin Python binding over the C ABI of ``libsc_gb300.so`` (declared in
 * ``sc_*`` functions with the C names and the C argument order (integer
   device pointers, element counts, a raw ``cudaStream_t``);
 * tensor helpers (``scan_inclusive``, ``scan_exclusive``, ``scan_batched``,
-  ``compact_if``, ``scan_hierarchical``, ``scan_host``) that take torch CUDA
-  tensors and the current torch stream.
+  ``compact_if``, ``scan_hierarchical``, ``scan_host``, and from ``seq.py``
+  ``embed``, ``causal_conv``, ``selective_scan`` with their gradients and
+  single-token forms) that take torch CUDA tensors and the current torch stream.
 
 Every step of the computation runs in the library's CUDA kernels.  There is no
 CPU fallback: if the library has not been built (``python -m
@@ -18,6 +19,11 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+
+from . import seq as _seq
+from .seq import (SC_BF16, SC_CONV_MAX_WIDTH, SC_F16, SC_SSM_MAX_STATES, SC_SSM_SAVE, causal_conv, causal_conv_grad,
+                  causal_conv_step, embed, embed_grad, selective_scan, selective_scan_grad, selective_scan_saved,
+                  selective_scan_step)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsc_gb300.so")
@@ -85,7 +91,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                 raise RuntimeError("libsc_gb300.so is not built (%s); run "
                                    "`python -m stream_compaction_gb300.build` on a machine with nvcc" % path)
             lib = ctypes.CDLL(path)
-            for name, (args, res) in SIGNATURES.items():
+            for name, (args, res) in {**SIGNATURES, **_seq.SIGNATURES}.items():
                 f = getattr(lib, name)
                 f.argtypes = args
                 f.restype = res

@@ -36,7 +36,7 @@ def sources():
 
 def _deps_mtime():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(ROOT, "include", "sc_scan.h"))
+    files += [os.path.join(ROOT, "include", h) for h in ("sc_scan.h", "sc_seq.h")]
     files.append(os.path.abspath(__file__))
     return max(os.path.getmtime(f) for f in files)
 

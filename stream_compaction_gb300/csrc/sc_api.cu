@@ -16,6 +16,7 @@
 
 #include "../../include/sc_scan.h"
 #include "sc_launch.h"
+#include "sc_seq_launch.h"
 #include "sc_shapes.h"
 
 namespace {
@@ -1069,6 +1070,27 @@ sc_status sc_debug_set_lookback(int64_t stall_tile, int64_t delay_tile, uint32_t
 }
 
 }  // extern "C"
+
+// What the sequence operators share: scratch behind the look-back part of the
+// stream's workspace, whose statuses a later look-back then clears.
+namespace scg {
+constexpr size_t kScratchOffset = 4096;
+static_assert(kScratchOffset >= kStatusOffset, "behind the counter and error words");
+
+size_t seq_scratch_total(size_t bytes) { return kScratchOffset + bytes; }
+
+sc_status seq_scratch(cudaStream_t s, size_t bytes, unsigned char** out) {
+    std::lock_guard<std::mutex> lk(g_ws_mu);
+    Workspace* ws = nullptr;
+    const sc_status st = acquire_ws(s, seq_scratch_total(bytes), &ws);
+    if (st != SC_OK) return st;
+    ws->junk_from = std::min(ws->junk_from, kScratchOffset);
+    *out = ws->base + kScratchOffset;
+    return SC_OK;
+}
+
+void count_launches(int n) { g_launches.fetch_add((uint64_t)n); }
+}  // namespace scg
 
 // Tile sizes (host side).
 namespace scg {

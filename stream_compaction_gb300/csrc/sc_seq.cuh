@@ -1,0 +1,150 @@
+// Shared pieces of the sequence operators (embedding, convolution, selective
+// scan): element types, 16-byte vector access, two-lane float32 arithmetic and
+// the activation functions.  All arithmetic is float32; an element is rounded
+// to its type once, when it is stored.
+#pragma once
+#include <cstdint>
+#include <cstring>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+namespace scg {
+
+using bf16 = __nv_bfloat16;
+using f16 = __half;
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(bf16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(f16 v) { return __half2float(v); }
+template <class T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ bf16 from_f32<bf16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ f16 from_f32<f16>(float v) { return __float2half_rn(v); }
+
+// N consecutive elements of T, moved in accesses of up to 16 bytes.
+template <class T, int N>
+struct Vec {
+    static constexpr int kBytes = (int)sizeof(T) * N;
+    static_assert(kBytes % 4 == 0, "whole 32-bit words");
+    static constexpr int kWords = kBytes / 4;
+    uint32_t w[kWords];
+    template <class U, bool kConst>
+    __device__ __forceinline__ void load_as(const T* p) {
+        constexpr int per = (int)sizeof(U) / 4;
+#pragma unroll
+        for (int i = 0; i < kWords / per; ++i) {
+            const U* q = reinterpret_cast<const U*>(p) + i;
+            U v;
+            if constexpr (kConst) v = __ldg(q);
+            else v = *q;
+            const uint32_t* e = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+            for (int j = 0; j < per; ++j) w[i * per + j] = e[j];
+        }
+    }
+    template <bool kConst>
+    __device__ __forceinline__ void load_any(const T* p) {
+        if constexpr (kBytes % 16 == 0) load_as<uint4, kConst>(p);
+        else if constexpr (kBytes % 8 == 0) load_as<uint2, kConst>(p);
+        else load_as<uint32_t, kConst>(p);
+    }
+    __device__ __forceinline__ void load(const T* p) { load_any<true>(p); }      // read-only for the kernel
+    __device__ __forceinline__ void load_rw(const T* p) { load_any<false>(p); }  // memory it also writes
+    __device__ __forceinline__ void store(T* p) const {
+        if constexpr (kBytes % 16 == 0) {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i)
+                reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        } else if constexpr (kBytes % 8 == 0) {
+#pragma unroll
+            for (int i = 0; i < kWords / 2; ++i) reinterpret_cast<uint2*>(p)[i] = make_uint2(w[2 * i], w[2 * i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0u;
+    }
+    // element i as float32 (i known at compile time)
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return to_f32(reinterpret_cast<const T*>(&w[i / 2])[i % 2]);
+    }
+    __device__ __forceinline__ void set(const float* v) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = __float_as_uint(v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                T e[2] = {from_f32<T>(v[i]), from_f32<T>(v[i + 1])};
+                uint32_t u;
+                memcpy(&u, e, 4);
+                w[i / 2] = u;
+            }
+        }
+    }
+};
+
+// Two float32 values in one 64-bit register pair; each operation rounds both.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float lo2(f2 v) {
+    return __uint_as_float((uint32_t)v);
+}
+__device__ __forceinline__ float hi2(f2 v) {
+    return __uint_as_float((uint32_t)(v >> 32));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float ex2(float v) {  // 2^v
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ f2 ex2_2(f2 v) { return pack2(ex2(lo2(v)), ex2(hi2(v))); }
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, 1.0f + expf(-v)); }
+
+// log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1], and
+// log1p(e) = 2 artanh(s), s = e / (2 + e) <= 1/3, by its power series
+// s + s^3/3 + s^5/5 + ...; the terms after s^15 are below 2^-27 of the sum.
+// No branch and no cancellation: relative error about 3 * 2^-24 for every v.
+__device__ __forceinline__ float softplus(float v) {
+    const float e = expf(-fabsf(v));
+    const float s = __fdividef(e, 2.0f + e), q = s * s;
+    float p = 1.0f / 15.0f;
+    p = fmaf(p, q, 1.0f / 13.0f);
+    p = fmaf(p, q, 1.0f / 11.0f);
+    p = fmaf(p, q, 1.0f / 9.0f);
+    p = fmaf(p, q, 1.0f / 7.0f);
+    p = fmaf(p, q, 1.0f / 5.0f);
+    p = fmaf(p, q, 1.0f / 3.0f);
+    p = fmaf(p * q, s, s);
+    return fmaxf(v, 0.0f) + 2.0f * p;  // NaN: e and p are NaN
+}
+
+}  // namespace scg

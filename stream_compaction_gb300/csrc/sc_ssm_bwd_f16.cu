@@ -1,0 +1,8 @@
+// Gradient of the selective scan, f16 activations.
+#include "sc_ssm_bwd.cuh"
+
+namespace scg {
+cudaError_t launch_ssm_grad_f16(const SsmParams& p, const SsmPlan& plan, int* launches, cudaStream_t s) {
+    return ssm_back_type<f16>(p, plan, launches, s);
+}
+}  // namespace scg

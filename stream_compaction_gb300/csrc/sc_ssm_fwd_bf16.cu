@@ -1,0 +1,8 @@
+// Forward selective scan, bf16 activations.
+#include "sc_ssm_fwd.cuh"
+
+namespace scg {
+cudaError_t launch_ssm_bf16(const SsmParams& p, const SsmPlan& plan, int* launches, cudaStream_t s) {
+    return ssm_type<bf16>(p, plan, launches, s);
+}
+}  // namespace scg

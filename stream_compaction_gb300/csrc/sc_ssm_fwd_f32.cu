@@ -1,0 +1,8 @@
+// Forward selective scan, f32 activations.
+#include "sc_ssm_fwd.cuh"
+
+namespace scg {
+cudaError_t launch_ssm_f32(const SsmParams& p, const SsmPlan& plan, int* launches, cudaStream_t s) {
+    return ssm_type<float>(p, plan, launches, s);
+}
+}  // namespace scg
