@@ -46,7 +46,7 @@ struct Tensor {
         return sb >= (__int128)(tokens - 1) * st + channels || st >= (__int128)(batch - 1) * sb + channels;
     }
     bool vec(int elems) const {
-        return multiple(p, 16) && (batch <= 1 || sb % elems == 0) && (tokens <= 1 || st % elems == 0);
+        return multiple(p, std::min(16, elems * eb)) && (batch <= 1 || sb % elems == 0) && (tokens <= 1 || st % elems == 0);
     }
 };
 Tensor flat(const void* p, int64_t n, int eb) { return {p, 1, 1, n, 0, 0, eb}; }
@@ -133,7 +133,7 @@ sc_status ssm_args(const sc_ssm_desc* d, bool step, SsmParams* p) {
         return SC_ERR_INVALID;
     // the smallest channel block and chunk of any kernel; the last sums' grids
     const int64_t tiles = (d->length + SC_SSM_SAVE - 1) / SC_SSM_SAVE;
-    const int64_t per = d->channels / d->groups, blocks = (per + 15) / 16 * d->groups;
+    const int64_t per = d->channels / d->groups, blocks = (per + 7) / 8 * d->groups;
     const int64_t grid = product(d->batch, std::max<int64_t>(blocks, 1), std::max<int64_t>(tiles, 1));
     const int64_t bc = product(d->batch, d->length, d->groups, d->states);
     if (grid < 0 || grid > kMaxGrid || bc / 256 >= kMaxGrid || d->channels * (d->states + 2) / 256 >= kMaxGrid)
@@ -194,7 +194,7 @@ Tensor ssm_x(const sc_ssm_desc* d, const void* p, int64_t sb, int64_t st) {
 // 16-byte accesses for every tensor that the tiled kernels read or write.
 bool ssm_vec(const sc_ssm_desc* d, const Tensor* more, int n_more) {
     const int e = 16 / bytes_of(d->dtype);
-    if ((d->channels / d->groups) % 8 != 0 || d->states % 8 != 0) return false;
+    if ((d->channels / d->groups) % e != 0 || d->states % e != 0) return false;
     if (!ssm_x(d, d->x, d->x_batch, d->x_token).vec(e) || !ssm_x(d, d->dt, d->dt_batch, d->dt_token).vec(e)) return false;
     if (d->z && !ssm_x(d, d->z, d->z_batch, d->z_token).vec(e)) return false;
     if (!ssm_x(d, d->B, d->B_batch, d->B_token).vec(e) || !ssm_x(d, d->C, d->C_batch, d->C_token).vec(e)) return false;

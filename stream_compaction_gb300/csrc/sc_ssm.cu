@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(256) ssm_sum_kernel(SsmParams p, int np) {
     float* dst;
     long long step;
     if (i < na) {
-        src = p.part_a + i / p.states * np + i % p.states;
+        src = p.part_a + (i % p.states / 4 * p.channels + i / p.states) * 4 + i % p.states % 4;
         step = p.channels * np;
         dst = p.dA + i;
     } else if (i < na + 2 * p.channels) {

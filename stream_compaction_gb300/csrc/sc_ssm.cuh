@@ -12,10 +12,15 @@
 //     <= 32    8          4                  16
 //     <= 64   16          4                   8
 //
-// Channels go in pairs through the two-lane float32 instructions; B and C lie
-// in shared memory as (v, v) pairs for them.  States beyond `states` have
-// A = B = C = 0 and stay 0.  Tokens beyond the length have d = d*x = 0: the
-// state passes them unchanged.
+// Channels go in pairs through the two-lane float32 instructions (one issue
+// slot for two multiply-adds; measured: two clocks each, so they relieve the
+// issue, not the multipliers); B and C lie in shared memory as (v, v) pairs for
+// them.  States beyond `states` have A = B = C = 0 and stay 0.  Tokens beyond
+// the length have d = d*x = 0: the state passes them unchanged.
+//
+// The elements of a tile (token, channel) are worked on in passes of 128, four
+// a lane: four channels of one token (kVec: 8 or 16-byte accesses, channels
+// and strides multiples of 4), or one channel of four tokens.
 #pragma once
 #include "sc_seq.cuh"
 #include "sc_seq_launch.h"
@@ -32,182 +37,249 @@ struct Geo {
     static constexpr int CL = 32 / S;        // lanes along the channels
     static constexpr int CH = CL * CPL;
     static constexpr int NP = 4 * S;         // padded states
-    static constexpr int kWarps = S == 16 ? 2 : 4;
-    static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kBlockCh = kWarps * CH;
+    static constexpr int TP = 128 / CH;      // tokens of a pass
+    // Sums over a channel's states: up to 4 lanes leave their parts in shared
+    // memory for the pass that uses the sum (one store and S loads for every four
+    // channels); 8 or 16 lanes' parts would crowd it, so those add across lanes first.
+    static constexpr bool kParts = S <= 4;
+    static constexpr int kSumRows = kParts ? S : 1;
+    static constexpr int kSumRow = kSumRows * CH;  // floats per token
+    // Row j of the parts has its channels at exchanged places, fours apart, so
+    // that the S lanes of a channel group meet in no bank.
+    __device__ __forceinline__ static int place(int j, int ch) { return j * CH + (ch ^ (j * (S == 4 ? 8 : 16))); }
+    static constexpr int kBwdWarps = S == 16 ? 2 : 4;
 };
 
 // Which channels, chunk of the length and row a CTA works on.
-template <class G>
+template <class G, int kWarps>
 struct SsmPlace {
-    long long b, chunk, cblock, group, ch0, left;  // ch0: the warp's first channel; left: its channels (may be <= 0)
-    __device__ __forceinline__ SsmPlace(const SsmParams& p, long long blocks_per_group, int chunks) {
-        const long long ncb = blocks_per_group * p.groups;
-        cblock = blockIdx.x % ncb;
-        const long long q = blockIdx.x / ncb;
-        chunk = q % chunks;
-        b = q / chunks;
+    long long b, chunk, cblock, group, ch0;  // ch0: the warp's first channel
+    int left;                                // its channels (0: none)
+    // warp: the one of kWarps whose channels these are
+    __device__ __forceinline__ SsmPlace(const SsmParams& p, int blocks_per_group, int chunks, int warp) {
+        const int ncb = blocks_per_group * (int)p.groups;
+        const unsigned q = blockIdx.x / (unsigned)ncb;
+        cblock = blockIdx.x % (unsigned)ncb;
+        chunk = q % (unsigned)chunks;
+        b = q / (unsigned)chunks;
         group = cblock / blocks_per_group;
         const long long per = p.channels / p.groups;
-        const long long in = (cblock % blocks_per_group) * G::kBlockCh + (threadIdx.x >> 5) * G::CH;
+        const long long in = (cblock % blocks_per_group) * (kWarps * G::CH) + warp * G::CH;
         ch0 = group * per + in;
-        left = per - in < G::CH ? per - in : G::CH;
+        left = per - in < G::CH ? (per > in ? (int)(per - in) : 0) : G::CH;
     }
 };
 
-// One tile of a batch x length x channels tensor: kTile tokens of the warp's
-// channels, each lane a fixed set of (token, channel).
-// kVec: eight neighbouring channels at a time in 16-byte accesses (channels a
-// multiple of 8); else one element at a time, lanes along the channels.
-template <class T, class G, bool kVec>
+// Tokens of the tile of kT that starts at t0.
+template <int kT>
+__device__ __forceinline__ int tile_tokens(const SsmParams& p, long long t0) {
+    const long long n = p.length - t0;
+    return n < kT ? (int)n : kT;
+}
+
+// One tile (kT tokens) of a batch x length x channels tensor.
+template <class T, class G, bool kVec, int kT>
 struct TileRows;
 
-template <class T, class G>
-struct TileRows<T, G, true> {
-    static constexpr int LPT = G::CH / 8;              // lanes per token
-    static constexpr int TP = 32 / LPT;                // tokens per access
-    static constexpr int NA = TP >= kTile ? 1 : kTile / TP;
-    static constexpr int kCount = 8 * NA;
-    static constexpr int kChannels = 8;                // distinct channels of a lane: those of elements 0 .. 7
-    Vec<T, 8> v[NA];
-    __device__ __forceinline__ static int tok(int i, int lane) { return lane / LPT + (i / 8) * TP; }
-    __device__ __forceinline__ static int ch(int i, int lane) { return (lane % LPT) * 8 + i % 8; }
-    __device__ __forceinline__ static bool valid(int i, int lane, int nt, int left) {
-        return tok(i, lane) < nt && (lane % LPT) * 8 < left;
+template <class T, class G, int kT>
+struct TileRows<T, G, true, kT> {
+    static constexpr int LPT = G::CH / 4;  // lanes per token
+    static constexpr int NA = kT / G::TP;  // passes
+    Vec<T, 4> v[NA];
+    __device__ __forceinline__ static int tok(int a, int lane) { return a * G::TP + lane / LPT; }
+    __device__ __forceinline__ static int ch(int lane) { return (lane % LPT) * 4; }
+    template <bool kFull>
+    __device__ __forceinline__ static Vec<T, 4> fetch(const T* p, long long stride, int a, int nt, int left, int lane) {
+        Vec<T, 4> q;
+        if constexpr (!kFull) q.zero();
+        if (kFull || (tok(a, lane) < nt && ch(lane) < left)) q.load(p + tok(a, lane) * stride + ch(lane));
+        return q;
     }
+    template <bool kFull>
     __device__ __forceinline__ void load(const T* p, long long stride, int nt, int left, int lane) {
 #pragma unroll
-        for (int a = 0; a < NA; ++a) {
-            v[a].zero();
-            if (valid(8 * a, lane, nt, left)) v[a].load(p + tok(8 * a, lane) * stride + (lane % LPT) * 8);
-        }
+        for (int a = 0; a < NA; ++a) v[a] = fetch<kFull>(p, stride, a, nt, left, lane);
     }
-    __device__ __forceinline__ float get(int i) const { return v[i / 8].get(i % 8); }
-    // a lane's values into a [kTile][CH] array of shared memory
-    __device__ __forceinline__ static void to_shared(float* s, const float (&f)[kCount], int lane) {
+    __device__ __forceinline__ f2 pair(int a, int i) const { return v[a].pair(i); }
+    __device__ __forceinline__ static f2 pair_of(const Vec<T, 4>& q, int i) { return q.pair(i); }
+    // zeros for elements past the tokens or channels
+    template <bool kFull>
+    __device__ __forceinline__ static void mask(f2 (&f)[2], int a, int nt, int left, int lane) {
+        if (!kFull && (tok(a, lane) >= nt || ch(lane) >= left)) f[0] = f[1] = 0ull;
+    }
+    // the pass's elements of a [tokens][CH] array whose row 0 is the pass's first token
+    __device__ __forceinline__ static void put(float* s, const f2 (&f)[2], int lane) {
+        *reinterpret_cast<ulonglong2*>(s + lane / LPT * G::CH + ch(lane)) = make_ulonglong2(f[0], f[1]);
+    }
+    __device__ __forceinline__ static void get(const float* s, f2 (&f)[2], int lane) {
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(s + lane / LPT * G::CH + ch(lane));
+        f[0] = q.x;
+        f[1] = q.y;
+    }
+    // the same of a [tokens][kSumRow] array, the lanes' parts added
+    __device__ __forceinline__ static void get_sums(const float* s, f2 (&f)[2], int lane) {
+        const float* r = s + lane / LPT * G::kSumRow;
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(r + ch(lane));
+        f[0] = q.x;
+        f[1] = q.y;
 #pragma unroll
-        for (int a = 0; a < NA; ++a) {
-            if (tok(8 * a, lane) < kTile) {
-                float4* q = reinterpret_cast<float4*>(s + tok(8 * a, lane) * G::CH + (lane % LPT) * 8);
-                q[0] = make_float4(f[8 * a], f[8 * a + 1], f[8 * a + 2], f[8 * a + 3]);
-                q[1] = make_float4(f[8 * a + 4], f[8 * a + 5], f[8 * a + 6], f[8 * a + 7]);
-            }
+        for (int j = 1; j < G::kSumRows; ++j) {
+            const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(r + G::place(j, ch(lane)));
+            f[0] = add2(f[0], o.x);
+            f[1] = add2(f[1], o.y);
         }
     }
-    __device__ __forceinline__ static void from_shared(const float* s, float (&f)[kCount], int lane) {
-#pragma unroll
-        for (int a = 0; a < NA; ++a) {
-            if (tok(8 * a, lane) < kTile) {
-                const float4* q = reinterpret_cast<const float4*>(s + tok(8 * a, lane) * G::CH + (lane % LPT) * 8);
-                const float4 x = q[0], y = q[1];
-                f[8 * a] = x.x; f[8 * a + 1] = x.y; f[8 * a + 2] = x.z; f[8 * a + 3] = x.w;
-                f[8 * a + 4] = y.x; f[8 * a + 5] = y.y; f[8 * a + 6] = y.z; f[8 * a + 7] = y.w;
-            }
-        }
-    }
-    __device__ __forceinline__ static void store(T* p, long long stride, const float (&f)[kCount], int nt, int left,
+    template <bool kFull>
+    __device__ __forceinline__ static void store(T* p, long long stride, const f2 (&f)[2], int a, int nt, int left,
                                                  int lane) {
-#pragma unroll
-        for (int a = 0; a < NA; ++a)
-            if (valid(8 * a, lane, nt, left)) {
-                Vec<T, 8> q;
-                q.set(f + 8 * a);
-                q.store(p + tok(8 * a, lane) * stride + (lane % LPT) * 8);
-            }
+        if (kFull || (tok(a, lane) < nt && ch(lane) < left)) {
+            Vec<T, 4> q;
+            q.set_pairs(f);
+            q.store(p + tok(a, lane) * stride + ch(lane));
+        }
     }
-    // sums over a lane's tokens -> over all tokens; true on the lanes that hold them
-    __device__ __forceinline__ static bool sum_tokens(float (&c)[kChannels], int lane) {
+    // a value per channel, as a lane's elements meet it
+    __device__ __forceinline__ static void per_channel(const float* p, int left, int lane, f2 (&f)[2]) {
+        const int c = ch(lane);
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = p && c + i < left ? __ldg(p + c + i) : 0.0f;
+        f[0] = pack2(v[0], v[1]);
+        f[1] = pack2(v[2], v[3]);
+    }
+    // sums per channel over all passes, written
+    __device__ __forceinline__ static void put_channel_sums(float* p, const f2 (&f)[2], int left, int lane) {
+        float v[4] = {lo2(f[0]), hi2(f[0]), lo2(f[1]), hi2(f[1])};
 #pragma unroll
         for (int m = LPT; m < 32; m <<= 1)
 #pragma unroll
-            for (int i = 0; i < kChannels; ++i) c[i] += __shfl_xor_sync(0xffffffffu, c[i], m);
-        return lane < LPT;
+            for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], m);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (lane < LPT && ch(lane) + i < left) p[ch(lane) + i] = v[i];
     }
-    __device__ __forceinline__ static int channel_of(int i) { return i % 8; }
 };
 
-template <class T, class G>
-struct TileRows<T, G, false> {
-    static constexpr int TP = 32 / G::CH;
-    static constexpr int kCount = kTile / TP;
-    static constexpr int kChannels = 1;
-    T v[kCount];
-    __device__ __forceinline__ static int tok(int i, int lane) { return lane / G::CH + i * TP; }
-    __device__ __forceinline__ static int ch(int, int lane) { return lane % G::CH; }
-    __device__ __forceinline__ static bool valid(int i, int lane, int nt, int left) {
-        return tok(i, lane) < nt && lane % G::CH < left;
+template <class T, class G, int kT>
+struct TileRows<T, G, false, kT> {
+    static constexpr int TL = 32 / G::CH;  // tokens side by side
+    static constexpr int NA = kT / G::TP;
+    struct Four { T e[4]; };
+    Four v[NA];
+    __device__ __forceinline__ static int tok(int a, int i, int lane) { return a * G::TP + i * TL + lane / G::CH; }
+    __device__ __forceinline__ static bool valid(int a, int i, int nt, int left, int lane) {
+        return tok(a, i, lane) < nt && lane % G::CH < left;
     }
+    template <bool kFull>
+    __device__ __forceinline__ static Four fetch(const T* p, long long stride, int a, int nt, int left, int lane) {
+        Four q;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (!kFull) q.e[i] = from_f32<T>(0.0f);
+            if (kFull || valid(a, i, nt, left, lane)) q.e[i] = __ldg(p + tok(a, i, lane) * stride + lane % G::CH);
+        }
+        return q;
+    }
+    template <bool kFull>
     __device__ __forceinline__ void load(const T* p, long long stride, int nt, int left, int lane) {
 #pragma unroll
-        for (int i = 0; i < kCount; ++i) {
-            v[i] = from_f32<T>(0.0f);
-            if (valid(i, lane, nt, left)) v[i] = __ldg(p + tok(i, lane) * stride + lane % G::CH);
+        for (int a = 0; a < NA; ++a) v[a] = fetch<kFull>(p, stride, a, nt, left, lane);
+    }
+    __device__ __forceinline__ f2 pair(int a, int i) const { return pair_of(v[a], i); }
+    __device__ __forceinline__ static f2 pair_of(const Four& q, int i) {
+        return pack2(to_f32(q.e[2 * i]), to_f32(q.e[2 * i + 1]));
+    }
+    template <bool kFull>
+    __device__ __forceinline__ static void mask(f2 (&f)[2], int a, int nt, int left, int lane) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (!kFull)
+                f[i] = pack2(valid(a, 2 * i, nt, left, lane) ? lo2(f[i]) : 0.0f,
+                             valid(a, 2 * i + 1, nt, left, lane) ? hi2(f[i]) : 0.0f);
+    }
+    __device__ __forceinline__ static int at(int i, int lane) {
+        return (i * TL + lane / G::CH) * G::CH + lane % G::CH;
+    }
+    __device__ __forceinline__ static void put(float* s, const f2 (&f)[2], int lane) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            s[at(2 * i, lane)] = lo2(f[i]);
+            s[at(2 * i + 1, lane)] = hi2(f[i]);
         }
     }
-    __device__ __forceinline__ float get(int i) const { return to_f32(v[i]); }
-    __device__ __forceinline__ static void to_shared(float* s, const float (&f)[kCount], int lane) {
+    __device__ __forceinline__ static void get(const float* s, f2 (&f)[2], int lane) {
 #pragma unroll
-        for (int i = 0; i < kCount; ++i) s[tok(i, lane) * G::CH + lane % G::CH] = f[i];
+        for (int i = 0; i < 2; ++i) f[i] = pack2(s[at(2 * i, lane)], s[at(2 * i + 1, lane)]);
     }
-    __device__ __forceinline__ static void from_shared(const float* s, float (&f)[kCount], int lane) {
+    __device__ __forceinline__ static void get_sums(const float* s, f2 (&f)[2], int lane) {
 #pragma unroll
-        for (int i = 0; i < kCount; ++i) f[i] = s[tok(i, lane) * G::CH + lane % G::CH];
+        for (int i = 0; i < 2; ++i) {
+            const float *x = s + (2 * i * TL + lane / G::CH) * G::kSumRow, *y = x + TL * G::kSumRow;
+            f[i] = pack2(x[lane % G::CH], y[lane % G::CH]);
+#pragma unroll
+            for (int j = 1; j < G::kSumRows; ++j)
+                f[i] = add2(f[i], pack2(x[G::place(j, lane % G::CH)], y[G::place(j, lane % G::CH)]));
+        }
     }
-    __device__ __forceinline__ static void store(T* p, long long stride, const float (&f)[kCount], int nt, int left,
+    template <bool kFull>
+    __device__ __forceinline__ static void store(T* p, long long stride, const f2 (&f)[2], int a, int nt, int left,
                                                  int lane) {
 #pragma unroll
-        for (int i = 0; i < kCount; ++i)
-            if (valid(i, lane, nt, left)) p[tok(i, lane) * stride + lane % G::CH] = from_f32<T>(f[i]);
+        for (int i = 0; i < 4; ++i)
+            if (kFull || valid(a, i, nt, left, lane))
+                p[tok(a, i, lane) * stride + lane % G::CH] = from_f32<T>(i & 1 ? hi2(f[i / 2]) : lo2(f[i / 2]));
     }
-    __device__ __forceinline__ static bool sum_tokens(float (&c)[kChannels], int lane) {
+    __device__ __forceinline__ static void per_channel(const float* p, int left, int lane, f2 (&f)[2]) {
+        f[0] = f[1] = both(p && lane % G::CH < left ? __ldg(p + lane % G::CH) : 0.0f);
+    }
+    __device__ __forceinline__ static void put_channel_sums(float* p, const f2 (&f)[2], int left, int lane) {
+        float v = (lo2(f[0]) + hi2(f[0])) + (lo2(f[1]) + hi2(f[1]));
 #pragma unroll
-        for (int m = G::CH; m < 32; m <<= 1) c[0] += __shfl_xor_sync(0xffffffffu, c[0], m);
-        return lane < G::CH;
+        for (int m = G::CH; m < 32; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+        if (lane < G::CH && lane < left) p[lane] = v;
     }
-    __device__ __forceinline__ static int channel_of(int) { return 0; }
 };
 
-// One tile of B or C (a group's states of kTile tokens), to (v, v) pairs.
-template <class T, class G, bool kVec>
+// One tile of B or C (a group's states of kT tokens), to (v, v) pairs.
+template <class T, class G, bool kVec, int kT>
 struct TileStates;
 
-template <class T, class G>
-struct TileStates<T, G, true> {  // states a multiple of 8
-    static constexpr int PT = G::NP / 8;                              // eights per token
-    static constexpr int NA = (kTile * PT + 31) / 32;
-    Vec<T, 8> v[NA];
+template <class T, class G, int kT>
+struct TileStates<T, G, true, kT> {  // states a multiple of 4
+    static constexpr int NA = (kT * G::S + 31) / 32;  // fours per lane
+    Vec<T, 4> v[NA];
+    template <bool kFull>  // all tokens and padded states are there
     __device__ __forceinline__ void load(const T* p, long long stride, int nt, int states, int lane) {
 #pragma unroll
         for (int a = 0; a < NA; ++a) {
-            const int q = lane + 32 * a, t = q / PT, n = (q % PT) * 8;
-            v[a].zero();
-            if (t < nt && n < states) v[a].load(p + t * stride + n);
+            const int q = lane + 32 * a, t = q / G::S, n = (q % G::S) * 4;
+            constexpr bool kAll = kFull && kT * G::S % 32 == 0;
+            if constexpr (!kAll) v[a].zero();
+            if (kAll || (t < nt && n < states)) v[a].load(p + t * stride + n);
         }
     }
     __device__ __forceinline__ void to_shared(float2* s, int lane) const {
 #pragma unroll
         for (int a = 0; a < NA; ++a) {
-            const int q = lane + 32 * a;
-            if (q < kTile * PT) {
-                float4* o = reinterpret_cast<float4*>(s + q * 8);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[i] = make_float4(v[a].get(2 * i), v[a].get(2 * i), v[a].get(2 * i + 1), v[a].get(2 * i + 1));
-            }
+            if (lane + 32 * a >= kT * G::S) break;
+            float4* o = reinterpret_cast<float4*>(s + (lane + 32 * a) * 4);
+            o[0] = make_float4(v[a].get(0), v[a].get(0), v[a].get(1), v[a].get(1));
+            o[1] = make_float4(v[a].get(2), v[a].get(2), v[a].get(3), v[a].get(3));
         }
     }
 };
 
-template <class T, class G>
-struct TileStates<T, G, false> {
-    static constexpr int NA = kTile * G::NP / 32;
+template <class T, class G, int kT>
+struct TileStates<T, G, false, kT> {
+    static constexpr int NA = kT * G::NP / 32;
     T v[NA];
+    template <bool kFull>
     __device__ __forceinline__ void load(const T* p, long long stride, int nt, int states, int lane) {
 #pragma unroll
         for (int a = 0; a < NA; ++a) {
             const int q = lane + 32 * a, t = q / G::NP, n = q % G::NP;
-            v[a] = from_f32<T>(0.0f);
-            if (t < nt && n < states) v[a] = __ldg(p + t * stride + n);
+            if constexpr (!kFull) v[a] = from_f32<T>(0.0f);
+            if (kFull || (t < nt && n < states)) v[a] = __ldg(p + t * stride + n);
         }
     }
     __device__ __forceinline__ void to_shared(float2* s, int lane) const {
@@ -216,7 +288,66 @@ struct TileStates<T, G, false> {
     }
 };
 
-// CPL neighbouring floats of shared memory as channel pairs, and four (v, v) pairs.
+// The elements of a tile in shared memory ([kT][CH], raw or float32), in passes
+// of 128: each lane four channels of one token.
+template <class T, int CH, int kT>
+struct TileElems {
+    static constexpr int LPT = CH / 4;       // lanes per token
+    static constexpr int TP = 128 / CH;      // tokens of a pass
+    static constexpr int NA = kT / TP;       // passes
+    __device__ __forceinline__ static int tok(int a, int lane) { return a * TP + lane / LPT; }
+    __device__ __forceinline__ static int ch(int lane) { return (lane % LPT) * 4; }
+    // s: the pass's first element
+    template <class E>
+    __device__ __forceinline__ static void get(const E* s, f2 (&f)[2], int lane) {
+        Vec<E, 4> q;
+        q.load_rw(s + 4 * lane);
+        f[0] = q.pair(0);
+        f[1] = q.pair(1);
+    }
+    template <bool kVec, bool kFull>
+    __device__ __forceinline__ static void store(T* p, long long stride, const f2 (&f)[2], int a, int nt, int left,
+                                                 int lane) {
+        T* to = p + tok(a, lane) * stride + ch(lane);
+        if (kFull || (tok(a, lane) < nt && ch(lane) < left)) {
+            if constexpr (kVec) {
+                Vec<T, 4> q;
+                q.set_pairs(f);
+                q.store(to);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (kFull || ch(lane) + i < left) to[i] = from_f32<T>(i & 1 ? hi2(f[i / 2]) : lo2(f[i / 2]));
+            }
+        }
+    }
+    // a value per channel, as a lane's elements meet it
+    __device__ __forceinline__ static void per_channel(const float* p, int left, int lane, f2 (&f)[2]) {
+        const int c = ch(lane);
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = p && c + i < left ? __ldg(p + c + i) : 0.0f;
+        f[0] = pack2(v[0], v[1]);
+        f[1] = pack2(v[2], v[3]);
+    }
+};
+
+// kN raw values to float32, by one warp.
+template <class T, int kN>
+__device__ __forceinline__ void put_floats(float* s, const T* raw, int lane) {
+    static_assert(kN % 4 == 0, "fours");
+#pragma unroll
+    for (int i = 0; i < (kN / 4 + 31) / 32; ++i) {
+        const int q = lane + 32 * i;
+        if (kN / 4 % 32 != 0 && q >= kN / 4) break;
+        Vec<T, 4> v;
+        v.load_rw(raw + 4 * q);
+        *reinterpret_cast<ulonglong2*>(s + 4 * q) = make_ulonglong2(v.pair(0), v.pair(1));
+    }
+}
+
+// A lane's channels at one token of a [tokens][CH] array as pairs, and its four
+// states of a [tokens][NP] array of (v, v) pairs.
 template <class G>
 __device__ __forceinline__ void read_channels(const float* s, f2 (&v)[G::PC]) {
     if constexpr (G::PC == 2) {
@@ -235,35 +366,44 @@ __device__ __forceinline__ void read_states(const float2* s, f2 (&v)[4]) {
     v[3] = b.y;
 }
 
-// Sum over the S lanes of a channel group; lane s < CPL of it gets channel s of
+// Sum over the S lanes of a channel group: lane s < CPL of it gets channel s of
 // the lane's CPL (the other lanes copies).
 template <class G>
 __device__ __forceinline__ float sum_states(const f2 (&v)[G::PC], int lane) {
-    float r;
-    if constexpr (G::PC == 2) {
-        const bool b0 = lane & 1, b1 = lane & 2;
-        const float a = lo2(v[0]), b = hi2(v[0]), c = lo2(v[1]), d = hi2(v[1]);
-        const float x = (b0 ? b : a) + __shfl_xor_sync(0xffffffffu, b0 ? a : b, 1);
-        const float y = (b0 ? d : c) + __shfl_xor_sync(0xffffffffu, b0 ? c : d, 1);
-        r = (b1 ? y : x) + __shfl_xor_sync(0xffffffffu, b1 ? x : y, 2);
+    static_assert(G::PC == 2, "four channels");
+    const bool b0 = lane & 1, b1 = lane & 2;
+    const float a = lo2(v[0]), b = hi2(v[0]), c = lo2(v[G::PC - 1]), d = hi2(v[G::PC - 1]);
+    const float x = (b0 ? b : a) + __shfl_xor_sync(0xffffffffu, b0 ? a : b, 1);
+    const float y = (b0 ? d : c) + __shfl_xor_sync(0xffffffffu, b0 ? c : d, 1);
+    float r = (b1 ? y : x) + __shfl_xor_sync(0xffffffffu, b1 ? x : y, 2);
 #pragma unroll
-        for (int m = 4; m < G::S; m <<= 1) r += __shfl_xor_sync(0xffffffffu, r, m);
-    } else {
-        const bool b0 = lane & 1;
-        const float a = lo2(v[0]), b = hi2(v[0]);
-        r = (b0 ? b : a) + __shfl_xor_sync(0xffffffffu, b0 ? a : b, 1);
-    }
+    for (int m = 4; m < G::S; m <<= 1) r += __shfl_xor_sync(0xffffffffu, r, m);
     return r;
 }
-
-// A lane's four states of each of its channels, in rows of NP floats per channel.
+// A lane's part of a sum over states, for TileRows::get_sums; row: the token's.
 template <class G>
-__device__ __forceinline__ void load_lane(const float* p, int left, int lane, float (&v)[G::CPL][4]) {
+__device__ __forceinline__ void put_sums(float* row, const f2 (&v)[G::PC], int lane) {
+    const int s = lane % G::S, c = lane / G::S;
+    if constexpr (!G::kParts) {
+        const float r = sum_states<G>(v, lane);
+        if (s < G::CPL) row[G::CPL * c + s] = r;
+    } else if constexpr (G::PC == 2) {
+        *reinterpret_cast<ulonglong2*>(row + G::place(s, G::CPL * c)) = make_ulonglong2(v[0], v[1]);
+    } else {
+        *reinterpret_cast<f2*>(row + G::place(s, G::CPL * c)) = v[0];
+    }
+}
+
+// A lane's four states of each of its channels in the library's own arrays,
+// [fours of states][channels][4]; p: the warp's first channel of the first four.
+template <class G>
+__device__ __forceinline__ void load_lane(const float* p, long long channels, int left, int lane,
+                                          float (&v)[G::CPL][4]) {
     const int s = lane % G::S, c = lane / G::S;
 #pragma unroll
     for (int j = 0; j < G::CPL; ++j) {
         float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (G::CPL * c + j < left) q = *reinterpret_cast<const float4*>(p + (long long)(G::CPL * c + j) * G::NP + 4 * s);
+        if (G::CPL * c + j < left) q = *reinterpret_cast<const float4*>(p + (s * channels + G::CPL * c + j) * 4);
         v[j][0] = q.x;
         v[j][1] = q.y;
         v[j][2] = q.z;
@@ -271,13 +411,13 @@ __device__ __forceinline__ void load_lane(const float* p, int left, int lane, fl
     }
 }
 template <class G>
-__device__ __forceinline__ void store_lane(float* p, int left, int lane, const f2 (&v)[G::PC][4]) {
+__device__ __forceinline__ void store_lane(float* p, long long channels, int left, int lane, const f2 (&v)[G::PC][4]) {
     const int s = lane % G::S, c = lane / G::S;
 #pragma unroll
     for (int j = 0; j < G::CPL; ++j)
         if (G::CPL * c + j < left) {
             const f2(&r)[4] = v[j / 2];
-            *reinterpret_cast<float4*>(p + (long long)(G::CPL * c + j) * G::NP + 4 * s) =
+            *reinterpret_cast<float4*>(p + (s * channels + G::CPL * c + j) * 4) =
                 j & 1 ? make_float4(hi2(r[0]), hi2(r[1]), hi2(r[2]), hi2(r[3]))
                       : make_float4(lo2(r[0]), lo2(r[1]), lo2(r[2]), lo2(r[3]));
         }
@@ -310,6 +450,13 @@ __device__ __forceinline__ void to_pairs(const float (&v)[G::CPL][4], float scal
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[q][k] = pack2(v[2 * q][k] * scale, v[2 * q + 1][k] * scale);
 }
+template <class G>
+__device__ __forceinline__ void clear(f2 (&v)[G::PC][4]) {
+#pragma unroll
+    for (int q = 0; q < G::PC; ++q)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[q][k] = 0ull;
+}
 
 // Bit t: a segment starts at token t of the tile.
 __device__ __forceinline__ unsigned tile_heads(const uint8_t* row, long long t0, int nt, int lane) {
@@ -323,7 +470,7 @@ __device__ __forceinline__ void fold_chunk(const SsmParams& p, const f2 (&A2)[G:
                                            long long ch0, int left, int lane, f2 (&carry)[G::PC][4]) {
     const long long row = b * p.chunks + j;
     float v[G::CPL][4], d[G::CPL];
-    load_lane<G>(p.carry + (row * p.channels + ch0) * G::NP, left, lane, v);
+    load_lane<G>(p.carry + row * p.channels * G::NP + ch0 * 4, p.channels, left, lane, v);
     const int c = lane / G::S;
 #pragma unroll
     for (int i = 0; i < G::CPL; ++i)
@@ -337,6 +484,19 @@ __device__ __forceinline__ void fold_chunk(const SsmParams& p, const f2 (&A2)[G:
             const f2 a = ex2_2(mul2(pack2(d[2 * q], d[2 * q + 1]), A2[q][k]));
             carry[q][k] = cut ? add : fma2(a, carry[q][k], add);
         }
+}
+// The chunk's own part, left for the others to fold.
+template <class G>
+__device__ __forceinline__ void leave_chunk(const SsmParams& p, long long b, long long chunk, long long ch0, int left,
+                                            int lane, const f2 (&carry)[G::PC][4], const f2 (&sum_d)[G::PC]) {
+    const long long row = b * p.chunks + chunk;
+    store_lane<G>(p.carry + row * p.channels * G::NP + ch0 * 4, p.channels, left, lane, carry);
+    const int c = lane / G::S;
+    if (lane % G::S == 0)
+#pragma unroll
+        for (int j = 0; j < G::CPL; ++j)
+            if (G::CPL * c + j < left)
+                p.sum_d[row * p.channels + ch0 + G::CPL * c + j] = j & 1 ? hi2(sum_d[j / 2]) : lo2(sum_d[j / 2]);
 }
 
 }  // namespace scg

@@ -16,63 +16,64 @@
 // that the forward pass saved at each tile's start.  Nothing of the states is
 // kept per token: a tile's states are recomputed, first in one run that leaves
 // the states at its quarters in shared memory, then quarter by quarter, where q
-// and q h[t-1] of four tokens stay in registers for the way back (in shared
-// memory they would cost more accesses than the second exponential).  The sums
-// over states go across the S lanes of a channel, those over channels across
-// the other lanes, then over the CTA's warps in shared memory, and the rest in
-// a second kernel over the CTAs' partial rows; each in a fixed order.
-// Instruction issue bounds it, then the exponentials.
+// and h of four tokens stay in registers for the way back (in shared memory
+// they would cost more accesses than the second exponential).  Sums over states
+// and over channels go through shared memory, four tokens at a time; the sum
+// over a CTA's warps per tile; and those over CTAs, rows and chunks in kernels
+// of their own over the CTAs' partial rows.  Each in a fixed order.
+// The multipliers bound it: per token and state 14 products and multiply-adds,
+// against 2 exponentials.
 //
 // Rows too few for the machine: the length is split as in the forward pass,
-// with a first kernel that runs each chunk backwards from zero (kSummary).
+// with a first kernel that runs each chunk backwards from zero.
 #pragma once
 #include "sc_ssm.cuh"
 
 namespace scg {
 
-constexpr int kQuarter = 4;
+constexpr int kQuarter = 4;  // tokens kept in registers
+constexpr int kQuarters = kTile / kQuarter;
+constexpr int kBackWarps = 2;  // of a CTA of the first kernel
 
 // A warp's part of the shared memory, in floats.
 template <class G>
 struct BwdShared {
-    static constexpr int kRow = kTile * G::CH, kStates = kTile * G::NP * 2, kHold = G::CPL * 4 * 32;
-    static constexpr int d = 0, u = kRow, g = 2 * kRow, y = 3 * kRow, gu = 4 * kRow, ga = 5 * kRow;
-    static constexpr int B = 6 * kRow, C = B + kStates, h = C + kStates, bc = h + kTile / kQuarter * kHold;
-    static constexpr int kFloats = bc + kTile * 2 * G::NP;
-    static constexpr size_t kBytes = (size_t)kFloats * 4 * G::kWarps;
+    static constexpr int kRow = kTile * G::CH, kSums = G::TP * G::kSumRow, kStates = kTile * G::NP * 2;
+    static constexpr int kHold = G::CPL * 4 * 32;                      // a warp's states
+    static constexpr int d = 0, u = kRow, g = 2 * kRow;                // [kTile][CH]
+    static constexpr int y = 3 * kRow, gu = y + kSums, ga = gu + kSums;  // [TP][kSumRow]
+    static constexpr int B = ga + kSums, C = B + kStates;              // [kTile][NP] pairs
+    static constexpr int h = C + kStates;                              // states before quarters 1 ..
+    static constexpr int bc = h + (kQuarters - 1) * kHold;             // [kQuarter][2][CL][S] fours of dB, dC
+    static constexpr int sums = bc + kQuarter * 2 * 32 * 4;            // [kTile][2][NP]
+    static constexpr int kFloats = sums + kTile * 2 * G::NP;
+    static constexpr size_t kBytes = (size_t)kFloats * 4 * G::kBwdWarps;
 };
 
 // dh of a chunk's first token, taken one token further back, with nothing
 // coming in from behind; and the chunk's sum of d.
 template <class T, class G, bool kVec>
-__global__ void __launch_bounds__(G::kThreads) ssm_back_summary_kernel(SsmParams p, long long blocks_per_group,
-                                                                       int grid_chunks) {
-    using Rows = TileRows<T, G, kVec>;
-    using States = TileStates<T, G, kVec>;
-    __shared__ alignas(16) float s_d[G::kWarps][kTile * G::CH], s_g[G::kWarps][kTile * G::CH];
-    __shared__ alignas(16) float2 s_C[G::kWarps][kTile * G::NP];
-    SsmPlace<G> at(p, blocks_per_group, grid_chunks);
-    if (at.left <= 0) return;
+__global__ void __launch_bounds__(32 * kBackWarps) ssm_back_summary_kernel(SsmParams p, int blocks_per_group,
+                                                                             int grid_chunks) {
+    using Rows = TileRows<T, G, kVec, kTile>;
+    using States = TileStates<T, G, kVec, kTile>;
+    constexpr int kWarps = kBackWarps;
+    __shared__ alignas(16) float s_d[kWarps][kTile * G::CH], s_g[kWarps][kTile * G::CH];
+    __shared__ alignas(16) float2 s_C[kWarps][kTile * G::NP];
+    SsmPlace<G, kWarps> at(p, blocks_per_group, grid_chunks, threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, left = at.left;
+    if (left == 0) return;
     at.chunk += 1;  // nobody waits for the first chunk's
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, left = (int)at.left;
     const int s = lane % G::S, c = lane / G::S;
     const long long b = at.b;
     float raw[G::CPL][4];
-    f2 A2[G::PC][4], dh[G::PC][4], dsum[G::PC];
+    f2 A2[G::PC][4], dh[G::PC][4], dsum[G::PC], bias[2];
     load_lane_of<G>(p.A + at.ch0 * p.states, p.states, left, lane, raw);
     to_pairs<G>(raw, kLog2e, A2);
+    clear<G>(dh);
 #pragma unroll
-    for (int q = 0; q < G::PC; ++q) {
-        dsum[q] = 0ull;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) dh[q][k] = 0ull;
-    }
-    float bias[Rows::kChannels];
-#pragma unroll
-    for (int i = 0; i < Rows::kChannels; ++i) {
-        const int ch = Rows::ch(i, lane);
-        bias[i] = p.dt_bias && ch < left ? p.dt_bias[at.ch0 + ch] : 0.0f;
-    }
+    for (int q = 0; q < G::PC; ++q) dsum[q] = 0ull;
+    Rows::per_channel(p.dt_bias ? p.dt_bias + at.ch0 : nullptr, left, lane, bias);
     const long long tiles = (p.length + kTile - 1) / kTile;
     const long long tile0 = at.chunk * p.chunk_tiles;
     const long long tile1 = tile0 + p.chunk_tiles < tiles ? tile0 + p.chunk_tiles : tiles;
@@ -85,38 +86,43 @@ __global__ void __launch_bounds__(G::kThreads) ssm_back_summary_kernel(SsmParams
     States C;
     auto fetch = [&](long long tile) {
         const long long t0 = tile * kTile;
-        const int nt = (int)(p.length - t0 < kTile ? p.length - t0 : kTile);
-        dt.load(dtp + t0 * p.dt_token, p.dt_token, nt, left, lane);
-        dy.load(dyp + t0 * p.dy_token, p.dy_token, nt, left, lane);
-        if (zp) z.load(zp + t0 * p.z_token, p.z_token, nt, left, lane);
-        C.load(Cp + t0 * p.C_token, p.C_token, nt, (int)p.states, lane);
+        const int nt = tile_tokens<kTile>(p, tile * kTile);
+        dt.template load<false>(dtp + t0 * p.dt_token, p.dt_token, nt, left, lane);
+        dy.template load<false>(dyp + t0 * p.dy_token, p.dy_token, nt, left, lane);
+        if (zp) z.template load<false>(zp + t0 * p.z_token, p.z_token, nt, left, lane);
+        C.template load<false>(Cp + t0 * p.C_token, p.C_token, nt, (int)p.states, lane);
     };
     unsigned cut = 0;
+    const float *ld = s_d[warp] + G::CPL * c, *lg = s_g[warp] + G::CPL * c;
+    const float2* lC = s_C[warp] + 4 * s;
     if (tile0 < tile1) fetch(tile1 - 1);
     for (long long tile = tile1 - 1; tile >= tile0; --tile) {
-        const long long t0 = tile * kTile;
-        const int nt = (int)(p.length - t0 < kTile ? p.length - t0 : kTile);
-        const unsigned hm = tile_heads(heads, t0, nt, lane);
+        const int nt = tile_tokens<kTile>(p, tile * kTile);
+        const unsigned hm = tile_heads(heads, tile * kTile, nt, lane);
         cut |= hm;
-        float fd[Rows::kCount], fg[Rows::kCount];
 #pragma unroll
-        for (int i = 0; i < Rows::kCount; ++i) {
-            const float v = dt.get(i) + bias[Rows::channel_of(i)];
-            fd[i] = Rows::valid(i, lane, nt, left) ? (p.softplus ? softplus(v) : v) : 0.0f;
-            fg[i] = dy.get(i);
-            if (zp) fg[i] *= z.get(i) * sigmoid(z.get(i));
+        for (int a = 0; a < Rows::NA; ++a) {
+            f2 d[2], g[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                d[i] = add2(dt.pair(a, i), bias[i]);
+                if (p.softplus) d[i] = softplus_2(d[i]);
+                g[i] = dy.pair(a, i);
+                if (zp) g[i] = mul2(g[i], mul2(z.pair(a, i), sigmoid_2(z.pair(a, i))));
+            }
+            Rows::template mask<false>(d, a, nt, left, lane);
+            Rows::put(s_d[warp] + a * G::TP * G::CH, d, lane);
+            Rows::put(s_g[warp] + a * G::TP * G::CH, g, lane);
         }
-        Rows::to_shared(s_d[warp], fd, lane);
-        Rows::to_shared(s_g[warp], fg, lane);
         C.to_shared(s_C[warp], lane);
         __syncwarp();
         if (tile > tile0) fetch(tile - 1);
 #pragma unroll 4
         for (int t = kTile - 1; t >= 0; --t) {
             f2 d[G::PC], g[G::PC], Cv[4];
-            read_channels<G>(s_d[warp] + t * G::CH + G::CPL * c, d);
-            read_channels<G>(s_g[warp] + t * G::CH + G::CPL * c, g);
-            read_states(s_C[warp] + t * G::NP + 4 * s, Cv);
+            read_channels<G>(ld + t * G::CH, d);
+            read_channels<G>(lg + t * G::CH, g);
+            read_states(lC + t * G::NP, Cv);
 #pragma unroll
             for (int q = 0; q < G::PC; ++q) {
                 dsum[q] = add2(dsum[q], d[q]);
@@ -124,87 +130,66 @@ __global__ void __launch_bounds__(G::kThreads) ssm_back_summary_kernel(SsmParams
                 for (int k = 0; k < 4; ++k)
                     dh[q][k] = mul2(ex2_2(mul2(d[q], A2[q][k])), fma2(Cv[k], g[q], dh[q][k]));
             }
-            if (hm >> t & 1u) {
-#pragma unroll
-                for (int q = 0; q < G::PC; ++q)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) dh[q][k] = 0ull;
-            }
+            if (hm >> t & 1u) clear<G>(dh);
         }
         __syncwarp();
     }
-    const long long row = b * p.chunks + at.chunk;
-    store_lane<G>(p.carry + (row * p.channels + at.ch0) * G::NP, left, lane, dh);
-    if (s == 0)
-#pragma unroll
-        for (int j = 0; j < G::CPL; ++j)
-            if (G::CPL * c + j < left)
-                p.sum_d[row * p.channels + at.ch0 + G::CPL * c + j] = j & 1 ? hi2(dsum[j / 2]) : lo2(dsum[j / 2]);
-    if (at.cblock == 0 && warp == 0 && lane == 0) p.cut[row] = cut != 0;
+    leave_chunk<G>(p, b, at.chunk, at.ch0, left, lane, dh, dsum);
+    if (at.cblock == 0 && threadIdx.x == 0) p.cut[b * p.chunks + at.chunk] = cut != 0;
 }
 
-// Sums of eight values (four of dB, four of dC) over the lanes along the
-// channels; `base` becomes the index of v[0], and v[0 .. 8 / CL) hold them
-// (8 / CL at least 1).
-template <class G>
-__device__ __forceinline__ int sum_channels(float (&v)[8], int lane) {
-    int base = 0;
-    int n = 8;
+// h = q h[t-1] + d x B over the tokens of a quarter.
+template <class G, bool kHeads>
+__device__ __forceinline__ void run_quarter(const float* ld, const float* lu, const float2* lB, int t0, unsigned hm,
+                                            const f2 (&A2)[G::PC][4], f2 (&h)[G::PC][4]) {
 #pragma unroll
-    for (int m = G::S; m < 32; m <<= 1) {
-        const bool up = lane & m;
-        if (n > 1) {
-            n /= 2;
+    for (int j = 0; j < kQuarter; ++j) {
+        f2 d[G::PC], u[G::PC], Bv[4];
+        read_channels<G>(ld + (t0 + j) * G::CH, d);
+        read_channels<G>(lu + (t0 + j) * G::CH, u);
+        read_states(lB + (t0 + j) * G::NP, Bv);
+        if (kHeads && (hm >> (t0 + j) & 1u)) clear<G>(h);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < n) {
-                    const float keep = up ? v[i + n] : v[i], send = up ? v[i] : v[i + n];
-                    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
-                }
-            base += up ? n : 0;
-        } else {
-            v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
-        }
+        for (int q = 0; q < G::PC; ++q)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) h[q][k] = fma2(ex2_2(mul2(d[q], A2[q][k])), h[q][k], mul2(u[q], Bv[k]));
     }
-    return base;
 }
 
 template <class T, class G, bool kVec>
-__global__ void __launch_bounds__(G::kThreads) ssm_back_kernel(SsmParams p, long long blocks_per_group) {
-    using Rows = TileRows<T, G, kVec>;
-    using States = TileStates<T, G, kVec>;
+__global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p, int blocks_per_group) {
+    using Rows = TileRows<T, G, kVec, kTile>;
+    using States = TileStates<T, G, kVec, kTile>;
     using Sh = BwdShared<G>;
+    constexpr int kWarps = G::kBwdWarps;
     extern __shared__ __align__(16) float s_all[];
-    const SsmPlace<G> at(p, blocks_per_group, p.chunks);
+    const SsmPlace<G, kWarps> at(p, blocks_per_group, p.chunks, threadIdx.x >> 5);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int left = at.left > 0 ? (int)at.left : 0;  // a warp without channels still meets the CTA's barriers
+    const int left = at.left;  // a warp without channels still meets the CTA's barriers
     const int s = lane % G::S, c = lane / G::S;
     const long long b = at.b;
     float* sm = s_all + warp * Sh::kFloats;
-    float4* hold = reinterpret_cast<float4*>(sm + Sh::h) + lane;
+    const float *ld = sm + Sh::d + G::CPL * c, *lu = sm + Sh::u + G::CPL * c, *lg = sm + Sh::g + G::CPL * c;
+    const float2 *lB = reinterpret_cast<const float2*>(sm + Sh::B) + 4 * s,
+                 *lC = reinterpret_cast<const float2*>(sm + Sh::C) + 4 * s;
+    ulonglong2* hold = reinterpret_cast<ulonglong2*>(sm + Sh::h) + lane;
     const long long tiles = (p.length + kTile - 1) / kTile;
     const long long tile0 = at.chunk * p.chunk_tiles;
     const long long tile1 = tile0 + p.chunk_tiles < tiles ? tile0 + p.chunk_tiles : tiles;
 
-    float raw[G::CPL][4];
     f2 A2[G::PC][4], dh[G::PC][4], dA[G::PC][4];
-    load_lane_of<G>(p.A + at.ch0 * p.states, p.states, left, lane, raw);
-    to_pairs<G>(raw, kLog2e, A2);
-    load_lane_of<G>(p.dfinal ? p.dfinal + (b * p.channels + at.ch0) * p.states : nullptr, p.states, left, lane, raw);
-    to_pairs<G>(raw, 1.0f, dh);
-    for (long long j = p.chunks - 1; j > at.chunk; --j) fold_chunk<G>(p, A2, b, j, at.ch0, left, lane, dh);
-#pragma unroll
-    for (int q = 0; q < G::PC; ++q)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) dA[q][k] = 0ull;
-    float bias[Rows::kChannels], D[Rows::kChannels], dD[Rows::kChannels], dbias[Rows::kChannels];
-#pragma unroll
-    for (int i = 0; i < Rows::kChannels; ++i) {
-        const int ch = Rows::ch(i, lane);
-        bias[i] = p.dt_bias && ch < left ? p.dt_bias[at.ch0 + ch] : 0.0f;
-        D[i] = p.D && ch < left ? p.D[at.ch0 + ch] : 0.0f;
-        dD[i] = dbias[i] = 0.0f;
+    {
+        float raw[G::CPL][4];
+        load_lane_of<G>(p.A + at.ch0 * p.states, p.states, left, lane, raw);
+        to_pairs<G>(raw, kLog2e, A2);
+        load_lane_of<G>(p.dfinal ? p.dfinal + (b * p.channels + at.ch0) * p.states : nullptr, p.states, left, lane, raw);
+        to_pairs<G>(raw, 1.0f, dh);
     }
+    for (long long j = p.chunks - 1; j > at.chunk; --j) fold_chunk<G>(p, A2, b, j, at.ch0, left, lane, dh);
+    clear<G>(dA);
+    f2 bias[2], D[2], dD[2] = {0ull, 0ull}, dbias[2] = {0ull, 0ull};
+    Rows::per_channel(p.dt_bias ? p.dt_bias + at.ch0 : nullptr, left, lane, bias);
+    Rows::per_channel(p.D ? p.D + at.ch0 : nullptr, left, lane, D);
     const T* xp = static_cast<const T*>(p.x) + b * p.x_batch + at.ch0;
     const T* dtp = static_cast<const T*>(p.dt) + b * p.dt_batch + at.ch0;
     const T* zp = p.z ? static_cast<const T*>(p.z) + b * p.z_batch + at.ch0 : nullptr;
@@ -216,204 +201,204 @@ __global__ void __launch_bounds__(G::kThreads) ssm_back_kernel(SsmParams p, long
 
     for (long long tile = tile1 - 1; tile >= tile0; --tile) {
         const long long t0 = tile * kTile;
-        const int nt = (int)(p.length - t0 < kTile ? p.length - t0 : kTile);
+        const int nt = tile_tokens<kTile>(p, tile * kTile);
         const unsigned hm = tile_heads(heads, t0, nt, lane);
-        Rows x, dt, z, dy;
         {
+            Rows x, dt, z, dy;
             States B, C;
-            x.load(xp + t0 * p.x_token, p.x_token, nt, left, lane);
-            dt.load(dtp + t0 * p.dt_token, p.dt_token, nt, left, lane);
-            dy.load(dyp + t0 * p.dy_token, p.dy_token, nt, left, lane);
-            if (zp) z.load(zp + t0 * p.z_token, p.z_token, nt, left, lane);
-            B.load(Bp + t0 * p.B_token, p.B_token, nt, (int)p.states, lane);
-            C.load(Cp + t0 * p.C_token, p.C_token, nt, (int)p.states, lane);
-            float fd[Rows::kCount], fu[Rows::kCount], fg[Rows::kCount];
+            dt.template load<false>(dtp + t0 * p.dt_token, p.dt_token, nt, left, lane);
+            x.template load<false>(xp + t0 * p.x_token, p.x_token, nt, left, lane);
+            dy.template load<false>(dyp + t0 * p.dy_token, p.dy_token, nt, left, lane);
+            if (zp) z.template load<false>(zp + t0 * p.z_token, p.z_token, nt, left, lane);
+            B.template load<false>(Bp + t0 * p.B_token, p.B_token, nt, (int)p.states, lane);
+            C.template load<false>(Cp + t0 * p.C_token, p.C_token, nt, (int)p.states, lane);
 #pragma unroll
-            for (int i = 0; i < Rows::kCount; ++i) {
-                const float v = dt.get(i) + bias[Rows::channel_of(i)];
-                fd[i] = Rows::valid(i, lane, nt, left) ? (p.softplus ? softplus(v) : v) : 0.0f;
-                fu[i] = fd[i] * x.get(i);
-                fg[i] = dy.get(i);
-                if (zp) fg[i] *= z.get(i) * sigmoid(z.get(i));
+            for (int a = 0; a < Rows::NA; ++a) {
+                f2 d[2], u[2], g[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    d[i] = add2(dt.pair(a, i), bias[i]);
+                    if (p.softplus) d[i] = softplus_2(d[i]);
+                    g[i] = dy.pair(a, i);
+                    if (zp) g[i] = mul2(g[i], mul2(z.pair(a, i), sigmoid_2(z.pair(a, i))));
+                }
+                Rows::template mask<false>(d, a, nt, left, lane);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) u[i] = mul2(d[i], x.pair(a, i));
+                Rows::put(sm + Sh::d + a * G::TP * G::CH, d, lane);
+                Rows::put(sm + Sh::u + a * G::TP * G::CH, u, lane);
+                Rows::put(sm + Sh::g + a * G::TP * G::CH, g, lane);
             }
-            Rows::to_shared(sm + Sh::d, fd, lane);
-            Rows::to_shared(sm + Sh::u, fu, lane);
-            Rows::to_shared(sm + Sh::g, fg, lane);
             B.to_shared(reinterpret_cast<float2*>(sm + Sh::B), lane);
             C.to_shared(reinterpret_cast<float2*>(sm + Sh::C), lane);
         }
-        const float2* sB = reinterpret_cast<const float2*>(sm + Sh::B);
-        const float2* sC = reinterpret_cast<const float2*>(sm + Sh::C);
-        f2 h[G::PC][4];
-        load_lane<G>(p.saved + ((b * tiles + tile) * p.channels + at.ch0) * G::NP, left, lane, raw);
-        to_pairs<G>(raw, 1.0f, h);
+        const float* saved = p.saved + (b * tiles + tile) * p.channels * G::NP + at.ch0 * 4;
         __syncwarp();
-        // the states before each quarter
+        auto work = [&](auto with_heads) {
+            constexpr bool kHeads = decltype(with_heads)::value;
+            {   // the states before quarters 1, 2, ...
+                f2 h[G::PC][4];
+                float raw[G::CPL][4];
+                load_lane<G>(saved, p.channels, left, lane, raw);
+                to_pairs<G>(raw, 1.0f, h);
 #pragma unroll 1
-        for (int q4 = 0; q4 < kTile / kQuarter; ++q4) {
+                for (int q4 = 0; q4 < kQuarters - 1; ++q4) {
+                    run_quarter<G, kHeads>(ld, lu, lB, q4 * kQuarter, hm, A2, h);
 #pragma unroll
-            for (int q = 0; q < G::PC; ++q) {
-                hold[(q4 * G::CPL + 2 * q) * 32] = make_float4(lo2(h[q][0]), hi2(h[q][0]), lo2(h[q][1]), hi2(h[q][1]));
-                hold[(q4 * G::CPL + 2 * q + 1) * 32] =
-                    make_float4(lo2(h[q][2]), hi2(h[q][2]), lo2(h[q][3]), hi2(h[q][3]));
-            }
-            if (q4 == kTile / kQuarter - 1) break;
-#pragma unroll
-            for (int j = 0; j < kQuarter; ++j) {
-                const int t = q4 * kQuarter + j;
-                f2 d[G::PC], u[G::PC], Bv[4];
-                read_channels<G>(sm + Sh::d + t * G::CH + G::CPL * c, d);
-                read_channels<G>(sm + Sh::u + t * G::CH + G::CPL * c, u);
-                read_states(sB + t * G::NP + 4 * s, Bv);
-                const bool head = hm >> t & 1u;
-#pragma unroll
-                for (int q = 0; q < G::PC; ++q)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        h[q][k] = fma2(ex2_2(mul2(d[q], A2[q][k])), head ? 0ull : h[q][k], mul2(u[q], Bv[k]));
-            }
-        }
-#pragma unroll 1
-        for (int q4 = kTile / kQuarter - 1; q4 >= 0; --q4) {
-            f2 a[kQuarter][G::PC][4], ah[kQuarter][G::PC][4];  // q and q h[t-1]
-#pragma unroll
-            for (int q = 0; q < G::PC; ++q) {
-                const float4 v = hold[(q4 * G::CPL + 2 * q) * 32], w = hold[(q4 * G::CPL + 2 * q + 1) * 32];
-                h[q][0] = pack2(v.x, v.y);
-                h[q][1] = pack2(v.z, v.w);
-                h[q][2] = pack2(w.x, w.y);
-                h[q][3] = pack2(w.z, w.w);
-            }
-#pragma unroll
-            for (int j = 0; j < kQuarter; ++j) {
-                const int t = q4 * kQuarter + j;
-                f2 d[G::PC], u[G::PC], Bv[4];
-                read_channels<G>(sm + Sh::d + t * G::CH + G::CPL * c, d);
-                read_channels<G>(sm + Sh::u + t * G::CH + G::CPL * c, u);
-                read_states(sB + t * G::NP + 4 * s, Bv);
-                const bool head = hm >> t & 1u;
-#pragma unroll
-                for (int q = 0; q < G::PC; ++q)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        a[j][q][k] = ex2_2(mul2(d[q], A2[q][k]));
-                        ah[j][q][k] = head ? 0ull : mul2(a[j][q][k], h[q][k]);
-                        h[q][k] = fma2(u[q], Bv[k], ah[j][q][k]);
-                    }
-            }
-#pragma unroll
-            for (int j = kQuarter - 1; j >= 0; --j) {
-                const int t = q4 * kQuarter + j;
-                f2 d[G::PC], u[G::PC], g[G::PC], Bv[4], Cv[4];
-                read_channels<G>(sm + Sh::d + t * G::CH + G::CPL * c, d);
-                read_channels<G>(sm + Sh::u + t * G::CH + G::CPL * c, u);
-                read_channels<G>(sm + Sh::g + t * G::CH + G::CPL * c, g);
-                read_states(sB + t * G::NP + 4 * s, Bv);
-                read_states(sC + t * G::NP + 4 * s, Cv);
-                f2 y[G::PC], gu[G::PC], ga[G::PC], dB[4], dC[4];
-#pragma unroll
-                for (int q = 0; q < G::PC; ++q) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        dh[q][k] = fma2(Cv[k], g[q], dh[q][k]);
-                        const f2 ht = fma2(u[q], Bv[k], ah[j][q][k]);
-                        const f2 r = mul2(dh[q][k], ah[j][q][k]);
-                        y[q] = k ? fma2(Cv[k], ht, y[q]) : mul2(Cv[k], ht);
-                        gu[q] = k ? fma2(dh[q][k], Bv[k], gu[q]) : mul2(dh[q][k], Bv[k]);
-                        ga[q] = k ? fma2(r, A2[q][k], ga[q]) : mul2(r, A2[q][k]);
-                        dA[q][k] = fma2(r, d[q], dA[q][k]);
-                        dC[k] = q ? fma2(g[q], ht, dC[k]) : mul2(g[q], ht);
-                        dB[k] = q ? fma2(dh[q][k], u[q], dB[k]) : mul2(dh[q][k], u[q]);
-                        dh[q][k] = mul2(dh[q][k], a[j][q][k]);
+                    for (int q = 0; q < G::PC; ++q) {
+                        hold[(q4 * G::CPL + 2 * q) * 32] = make_ulonglong2(h[q][0], h[q][1]);
+                        hold[(q4 * G::CPL + 2 * q + 1) * 32] = make_ulonglong2(h[q][2], h[q][3]);
                     }
                 }
-                if (hm >> t & 1u) {
+            }
+#pragma unroll 1
+            for (int q4 = kQuarters - 1; q4 >= 0; --q4) {
+                const int tq = q4 * kQuarter;
+                f2 a[kQuarter][G::PC][4], h[kQuarter + 1][G::PC][4];  // q, and h before each token
+                if (q4 == 0) {
+                    float raw[G::CPL][4];
+                    load_lane<G>(saved, p.channels, left, lane, raw);
+                    to_pairs<G>(raw, 1.0f, h[0]);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < G::PC; ++q) {
+                        const ulonglong2 v = hold[((q4 - 1) * G::CPL + 2 * q) * 32];
+                        const ulonglong2 w = hold[((q4 - 1) * G::CPL + 2 * q + 1) * 32];
+                        h[0][q][0] = v.x;
+                        h[0][q][1] = v.y;
+                        h[0][q][2] = w.x;
+                        h[0][q][3] = w.y;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kQuarter; ++j) {
+                    f2 d[G::PC], u[G::PC], Bv[4];
+                    read_channels<G>(ld + (tq + j) * G::CH, d);
+                    read_channels<G>(lu + (tq + j) * G::CH, u);
+                    read_states(lB + (tq + j) * G::NP, Bv);
+                    const bool head = kHeads && (hm >> (tq + j) & 1u);
 #pragma unroll
                     for (int q = 0; q < G::PC; ++q)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) dh[q][k] = 0ull;
+                        for (int k = 0; k < 4; ++k) {
+                            a[j][q][k] = ex2_2(mul2(d[q], A2[q][k]));
+                            h[j + 1][q][k] = fma2(a[j][q][k], head ? 0ull : h[j][q][k], mul2(u[q], Bv[k]));
+                        }
                 }
-                const float sy = sum_states<G>(y, lane), su = sum_states<G>(gu, lane), sa = sum_states<G>(ga, lane);
-                if (s < G::CPL) {
-                    const int o = t * G::CH + G::CPL * c + s;
-                    sm[Sh::y + o] = sy;
-                    sm[Sh::gu + o] = su;
-                    sm[Sh::ga + o] = sa;
-                }
-                float bc[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    bc[k] = lo2(dB[k]) + hi2(dB[k]);
-                    bc[4 + k] = lo2(dC[k]) + hi2(dC[k]);
-                }
-                const int base = sum_channels<G>(bc, lane);
-                constexpr int kHeld = G::CL >= 8 ? 1 : 8 / G::CL;
-                if (G::CL <= 8 || lane < 16) {
+                for (int j = kQuarter - 1; j >= 0; --j) {
+                    const int t = tq + j;
+                    const bool head = kHeads && (hm >> t & 1u);
+                    f2 d[G::PC], u[G::PC], g[G::PC], Bv[4], Cv[4];
+                    read_channels<G>(ld + t * G::CH, d);
+                    read_channels<G>(lu + t * G::CH, u);
+                    read_channels<G>(lg + t * G::CH, g);
+                    read_states(lB + t * G::NP, Bv);
+                    read_states(lC + t * G::NP, Cv);
+                    f2 y[G::PC], gu[G::PC], ga[G::PC], dB[4], dC[4];
 #pragma unroll
-                    for (int i = 0; i < kHeld; ++i) {
-                        const int v = base + i;  // dB of state v, or dC of state v - 4
-                        sm[Sh::bc + (t * 2 + (v >> 2)) * G::NP + 4 * s + (v & 3)] = bc[i];
+                    for (int q = 0; q < G::PC; ++q) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const f2 ht = h[j + 1][q][k];
+                            dh[q][k] = fma2(Cv[k], g[q], dh[q][k]);
+                            y[q] = k ? fma2(Cv[k], ht, y[q]) : mul2(Cv[k], ht);
+                            dC[k] = q ? fma2(g[q], ht, dC[k]) : mul2(g[q], ht);
+                            gu[q] = k ? fma2(dh[q][k], Bv[k], gu[q]) : mul2(dh[q][k], Bv[k]);
+                            dB[k] = q ? fma2(dh[q][k], u[q], dB[k]) : mul2(dh[q][k], u[q]);
+                            dh[q][k] = head ? 0ull : mul2(dh[q][k], a[j][q][k]);
+                            const f2 r = mul2(dh[q][k], head ? 0ull : h[j][q][k]);
+                            ga[q] = k ? fma2(r, A2[q][k], ga[q]) : mul2(r, A2[q][k]);
+                            dA[q][k] = fma2(r, d[q], dA[q][k]);
+                        }
+                    }
+                    const int row = (t % G::TP) * G::kSumRow;
+                    put_sums<G>(sm + Sh::y + row, y, lane);
+                    put_sums<G>(sm + Sh::gu + row, gu, lane);
+                    put_sums<G>(sm + Sh::ga + row, ga, lane);
+                    float4* o = reinterpret_cast<float4*>(sm + Sh::bc) + j * 64 + lane;  // lane = c * S + s
+                    o[0] = make_float4(lo2(dB[0]) + hi2(dB[0]), lo2(dB[1]) + hi2(dB[1]), lo2(dB[2]) + hi2(dB[2]),
+                                       lo2(dB[3]) + hi2(dB[3]));
+                    o[32] = make_float4(lo2(dC[0]) + hi2(dC[0]), lo2(dC[1]) + hi2(dC[1]), lo2(dC[2]) + hi2(dC[2]),
+                                        lo2(dC[3]) + hi2(dC[3]));
+                }
+                __syncwarp();
+                // the quarter's dB and dC over the warp's channels: four states (o) of one token and kind at a time
+#pragma unroll
+                for (int o = lane; o < kQuarter * 2 * G::S; o += 32) {
+                    const int kind = o / G::S;  // token * 2 + (0: dB, 1: dC)
+                    const ulonglong2* in = reinterpret_cast<const ulonglong2*>(sm + Sh::bc) + kind * 32 + o % G::S;
+                    ulonglong2 v = in[kind % G::CL * G::S];
+#pragma unroll
+                    for (int i = 1; i < G::CL; ++i) {  // starting points apart: the kinds meet in no bank
+                        const ulonglong2 w = in[(kind + i) % G::CL * G::S];
+                        v.x = add2(v.x, w.x);
+                        v.y = add2(v.y, w.y);
+                    }
+                    reinterpret_cast<ulonglong2*>(sm + Sh::sums)[tq * 2 * G::S + o] = v;
+                }
+                if (tq % G::TP == 0) {  // the pass's elements
+                    const int pa = tq / G::TP;
+                    const auto rx = Rows::template fetch<false>(xp + t0 * p.x_token, p.x_token, pa, nt, left, lane);
+                    const auto rt = Rows::template fetch<false>(dtp + t0 * p.dt_token, p.dt_token, pa, nt, left, lane);
+                    const auto ry = Rows::template fetch<false>(dyp + t0 * p.dy_token, p.dy_token, pa, nt, left, lane);
+                    f2 y[2], gu[2], ga[2], d[2], g[2], dd[2];
+                    Rows::get_sums(sm + Sh::gu, gu, lane);
+                    Rows::get_sums(sm + Sh::ga, ga, lane);
+                    Rows::get(sm + Sh::d + tq * G::CH, d, lane);
+                    Rows::get(sm + Sh::g + tq * G::CH, g, lane);
+                    const long long o = orow + t0 * p.channels;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const f2 x = Rows::pair_of(rx, i);
+                        dd[i] = fma2(gu[i], x, mul2(ga[i], both(kLn2)));
+                        if (p.softplus) dd[i] = mul2(dd[i], sigmoid_2(add2(Rows::pair_of(rt, i), bias[i])));
+                        gu[i] = fma2(gu[i], d[i], mul2(g[i], D[i]));  // dx
+                        dD[i] = fma2(g[i], x, dD[i]);
+                    }
+                    Rows::template store<false>(static_cast<T*>(p.dx) + o, p.channels, gu, pa, nt, left, lane);
+                    Rows::template store<false>(static_cast<T*>(p.ddt) + o, p.channels, dd, pa, nt, left, lane);
+                    Rows::template mask<false>(dd, pa, nt, left, lane);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) dbias[i] = add2(dbias[i], dd[i]);
+                    if (zp) {
+                        const auto rz = Rows::template fetch<false>(zp + t0 * p.z_token, p.z_token, pa, nt, left, lane);
+                        Rows::get_sums(sm + Sh::y, y, lane);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const f2 z = Rows::pair_of(rz, i), sg = sigmoid_2(z);
+                            const f2 slope = mul2(sg, fma2(z, fma2(sg, both(-1.0f), both(1.0f)), both(1.0f)));
+                            y[i] = mul2(mul2(Rows::pair_of(ry, i), fma2(D[i], Rows::pair_of(rx, i), y[i])), slope);
+                        }
+                        Rows::template store<false>(static_cast<T*>(p.dz) + o, p.channels, y, pa, nt, left, lane);
                     }
                 }
+                __syncwarp();
             }
-        }
-        __syncwarp();
-        {
-            float fy[Rows::kCount], fu[Rows::kCount], fa[Rows::kCount], fd[Rows::kCount], fg[Rows::kCount];
-            Rows::from_shared(sm + Sh::y, fy, lane);
-            Rows::from_shared(sm + Sh::gu, fu, lane);
-            Rows::from_shared(sm + Sh::ga, fa, lane);
-            Rows::from_shared(sm + Sh::d, fd, lane);
-            Rows::from_shared(sm + Sh::g, fg, lane);
-#pragma unroll
-            for (int i = 0; i < Rows::kCount; ++i) {
-                const int ch = Rows::channel_of(i);
-                const bool ok = Rows::valid(i, lane, nt, left);
-                const float xi = x.get(i);
-                if (zp) {
-                    const float zi = z.get(i), sg = sigmoid(zi);
-                    fy[i] = dy.get(i) * fmaf(D[ch], xi, fy[i]) * sg * fmaf(zi, 1.0f - sg, 1.0f);  // dz
-                }
-                float dd = fmaf(fu[i], xi, fa[i] * kLn2);
-                if (p.softplus) dd *= sigmoid(dt.get(i) + bias[ch]);
-                fu[i] = fmaf(fu[i], fd[i], fg[i] * D[ch]);  // dx
-                fa[i] = dd;
-                if (ok) {
-                    dbias[ch] += dd;
-                    dD[ch] = fmaf(fg[i], xi, dD[ch]);
-                }
-            }
-            const long long o = orow + t0 * p.channels;
-            Rows::store(static_cast<T*>(p.dx) + o, p.channels, fu, nt, left, lane);
-            Rows::store(static_cast<T*>(p.ddt) + o, p.channels, fa, nt, left, lane);
-            if (zp) Rows::store(static_cast<T*>(p.dz) + o, p.channels, fy, nt, left, lane);
-        }
+        };
+        if (hm) work(std::true_type{});
+        else work(std::false_type{});
         __syncthreads();
-        float* part = p.part_bc + ((at.cblock * p.batch + b) * p.length + t0) * 2 * G::NP;
-        for (int i = threadIdx.x; i < nt * 2 * G::NP; i += G::kThreads) {
-            float sum = s_all[Sh::bc + i];
+        float4* part = reinterpret_cast<float4*>(p.part_bc + ((at.cblock * p.batch + b) * p.length + t0) * 2 * G::NP);
+        for (int i = threadIdx.x; i < nt * 2 * G::S; i += 32 * kWarps) {
+            float4 sum = reinterpret_cast<const float4*>(s_all + Sh::sums)[i];
 #pragma unroll
-            for (int w = 1; w < G::kWarps; ++w) sum += s_all[w * Sh::kFloats + Sh::bc + i];
+            for (int w = 1; w < kWarps; ++w) {
+                const float4 v = reinterpret_cast<const float4*>(s_all + w * Sh::kFloats + Sh::sums)[i];
+                sum.x += v.x;
+                sum.y += v.y;
+                sum.z += v.z;
+                sum.w += v.w;
+            }
             part[i] = sum;
         }
         __syncthreads();
     }
-    if (left <= 0) return;
-    const long long row = b * p.chunks + at.chunk;
-    store_lane<G>(p.part_a + (row * p.channels + at.ch0) * G::NP, left, lane, dA);
-    {
-        const long long rows = p.batch * p.chunks;
-        Rows::sum_tokens(dD, lane);
-        const bool mine = Rows::sum_tokens(dbias, lane);
-#pragma unroll
-        for (int i = 0; i < Rows::kChannels; ++i) {
-            const int ch = Rows::ch(i, lane);
-            if (mine && ch < left) {
-                p.part_d[row * p.channels + at.ch0 + ch] = dD[i];
-                p.part_d[(rows + row) * p.channels + at.ch0 + ch] = dbias[i];
-            }
-        }
-    }
+    if (left == 0) return;
+    const long long row = b * p.chunks + at.chunk, rows = p.batch * p.chunks;
+    store_lane<G>(p.part_a + row * p.channels * G::NP + at.ch0 * 4, p.channels, left, lane, dA);
+    Rows::put_channel_sums(p.part_d + row * p.channels + at.ch0, dD, left, lane);
+    Rows::put_channel_sums(p.part_d + (rows + row) * p.channels + at.ch0, dbias, left, lane);
     if (p.dstate && at.chunk == 0)
         store_lane_of<G>(p.dstate + (b * p.channels + at.ch0) * p.states, p.states, left, lane, dh);
 }
@@ -438,16 +423,20 @@ __global__ void __launch_bounds__(256) ssm_back_bc_kernel(SsmParams p, long long
 
 template <class T, class G, bool kVec>
 cudaError_t ssm_back_of(const SsmParams& p, const SsmPlan& plan, int* launches, cudaStream_t s) {
-    const long long ncb = plan.blocks_per_group * p.groups;
-    *launches = p.chunks > 1 ? 4 : 3;
-    if (p.chunks > 1)
-        ssm_back_summary_kernel<T, G, kVec><<<(unsigned)(ncb * (p.chunks - 1) * p.batch), G::kThreads, 0, s>>>(
-            p, plan.blocks_per_group, p.chunks - 1);
+    const long long per = p.channels / p.groups;
+    *launches = p.chunks > 1 ? 4 : 3;  // with the last sums, which the caller launches
+    if (p.chunks > 1) {
+        const long long block = kBackWarps * G::CH;
+        const int bpg = (int)((per + block - 1) / block);
+        ssm_back_summary_kernel<T, G, kVec>
+            <<<(unsigned)(bpg * p.groups * (p.chunks - 1) * p.batch), 32 * kBackWarps, 0, s>>>(p, bpg, p.chunks - 1);
+    }
     auto kernel = ssm_back_kernel<T, G, kVec>;
     constexpr size_t bytes = BwdShared<G>::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(ncb * p.chunks * p.batch), G::kThreads, bytes, s>>>(p, plan.blocks_per_group);
+    const int bpg = (int)plan.blocks_per_group;
+    kernel<<<(unsigned)(bpg * p.groups * p.chunks * p.batch), 32 * G::kBwdWarps, bytes, s>>>(p, bpg);
     const long long n = p.batch * p.length * p.groups * p.states;
     ssm_back_bc_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, plan.blocks_per_group, G::NP);
     return cudaGetLastError();

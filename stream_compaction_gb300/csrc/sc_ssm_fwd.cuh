@@ -1,11 +1,19 @@
 // Forward selective scan.
 //
 // Per token, channel and state: one exponential, two products and two
-// multiply-adds; per token and channel 4 elements of memory.  With 16 states the
-// exponentials bound it (32 a clock and SM), close to the memory's time.  The
-// tile of a warp is staged through shared memory by the warp itself (no CTA
-// barrier): the next tile's elements travel to registers while this one is
-// computed.
+// multiply-adds; per token and channel 4 elements of memory, a softplus and a
+// SiLU.  With 16 states a warp's 32 channels take, per token, 64 clocks of its
+// SM quarter's exponentials and as many of its multipliers (measured rates: 8
+// exponentials, 32 multiply-adds a clock), and another 16 and 12 for the
+// softplus and the SiLU.
+//
+// Two warps share 32 channels (of up to 16 states; 16 of up to 32, 8 of up to
+// 64).  The element warp reads x, dt, B and C, makes d = softplus(..) and d * x
+// and lays them out in shared memory one tile of kT tokens ahead, and turns the
+// sums over states of the tile before into y; the token warp runs the
+// recurrence, a lane one channel and 16 of its states.  One barrier a tile.  The
+// raw elements are copied asynchronously, several tiles ahead, so that enough
+// bytes are under way.
 //
 // Where rows x channels give the machine too few warps the length is split
 // into chunks: a first kernel scans each chunk from a zero state (kSummary: no
@@ -17,175 +25,411 @@
 
 namespace scg {
 
-template <class T, class G, bool kVec, bool kSummary>
-__global__ void __launch_bounds__(G::kThreads) ssm_kernel(SsmParams p, long long blocks_per_group, int grid_chunks) {
-    using Rows = TileRows<T, G, kVec>;
-    using States = TileStates<T, G, kVec>;
-    __shared__ alignas(16) float s_d[G::kWarps][kTile * G::CH], s_u[G::kWarps][kTile * G::CH];
-    __shared__ alignas(16) float s_y[kSummary ? 1 : G::kWarps][kSummary ? 4 : kTile * G::CH];
-    __shared__ alignas(16) float2 s_B[G::kWarps][kTile * G::NP];
-    __shared__ alignas(16) float2 s_C[kSummary ? 1 : G::kWarps][kSummary ? 2 : kTile * G::NP];
-    const SsmPlace<G> at(p, blocks_per_group, grid_chunks);
-    if (at.left <= 0) return;  // warps of a CTA do not meet
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, left = (int)at.left;
-    const int s = lane % G::S, c = lane / G::S;
-    const long long b = at.b;
+// 16, or 4, bytes on their way from memory to shared memory.
+__device__ __forceinline__ void copy16(void* s, const void* g) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(s)), "l"(g)
+                 : "memory");
+}
+__device__ __forceinline__ void copy4(void* s, const void* g) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((unsigned)__cvta_generic_to_shared(s)), "l"(g)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>  // until at most kLeft groups are on their way
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
 
-    float raw[G::CPL][4];
-    f2 A2[G::PC][4], h[G::PC][4];
-    load_lane_of<G>(p.A + at.ch0 * p.states, p.states, left, lane, raw);
-    to_pairs<G>(raw, kLog2e, A2);
-    if constexpr (kSummary) {
-#pragma unroll
-        for (int q = 0; q < G::PC; ++q)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) h[q][k] = 0ull;
-    } else {
-        load_lane_of<G>(p.state ? p.state + (b * p.channels + at.ch0) * p.states : nullptr, p.states, left, lane, raw);
-        to_pairs<G>(raw, 1.0f, h);
-        for (long long j = 0; j < at.chunk; ++j) fold_chunk<G>(p, A2, b, j, at.ch0, left, lane, h);
-    }
-    float bias[Rows::kChannels], D[Rows::kChannels];
-#pragma unroll
-    for (int i = 0; i < Rows::kChannels; ++i) {
-        const int ch = Rows::ch(i, lane);
-        bias[i] = p.dt_bias && ch < left ? p.dt_bias[at.ch0 + ch] : 0.0f;
-        D[i] = p.D && ch < left ? p.D[at.ch0 + ch] : 0.0f;
-    }
+// A lane's share: SP states of one channel; S lanes share a channel.
+template <int SP_, int S_>
+struct FwdGeo {
+    static constexpr int SP = SP_, S = S_, P = SP / 2;  // pairs of states
+    static constexpr int CH = 32 / S;                   // channels of a warp: lane = s * CH + channel
+    static constexpr int NP = SP * S;                   // padded states
+    static constexpr int kT = CH == 8 ? 16 : 8;         // tokens that the warps hand over at a time
+};
 
-    const long long tiles = (p.length + kTile - 1) / kTile;
-    const long long tile0 = at.chunk * p.chunk_tiles;
-    const long long tile1 = tile0 + p.chunk_tiles < tiles ? tile0 + p.chunk_tiles : tiles;
-    const T* xp = static_cast<const T*>(p.x) + b * p.x_batch + at.ch0;
-    const T* dtp = static_cast<const T*>(p.dt) + b * p.dt_batch + at.ch0;
-    const T* zp = p.z && !kSummary ? static_cast<const T*>(p.z) + b * p.z_batch + at.ch0 : nullptr;
-    const T* Bp = static_cast<const T*>(p.B) + b * p.B_batch + at.group * p.B_group;
-    const T* Cp = static_cast<const T*>(p.C) + b * p.C_batch + at.group * p.C_group;
-    T* yp = kSummary ? nullptr : static_cast<T*>(p.y) + b * p.y_batch + at.ch0;
-    const uint8_t* heads = p.heads ? p.heads + b * p.length : nullptr;
+// The forward kernel's shared memory, in bytes.
+template <class T, class G, bool kSummary>
+struct FwdShared {
+    static constexpr int kT = G::kT;
+    // tiles of raw elements under way or in use: two behind, the rest ahead
+    static constexpr int kRing = sizeof(T) == 4 || G::S == 4 ? 4 : 6;
+    static constexpr int kRow = kT * G::CH, kStates = kT * G::NP;
+    static constexpr int kRawX = kRow * (int)sizeof(T), kRawB = kStates * (int)sizeof(T);
+    static constexpr int x = 0, dt = kRawX, z = 2 * kRawX, B = 3 * kRawX, C = B + kRawB, kRaw = C + kRawB;  // a ring place
+    static constexpr int du = kRing * kRaw;                     // [2][kT][CH] of (d, d, d x, d x)
+    static constexpr int fB = du + 2 * kRow * 16, fC = fB + 2 * kStates * 4;  // [2][kT][NP]
+    static constexpr int y = fC + (kSummary ? 0 : 2 * kStates * 4);           // [2][kT][CH]
+    static constexpr int kBytes = y + (kSummary ? 0 : 2 * kRow * 4);
+    // Place of a channel's (d, d, d x, d x) in its token's row: neither the four
+    // channels that an element lane writes nor the eight that a quarter of the
+    // token warp reads meet in a bank.
+    __device__ __forceinline__ static int place(int ch) { return ch ^ (ch >> 3); }
+};
 
-    Rows x, dt, z;
-    States B, C;
-    auto fetch = [&](long long tile) {
-        const long long t0 = tile * kTile;
-        const int nt = (int)(p.length - t0 < kTile ? p.length - t0 : kTile);
-        x.load(xp + t0 * p.x_token, p.x_token, nt, left, lane);
-        dt.load(dtp + t0 * p.dt_token, p.dt_token, nt, left, lane);
-        B.load(Bp + t0 * p.B_token, p.B_token, nt, (int)p.states, lane);
-        if constexpr (!kSummary) {
-            if (zp) z.load(zp + t0 * p.z_token, p.z_token, nt, left, lane);
-            C.load(Cp + t0 * p.C_token, p.C_token, nt, (int)p.states, lane);
-        }
-    };
-    f2 dsum[G::PC];
+// Copies of kRows rows of kCols elements, `stride` apart in memory, to a dense
+// array in shared memory by one warp, tile after tile; rows from nt on and
+// columns from `cols` on get zeros (kFull: there are none).  kVec: row starts
+// and cols in 16-byte steps.
+template <class T, int kRows, int kCols, bool kVec>
+struct RowCopy {
+    static constexpr int kPer = kVec ? 16 / (int)sizeof(T) : 1;  // elements of one copy
+    static constexpr int kLine = kCols / kPer, kAll = kRows * kLine;
+    static_assert(kCols % kPer == 0, "whole copies");
+    static_assert(kLine <= 32 ? 32 % kLine == 0 : kLine % 32 == 0, "lanes keep their columns");
+    const T* at;
+    long long stride;
+    __device__ __forceinline__ RowCopy(const T* p, long long token, int lane)
+        : at(p + lane / kLine * token + lane % kLine * kPer), stride(token) {}
+    template <bool kFull>
+    __device__ __forceinline__ void run(T* s, int nt, int cols, int lane) {
+        T* to0 = s + lane * kPer;
 #pragma unroll
-    for (int q = 0; q < G::PC; ++q) dsum[q] = 0ull;
-    unsigned cut = 0;
-    if (tile0 < tile1) fetch(tile0);
-    for (long long tile = tile0; tile < tile1; ++tile) {
-        const long long t0 = tile * kTile;
-        const int nt = (int)(p.length - t0 < kTile ? p.length - t0 : kTile);
-        const unsigned hm = tile_heads(heads, t0, nt, lane);
-        cut |= hm;
-        {
-            float fd[Rows::kCount], fu[Rows::kCount];
-#pragma unroll
-            for (int i = 0; i < Rows::kCount; ++i) {
-                const float v = dt.get(i) + bias[Rows::channel_of(i)];
-                // d of a token past the end is 0, whatever the bias
-                fd[i] = Rows::valid(i, lane, nt, left) ? (p.softplus ? softplus(v) : v) : 0.0f;
-                fu[i] = fd[i] * x.get(i);
-            }
-            Rows::to_shared(s_d[warp], fd, lane);
-            Rows::to_shared(s_u[warp], fu, lane);
-            B.to_shared(s_B[warp], lane);
-            if constexpr (!kSummary) C.to_shared(s_C[warp], lane);
-        }
-        const Rows xc = x, zc = z;
-        if (!kSummary && p.saved)
-            store_lane<G>(p.saved + ((b * tiles + tile) * p.channels + at.ch0) * G::NP, left, lane, h);
-        __syncwarp();
-        if (tile + 1 < tile1) fetch(tile + 1);
-#pragma unroll 4
-        for (int t = 0; t < kTile; ++t) {
-            f2 d[G::PC], u[G::PC], Bv[4], acc[G::PC];
-            read_channels<G>(s_d[warp] + t * G::CH + G::CPL * c, d);
-            read_channels<G>(s_u[warp] + t * G::CH + G::CPL * c, u);
-            read_states(s_B[warp] + t * G::NP + 4 * s, Bv);
-            if (hm >> t & 1u) {
-#pragma unroll
-                for (int q = 0; q < G::PC; ++q)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) h[q][k] = 0ull;
-            }
-#pragma unroll
-            for (int q = 0; q < G::PC; ++q)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) h[q][k] = fma2(ex2_2(mul2(d[q], A2[q][k])), h[q][k], mul2(u[q], Bv[k]));
-            if constexpr (kSummary) {
-#pragma unroll
-                for (int q = 0; q < G::PC; ++q) dsum[q] = add2(dsum[q], d[q]);
+        for (int i = 0; i < (kAll + 31) / 32; ++i) {
+            if (kAll % 32 != 0 && lane + 32 * i >= kAll) break;
+            const int row = 32 * i / kLine, col = kLine <= 32 ? 0 : 32 * i % kLine * kPer;  // beyond the lane's own
+            T* to = to0 + 32 * i * kPer;
+            const T* from = at + row * stride + col;
+            if (kFull || (lane / kLine + row < nt && lane % kLine * kPer + col < cols)) {
+                if constexpr (kVec) copy16(to, from);
+                else if constexpr (sizeof(T) == 4) copy4(to, from);
+                else *to = __ldg(from);
+            } else if constexpr (kVec) {
+                *reinterpret_cast<uint4*>(to) = make_uint4(0u, 0u, 0u, 0u);
             } else {
-                f2 Cv[4];
-                read_states(s_C[warp] + t * G::NP + 4 * s, Cv);
-#pragma unroll
-                for (int q = 0; q < G::PC; ++q) {
-                    acc[q] = mul2(Cv[0], h[q][0]);
-#pragma unroll
-                    for (int k = 1; k < 4; ++k) acc[q] = fma2(Cv[k], h[q][k], acc[q]);
+                *to = from_f32<T>(0.0f);
+            }
+        }
+        at += kRows * stride;
+    }
+};
+
+template <class T, class G, bool kVec, bool kSummary>
+__global__ void __launch_bounds__(64) ssm_kernel(SsmParams p, int blocks_per_group, int grid_chunks) {
+    using Sh = FwdShared<T, G, kSummary>;
+    constexpr int kT = Sh::kT, kRing = Sh::kRing;
+    using Elems = TileElems<T, G::CH, kT>;
+    extern __shared__ __align__(16) unsigned char s_all[];
+    __shared__ unsigned s_heads[2], s_flip;
+    ulonglong2* s_du = reinterpret_cast<ulonglong2*>(s_all + Sh::du);
+    float* s_y = reinterpret_cast<float*>(s_all + Sh::y);
+    float *s_B = reinterpret_cast<float*>(s_all + Sh::fB), *s_C = reinterpret_cast<float*>(s_all + Sh::fC);
+    const SsmPlace<G, 1> at(p, blocks_per_group, grid_chunks, 0);
+    const int lane = threadIdx.x & 31, left = at.left;
+    const long long b = at.b;
+    const long long t_begin = at.chunk * p.chunk_tiles * kTile;
+    const long long t_end = min(t_begin + p.chunk_tiles * kTile, p.length);
+    const int n = (int)((t_end - t_begin + kT - 1) / kT);  // tiles
+    // An SM gives its warp slots to its four quarters in turn, and a CTA two
+    // neighbouring ones: with the roles by the thread index alone every token
+    // warp would land on the same two quarters.  Every other pair of slots swaps
+    // them (a hint: any outcome is correct, and both warps see warp 0's).
+    if (threadIdx.x == 0) {
+        unsigned slot;
+        asm volatile("mov.u32 %0, %%warpid;" : "=r"(slot));
+        s_flip = slot >> 2 & 1u;
+    }
+    __syncthreads();
+
+    if ((threadIdx.x >> 5) != s_flip) {  // ------------------------------- the element warp
+        f2 bias[2], D[2];
+        Elems::per_channel(p.dt_bias ? p.dt_bias + at.ch0 : nullptr, left, lane, bias);
+        Elems::per_channel(p.D ? p.D + at.ch0 : nullptr, left, lane, D);
+        const bool gated = p.z != nullptr && !kSummary;
+        const T* xp = static_cast<const T*>(p.x) + b * p.x_batch + t_begin * p.x_token + at.ch0;
+        const T* dtp = static_cast<const T*>(p.dt) + b * p.dt_batch + t_begin * p.dt_token + at.ch0;
+        const T* zp = gated ? static_cast<const T*>(p.z) + b * p.z_batch + t_begin * p.z_token + at.ch0 : nullptr;
+        const T* Bp = static_cast<const T*>(p.B) + b * p.B_batch + t_begin * p.B_token + at.group * p.B_group;
+        const T* Cp = static_cast<const T*>(p.C) + b * p.C_batch + t_begin * p.C_token + at.group * p.C_group;
+        T* yp = kSummary ? nullptr : static_cast<T*>(p.y) + b * p.y_batch + t_begin * p.y_token + at.ch0;
+        const uint8_t* heads = p.heads ? p.heads + b * p.length + t_begin : nullptr;
+        const long long tokens = t_end - t_begin;
+        auto tile_len = [&](int k) { return (int)min((long long)kT, tokens - (long long)k * kT); };
+        auto raw = [&](int k, int what) { return reinterpret_cast<T*>(s_all + (k % kRing) * Sh::kRaw + what); };
+        // The copies of one tile, addresses as far as possible made beforehand: a
+        // lane's first element of each tensor, moved on by a tile each time.
+        const bool whole = left == G::CH && p.states == G::NP;
+        RowCopy<T, kT, G::CH, kVec> cx(xp, p.x_token, lane), cdt(dtp, p.dt_token, lane), cz(zp, p.z_token, lane);
+        RowCopy<T, kT, G::NP, kVec> cB(Bp, p.B_token, lane), cC(Cp, p.C_token, lane);
+        auto fetch = [&](int k) {
+            if (k < n) {
+                const int nt = tile_len(k);
+                if (whole && nt == kT) {
+                    cx.template run<true>(raw(k, Sh::x), nt, left, lane);
+                    cdt.template run<true>(raw(k, Sh::dt), nt, left, lane);
+                    if (gated) cz.template run<true>(raw(k, Sh::z), nt, left, lane);
+                    cB.template run<true>(raw(k, Sh::B), nt, G::NP, lane);
+                    if constexpr (!kSummary) cC.template run<true>(raw(k, Sh::C), nt, G::NP, lane);
+                } else {
+                    cx.template run<false>(raw(k, Sh::x), nt, left, lane);
+                    cdt.template run<false>(raw(k, Sh::dt), nt, left, lane);
+                    if (gated) cz.template run<false>(raw(k, Sh::z), nt, left, lane);
+                    cB.template run<false>(raw(k, Sh::B), nt, (int)p.states, lane);
+                    if constexpr (!kSummary) cC.template run<false>(raw(k, Sh::C), nt, (int)p.states, lane);
                 }
-                const float y = sum_states<G>(acc, lane);
-                if (s < G::CPL) s_y[warp][t * G::CH + G::CPL * c + s] = y;
             }
-        }
-        __syncwarp();
-        if constexpr (!kSummary) {
-            float y[Rows::kCount];
-            Rows::from_shared(s_y[warp], y, lane);
+            copies_commit();
+        };
+        // One step: d and d x of tile k + 1 (kStage), and y of tile k - 1
+        // (kFinish), side by side so that the latencies of one hide the other's.
+        // Every choice is made outside: a branch among the elements would keep
+        // them apart.  kFull: whole tiles of whole channel groups.
+        auto step = [&](int k, auto full, auto with_stage, auto with_finish, auto with_softplus, auto with_gate) {
+            constexpr bool kFull = decltype(full)::value, kStage = decltype(with_stage)::value;
+            constexpr bool kFinish = decltype(with_finish)::value && !kSummary, kGate = decltype(with_gate)::value;
+            f2 d[Elems::NA][2], x[Elems::NA][2], y[Elems::NA][2], xe[Elems::NA][2], z[Elems::NA][2];
+            const int ks = (k + 1) & 1, nts = kFull || !kStage ? kT : tile_len(k + 1);
+            if constexpr (kStage) {
+                copies_wait<kRing - 3>();  // tile k + 1 is there: that many groups were committed after its own
+                __syncwarp();
 #pragma unroll
-            for (int i = 0; i < Rows::kCount; ++i) {
-                y[i] = fmaf(D[Rows::channel_of(i)], xc.get(i), y[i]);
-                if (zp) y[i] *= zc.get(i) * sigmoid(zc.get(i));
+                for (int a = 0; a < Elems::NA; ++a) {
+                    Elems::get(raw(k + 1, Sh::dt) + a * 128, d[a], lane);
+                    Elems::get(raw(k + 1, Sh::x) + a * 128, x[a], lane);
+                }
             }
-            Rows::store(yp + t0 * p.y_token, p.y_token, y, nt, left, lane);
+            if constexpr (kFinish) {
+#pragma unroll
+                for (int a = 0; a < Elems::NA; ++a) {
+                    Elems::get(s_y + ((k - 1) & 1) * Sh::kRow + a * 128, y[a], lane);
+                    Elems::get(raw(k - 1, Sh::x) + a * 128, xe[a], lane);
+                    if constexpr (kGate) Elems::get(raw(k - 1, Sh::z) + a * 128, z[a], lane);
+                }
+            }
+            if constexpr (kStage) {
+                put_floats<T, Sh::kStates>(s_B + ks * Sh::kStates, raw(k + 1, Sh::B), lane);
+                if constexpr (!kSummary) put_floats<T, Sh::kStates>(s_C + ks * Sh::kStates, raw(k + 1, Sh::C), lane);
+            }
+#pragma unroll
+            for (int a = 0; a < Elems::NA; ++a)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if constexpr (kStage) {
+                        d[a][i] = add2(d[a][i], bias[i]);
+                        if constexpr (decltype(with_softplus)::value) d[a][i] = softplus_2(d[a][i]);
+                        // past the end d = 0, whatever the bias
+                        if constexpr (!kFull) d[a][i] = Elems::tok(a, lane) < nts ? d[a][i] : 0ull;
+                        x[a][i] = mul2(d[a][i], x[a][i]);
+                    }
+                    if constexpr (kFinish) {
+                        y[a][i] = fma2(D[i], xe[a][i], y[a][i]);
+                        if constexpr (kGate) y[a][i] = mul2(y[a][i], mul2(z[a][i], sigmoid_2(z[a][i])));
+                    }
+                }
+            if constexpr (kStage) {
+                ulonglong2* out = s_du + ks * Sh::kRow;
+#pragma unroll
+                for (int a = 0; a < Elems::NA; ++a)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float dv = i & 1 ? hi2(d[a][i / 2]) : lo2(d[a][i / 2]);
+                        const float uv = i & 1 ? hi2(x[a][i / 2]) : lo2(x[a][i / 2]);
+                        out[Elems::tok(a, lane) * G::CH + Sh::place(Elems::ch(lane) + i)] =
+                            make_ulonglong2(both(dv), both(uv));
+                    }
+            }
+            if constexpr (kFinish) {
+                const int nt = kFull ? kT : tile_len(k - 1);
+#pragma unroll
+                for (int a = 0; a < Elems::NA; ++a)
+                    Elems::template store<kVec, kFull>(yp, p.y_token, y[a], a, nt, left, lane);
+                yp += kT * p.y_token;
+            }
+        };
+        using Yes = std::true_type;
+        using No = std::false_type;
+        auto any_step = [&](int k, auto full, auto with_stage, auto with_finish) {
+            if (p.softplus) {
+                if (gated) step(k, full, with_stage, with_finish, Yes{}, Yes{});
+                else step(k, full, with_stage, with_finish, Yes{}, No{});
+            } else {
+                if (gated) step(k, full, with_stage, with_finish, No{}, Yes{});
+                else step(k, full, with_stage, with_finish, No{}, No{});
+            }
+        };
+        auto put_heads = [&](int k, bool head) {
+            const unsigned mask = __ballot_sync(0xffffffffu, head);
+            if (lane == 0) s_heads[k & 1] = mask;
+        };
+        auto head_at = [&](int k) {
+            const long long t = (long long)k * kT + lane;
+            return heads && lane < kT && t < tokens && heads[t] != 0;
+        };
+#pragma unroll
+        for (int k = 0; k < kRing - 2; ++k) fetch(k);
+        put_heads(0, head_at(0));
+        any_step(-1, No{}, Yes{}, No{});  // stages tile 0
+        __syncthreads();
+        for (int k = 0; k < n; ++k) {  // the token warp is at tile k
+            const bool head = head_at(k + 1);
+            fetch(k + kRing - 2);      // to the place of tile k - 2, which is finished
+            if (k > 0 && k + 1 < n) {
+                if (p.softplus && whole && (long long)(k + 2) * kT <= tokens) {
+                    if (gated) step(k, Yes{}, Yes{}, Yes{}, Yes{}, Yes{});
+                    else step(k, Yes{}, Yes{}, Yes{}, Yes{}, No{});
+                } else {
+                    any_step(k, No{}, Yes{}, Yes{});
+                }
+            } else {
+                if (k + 1 < n) any_step(k, No{}, Yes{}, No{});
+                if (k > 0) any_step(k, No{}, No{}, Yes{});
+            }
+            put_heads(k + 1, head);
+            __syncthreads();
         }
+        any_step(n, No{}, No{}, Yes{});
+        return;
+    }
+
+    // -------------------------------------------------------------- the token warp
+    const int s = lane / G::CH, c = lane % G::CH;
+    const bool mine = c < left;
+    const long long e = at.ch0 + c;
+    f2 A2[G::P], h[G::P];
+    float dsum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < G::P; ++i) {
+        const int n0 = s * G::SP + 2 * i;
+        const float* Ap = p.A + e * p.states + n0;
+        const float* hp = p.state ? p.state + (b * p.channels + e) * p.states + n0 : nullptr;
+        const bool in0 = mine && n0 < p.states, in1 = mine && n0 + 1 < p.states;
+        A2[i] = pack2(in0 ? Ap[0] * kLog2e : 0.0f, in1 ? Ap[1] * kLog2e : 0.0f);
+        h[i] = kSummary || !hp ? 0ull : pack2(in0 ? hp[0] : 0.0f, in1 ? hp[1] : 0.0f);
+    }
+    // states of this lane in the library's own arrays: [fours of states][channels][4]
+    auto own = [&](float* base, long long row) {
+        return reinterpret_cast<ulonglong2*>(base) + (row * (G::NP / 4) + s * (G::SP / 4)) * p.channels + e;
+    };
+    if constexpr (!kSummary) {
+        for (long long j = 0; j < at.chunk; ++j) {  // the chunks before this one
+            const long long row = b * p.chunks + j;
+            const ulonglong2* cp = own(p.carry, row);
+            const f2 d = both(mine ? p.sum_d[row * p.channels + e] : 0.0f);
+            const bool cut = p.cut[row] != 0;
+#pragma unroll
+            for (int i = 0; i < G::P / 2; ++i) {
+                const ulonglong2 v = mine ? cp[i * p.channels] : make_ulonglong2(0ull, 0ull);
+                h[2 * i] = cut ? v.x : fma2(ex2_2(mul2(d, A2[2 * i])), h[2 * i], v.x);
+                h[2 * i + 1] = cut ? v.y : fma2(ex2_2(mul2(d, A2[2 * i + 1])), h[2 * i + 1], v.y);
+            }
+        }
+    }
+    const long long saves = (p.length + kTile - 1) / kTile;
+    unsigned cut = 0;
+    __syncthreads();
+    for (int k = 0; k < n; ++k) {
+        const ulonglong2* ldu = s_du + (k & 1) * Sh::kRow + Sh::place(c);
+        const ulonglong2* lB = reinterpret_cast<const ulonglong2*>(s_B + (k & 1) * Sh::kStates + s * G::SP);
+        const ulonglong2* lC = reinterpret_cast<const ulonglong2*>(s_C + (k & 1) * Sh::kStates + s * G::SP);
+        float* ly = s_y + (k & 1) * Sh::kRow + c;
+        const unsigned hm = s_heads[k & 1];
+        cut |= hm;
+        if (!kSummary && p.saved && k % (kTile / kT) == 0 && mine) {
+            ulonglong2* sp = own(p.saved, b * saves + at.chunk * p.chunk_tiles + k / (kTile / kT));
+#pragma unroll
+            for (int i = 0; i < G::P / 2; ++i) sp[i * p.channels] = make_ulonglong2(h[2 * i], h[2 * i + 1]);
+        }
+        // One token ahead: the decays and inputs of token t + 1 are on their way
+        // while token t is applied, so that neither the exponentials nor the
+        // multipliers wait for the other.
+        auto tokens = [&](auto with_heads) {
+            f2 a[G::P], ub[G::P];
+            auto ahead = [&](int t) {
+                const ulonglong2 du = ldu[t * G::CH];
+#pragma unroll
+                for (int i = 0; i < G::P / 2; ++i) {
+                    const ulonglong2 Bv = lB[t * (G::NP / 4) + i];
+                    a[2 * i] = ex2_2(mul2(du.x, A2[2 * i]));
+                    a[2 * i + 1] = ex2_2(mul2(du.x, A2[2 * i + 1]));
+                    ub[2 * i] = mul2(du.y, Bv.x);
+                    ub[2 * i + 1] = mul2(du.y, Bv.y);
+                }
+                if constexpr (kSummary) dsum += lo2(du.x);
+            };
+            ahead(0);
+#pragma unroll
+            for (int t = 0; t < kT; ++t) {
+                f2 now[G::P], in[G::P];
+#pragma unroll
+                for (int i = 0; i < G::P; ++i) {
+                    now[i] = a[i];
+                    in[i] = ub[i];
+                }
+                if (t + 1 < kT) ahead(t + 1);
+                if (decltype(with_heads)::value && (hm >> t & 1u)) {
+#pragma unroll
+                    for (int i = 0; i < G::P; ++i) h[i] = 0ull;
+                }
+#pragma unroll
+                for (int i = 0; i < G::P; ++i) h[i] = fma2(now[i], h[i], in[i]);
+                if constexpr (!kSummary) {
+                    f2 y0 = 0ull, y1 = 0ull;
+#pragma unroll
+                    for (int i = 0; i < G::P / 2; ++i) {
+                        const ulonglong2 Cv = lC[t * (G::NP / 4) + i];
+                        y0 = i ? fma2(Cv.x, h[2 * i], y0) : mul2(Cv.x, h[2 * i]);
+                        y1 = i ? fma2(Cv.y, h[2 * i + 1], y1) : mul2(Cv.y, h[2 * i + 1]);
+                    }
+                    y0 = add2(y0, y1);
+                    float y = lo2(y0) + hi2(y0);
+#pragma unroll
+                    for (int m = G::CH; m < 32; m <<= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
+                    if (G::S == 1 || s == 0) ly[t * G::CH] = y;
+                }
+            }
+        };
+        if (hm) tokens(std::true_type{});
+        else tokens(std::false_type{});
+        __syncthreads();
     }
     if constexpr (kSummary) {
         const long long row = b * p.chunks + at.chunk;
-        store_lane<G>(p.carry + (row * p.channels + at.ch0) * G::NP, left, lane, h);
-        if (s == 0)
+        if (mine) {
+            ulonglong2* cp = own(p.carry, row);
 #pragma unroll
-            for (int j = 0; j < G::CPL; ++j)
-                if (G::CPL * c + j < left)
-                    p.sum_d[row * p.channels + at.ch0 + G::CPL * c + j] = j & 1 ? hi2(dsum[j / 2]) : lo2(dsum[j / 2]);
-        if (at.cblock == 0 && warp == 0 && lane == 0) p.cut[row] = cut != 0;
-    } else if (p.final_state && tile1 == tiles) {
-        store_lane_of<G>(p.final_state + (b * p.channels + at.ch0) * p.states, p.states, left, lane, h);
+            for (int i = 0; i < G::P / 2; ++i) cp[i * p.channels] = make_ulonglong2(h[2 * i], h[2 * i + 1]);
+            if (s == 0) p.sum_d[row * p.channels + e] = dsum;
+        }
+        if (at.cblock == 0 && lane == 0) p.cut[row] = cut != 0;
+    } else if (p.final_state && t_end == p.length && mine) {
+        float* fp = p.final_state + (b * p.channels + e) * p.states + s * G::SP;
+#pragma unroll
+        for (int i = 0; i < G::SP; ++i)
+            if (s * G::SP + i < p.states) fp[i] = i & 1 ? hi2(h[i / 2]) : lo2(h[i / 2]);
     }
 }
 
 template <class T, class G, bool kVec>
 cudaError_t ssm_of(const SsmParams& p, const SsmPlan& plan, int* launches, cudaStream_t s) {
-    const long long ncb = plan.blocks_per_group * p.groups;
+    const long long per = p.channels / p.groups;
+    const int bpg = (int)((per + G::CH - 1) / G::CH);
+    const long long ncb = bpg * p.groups;
     *launches = 1;
+    auto go = [&](auto kernel, int bytes, int chunks) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) kernel<<<(unsigned)(ncb * chunks * p.batch), 64, bytes, s>>>(p, bpg, chunks);
+        return e;
+    };
     if (p.chunks > 1) {  // nobody waits for the last chunk's summary
-        ssm_kernel<T, G, kVec, true><<<(unsigned)(ncb * (p.chunks - 1) * p.batch), G::kThreads, 0, s>>>(
-            p, plan.blocks_per_group, p.chunks - 1);
+        const cudaError_t e = go(ssm_kernel<T, G, kVec, true>, FwdShared<T, G, true>::kBytes, p.chunks - 1);
+        if (e != cudaSuccess) return e;
         *launches = 2;
     }
-    ssm_kernel<T, G, kVec, false><<<(unsigned)(ncb * p.chunks * p.batch), G::kThreads, 0, s>>>(
-        p, plan.blocks_per_group, p.chunks);
+    const cudaError_t e = go(ssm_kernel<T, G, kVec, false>, FwdShared<T, G, false>::kBytes, p.chunks);
+    if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 
 template <class T>
 cudaError_t ssm_type(const SsmParams& p, const SsmPlan& plan, int* launches, cudaStream_t s) {
+    auto go = [&](auto g) {
+        using G = decltype(g);
+        return p.vec ? ssm_of<T, G, true>(p, plan, launches, s) : ssm_of<T, G, false>(p, plan, launches, s);
+    };
     switch (plan.lanes) {
-    case 2: return p.vec ? ssm_of<T, Geo<2>, true>(p, plan, launches, s) : ssm_of<T, Geo<2>, false>(p, plan, launches, s);
-    case 4: return p.vec ? ssm_of<T, Geo<4>, true>(p, plan, launches, s) : ssm_of<T, Geo<4>, false>(p, plan, launches, s);
-    case 8: return p.vec ? ssm_of<T, Geo<8>, true>(p, plan, launches, s) : ssm_of<T, Geo<8>, false>(p, plan, launches, s);
-    case 16:
-        return p.vec ? ssm_of<T, Geo<16>, true>(p, plan, launches, s) : ssm_of<T, Geo<16>, false>(p, plan, launches, s);
+    case 2: return go(FwdGeo<8, 1>{});
+    case 4: return go(FwdGeo<16, 1>{});
+    case 8: return go(FwdGeo<16, 2>{});
+    case 16: return go(FwdGeo<16, 4>{});
     default: return cudaErrorInvalidValue;
     }
 }
