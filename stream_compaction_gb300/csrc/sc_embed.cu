@@ -5,19 +5,23 @@
 // gradient writes each row of dweight once and reads each row of dout once:
 //
 //   sort       the (id, t) pairs by id, stable, least significant digit first,
-//              at most 10 bits a pass (so two passes below 2^20 ids): per tile
-//              digit counts, then the placement, whose CTAs add up the counts
-//              of the earlier tiles themselves (beyond kFoldTiles tiles a
-//              kernel of its own scans them);
+//              at most 10 bits a pass (so two passes below 2^20 ids).  Up to
+//              kClusterKeys tokens: one launch, one cluster of up to 8 CTAs whose
+//              digit counts meet in distributed shared memory (16384 tokens:
+//              XX us against 38 us of the four launches below).  Beyond: per
+//              tile digit counts, their sums over tiles, the placement.  Then
+//              where each id's run starts and ends.
 //   long runs  tokens of one id may be a large part of all (padding, a frequent
 //              word): runs longer than kRun are cut at multiples of kRun of the
 //              sorted order and each piece summed by a CTA of its own;
-//   rows       each CTA takes kRowsPerCta rows of dweight, finds their runs in
-//              the sorted ids by binary search, and writes zeros, a sum of at
-//              most kRun rows of dout, or the sum of the row's pieces.
+//   rows       each CTA takes kRowsPerCta rows of dweight: first it writes the
+//              zeros of those without a token, which wait for nothing, then the
+//              sums of at most kRun rows of dout, or of the row's pieces.
 // Sums are taken in the order of t in float32, so a result is the same on
 // every run, whatever the schedule (no atomics on values).
 #include <algorithm>
+
+#include <cooperative_groups.h>
 
 #include "sc_seq.cuh"
 #include "sc_seq_launch.h"
@@ -31,8 +35,9 @@ constexpr int kSortKeys = 8;                    // keys per thread of a sort til
 constexpr int kSortTile = kNT * kSortKeys;      // 2048
 constexpr int kSortWarps = kNT / 32;
 constexpr int kMaxDigit = 1024;
-constexpr int kFoldTiles = 16;
-constexpr int kRun = 128;
+constexpr int kClusterNT = 1024, kClusterWarps = kClusterNT / 32, kClusterCtas = 8;
+constexpr long long kClusterKeys = 8ll * kClusterNT * kClusterCtas;  // 8 a thread: 65536
+constexpr int kRun = 64;
 constexpr int kRowsPerCta = 32;
 
 __device__ __forceinline__ long long load_id(const void* ids, int ids64, long long i) {
@@ -124,7 +129,6 @@ __global__ void __launch_bounds__(kNT) sort_columns_kernel(uint32_t* counts, lon
 // consecutive keys, 32 at a time in order) with running counts per warp and
 // digit; a key goes to (keys of smaller digits) + (its digit's keys in earlier
 // tiles) + (in earlier warps) + its rank.
-template <bool kFold>
 __global__ void __launch_bounds__(kNT) sort_place_kernel(EmbedParams p, const uint32_t* keys, const uint32_t* vals,
                                                          int shift, int bits, const uint32_t* counts, long long tiles,
                                                          uint32_t* keys_out, uint32_t* vals_out) {
@@ -161,16 +165,8 @@ __global__ void __launch_bounds__(kNT) sort_place_kernel(EmbedParams p, const ui
         const int d = kPer * tid + q;
         prev[q] = total[q] = 0u;
         if (d < digits) {
-            if constexpr (kFold) {
-                for (long long t = 0; t < tiles; ++t) {
-                    const uint32_t c = __ldg(counts + t * digits + d);
-                    total[q] += c;
-                    prev[q] += t < blockIdx.x ? c : 0u;
-                }
-            } else {
-                prev[q] = __ldg(counts + (long long)blockIdx.x * digits + d);
-                total[q] = __ldg(counts + tiles * digits + d);
-            }
+            prev[q] = __ldg(counts + (long long)blockIdx.x * digits + d);
+            total[q] = __ldg(counts + tiles * digits + d);
         }
         sum += total[q];
     }
@@ -213,18 +209,124 @@ __global__ void __launch_bounds__(kNT) sort_place_kernel(EmbedParams p, const ui
     }
 }
 
-// ----------------------------------------------------------------- sums
-// First position of the sorted keys that is >= v.
-__device__ __forceinline__ long long lower_bound(const uint32_t* keys, long long n, uint32_t v) {
-    long long lo = 0, hi = n;
-    while (lo < hi) {
-        const long long mid = (lo + hi) >> 1;
-        if (__ldg(keys + mid) < v) lo = mid + 1;
-        else hi = mid;
-    }
-    return lo;
+// Token positions [first, last) of each id in the sorted order; last == 0 (set
+// beforehand) where an id has none.
+struct Runs {
+    uint32_t *first, *last;
+};
+__device__ __forceinline__ void mark_run(const uint32_t* keys, long long i, long long n, uint32_t vocab, const Runs& runs) {
+    const uint32_t k = keys[i];
+    if (k >= vocab) return;
+    if (i == 0 || keys[i - 1] != k) runs.first[k] = (uint32_t)i;
+    if (i + 1 == n || keys[i + 1] != k) runs.last[k] = (uint32_t)(i + 1);
+}
+__global__ void __launch_bounds__(kNT) sort_runs_kernel(const uint32_t* keys, long long n, uint32_t vocab, Runs runs) {
+    const long long i = (long long)blockIdx.x * kNT + threadIdx.x;
+    if (i < n) mark_run(keys, i, n, vocab, runs);
 }
 
+// The whole sort by one cluster: CTA r has the keys [r, r + 1) * kClusterNT * K of
+// each pass's input, K as few as 8 CTAs allow.  As in the kernels above, but the
+// CTAs' digit counts are read from one another's shared memory, and a barrier of
+// the cluster stands between one pass's placement and the next pass's loads.
+// Lanes with the same digit find one another by a ballot per bit.
+template <int K>
+__global__ void __launch_bounds__(kClusterNT) sort_cluster_kernel(EmbedParams p, int passes, int bits, uint32_t* keys0,
+                                                                  uint32_t* vals0, uint32_t* keys1, uint32_t* vals1,
+                                                                  Runs runs) {
+    namespace cg = cooperative_groups;
+    extern __shared__ uint16_t s_cnt[];  // [kClusterWarps][digits]
+    __shared__ uint32_t s_total[kMaxDigit], s_base[kMaxDigit], s_warp[kClusterWarps];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+    const int digits = 1 << bits, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t mask = (uint32_t)digits - 1;
+    const long long base = (long long)rank * (kClusterNT * K) + warp * (32 * K);
+    uint32_t *kin = nullptr, *vin = nullptr;
+    for (int pass = 0; pass < passes; ++pass) {
+        const int shift = pass * bits;
+        uint32_t *ko = pass & 1 ? keys1 : keys0, *vo = pass & 1 ? vals1 : vals0;
+        uint32_t key[K], val[K], rk[K];
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const long long i = base + j * 32 + lane;
+            key[j] = val[j] = 0u;
+            if (i < p.tokens) {
+                key[j] = sort_key(p, kin, i);
+                val[j] = vin ? vin[i] : (uint32_t)i;
+            }
+        }
+        for (int i = tid; i < kClusterWarps * digits / 2; i += kClusterNT) reinterpret_cast<uint32_t*>(s_cnt)[i] = 0u;
+        __syncthreads();
+        uint16_t* mine = s_cnt + warp * digits;
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const bool live = base + j * 32 + lane < p.tokens;
+            const uint32_t d = (key[j] >> shift) & mask;
+            uint32_t m = __ballot_sync(0xffffffffu, live);
+            for (int q = 0; q < bits; ++q) {
+                const uint32_t one = __ballot_sync(0xffffffffu, d >> q & 1u);
+                m &= d >> q & 1u ? one : ~one;
+            }
+            const uint32_t before = live ? mine[d] : 0u;
+            __syncwarp();
+            rk[j] = before + __popc(m & ((1u << lane) - 1u));
+            if (live && lane == __ffs(m) - 1) mine[d] = (uint16_t)(before + __popc(m));
+            __syncwarp();
+        }
+        __syncthreads();
+        if (tid < digits) {  // the warps before, per digit; the CTA's total
+            uint32_t run = 0;
+#pragma unroll 8
+            for (int w = 0; w < kClusterWarps; ++w) {
+                const uint32_t c = s_cnt[w * digits + tid];
+                s_cnt[w * digits + tid] = (uint16_t)run;
+                run += c;
+            }
+            s_total[tid] = run;
+        }
+        cluster.sync();
+        uint32_t prev = 0, total = 0;
+        if (tid < digits)
+            for (int r = 0; r < ctas; ++r) {
+                const uint32_t c = cluster.map_shared_rank(s_total, r)[tid];
+                prev += r < rank ? c : 0u;
+                total += c;
+            }
+        uint32_t incl = total;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) s_warp[warp] = incl;
+        __syncthreads();
+        uint32_t at = incl - total + prev;
+        for (int w = 0; w < warp; ++w) at += s_warp[w];
+        if (tid < digits) s_base[tid] = at;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            if (base + j * 32 + lane < p.tokens) {
+                const uint32_t d = (key[j] >> shift) & mask, to = s_base[d] + mine[d] + rk[j];
+                if (to < (uint32_t)p.tokens) {  // holds by construction
+                    ko[to] = key[j];
+                    vo[to] = val[j];
+                }
+            }
+        }
+        cluster.sync();  // the pass's output is there, and nobody reads s_total any more
+        kin = ko;
+        vin = vo;
+    }
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        const long long i = base + j * 32 + lane;
+        if (i < p.tokens) mark_run(kin, i, p.tokens, (uint32_t)p.vocab, runs);
+    }
+}
+
+// ----------------------------------------------------------------- sums
 // acc += the rows of dout at sorted positions [lo, hi), in order, for this
 // thread's columns: kVec: c .. c + W - 1, else c, c + step, ...
 template <class T, int W, bool kVec>
@@ -233,10 +335,19 @@ __device__ __forceinline__ void add_rows(const T* dout, long long ldd, const uin
     long long i = lo;
     if constexpr (kVec) {
         if (c >= dim) return;
+        for (; i + 16 <= hi; i += 16) {
+            Vec<T, W> v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j].load(dout + (long long)vals[i + j] * ldd + c);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+#pragma unroll
+                for (int k = 0; k < W; ++k) acc[k] += v[j].get(k);
+        }
         for (; i + 4 <= hi; i += 4) {
             Vec<T, W> v[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j].load(dout + (long long)__ldg(vals + i + j) * ldd + c);
+            for (int j = 0; j < 4; ++j) v[j].load(dout + (long long)vals[i + j] * ldd + c);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -244,13 +355,13 @@ __device__ __forceinline__ void add_rows(const T* dout, long long ldd, const uin
         }
         for (; i < hi; ++i) {
             Vec<T, W> v;
-            v.load(dout + (long long)__ldg(vals + i) * ldd + c);
+            v.load(dout + (long long)vals[i] * ldd + c);
 #pragma unroll
             for (int k = 0; k < W; ++k) acc[k] += v.get(k);
         }
     } else {
         for (; i < hi; ++i) {
-            const T* row = dout + (long long)__ldg(vals + i) * ldd;
+            const T* row = dout + (long long)vals[i] * ldd;
 #pragma unroll
             for (int k = 0; k < W; ++k) {
                 const long long cc = c + (long long)k * step;
@@ -266,15 +377,18 @@ __device__ __forceinline__ void add_rows(const T* dout, long long ldd, const uin
 // token) or 2x + 1 (it starts inside).
 template <class T, int W, bool kVec>
 __global__ void __launch_bounds__(kNT) embed_pieces_kernel(EmbedParams p, const uint32_t* keys, const uint32_t* vals,
-                                                           float* partials, int tpr) {
+                                                           Runs runs, float* partials, int tpr) {
     __shared__ long long s_lo[2], s_hi[2];
+    __shared__ uint32_t s_vals[kRun];
     const long long b0 = (long long)blockIdx.x * kRun, b1 = min(b0 + kRun, p.tokens);
+    if (threadIdx.x >= 32 && threadIdx.x < 32 + kRun && b0 + threadIdx.x - 32 < b1)
+        s_vals[threadIdx.x - 32] = vals[b0 + threadIdx.x - 32];
     if (threadIdx.x < 2) {
         const uint32_t k = keys[threadIdx.x == 0 ? b0 : b1 - 1];
         long long lo = 0, hi = 0;
         if (k < (uint32_t)p.vocab) {
-            lo = lower_bound(keys, p.tokens, k);
-            hi = lower_bound(keys, p.tokens, k + 1);
+            lo = runs.first[k];
+            hi = runs.last[k];
         }
         if (hi - lo <= kRun) lo = hi = 0;
         s_lo[threadIdx.x] = lo;
@@ -291,7 +405,8 @@ __global__ void __launch_bounds__(kNT) embed_pieces_kernel(EmbedParams p, const 
 #pragma unroll
         for (int k = 0; k < W; ++k) acc[k] = 0.0f;
         const long long c = (long long)blockIdx.y * tpr * W + (long long)lane * (kVec ? W : 1);
-        add_rows<T, W, kVec>(static_cast<const T*>(p.weight), p.ldw, vals, max(lo, b0), min(hi, b1), c, tpr, p.dim, acc);
+        add_rows<T, W, kVec>(static_cast<const T*>(p.weight), p.ldw, s_vals, max(lo, b0) - b0, min(hi, b1) - b0, c, tpr,
+                             p.dim, acc);
         float* row = partials + (2 * (long long)blockIdx.x + which) * p.dim;
 #pragma unroll
         for (int k = 0; k < W; ++k) {
@@ -302,24 +417,46 @@ __global__ void __launch_bounds__(kNT) embed_pieces_kernel(EmbedParams p, const 
 }
 
 template <class T, class O, int W, bool kVec>
-__global__ void __launch_bounds__(kNT) embed_rows_kernel(EmbedParams p, const uint32_t* keys, const uint32_t* vals,
+__global__ void __launch_bounds__(kNT) embed_rows_kernel(EmbedParams p, const uint32_t* vals, Runs runs,
                                                          const float* partials, int tpr) {
-    __shared__ long long s_at[kRowsPerCta + 1];
+    __shared__ uint32_t s_first[kRowsPerCta], s_last[kRowsPerCta];
     const long long row0 = (long long)blockIdx.x * kRowsPerCta;
-    if (threadIdx.x <= kRowsPerCta)
-        s_at[threadIdx.x] = lower_bound(keys, p.tokens, (uint32_t)min(row0 + threadIdx.x, p.vocab));
+    if (threadIdx.x < kRowsPerCta) {
+        const bool in = row0 + threadIdx.x < p.vocab;
+        s_last[threadIdx.x] = in ? runs.last[row0 + threadIdx.x] : 0u;
+        s_first[threadIdx.x] = in ? runs.first[row0 + threadIdx.x] : 0u;  // anything where last is 0
+    }
     __syncthreads();
-    const int sub = threadIdx.x / tpr, lane = threadIdx.x % tpr;
+    const int sub = threadIdx.x / tpr, lane = threadIdx.x % tpr, step = kNT / tpr;
+    const int rows = (int)min((long long)kRowsPerCta, p.vocab - row0);
     const long long c = (long long)blockIdx.y * tpr * W + (long long)lane * (kVec ? W : 1);
-    for (int r = sub; r < kRowsPerCta && row0 + r < p.vocab; r += kNT / tpr) {
-        const long long lo = s_at[r], hi = s_at[r + 1];
-        if (lo == hi && p.accumulate) continue;
+    if (kVec && c >= p.dim) return;
+    O* out0 = static_cast<O*>(p.out) + row0 * p.ldo + c;
+    if (!p.accumulate) {
+        for (int r = sub; r < rows; r += step) {
+            if (s_last[r] != 0u) continue;
+            O* out = out0 + r * p.ldo;
+            if constexpr (kVec) {
+                Vec<O, W> v;
+                v.zero();
+                v.store(out);
+            } else {
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+                    if (c + (long long)k * tpr < p.dim) out[(long long)k * tpr] = from_f32<O>(0.0f);
+            }
+        }
+    }
+    for (int r = sub; r < rows; r += step) {
+        const long long lo = s_first[r], hi = s_last[r];
+        if (hi == 0) continue;
         float acc[W];
 #pragma unroll
         for (int k = 0; k < W; ++k) acc[k] = 0.0f;
         if (hi - lo <= kRun) {
             add_rows<T, W, kVec>(static_cast<const T*>(p.weight), p.ldw, vals, lo, hi, c, tpr, p.dim, acc);
         } else {
+#pragma unroll 4
             for (long long piece = lo / kRun; piece * kRun < hi; ++piece) {
                 const float* row = partials + (2 * piece + (lo <= piece * kRun ? 0 : 1)) * p.dim;
 #pragma unroll
@@ -329,20 +466,19 @@ __global__ void __launch_bounds__(kNT) embed_rows_kernel(EmbedParams p, const ui
                 }
             }
         }
-        O* out = static_cast<O*>(p.out) + (row0 + r) * p.ldo;
+        O* out = out0 + r * p.ldo;
         if constexpr (kVec) {
-            if (c >= p.dim) continue;
             Vec<O, W> v;
-            if (p.accumulate) v.load_rw(out + c);
+            if (p.accumulate) v.load_rw(out);
 #pragma unroll
             for (int k = 0; k < W; ++k) acc[k] = acc[k] * p.scale + (p.accumulate ? v.get(k) : 0.0f);
             v.set(acc);
-            v.store(out + c);
+            v.store(out);
         } else {
 #pragma unroll
             for (int k = 0; k < W; ++k) {
-                const long long cc = c + (long long)k * tpr;
-                if (cc < p.dim) out[cc] = from_f32<O>(acc[k] * p.scale + (p.accumulate ? to_f32(out[cc]) : 0.0f));
+                const long long o = (long long)k * tpr;
+                if (c + o < p.dim) out[o] = from_f32<O>(acc[k] * p.scale + (p.accumulate ? to_f32(out[o]) : 0.0f));
             }
         }
     }
@@ -368,19 +504,20 @@ cudaError_t embed_of(const EmbedParams& p, cudaStream_t s) {
 }
 
 template <class T, class O>
-cudaError_t sums_of(const EmbedParams& p, const uint32_t* keys, const uint32_t* vals, float* partials, cudaStream_t s) {
+cudaError_t sums_of(const EmbedParams& p, const uint32_t* keys, const uint32_t* vals, const Runs& runs, float* partials,
+                    cudaStream_t s) {
     constexpr int W = 16 / sizeof(T);
     const int tpr = threads_per_row(p.dim, W);
     const unsigned slices = (unsigned)ceil_div(p.dim, (long long)tpr * W);
     if (p.tokens > kRun) {
         const dim3 grid((unsigned)ceil_div(p.tokens, kRun), slices);
-        if (p.vec) embed_pieces_kernel<T, W, true><<<grid, kNT, 0, s>>>(p, keys, vals, partials, tpr);
-        else embed_pieces_kernel<T, W, false><<<grid, kNT, 0, s>>>(p, keys, vals, partials, tpr);
+        if (p.vec) embed_pieces_kernel<T, W, true><<<grid, kNT, 0, s>>>(p, keys, vals, runs, partials, tpr);
+        else embed_pieces_kernel<T, W, false><<<grid, kNT, 0, s>>>(p, keys, vals, runs, partials, tpr);
         count_launches(1);
     }
     const dim3 grid((unsigned)ceil_div(p.vocab, kRowsPerCta), slices);
-    if (p.vec) embed_rows_kernel<T, O, W, true><<<grid, kNT, 0, s>>>(p, keys, vals, partials, tpr);
-    else embed_rows_kernel<T, O, W, false><<<grid, kNT, 0, s>>>(p, keys, vals, partials, tpr);
+    if (p.vec) embed_rows_kernel<T, O, W, true><<<grid, kNT, 0, s>>>(p, vals, runs, partials, tpr);
+    else embed_rows_kernel<T, O, W, false><<<grid, kNT, 0, s>>>(p, vals, runs, partials, tpr);
     count_launches(1);
     return cudaGetLastError();
 }
@@ -414,7 +551,9 @@ EmbedGradPlan embed_grad_plan(long long tokens, long long vocab, long long dim) 
     g.keys1 = take((size_t)tokens * 4);
     g.vals0 = take((size_t)tokens * 4);
     g.vals1 = take((size_t)tokens * 4);
-    g.counts = take((size_t)(g.tiles + 1) * (size_t)(1 << g.digit_bits) * 4);
+    g.first = take((size_t)vocab * 4);
+    g.last = take((size_t)vocab * 4);
+    g.counts = take(tokens <= kClusterKeys ? 0 : (size_t)(g.tiles + 1) * (size_t)(1 << g.digit_bits) * 4);
     g.partials = take(tokens > kRun ? (size_t)ceil_div(tokens, kRun) * 2 * (size_t)dim * 4 : 0);
     g.total = at;
     return g;
@@ -426,34 +565,57 @@ sc_status launch_embed_grad(int dtype, int wtype, const EmbedParams& p, const Em
     uint32_t* vals[2] = {reinterpret_cast<uint32_t*>(base + g.vals0), reinterpret_cast<uint32_t*>(base + g.vals1)};
     uint32_t* counts = reinterpret_cast<uint32_t*>(base + g.counts);
     float* partials = reinterpret_cast<float*>(base + g.partials);
+    const Runs runs{reinterpret_cast<uint32_t*>(base + g.first), reinterpret_cast<uint32_t*>(base + g.last)};
     const uint32_t *kin = nullptr, *vin = nullptr;
-    if (p.tokens > 0) {
+    if (cudaMemsetAsync(runs.last, 0, (size_t)p.vocab * 4, s) != cudaSuccess) return SC_ERR_CUDA;
+    if (p.tokens > 0 && p.tokens <= kClusterKeys) {
+        auto go = [&](auto kernel, long long k) {
+            const int bytes = kClusterWarps * (1 << g.digit_bits) * 2;
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            if (e != cudaSuccess) return e;
+            cudaLaunchAttribute attr{};
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim = {(unsigned)ceil_div(p.tokens, kClusterNT * k), 1, 1};
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(attr.val.clusterDim.x);
+            cfg.blockDim = dim3(kClusterNT);
+            cfg.dynamicSmemBytes = (size_t)bytes;
+            cfg.stream = s;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            return cudaLaunchKernelEx(&cfg, kernel, p, g.passes, g.digit_bits, keys[0], vals[0], keys[1], vals[1], runs);
+        };
+        const long long each = ceil_div(p.tokens, (long long)kClusterNT * kClusterCtas);
+        const cudaError_t e = each <= 1   ? go(sort_cluster_kernel<1>, 1)
+                              : each <= 2 ? go(sort_cluster_kernel<2>, 2)
+                              : each <= 4 ? go(sort_cluster_kernel<4>, 4)
+                                          : go(sort_cluster_kernel<8>, 8);
+        if (e != cudaSuccess) return SC_ERR_CUDA;
+        count_launches(1);
+        kin = keys[(g.passes - 1) & 1];
+        vin = vals[(g.passes - 1) & 1];
+    } else if (p.tokens > 0) {
+        const int digits = 1 << g.digit_bits;
         for (int pass = 0; pass < g.passes; ++pass) {
             const int shift = pass * g.digit_bits;
             uint32_t *ko = keys[pass & 1], *vo = vals[pass & 1];
             sort_count_kernel<<<(unsigned)g.tiles, kNT, 0, s>>>(p, kin, shift, g.digit_bits, counts);
-            if (g.tiles <= kFoldTiles) {
-                sort_place_kernel<true><<<(unsigned)g.tiles, kNT, 0, s>>>(p, kin, vin, shift, g.digit_bits, counts,
-                                                                         g.tiles, ko, vo);
-                count_launches(2);
-            } else {
-                const int digits = 1 << g.digit_bits;
-                sort_columns_kernel<<<(unsigned)ceil_div(digits, kNT), kNT, 0, s>>>(counts, g.tiles, digits);
-                sort_place_kernel<false><<<(unsigned)g.tiles, kNT, 0, s>>>(p, kin, vin, shift, g.digit_bits, counts,
-                                                                          g.tiles, ko, vo);
-                count_launches(3);
-            }
-            if (cudaGetLastError() != cudaSuccess) return SC_ERR_CUDA;
+            sort_columns_kernel<<<(unsigned)ceil_div(digits, kNT), kNT, 0, s>>>(counts, g.tiles, digits);
+            sort_place_kernel<<<(unsigned)g.tiles, kNT, 0, s>>>(p, kin, vin, shift, g.digit_bits, counts, g.tiles, ko, vo);
+            count_launches(3);
             kin = ko;
             vin = vo;
         }
+        sort_runs_kernel<<<(unsigned)ceil_div(p.tokens, kNT), kNT, 0, s>>>(kin, p.tokens, (uint32_t)p.vocab, runs);
+        count_launches(1);
+        if (cudaGetLastError() != cudaSuccess) return SC_ERR_CUDA;
     }
     cudaError_t e = cudaErrorInvalidValue;
-    if (dtype == SC_F32) e = sums_of<float, float>(p, kin, vin, partials, s);
-    else if (dtype == SC_F16) e = wtype == SC_F32 ? sums_of<f16, float>(p, kin, vin, partials, s)
-                                                  : sums_of<f16, f16>(p, kin, vin, partials, s);
-    else if (dtype == SC_BF16) e = wtype == SC_F32 ? sums_of<bf16, float>(p, kin, vin, partials, s)
-                                                   : sums_of<bf16, bf16>(p, kin, vin, partials, s);
+    if (dtype == SC_F32) e = sums_of<float, float>(p, kin, vin, runs, partials, s);
+    else if (dtype == SC_F16) e = wtype == SC_F32 ? sums_of<f16, float>(p, kin, vin, runs, partials, s)
+                                                  : sums_of<f16, f16>(p, kin, vin, runs, partials, s);
+    else if (dtype == SC_BF16) e = wtype == SC_F32 ? sums_of<bf16, float>(p, kin, vin, runs, partials, s)
+                                                   : sums_of<bf16, bf16>(p, kin, vin, runs, partials, s);
     return e == cudaSuccess ? SC_OK : SC_ERR_CUDA;
 }
 

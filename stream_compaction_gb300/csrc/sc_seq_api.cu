@@ -90,7 +90,7 @@ sc_status conv_args(const sc_conv_desc* d, bool step, ConvParams* p) {
         return SC_ERR_INVALID;
     if (product(d->batch, std::max<int64_t>(d->length, 1), d->channels, 64) < 0) return SC_ERR_INVALID;
     // the smallest run and channel group of any kernel
-    const int64_t runs = (d->length + 7) / 8, blocks = (d->channels + 255) / 256;
+    const int64_t runs = (d->length + 7) / 8, blocks = (d->channels + 511) / 512;
     const int64_t grid = product(d->batch, std::max<int64_t>(runs, 1), std::max<int64_t>(blocks, 1));
     if (grid < 0 || grid > kMaxGrid || product(d->channels, d->width + 1) / 128 >= kMaxGrid) return SC_ERR_INVALID;
     const bool any = d->batch > 0 && d->length > 0 && d->channels > 0;
@@ -318,12 +318,12 @@ sc_status sc_causal_conv(const sc_conv_desc* d, void* y, int64_t y_batch, int64_
     const Tensor x{d->x, d->batch, d->length, d->channels, d->x_batch, d->x_token, eb};
     const Tensor o{y, d->batch, d->length, d->channels, y_batch, y_token, eb};
     if (!o.ok() || !o.distinct() || share(o, x) || share(o, is) || share(o, fs) || share(fs, x)) return SC_ERR_INVALID;
-    const int e = 16 / eb;
+    const int e = 4;  // channels of a thread
     p.y = y;
     p.y_batch = y_batch;
     p.y_token = y_token;
     p.final_state = d->width > 1 ? final_state : nullptr;
-    p.vec = d->channels % e == 0 && x.vec(e) && o.vec(e) && multiple(d->state, 16) && multiple(final_state, 16);
+    p.vec = d->channels % e == 0 && x.vec(e) && o.vec(e) && multiple(d->state, 4 * eb) && multiple(final_state, 4 * eb);
     return status_of(launch_conv(d->dtype, p, cu(stream)));
 }
 
@@ -356,7 +356,7 @@ sc_status sc_causal_conv_grad(const sc_conv_desc* d, const void* dy, int64_t dy_
     if (!g.ok() || (dx && (!o.ok() || !o.distinct())) || share(o, x) || share(o, g) || share(o, is) || share(ds, x) ||
         share(ds, g) || share(ds, is) || share(ds, o))
         return SC_ERR_INVALID;
-    const int e = 16 / eb;
+    const int e = 4;  // channels of a thread
     p.dy = dy;
     p.dy_batch = dy_batch;
     p.dy_token = dy_token;
@@ -366,8 +366,8 @@ sc_status sc_causal_conv_grad(const sc_conv_desc* d, const void* dy, int64_t dy_
     p.dweight = dweight;
     p.dbias = dbias;
     p.dstate = d->width > 1 ? dstate : nullptr;
-    p.vec = d->channels % e == 0 && x.vec(e) && g.vec(e) && (!dx || o.vec(e)) && multiple(d->state, 16) &&
-            multiple(dstate, 16);
+    p.vec = d->channels % e == 0 && x.vec(e) && g.vec(e) && (!dx || o.vec(e)) && multiple(d->state, 4 * eb) &&
+            multiple(dstate, 4 * eb);
     if (dweight || dbias) {
         unsigned char* base = nullptr;
         st = seq_scratch(s, conv_grad_scratch(d->batch, d->length, d->channels, d->width), &base);
@@ -390,13 +390,13 @@ sc_status sc_causal_conv_step(const sc_conv_desc* d, void* pool, int64_t pool_ro
     const Tensor ps = flat(pool, pool_rows * (d->width - 1) * d->channels, eb);
     if (!o.ok() || !o.distinct() || (ps.channels > 0 && !ps.ok()) || share(o, x) || share(o, ps) || share(ps, x))
         return SC_ERR_INVALID;
-    const int e = 16 / eb;
+    const int e = 4;  // channels of a thread
     p.y = y;
     p.y_batch = y_batch;
     p.pool = pool;
     p.pool_rows = pool_rows;
     p.slots = slots;
-    p.vec = d->channels % e == 0 && x.vec(e) && o.vec(e) && multiple(pool, 16);
+    p.vec = d->channels % e == 0 && x.vec(e) && o.vec(e) && multiple(pool, 4 * eb) && multiple(d->weight, 16);
     return status_of(launch_conv_step(d->dtype, p, cu(stream)));
 }
 
@@ -522,7 +522,8 @@ sc_status sc_selective_scan_step(const sc_ssm_desc* d, float* pool, int64_t pool
     SsmParams p;
     const sc_status st = ssm_args(d, true, &p);
     if (st != SC_OK) return st;
-    if (pool_rows < 0 || (!slots && pool_rows < d->batch) || !multiple(slots, 4)) return SC_ERR_INVALID;
+    if (pool_rows < 0 || pool_rows > kMaxGrid || (!slots && pool_rows < d->batch) || !multiple(slots, 4))
+        return SC_ERR_INVALID;
     if (product(pool_rows, d->states, d->channels, 8) < 0) return SC_ERR_INVALID;
     if (d->batch == 0 || d->channels == 0) return SC_OK;
     const int eb = bytes_of(d->dtype);

@@ -33,7 +33,7 @@ cudaError_t launch_embed(int dtype, const EmbedParams& p, cudaStream_t s);
 struct EmbedGradPlan {
     int digit_bits, passes;
     long long tiles;  // of the sort
-    size_t keys0, keys1, vals0, vals1, counts, partials, total;  // offsets, then the size
+    size_t keys0, keys1, vals0, vals1, first, last, counts, partials, total;  // offsets, then the size
 };
 EmbedGradPlan embed_grad_plan(long long tokens, long long vocab, long long dim);
 sc_status launch_embed_grad(int dtype, int wtype, const EmbedParams& p, const EmbedGradPlan& plan,

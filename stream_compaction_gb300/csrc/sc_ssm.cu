@@ -15,7 +15,7 @@ cudaError_t launch_ssm_grad_f32(const SsmParams&, const SsmPlan&, int*, cudaStre
 
 namespace {
 
-constexpr int kStepNT = 256;
+constexpr int kStepNT = 128;
 constexpr long long kSms = 152;
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
@@ -54,88 +54,120 @@ __global__ void __launch_bounds__(256) ssm_sum_kernel(SsmParams p, int np) {
 }
 
 // One token: S lanes per channel, four states each; the state is read and
-// written once, the floor of the call.
+// written once, the floor of the call.  A thread serves R rows of the batch, so
+// that R states are under way in it, A is read once for them, and the work per
+// row and channel (softplus, gate) is done once: by lane r of the channel's
+// lanes for row r, the others get d and d x from it.  (256 x 4096 x 16 states:
+// 42 us with one row a thread, whose S lanes all did that work; 25 us so.)
 template <class T, int S, bool kVec>
 __global__ void __launch_bounds__(kStepNT) ssm_step_kernel(SsmParams p, unsigned cblocks) {
-    const long long b = blockIdx.x / cblocks;
+    constexpr int R = S < 4 ? S : 4;
+    const long long b0 = (long long)(blockIdx.x / cblocks) * R;
     const long long e = (long long)(blockIdx.x % cblocks) * (kStepNT / S) + threadIdx.x / S;
-    const int n0 = 4 * (threadIdx.x % S);
-    const bool live = e < p.channels;
-    const long long slot = p.slots ? (long long)__ldg(p.slots + b) : b;
-    T* yp = static_cast<T*>(p.y) + b * p.y_batch + e;
-    if (slot < 0 || slot >= p.pool_rows) {  // the whole row
-        if (live && n0 == 0) *yp = from_f32<T>(0.0f);
-        return;
+    const int s = threadIdx.x % S, n0 = 4 * s, first = (int)(threadIdx.x & 31) - s;  // first: the channel's first lane
+    const bool live = e < p.channels, on = live && n0 < p.states;
+    // the row that this lane does the elements of
+    const long long b = b0 + s % R;
+    int slot = -1;
+    if (live && b < p.batch) {
+        const long long q = p.slots ? (long long)__ldg(p.slots + b) : b;
+        slot = q >= 0 && q < p.pool_rows ? (int)q : -1;
     }
-    float sum = 0.0f, x = 0.0f;
-    if (live) {
-        const long long group = e / (p.channels / p.groups);
-        float* hp = p.pool + (slot * p.channels + e) * p.states + n0;
-        const float* Ap = p.A + e * p.states + n0;
-        const T* Bp = static_cast<const T*>(p.B) + b * p.B_batch + group * p.B_group + n0;
-        const T* Cp = static_cast<const T*>(p.C) + b * p.C_batch + group * p.C_group + n0;
-        float h[4], A[4], B[4], C[4];
-        const bool on = n0 < p.states;
-        if constexpr (kVec) {  // states a multiple of 4
-            float4 hv = make_float4(0.0f, 0.0f, 0.0f, 0.0f), av = hv;
+    const bool run = slot >= 0;
+    const long long group = live ? e / (p.channels / p.groups) : 0;
+    const float x = run ? to_f32(__ldg(static_cast<const T*>(p.x) + b * p.x_batch + e)) : 0.0f;
+    float d = run ? to_f32(__ldg(static_cast<const T*>(p.dt) + b * p.dt_batch + e)) : 0.0f;
+    const float z = run && p.z ? to_f32(__ldg(static_cast<const T*>(p.z) + b * p.z_batch + e)) : 0.0f;
+    const float bias = run && p.dt_bias ? __ldg(p.dt_bias + e) : 0.0f, D = run && p.D ? __ldg(p.D + e) : 0.0f;
+    float A[4] = {0.0f, 0.0f, 0.0f, 0.0f}, h[R][4], B[R][4], C[R][4];
+    float* hp[R];
+    const float* Ap = p.A + e * p.states + n0;
+    if constexpr (kVec) {  // states a multiple of 4
+        if (on) {
+            const float4 av = __ldg(reinterpret_cast<const float4*>(Ap));
+            A[0] = av.x; A[1] = av.y; A[2] = av.z; A[3] = av.w;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (live && n0 + k < p.states) A[k] = __ldg(Ap + k);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int row = __shfl_sync(0xffffffffu, slot, first + r);
+        hp[r] = row >= 0 && on ? p.pool + ((long long)row * p.channels + e) * p.states + n0 : nullptr;
+        const T* Bp = static_cast<const T*>(p.B) + (b0 + r) * p.B_batch + group * p.B_group + n0;
+        const T* Cp = static_cast<const T*>(p.C) + (b0 + r) * p.C_batch + group * p.C_group + n0;
+        if constexpr (kVec) {
+            float4 hv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             Vec<T, 4> bv, cv;
             bv.zero();
             cv.zero();
-            if (on) {
-                hv = *reinterpret_cast<const float4*>(hp);
-                av = __ldg(reinterpret_cast<const float4*>(Ap));
+            if (hp[r]) {
+                hv = *reinterpret_cast<const float4*>(hp[r]);
                 bv.load(Bp);
                 cv.load(Cp);
             }
-            h[0] = hv.x; h[1] = hv.y; h[2] = hv.z; h[3] = hv.w;
-            A[0] = av.x; A[1] = av.y; A[2] = av.z; A[3] = av.w;
+            h[r][0] = hv.x; h[r][1] = hv.y; h[r][2] = hv.z; h[r][3] = hv.w;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                B[k] = bv.get(k);
-                C[k] = cv.get(k);
+                B[r][k] = bv.get(k);
+                C[r][k] = cv.get(k);
             }
         } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const bool in = n0 + k < p.states;
-                h[k] = in ? hp[k] : 0.0f;
-                A[k] = in ? __ldg(Ap + k) : 0.0f;
-                B[k] = in ? to_f32(__ldg(Bp + k)) : 0.0f;
-                C[k] = in ? to_f32(__ldg(Cp + k)) : 0.0f;
+                const bool in = hp[r] && n0 + k < p.states;
+                h[r][k] = in ? hp[r][k] : 0.0f;
+                B[r][k] = in ? to_f32(__ldg(Bp + k)) : 0.0f;
+                C[r][k] = in ? to_f32(__ldg(Cp + k)) : 0.0f;
             }
         }
-        x = to_f32(__ldg(static_cast<const T*>(p.x) + b * p.x_batch + e));
-        float d = to_f32(__ldg(static_cast<const T*>(p.dt) + b * p.dt_batch + e)) + (p.dt_bias ? __ldg(p.dt_bias + e) : 0.0f);
-        if (p.softplus) d = softplus(d);
-        const float u = d * x, d2 = d * kLog2e;
+    }
+    d += bias;
+    if (p.softplus) d = softplus(d);
+    const float u = d * x, d2 = d * kLog2e;
+    float sum[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float dr = __shfl_sync(0xffffffffu, d2, first + r), ur = __shfl_sync(0xffffffffu, u, first + r);
+        sum[r] = 0.0f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            h[k] = fmaf(ex2(d2 * A[k]), h[k], u * B[k]);
-            sum = fmaf(C[k], h[k], sum);
+            h[r][k] = fmaf(ex2(dr * A[k]), h[r][k], ur * B[r][k]);
+            sum[r] = fmaf(C[r][k], h[r][k], sum[r]);
         }
         if constexpr (kVec) {
-            if (on) *reinterpret_cast<float4*>(hp) = make_float4(h[0], h[1], h[2], h[3]);
+            if (hp[r]) *reinterpret_cast<float4*>(hp[r]) = make_float4(h[r][0], h[r][1], h[r][2], h[r][3]);
         } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (n0 + k < p.states) hp[k] = h[k];
+                if (hp[r] && n0 + k < p.states) hp[r][k] = h[r][k];
         }
     }
+    // over the channel's lanes; lane r keeps row r's
+    float y;
+    const bool b0s = s & 1, b1s = s & 2;
+    const float t0 = (b0s ? sum[1] : sum[0]) + __shfl_xor_sync(0xffffffffu, b0s ? sum[0] : sum[1], 1);
+    if constexpr (R == 4) {
+        const float t1 = (b0s ? sum[3] : sum[2]) + __shfl_xor_sync(0xffffffffu, b0s ? sum[2] : sum[3], 1);
+        y = (b1s ? t1 : t0) + __shfl_xor_sync(0xffffffffu, b1s ? t0 : t1, 2);
 #pragma unroll
-    for (int m = 1; m < S; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    if (live && n0 == 0) {
-        float y = fmaf(p.D ? __ldg(p.D + e) : 0.0f, x, sum);
-        if (p.z) {
-            const float z = to_f32(__ldg(static_cast<const T*>(p.z) + b * p.z_batch + e));
-            y *= z * sigmoid(z);
-        }
-        *yp = from_f32<T>(y);
+        for (int m = 4; m < S; m <<= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
+    } else {
+        y = t0;
+    }
+    if (live && s < R && b < p.batch) {
+        y = fmaf(D, x, y);
+        if (p.z) y *= z * sigmoid(z);
+        static_cast<T*>(p.y)[b * p.y_batch + e] = from_f32<T>(run ? y : 0.0f);  // a row that sits out: 0
     }
 }
 
 template <class T, int S>
 cudaError_t step_lanes(const SsmParams& p, cudaStream_t s) {
-    const unsigned cblocks = (unsigned)ceil_div(p.channels, kStepNT / S), grid = cblocks * (unsigned)p.batch;
+    const unsigned cblocks = (unsigned)ceil_div(p.channels, kStepNT / S);
+    const unsigned grid = cblocks * (unsigned)ceil_div(p.batch, S < 4 ? S : 4);
     if (p.vec) ssm_step_kernel<T, S, true><<<grid, kStepNT, 0, s>>>(p, cblocks);
     else ssm_step_kernel<T, S, false><<<grid, kStepNT, 0, s>>>(p, cblocks);
     return cudaGetLastError();
@@ -162,9 +194,20 @@ SsmPlan ssm_plan(long long batch, long long length, long long channels, long lon
     const long long block = ch * (g.lanes == 16 ? 2 : 4), np = 4 * g.lanes;
     g.blocks_per_group = ceil_div(per, block);
     const long long warps = batch * groups * ceil_div(per, ch), tiles = ceil_div(length, kTile);
-    // Split where even one warp per SM sub-partition is not there.
+    // Forward: a pair of warps alone takes about 90 ns a token, and an SM's pairs
+    // together 27 ns each, so three or four keep it busy; a split costs the
+    // recurrence nearly twice.  Below 1.7 pairs an SM it pays, and then into about
+    // 7 pairs an SM (1 x 4096 x 4096, 128 pairs: 192 us in 4 chunks, 167 in 8 to 10;
+    // 4 x 4096 x 4096, 512 pairs, with gradient: 2.17 ms whole, 2.29 in 2).
+    // Backward: one wave of the CTAs that the SMs hold (of 512 warps, 128 CTAs:
+    // 2.87 ms whole, 2.17 in 2 chunks = 256 CTAs, 2.38 in 3 = 384).
     long long chunks = 1;
-    if (warps < 4 * kSms) chunks = std::min(ceil_div(8 * kSms, warps), std::max(tiles / 4, 1ll));
+    if (grad) {
+        const long long ctas = g.blocks_per_group * groups * batch, slots = (g.lanes == 16 ? 3 : 2) * kSms;
+        chunks = std::min(std::max(slots / ctas, 1ll), std::max(tiles / 2, 1ll));
+    } else if (10 * warps < 17 * kSms) {
+        chunks = std::min(ceil_div(7 * kSms, warps), std::max(tiles / 4, 1ll));
+    }
     g.chunk_tiles = ceil_div(tiles, chunks);
     g.chunks = (int)ceil_div(tiles, g.chunk_tiles);
     size_t at = 0;

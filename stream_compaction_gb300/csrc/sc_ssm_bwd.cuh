@@ -100,38 +100,50 @@ __global__ void __launch_bounds__(32 * kBackWarps) ssm_back_summary_kernel(SsmPa
         const int nt = tile_tokens<kTile>(p, tile * kTile);
         const unsigned hm = tile_heads(heads, tile * kTile, nt, lane);
         cut |= hm;
+        auto stage = [&](auto as_plain) {
+            constexpr bool F = decltype(as_plain)::value;
+            f2 d[Rows::NA][2], g[Rows::NA][2];
 #pragma unroll
-        for (int a = 0; a < Rows::NA; ++a) {
-            f2 d[2], g[2];
+            for (int a = 0; a < Rows::NA; ++a) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                d[i] = add2(dt.pair(a, i), bias[i]);
-                if (p.softplus) d[i] = softplus_2(d[i]);
-                g[i] = dy.pair(a, i);
-                if (zp) g[i] = mul2(g[i], mul2(z.pair(a, i), sigmoid_2(z.pair(a, i))));
+                for (int i = 0; i < 2; ++i) {
+                    d[a][i] = add2(dt.pair(a, i), bias[i]);
+                    if (F || p.softplus) d[a][i] = softplus_2(d[a][i]);
+                    g[a][i] = dy.pair(a, i);
+                    if (F || zp) g[a][i] = mul2(g[a][i], mul2(z.pair(a, i), sigmoid_2(z.pair(a, i))));
+                }
+                Rows::template mask<F>(d[a], a, nt, left, lane);
             }
-            Rows::template mask<false>(d, a, nt, left, lane);
-            Rows::put(s_d[warp] + a * G::TP * G::CH, d, lane);
-            Rows::put(s_g[warp] + a * G::TP * G::CH, g, lane);
-        }
+#pragma unroll
+            for (int a = 0; a < Rows::NA; ++a) {
+                Rows::put(s_d[warp] + a * G::TP * G::CH, d[a], lane);
+                Rows::put(s_g[warp] + a * G::TP * G::CH, g[a], lane);
+            }
+        };
+        if (left == G::CH && nt == kTile && zp && p.softplus) stage(std::true_type{});
+        else stage(std::false_type{});
         C.to_shared(s_C[warp], lane);
         __syncwarp();
         if (tile > tile0) fetch(tile - 1);
-#pragma unroll 4
-        for (int t = kTile - 1; t >= 0; --t) {
-            f2 d[G::PC], g[G::PC], Cv[4];
-            read_channels<G>(ld + t * G::CH, d);
-            read_channels<G>(lg + t * G::CH, g);
-            read_states(lC + t * G::NP, Cv);
+        auto tokens = [&](auto with_heads) {
 #pragma unroll
-            for (int q = 0; q < G::PC; ++q) {
-                dsum[q] = add2(dsum[q], d[q]);
+            for (int t = kTile - 1; t >= 0; --t) {
+                f2 d[G::PC], g[G::PC], Cv[4];
+                read_channels<G>(ld + t * G::CH, d);
+                read_channels<G>(lg + t * G::CH, g);
+                read_states(lC + t * G::NP, Cv);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    dh[q][k] = mul2(ex2_2(mul2(d[q], A2[q][k])), fma2(Cv[k], g[q], dh[q][k]));
+                for (int q = 0; q < G::PC; ++q) {
+                    dsum[q] = add2(dsum[q], d[q]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        dh[q][k] = mul2(ex2_2(mul2(d[q], A2[q][k])), fma2(Cv[k], g[q], dh[q][k]));
+                }
+                if (decltype(with_heads)::value && (hm >> t & 1u)) clear<G>(dh);
             }
-            if (hm >> t & 1u) clear<G>(dh);
-        }
+        };
+        if (hm) tokens(std::true_type{});
+        else tokens(std::false_type{});
         __syncwarp();
     }
     leave_chunk<G>(p, b, at.chunk, at.ch0, left, lane, dh, dsum);
@@ -197,41 +209,87 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
     const T* Bp = static_cast<const T*>(p.B) + b * p.B_batch + at.group * p.B_group;
     const T* Cp = static_cast<const T*>(p.C) + b * p.C_batch + at.group * p.C_group;
     const long long orow = b * p.length * p.channels + at.ch0;  // dx, ddt, dz are contiguous
+    const bool whole = left == G::CH && p.states == G::NP;
     const uint8_t* heads = p.heads ? p.heads + b * p.length : nullptr;
 
     for (long long tile = tile1 - 1; tile >= tile0; --tile) {
         const long long t0 = tile * kTile;
         const int nt = tile_tokens<kTile>(p, tile * kTile);
         const unsigned hm = tile_heads(heads, t0, nt, lane);
-        {
+        // Whole tiles of whole channel groups with a gate and a softplus, the
+        // common ones, take loops without a branch among the elements, which would
+        // keep their latencies from overlapping; so below.
+        const bool plain = whole && nt == kTile && zp && p.softplus;
+        auto stage = [&](auto as_plain) {
+            constexpr bool F = decltype(as_plain)::value;
             Rows x, dt, z, dy;
             States B, C;
-            dt.template load<false>(dtp + t0 * p.dt_token, p.dt_token, nt, left, lane);
-            x.template load<false>(xp + t0 * p.x_token, p.x_token, nt, left, lane);
-            dy.template load<false>(dyp + t0 * p.dy_token, p.dy_token, nt, left, lane);
-            if (zp) z.template load<false>(zp + t0 * p.z_token, p.z_token, nt, left, lane);
-            B.template load<false>(Bp + t0 * p.B_token, p.B_token, nt, (int)p.states, lane);
-            C.template load<false>(Cp + t0 * p.C_token, p.C_token, nt, (int)p.states, lane);
+            dt.template load<F>(dtp + t0 * p.dt_token, p.dt_token, nt, left, lane);
+            x.template load<F>(xp + t0 * p.x_token, p.x_token, nt, left, lane);
+            dy.template load<F>(dyp + t0 * p.dy_token, p.dy_token, nt, left, lane);
+            if (F || zp) z.template load<F>(zp + t0 * p.z_token, p.z_token, nt, left, lane);
+            B.template load<F>(Bp + t0 * p.B_token, p.B_token, nt, (int)p.states, lane);
+            C.template load<F>(Cp + t0 * p.C_token, p.C_token, nt, (int)p.states, lane);
+            f2 d[Rows::NA][2], u[Rows::NA][2], g[Rows::NA][2];
 #pragma unroll
             for (int a = 0; a < Rows::NA; ++a) {
-                f2 d[2], u[2], g[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    d[i] = add2(dt.pair(a, i), bias[i]);
-                    if (p.softplus) d[i] = softplus_2(d[i]);
-                    g[i] = dy.pair(a, i);
-                    if (zp) g[i] = mul2(g[i], mul2(z.pair(a, i), sigmoid_2(z.pair(a, i))));
+                    d[a][i] = add2(dt.pair(a, i), bias[i]);
+                    if (F || p.softplus) d[a][i] = softplus_2(d[a][i]);
+                    g[a][i] = dy.pair(a, i);
+                    if (F || zp) g[a][i] = mul2(g[a][i], mul2(z.pair(a, i), sigmoid_2(z.pair(a, i))));
                 }
-                Rows::template mask<false>(d, a, nt, left, lane);
+                Rows::template mask<F>(d[a], a, nt, left, lane);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) u[i] = mul2(d[i], x.pair(a, i));
-                Rows::put(sm + Sh::d + a * G::TP * G::CH, d, lane);
-                Rows::put(sm + Sh::u + a * G::TP * G::CH, u, lane);
-                Rows::put(sm + Sh::g + a * G::TP * G::CH, g, lane);
+                for (int i = 0; i < 2; ++i) u[a][i] = mul2(d[a][i], x.pair(a, i));
+            }
+#pragma unroll
+            for (int a = 0; a < Rows::NA; ++a) {
+                Rows::put(sm + Sh::d + a * G::TP * G::CH, d[a], lane);
+                Rows::put(sm + Sh::u + a * G::TP * G::CH, u[a], lane);
+                Rows::put(sm + Sh::g + a * G::TP * G::CH, g[a], lane);
             }
             B.to_shared(reinterpret_cast<float2*>(sm + Sh::B), lane);
             C.to_shared(reinterpret_cast<float2*>(sm + Sh::C), lane);
-        }
+        };
+        if (plain) stage(std::true_type{});
+        else stage(std::false_type{});
+        // the gradients by the elements of pass pa, whose first token is tq
+        auto finish = [&](int pa, int tq, auto as_plain) {
+            constexpr bool F = decltype(as_plain)::value;
+            const auto rx = Rows::template fetch<F>(xp + t0 * p.x_token, p.x_token, pa, nt, left, lane);
+            const auto rt = Rows::template fetch<F>(dtp + t0 * p.dt_token, p.dt_token, pa, nt, left, lane);
+            const auto ry = Rows::template fetch<F>(dyp + t0 * p.dy_token, p.dy_token, pa, nt, left, lane);
+            auto rz = ry;
+            if (F || zp) rz = Rows::template fetch<F>(zp + t0 * p.z_token, p.z_token, pa, nt, left, lane);
+            f2 y[2], gu[2], ga[2], d[2], g[2], dd[2];
+            Rows::get_sums(sm + Sh::gu, gu, lane);
+            Rows::get_sums(sm + Sh::ga, ga, lane);
+            Rows::get_sums(sm + Sh::y, y, lane);
+            Rows::get(sm + Sh::d + tq * G::CH, d, lane);
+            Rows::get(sm + Sh::g + tq * G::CH, g, lane);
+            const long long o = orow + t0 * p.channels;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const f2 x = Rows::pair_of(rx, i);
+                dd[i] = fma2(gu[i], x, mul2(ga[i], both(kLn2)));
+                if (F || p.softplus) dd[i] = mul2(dd[i], sigmoid_2(add2(Rows::pair_of(rt, i), bias[i])));
+                gu[i] = fma2(gu[i], d[i], mul2(g[i], D[i]));  // dx
+                dD[i] = fma2(g[i], x, dD[i]);
+                if (F || zp) {
+                    const f2 z = Rows::pair_of(rz, i), sg = sigmoid_2(z);
+                    const f2 slope = mul2(sg, fma2(z, fma2(sg, both(-1.0f), both(1.0f)), both(1.0f)));
+                    y[i] = mul2(mul2(Rows::pair_of(ry, i), fma2(D[i], x, y[i])), slope);
+                }
+            }
+            Rows::template store<F>(static_cast<T*>(p.dx) + o, p.channels, gu, pa, nt, left, lane);
+            Rows::template store<F>(static_cast<T*>(p.ddt) + o, p.channels, dd, pa, nt, left, lane);
+            if (F || zp) Rows::template store<F>(static_cast<T*>(p.dz) + o, p.channels, y, pa, nt, left, lane);
+            Rows::template mask<F>(dd, pa, nt, left, lane);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) dbias[i] = add2(dbias[i], dd[i]);
+        };
         const float* saved = p.saved + (b * tiles + tile) * p.channels * G::NP + at.ch0 * 4;
         __syncwarp();
         auto work = [&](auto with_heads) {
@@ -337,41 +395,9 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
                     }
                     reinterpret_cast<ulonglong2*>(sm + Sh::sums)[tq * 2 * G::S + o] = v;
                 }
-                if (tq % G::TP == 0) {  // the pass's elements
-                    const int pa = tq / G::TP;
-                    const auto rx = Rows::template fetch<false>(xp + t0 * p.x_token, p.x_token, pa, nt, left, lane);
-                    const auto rt = Rows::template fetch<false>(dtp + t0 * p.dt_token, p.dt_token, pa, nt, left, lane);
-                    const auto ry = Rows::template fetch<false>(dyp + t0 * p.dy_token, p.dy_token, pa, nt, left, lane);
-                    f2 y[2], gu[2], ga[2], d[2], g[2], dd[2];
-                    Rows::get_sums(sm + Sh::gu, gu, lane);
-                    Rows::get_sums(sm + Sh::ga, ga, lane);
-                    Rows::get(sm + Sh::d + tq * G::CH, d, lane);
-                    Rows::get(sm + Sh::g + tq * G::CH, g, lane);
-                    const long long o = orow + t0 * p.channels;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const f2 x = Rows::pair_of(rx, i);
-                        dd[i] = fma2(gu[i], x, mul2(ga[i], both(kLn2)));
-                        if (p.softplus) dd[i] = mul2(dd[i], sigmoid_2(add2(Rows::pair_of(rt, i), bias[i])));
-                        gu[i] = fma2(gu[i], d[i], mul2(g[i], D[i]));  // dx
-                        dD[i] = fma2(g[i], x, dD[i]);
-                    }
-                    Rows::template store<false>(static_cast<T*>(p.dx) + o, p.channels, gu, pa, nt, left, lane);
-                    Rows::template store<false>(static_cast<T*>(p.ddt) + o, p.channels, dd, pa, nt, left, lane);
-                    Rows::template mask<false>(dd, pa, nt, left, lane);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) dbias[i] = add2(dbias[i], dd[i]);
-                    if (zp) {
-                        const auto rz = Rows::template fetch<false>(zp + t0 * p.z_token, p.z_token, pa, nt, left, lane);
-                        Rows::get_sums(sm + Sh::y, y, lane);
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const f2 z = Rows::pair_of(rz, i), sg = sigmoid_2(z);
-                            const f2 slope = mul2(sg, fma2(z, fma2(sg, both(-1.0f), both(1.0f)), both(1.0f)));
-                            y[i] = mul2(mul2(Rows::pair_of(ry, i), fma2(D[i], Rows::pair_of(rx, i), y[i])), slope);
-                        }
-                        Rows::template store<false>(static_cast<T*>(p.dz) + o, p.channels, y, pa, nt, left, lane);
-                    }
+                if (tq % G::TP == 0) {
+                    if (plain) finish(tq / G::TP, tq, std::true_type{});
+                    else finish(tq / G::TP, tq, std::false_type{});
                 }
                 __syncwarp();
             }
