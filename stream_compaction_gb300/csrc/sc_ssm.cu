@@ -85,12 +85,12 @@ __global__ void __launch_bounds__(kStepNT) ssm_step_kernel(SsmParams p, unsigned
     if constexpr (kVec) {  // states a multiple of 4
         if (on) {
             const float4 av = __ldg(reinterpret_cast<const float4*>(Ap));
-            A[0] = av.x; A[1] = av.y; A[2] = av.z; A[3] = av.w;
+            A[0] = av.x * kLog2e; A[1] = av.y * kLog2e; A[2] = av.z * kLog2e; A[3] = av.w * kLog2e;
         }
     } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (live && n0 + k < p.states) A[k] = __ldg(Ap + k);
+            if (live && n0 + k < p.states) A[k] = __ldg(Ap + k) * kLog2e;
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -126,15 +126,15 @@ __global__ void __launch_bounds__(kStepNT) ssm_step_kernel(SsmParams p, unsigned
     }
     d += bias;
     if (p.softplus) d = softplus(d);
-    const float u = d * x, d2 = d * kLog2e;
+    const float u = d * x;
     float sum[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const float dr = __shfl_sync(0xffffffffu, d2, first + r), ur = __shfl_sync(0xffffffffu, u, first + r);
+        const float dr = __shfl_sync(0xffffffffu, d, first + r), ur = __shfl_sync(0xffffffffu, u, first + r);
         sum[r] = 0.0f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            h[r][k] = fmaf(ex2(dr * A[k]), h[r][k], ur * B[r][k]);
+            h[r][k] = fmaf(decay(dr, A[k]), h[r][k], ur * B[r][k]);
             sum[r] = fmaf(C[r][k], h[r][k], sum[r]);
         }
         if constexpr (kVec) {

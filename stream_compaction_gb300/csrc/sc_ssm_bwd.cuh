@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(32 * kBackWarps) ssm_back_summary_kernel(SsmPa
                     dsum[q] = add2(dsum[q], d[q]);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        dh[q][k] = mul2(ex2_2(mul2(d[q], A2[q][k])), fma2(Cv[k], g[q], dh[q][k]));
+                        dh[q][k] = mul2(decay_2(d[q], A2[q][k]), fma2(Cv[k], g[q], dh[q][k]));
                 }
                 if (decltype(with_heads)::value && (hm >> t & 1u)) clear<G>(dh);
             }
@@ -149,6 +149,8 @@ __global__ void __launch_bounds__(32 * kBackWarps) ssm_back_summary_kernel(SsmPa
     leave_chunk<G>(p, b, at.chunk, at.ch0, left, lane, dh, dsum);
     if (at.cblock == 0 && threadIdx.x == 0) p.cut[b * p.chunks + at.chunk] = cut != 0;
 }
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // h = q h[t-1] + d x B over the tokens of a quarter.
 template <class G, bool kHeads>
@@ -164,7 +166,7 @@ __device__ __forceinline__ void run_quarter(const float* ld, const float* lu, co
 #pragma unroll
         for (int q = 0; q < G::PC; ++q)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) h[q][k] = fma2(ex2_2(mul2(d[q], A2[q][k])), h[q][k], mul2(u[q], Bv[k]));
+            for (int k = 0; k < 4; ++k) h[q][k] = fma2(decay_2(d[q], A2[q][k]), h[q][k], mul2(u[q], Bv[k]));
     }
 }
 
@@ -255,14 +257,34 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
         };
         if (plain) stage(std::true_type{});
         else stage(std::false_type{});
-        // the gradients by the elements of pass pa, whose first token is tq
-        auto finish = [&](int pa, int tq, auto as_plain) {
+        if (tile > tile0 && left > 0) {  // the next tile and its states on their way into the L2
+            const long long t = t0 - kTile + lane % kTile;  // lanes 0 .. 15: x and dy, 16 ..: dt and z
+            prefetch_l2(lane < kTile ? xp + t * p.x_token : dtp + t * p.dt_token);
+            prefetch_l2(lane < kTile ? dyp + t * p.dy_token : zp ? zp + t * p.z_token : dtp + t * p.dt_token);
+            const float* sv = p.saved + (b * tiles + tile - 1) * p.channels * G::NP + at.ch0 * 4;
+            constexpr int kLines = G::CH * 16 / 128 > 0 ? G::CH * 16 / 128 : 1;  // of 128 bytes a four of states
+            if (lane < G::S * kLines && lane % kLines * 8 < left) prefetch_l2(sv + (lane / kLines * p.channels + lane % kLines * 8) * 4);
+        }
+        // The elements of pass pa once more, asked for before the pass's states are
+        // worked on and used after.
+        using Raw = decltype(Rows::template fetch<true>(xp, 0, 0, 0, 0, 0));
+        struct Pass {
+            Raw x, dt, dy, z;
+        };
+        auto again = [&](int pa, auto as_plain) {
             constexpr bool F = decltype(as_plain)::value;
-            const auto rx = Rows::template fetch<F>(xp + t0 * p.x_token, p.x_token, pa, nt, left, lane);
-            const auto rt = Rows::template fetch<F>(dtp + t0 * p.dt_token, p.dt_token, pa, nt, left, lane);
-            const auto ry = Rows::template fetch<F>(dyp + t0 * p.dy_token, p.dy_token, pa, nt, left, lane);
-            auto rz = ry;
-            if (F || zp) rz = Rows::template fetch<F>(zp + t0 * p.z_token, p.z_token, pa, nt, left, lane);
+            Pass r;
+            r.x = Rows::template fetch<F>(xp + t0 * p.x_token, p.x_token, pa, nt, left, lane);
+            r.dt = Rows::template fetch<F>(dtp + t0 * p.dt_token, p.dt_token, pa, nt, left, lane);
+            r.dy = Rows::template fetch<F>(dyp + t0 * p.dy_token, p.dy_token, pa, nt, left, lane);
+            r.z = r.dy;
+            if (F || zp) r.z = Rows::template fetch<F>(zp + t0 * p.z_token, p.z_token, pa, nt, left, lane);
+            return r;
+        };
+        // the gradients by the elements of pass pa, whose first token is tq
+        auto finish = [&](int pa, int tq, const Pass& e, auto as_plain) {
+            constexpr bool F = decltype(as_plain)::value;
+            const auto &rx = e.x, &rt = e.dt, &ry = e.dy, &rz = e.z;
             f2 y[2], gu[2], ga[2], d[2], g[2], dd[2];
             Rows::get_sums(sm + Sh::gu, gu, lane);
             Rows::get_sums(sm + Sh::ga, ga, lane);
@@ -312,6 +334,8 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
 #pragma unroll 1
             for (int q4 = kQuarters - 1; q4 >= 0; --q4) {
                 const int tq = q4 * kQuarter;
+                Pass raws;
+                if (tq % G::TP == 0) raws = plain ? again(tq / G::TP, std::true_type{}) : again(tq / G::TP, std::false_type{});
                 f2 a[kQuarter][G::PC][4], h[kQuarter + 1][G::PC][4];  // q, and h before each token
                 if (q4 == 0) {
                     float raw[G::CPL][4];
@@ -339,7 +363,7 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
                     for (int q = 0; q < G::PC; ++q)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            a[j][q][k] = ex2_2(mul2(d[q], A2[q][k]));
+                            a[j][q][k] = decay_2(d[q], A2[q][k]);
                             h[j + 1][q][k] = fma2(a[j][q][k], head ? 0ull : h[j][q][k], mul2(u[q], Bv[k]));
                         }
                 }
@@ -396,14 +420,31 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
                     reinterpret_cast<ulonglong2*>(sm + Sh::sums)[tq * 2 * G::S + o] = v;
                 }
                 if (tq % G::TP == 0) {
-                    if (plain) finish(tq / G::TP, tq, std::true_type{});
-                    else finish(tq / G::TP, tq, std::false_type{});
+                    if (plain) finish(tq / G::TP, tq, raws, std::true_type{});
+                    else finish(tq / G::TP, tq, raws, std::false_type{});
                 }
                 __syncwarp();
             }
         };
         if (hm) work(std::true_type{});
         else work(std::false_type{});
+        // dA goes to its partial row every 128 tokens: one running sum over
+        // thousands of tokens of either sign would lose a digit to rounding
+        if ((tile - tile0) % 8 == 0 && left > 0) {
+            float* pa = p.part_a + (b * p.chunks + at.chunk) * p.channels * G::NP + at.ch0 * 4;
+            if (tile + 8 < tile1) {
+                float raw[G::CPL][4];
+                f2 old[G::PC][4];
+                load_lane<G>(pa, p.channels, left, lane, raw);
+                to_pairs<G>(raw, 1.0f, old);
+#pragma unroll
+                for (int q = 0; q < G::PC; ++q)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) dA[q][k] = add2(dA[q][k], old[q][k]);
+            }
+            store_lane<G>(pa, p.channels, left, lane, dA);
+            clear<G>(dA);
+        }
         __syncthreads();
         float4* part = reinterpret_cast<float4*>(p.part_bc + ((at.cblock * p.batch + b) * p.length + t0) * 2 * G::NP);
         for (int i = threadIdx.x; i < nt * 2 * G::S; i += 32 * kWarps) {
@@ -422,7 +463,6 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
     }
     if (left == 0) return;
     const long long row = b * p.chunks + at.chunk, rows = p.batch * p.chunks;
-    store_lane<G>(p.part_a + row * p.channels * G::NP + at.ch0 * 4, p.channels, left, lane, dA);
     Rows::put_channel_sums(p.part_d + row * p.channels + at.ch0, dD, left, lane);
     Rows::put_channel_sums(p.part_d + (rows + row) * p.channels + at.ch0, dbias, left, lane);
     if (p.dstate && at.chunk == 0)

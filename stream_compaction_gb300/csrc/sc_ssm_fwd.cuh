@@ -338,8 +338,8 @@ __global__ void __launch_bounds__(64) ssm_kernel(SsmParams p, int blocks_per_gro
 #pragma unroll
                 for (int i = 0; i < G::P / 2; ++i) {
                     const ulonglong2 Bv = lB[t * (G::NP / 4) + i];
-                    a[2 * i] = ex2_2(mul2(du.x, A2[2 * i]));
-                    a[2 * i + 1] = ex2_2(mul2(du.x, A2[2 * i + 1]));
+                    a[2 * i] = decay_2(du.x, A2[2 * i]);
+                    a[2 * i + 1] = decay_2(du.x, A2[2 * i + 1]);
                     ub[2 * i] = mul2(du.y, Bv.x);
                     ub[2 * i + 1] = mul2(du.y, Bv.y);
                 }
