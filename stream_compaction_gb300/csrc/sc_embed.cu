@@ -14,7 +14,7 @@
 //   long runs  tokens of one id may be a large part of all (padding, a frequent
 //              word): runs longer than kRun are cut at multiples of kRun of the
 //              sorted order and each piece summed by a CTA of its own;
-//   rows       each CTA takes kRowsPerCta rows of dweight: first it writes the
+//   rows       each CTA takes up to kRowsPerCta rows of dweight: first it writes the
 //              zeros of those without a token, which wait for nothing, then the
 //              sums of at most kRun rows of dout, or of the row's pieces.
 // Sums are taken in the order of t in float32, so a result is the same on
@@ -37,7 +37,7 @@ constexpr int kSortWarps = kNT / 32;
 constexpr int kMaxDigit = 1024;
 constexpr int kClusterNT = 1024, kClusterWarps = kClusterNT / 32, kClusterCtas = 8;
 constexpr long long kClusterKeys = 8ll * kClusterNT * kClusterCtas;  // 8 a thread: 65536
-constexpr int kRun = 64;
+constexpr int kRun = 32;
 constexpr int kRowsPerCta = 32;
 
 __device__ __forceinline__ long long load_id(const void* ids, int ids64, long long i) {
@@ -360,13 +360,20 @@ __device__ __forceinline__ void add_rows(const T* dout, long long ldd, const uin
             for (int k = 0; k < W; ++k) acc[k] += v.get(k);
         }
     } else {
-        for (; i < hi; ++i) {
-            const T* row = dout + (long long)vals[i] * ldd;
+        for (; i < hi; i += 4) {
+            T v[4][W];
 #pragma unroll
-            for (int k = 0; k < W; ++k) {
-                const long long cc = c + (long long)k * step;
-                if (cc < dim) acc[k] += to_f32(__ldg(row + cc));
+            for (int j = 0; j < 4; ++j) {
+                const T* row = dout + (i + j < hi ? (long long)vals[i + j] : 0) * ldd + c;
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+                    v[j][k] = i + j < hi && c + (long long)k * step < dim ? __ldg(row + (long long)k * step)
+                                                                         : from_f32<T>(0.0f);
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int k = 0; k < W; ++k) acc[k] += to_f32(v[j][k]);
         }
     }
 }
@@ -380,6 +387,7 @@ __global__ void __launch_bounds__(kNT) embed_pieces_kernel(EmbedParams p, const 
                                                            Runs runs, float* partials, int tpr) {
     __shared__ long long s_lo[2], s_hi[2];
     __shared__ uint32_t s_vals[kRun];
+    __shared__ float s_sum[W * kNT];
     const long long b0 = (long long)blockIdx.x * kRun, b1 = min(b0 + kRun, p.tokens);
     if (threadIdx.x >= 32 && threadIdx.x < 32 + kRun && b0 + threadIdx.x - 32 < b1)
         s_vals[threadIdx.x - 32] = vals[b0 + threadIdx.x - 32];
@@ -395,18 +403,29 @@ __global__ void __launch_bounds__(kNT) embed_pieces_kernel(EmbedParams p, const 
         s_hi[threadIdx.x] = hi;
     }
     __syncthreads();
-    const int sub = threadIdx.x / tpr, lane = threadIdx.x % tpr;
-    // with few columns the threads left over take the second run's sum
-    for (int which = sub; which < 2; which += kNT / tpr) {
+    // with few columns the piece's rows go to several thread rows, whose sums are
+    // then added in order
+    const int sub = threadIdx.x / tpr, lane = threadIdx.x % tpr, subs = kNT / tpr, share = (kRun + subs - 1) / subs;
+    const long long c = (long long)blockIdx.y * tpr * W + (long long)lane * (kVec ? W : 1);
+    for (int which = 0; which < 2; ++which) {
         const long long lo = s_lo[which], hi = s_hi[which];
         if (hi == lo) continue;
         if (which == 1 && lo <= b0) continue;  // the same run as `which == 0`
         float acc[W];
 #pragma unroll
         for (int k = 0; k < W; ++k) acc[k] = 0.0f;
-        const long long c = (long long)blockIdx.y * tpr * W + (long long)lane * (kVec ? W : 1);
-        add_rows<T, W, kVec>(static_cast<const T*>(p.weight), p.ldw, s_vals, max(lo, b0) - b0, min(hi, b1) - b0, c, tpr,
-                             p.dim, acc);
+        const long long from = max(lo, b0) - b0 + sub * share, to = min(min(hi, b1) - b0, from + share);
+        add_rows<T, W, kVec>(static_cast<const T*>(p.weight), p.ldw, s_vals, from, to, c, tpr, p.dim, acc);
+        if (subs > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < W; ++k) s_sum[k * kNT + threadIdx.x] = acc[k];
+            __syncthreads();
+            if (sub != 0) continue;
+            for (int q = 1; q < subs; ++q)
+#pragma unroll
+                for (int k = 0; k < W; ++k) acc[k] += s_sum[k * kNT + q * tpr + lane];
+        }
         float* row = partials + (2 * (long long)blockIdx.x + which) * p.dim;
 #pragma unroll
         for (int k = 0; k < W; ++k) {
@@ -418,21 +437,33 @@ __global__ void __launch_bounds__(kNT) embed_pieces_kernel(EmbedParams p, const 
 
 template <class T, class O, int W, bool kVec>
 __global__ void __launch_bounds__(kNT) embed_rows_kernel(EmbedParams p, const uint32_t* vals, Runs runs,
-                                                         const float* partials, int tpr) {
+                                                         const float* partials, int tpr, int per_cta) {
     __shared__ uint32_t s_first[kRowsPerCta], s_last[kRowsPerCta];
-    const long long row0 = (long long)blockIdx.x * kRowsPerCta;
-    if (threadIdx.x < kRowsPerCta) {
+    const long long row0 = (long long)blockIdx.x * per_cta;
+    if (threadIdx.x < per_cta) {
         const bool in = row0 + threadIdx.x < p.vocab;
         s_last[threadIdx.x] = in ? runs.last[row0 + threadIdx.x] : 0u;
         s_first[threadIdx.x] = in ? runs.first[row0 + threadIdx.x] : 0u;  // anything where last is 0
     }
     __syncthreads();
     const int sub = threadIdx.x / tpr, lane = threadIdx.x % tpr, step = kNT / tpr;
-    const int rows = (int)min((long long)kRowsPerCta, p.vocab - row0);
+    const int rows = (int)min((long long)per_cta, p.vocab - row0);
     const long long c = (long long)blockIdx.y * tpr * W + (long long)lane * (kVec ? W : 1);
     if (kVec && c >= p.dim) return;
     O* out0 = static_cast<O*>(p.out) + row0 * p.ldo + c;
-    if (!p.accumulate) {
+    if (!kVec && !p.accumulate && p.ldo == p.dim && gridDim.y == 1) {
+        // rows without gaps, but not in 16-byte words: zeros over the CTA's whole
+        // stretch, in words as far as it has them, then the sums over those
+        O* begin = static_cast<O*>(p.out) + row0 * p.ldo;
+        const long long n = (long long)rows * p.dim;
+        const long long head = min((long long)((16 - reinterpret_cast<uintptr_t>(begin) % 16) % 16 / sizeof(O)), n);
+        const long long words = (n - head) / (16 / (int)sizeof(O)), tail = head + words * (16 / (int)sizeof(O));
+        for (long long i = threadIdx.x; i < words; i += kNT)
+            reinterpret_cast<uint4*>(begin + head)[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (threadIdx.x < head) begin[threadIdx.x] = from_f32<O>(0.0f);
+        if (tail + threadIdx.x < n) begin[tail + threadIdx.x] = from_f32<O>(0.0f);
+        __syncthreads();
+    } else if (!p.accumulate) {
         for (int r = sub; r < rows; r += step) {
             if (s_last[r] != 0u) continue;
             O* out = out0 + r * p.ldo;
@@ -515,9 +546,13 @@ cudaError_t sums_of(const EmbedParams& p, const uint32_t* keys, const uint32_t* 
         else embed_pieces_kernel<T, W, false><<<grid, kNT, 0, s>>>(p, keys, vals, runs, partials, tpr);
         count_launches(1);
     }
-    const dim3 grid((unsigned)ceil_div(p.vocab, kRowsPerCta), slices);
-    if (p.vec) embed_rows_kernel<T, O, W, true><<<grid, kNT, 0, s>>>(p, vals, runs, partials, tpr);
-    else embed_rows_kernel<T, O, W, false><<<grid, kNT, 0, s>>>(p, vals, runs, partials, tpr);
+    // fewer rows a CTA, down to one for each of its thread rows, where 32 would
+    // leave SMs without a CTA
+    int per_cta = kRowsPerCta;
+    while (per_cta > std::max(kNT / tpr / 2, 1) && ceil_div(p.vocab, per_cta) * slices < 8 * 152) per_cta /= 2;
+    const dim3 grid((unsigned)ceil_div(p.vocab, per_cta), slices);
+    if (p.vec) embed_rows_kernel<T, O, W, true><<<grid, kNT, 0, s>>>(p, vals, runs, partials, tpr, per_cta);
+    else embed_rows_kernel<T, O, W, false><<<grid, kNT, 0, s>>>(p, vals, runs, partials, tpr, per_cta);
     count_launches(1);
     return cudaGetLastError();
 }
