@@ -143,7 +143,7 @@ struct Filter {
 
 // Thread: channels c .. c + 3, one run of tokens of one row.
 template <class T, int WD, bool kVec, bool kHeads>
-__global__ void __launch_bounds__(kNT) conv_kernel(ConvParams p, int run, unsigned cblocks, unsigned runs) {
+__global__ void __launch_bounds__(kNT, WD == 4 && kVec && !kHeads ? 8 : 4) conv_kernel(ConvParams p, int run, unsigned cblocks, unsigned runs) {
     const Place at(cblocks, runs, kCh);
     const long long c = at.c, b = at.b, left = p.channels - c;
     if (left <= 0) return;
@@ -445,8 +445,11 @@ int run_length(long long batch, long long length, long long channels, int n, int
     return run;
 }
 
-constexpr int kLeast = 8, kMost = 32;            // tokens of a run, forward
-constexpr int kGradLeast = 8, kGradMost = 64;    // and backward
+// Tokens of a run: 8 x 4096 x 4096 bfloat16, forward and gradient, took 345 us
+// with at most 32 and 64, 325 with 64 and 128, 320 with 64 and 256, 342 with 256
+// and 256 (and 312 with the forward kernel held to 64 registers).
+constexpr int kLeast = 8, kMost = 64;
+constexpr int kGradLeast = 8, kGradMost = 256;
 
 template <class T, int WD>
 cudaError_t conv_of(const ConvParams& p, cudaStream_t s) {

@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
     const T* Bp = static_cast<const T*>(p.B) + b * p.B_batch + at.group * p.B_group;
     const T* Cp = static_cast<const T*>(p.C) + b * p.C_batch + at.group * p.C_group;
     const long long orow = b * p.length * p.channels + at.ch0;  // dx, ddt, dz are contiguous
-    const bool whole = left == G::CH && p.states == G::NP;
+    const bool whole = left == G::CH;
     const uint8_t* heads = p.heads ? p.heads + b * p.length : nullptr;
 
     for (long long tile = tile1 - 1; tile >= tile0; --tile) {
@@ -230,8 +230,8 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
             x.template load<F>(xp + t0 * p.x_token, p.x_token, nt, left, lane);
             dy.template load<F>(dyp + t0 * p.dy_token, p.dy_token, nt, left, lane);
             if (F || zp) z.template load<F>(zp + t0 * p.z_token, p.z_token, nt, left, lane);
-            B.template load<F>(Bp + t0 * p.B_token, p.B_token, nt, (int)p.states, lane);
-            C.template load<F>(Cp + t0 * p.C_token, p.C_token, nt, (int)p.states, lane);
+            B.template load<false>(Bp + t0 * p.B_token, p.B_token, nt, (int)p.states, lane);
+            C.template load<false>(Cp + t0 * p.C_token, p.C_token, nt, (int)p.states, lane);
             f2 d[Rows::NA][2], u[Rows::NA][2], g[Rows::NA][2];
 #pragma unroll
             for (int a = 0; a < Rows::NA; ++a) {

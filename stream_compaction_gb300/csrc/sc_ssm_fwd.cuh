@@ -147,13 +147,13 @@ __global__ void __launch_bounds__(64) ssm_kernel(SsmParams p, int blocks_per_gro
         auto raw = [&](int k, int what) { return reinterpret_cast<T*>(s_all + (k % kRing) * Sh::kRaw + what); };
         // The copies of one tile, addresses as far as possible made beforehand: a
         // lane's first element of each tensor, moved on by a tile each time.
-        const bool whole = left == G::CH && p.states == G::NP;
+        const bool whole = left == G::CH;
         RowCopy<T, kT, G::CH, kVec> cx(xp, p.x_token, lane), cdt(dtp, p.dt_token, lane), cz(zp, p.z_token, lane);
         RowCopy<T, kT, G::NP, kVec> cB(Bp, p.B_token, lane), cC(Cp, p.C_token, lane);
         auto fetch = [&](int k) {
             if (k < n) {
                 const int nt = tile_len(k);
-                if (whole && nt == kT) {
+                if (whole && nt == kT && p.states == G::NP) {
                     cx.template run<true>(raw(k, Sh::x), nt, left, lane);
                     cdt.template run<true>(raw(k, Sh::dt), nt, left, lane);
                     if (gated) cz.template run<true>(raw(k, Sh::z), nt, left, lane);
