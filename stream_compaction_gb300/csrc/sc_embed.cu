@@ -8,7 +8,7 @@
 //              at most 10 bits a pass (so two passes below 2^20 ids).  Up to
 //              kClusterKeys tokens: one launch, one cluster of up to 8 CTAs whose
 //              digit counts meet in distributed shared memory (16384 tokens:
-//              XX us against 38 us of the four launches below).  Beyond: per
+//              17 us against 38 us of the four launches below).  Beyond: per
 //              tile digit counts, their sums over tiles, the placement.  Then
 //              where each id's run starts and ends.
 //   long runs  tokens of one id may be a large part of all (padding, a frequent

@@ -207,6 +207,8 @@ bool ssm_vec(const sc_ssm_desc* d, const Tensor* more, int n_more) {
 void ssm_place(SsmParams* p, const SsmPlan& g, unsigned char* base) {
     p->chunks = g.chunks;
     p->chunk_tiles = g.chunk_tiles;
+    p->runs = g.runs;
+    p->run_tiles = g.run_tiles;
     p->carry = reinterpret_cast<float*>(base + g.carry);
     p->sum_d = reinterpret_cast<float*>(base + g.sum_d);
     p->cut = base + g.cut;

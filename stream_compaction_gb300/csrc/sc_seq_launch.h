@@ -88,9 +88,13 @@ struct SsmParams {
     // a length split into `chunks` runs of chunk_tiles tiles of SC_SSM_SAVE tokens
     int chunks;
     long long chunk_tiles;
-    float* carry;    // [batch][chunks][channels][padded states] what a chunk makes of a zero state
-    float* sum_d;    // [batch][chunks][channels] the chunk's sum of d
-    uint8_t* cut;    // [batch][chunks] a segment starts inside the chunk
+    // what a run of run_tiles tiles makes of a zero state; a chunk is one run, or
+    // some of them in the gradient
+    int runs;
+    long long run_tiles;
+    float* carry;    // [batch][runs][channels][padded states]
+    float* sum_d;    // [batch][runs][channels] the run's sum of d
+    uint8_t* cut;    // [batch][runs] a segment starts inside the run
     // gradient
     const void* dy;
     long long dy_batch, dy_token;
@@ -108,8 +112,8 @@ struct SsmParams {
 // Lanes that share a channel (4 states each) for a number of states: 2, 4, 8 or 16.
 int ssm_lanes(long long states);
 struct SsmPlan {
-    int lanes, chunks;
-    long long chunk_tiles, blocks_per_group;  // channel blocks of one CTA
+    int lanes, chunks, runs;
+    long long chunk_tiles, run_tiles, blocks_per_group;  // channel blocks of one CTA
     size_t carry, sum_d, cut, part_bc, part_a, part_d, total;
 };
 SsmPlan ssm_plan(long long batch, long long length, long long channels, long long states, long long groups, bool grad);

@@ -200,7 +200,10 @@ SsmPlan ssm_plan(long long batch, long long length, long long channels, long lon
     // 7 pairs an SM (1 x 4096 x 4096, 128 pairs: 192 us in 4 chunks, 167 in 8 to 10;
     // 4 x 4096 x 4096, 512 pairs, with gradient: 2.17 ms whole, 2.29 in 2).
     // Backward: one wave of the CTAs that the SMs hold (of 512 warps, 128 CTAs:
-    // 2.87 ms whole, 2.17 in 2 chunks = 256 CTAs, 2.38 in 3 = 384).
+    // 2.87 ms whole, 2.17 in 2 chunks = 256 CTAs, 2.38 in 3 = 384), whose chunks a
+    // first kernel walks in runs, about 4 warps' an SM (4 x 4096 x 4096, with the
+    // forward pass: 2.03 ms with a run a chunk, 1.98 so, and the same with 8 or 16;
+    // 2 x 1000 x 1002 with 24 states: 209 us, 206, 213 and 234).
     long long chunks = 1;
     if (grad) {
         const long long ctas = g.blocks_per_group * groups * batch, slots = (g.lanes == 16 ? 3 : 2) * kSms;
@@ -209,18 +212,22 @@ SsmPlan ssm_plan(long long batch, long long length, long long channels, long lon
         chunks = std::min(ceil_div(7 * kSms, warps), std::max(tiles / 4, 1ll));
     }
     g.chunk_tiles = ceil_div(tiles, chunks);
+    const long long split = grad && chunks > 1 ? std::min(ceil_div(4 * kSms, warps * (chunks - 1)), g.chunk_tiles) : 1;
+    g.run_tiles = ceil_div(g.chunk_tiles, split);
+    g.chunk_tiles = g.run_tiles * split;
     g.chunks = (int)ceil_div(tiles, g.chunk_tiles);
+    g.runs = (int)ceil_div(tiles, g.run_tiles);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t o = at;
         at += (bytes + 255) / 256 * 256;
         return o;
     };
-    const size_t rows = (size_t)batch * g.chunks;
+    const size_t rows = (size_t)batch * g.chunks, runs = (size_t)batch * g.runs;
     if (g.chunks > 1) {
-        g.carry = take(rows * channels * np * 4);
-        g.sum_d = take(rows * channels * 4);
-        g.cut = take(rows);
+        g.carry = take(runs * channels * np * 4);
+        g.sum_d = take(runs * channels * 4);
+        g.cut = take(runs);
     }
     if (grad) {
         g.part_bc = take((size_t)(g.blocks_per_group * groups) * batch * length * 2 * np * 4);

@@ -147,6 +147,12 @@ struct TileRows<T, G, true, kT> {
         f[0] = pack2(v[0], v[1]);
         f[1] = pack2(v[2], v[3]);
     }
+    // the same from a [CH] array in shared memory
+    __device__ __forceinline__ static void channel_values(const float* s, f2 (&f)[2], int lane) {
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(s + ch(lane));
+        f[0] = q.x;
+        f[1] = q.y;
+    }
     // sums per channel over all passes, written
     __device__ __forceinline__ static void put_channel_sums(float* p, const f2 (&f)[2], int left, int lane) {
         float v[4] = {lo2(f[0]), hi2(f[0]), lo2(f[1]), hi2(f[1])};
@@ -231,6 +237,9 @@ struct TileRows<T, G, false, kT> {
     }
     __device__ __forceinline__ static void per_channel(const float* p, int left, int lane, f2 (&f)[2]) {
         f[0] = f[1] = both(p && lane % G::CH < left ? __ldg(p + lane % G::CH) : 0.0f);
+    }
+    __device__ __forceinline__ static void channel_values(const float* s, f2 (&f)[2], int lane) {
+        f[0] = f[1] = both(s[lane % G::CH]);
     }
     __device__ __forceinline__ static void put_channel_sums(float* p, const f2 (&f)[2], int left, int lane) {
         float v = (lo2(f[0]) + hi2(f[0])) + (lo2(f[1]) + hi2(f[1]));
@@ -464,11 +473,11 @@ __device__ __forceinline__ unsigned tile_heads(const uint8_t* row, long long t0,
     return __ballot_sync(0xffffffffu, lane < nt && row[t0 + (lane < nt ? lane : 0)] != 0);
 }
 
-// carry = decay of chunk j over its whole length * carry + what the chunk adds.
+// carry = decay of run j over its whole length * carry + what the run adds.
 template <class G>
-__device__ __forceinline__ void fold_chunk(const SsmParams& p, const f2 (&A2)[G::PC][4], long long b, long long j,
-                                           long long ch0, int left, int lane, f2 (&carry)[G::PC][4]) {
-    const long long row = b * p.chunks + j;
+__device__ __forceinline__ void fold_run(const SsmParams& p, const f2 (&A2)[G::PC][4], long long b, long long j,
+                                         long long ch0, int left, int lane, f2 (&carry)[G::PC][4]) {
+    const long long row = b * p.runs + j;
     float v[G::CPL][4], d[G::CPL];
     load_lane<G>(p.carry + row * p.channels * G::NP + ch0 * 4, p.channels, left, lane, v);
     const int c = lane / G::S;
@@ -485,11 +494,11 @@ __device__ __forceinline__ void fold_chunk(const SsmParams& p, const f2 (&A2)[G:
             carry[q][k] = cut ? add : fma2(a, carry[q][k], add);
         }
 }
-// The chunk's own part, left for the others to fold.
+// The run's own part, left for the others to fold.
 template <class G>
-__device__ __forceinline__ void leave_chunk(const SsmParams& p, long long b, long long chunk, long long ch0, int left,
-                                            int lane, const f2 (&carry)[G::PC][4], const f2 (&sum_d)[G::PC]) {
-    const long long row = b * p.chunks + chunk;
+__device__ __forceinline__ void leave_run(const SsmParams& p, long long b, long long run, long long ch0, int left,
+                                          int lane, const f2 (&carry)[G::PC][4], const f2 (&sum_d)[G::PC]) {
+    const long long row = b * p.runs + run;
     store_lane<G>(p.carry + row * p.channels * G::NP + ch0 * 4, p.channels, left, lane, carry);
     const int c = lane / G::S;
     if (lane % G::S == 0)

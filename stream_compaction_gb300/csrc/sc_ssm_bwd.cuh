@@ -14,18 +14,28 @@
 //
 // A warp walks its channels' tokens backwards in tiles of kTile, from the state
 // that the forward pass saved at each tile's start.  Nothing of the states is
-// kept per token: a tile's states are recomputed, first in one run that leaves
+// kept per token: a tile's states are recomputed, first in one walk that leaves
 // the states at its quarters in shared memory, then quarter by quarter, where q
 // and h of four tokens stay in registers for the way back (in shared memory
 // they would cost more accesses than the second exponential).  Sums over states
 // and over channels go through shared memory, four tokens at a time; the sum
 // over a CTA's warps per tile; and those over CTAs, rows and chunks in kernels
 // of their own over the CTAs' partial rows.  Each in a fixed order.
-// The multipliers bound it: per token and state 14 products and multiply-adds,
-// against 2 exponentials.
+//
+// Per token and state 14 products and multiply-adds against 1.75 exponentials:
+// the multipliers' time, 0.63 ms at 4 x 4096 tokens, 4096 channels and 16 states
+// in bfloat16, is the nearest bound; the pass takes 1.35 ms (the whole step,
+// forward pass included, 1.98).  What keeps it from it is that an SM holds 8
+// warps, 2 a quarter: 255 registers (A, dh and dA of 16 states a lane, q and h of
+// a quarter) and 27 KB of shared memory a warp.  The quarters' work takes 44 % of
+// a warp's time, the walk before it 8 %, the elements at both ends 22 %.  What
+// shared memory leaves of the L1 is too little for spilled registers to stay in
+// it, so what is used seldom (bias, D, their sums, a quarter's first state) lies
+// in shared memory (2.05 ms before, with spills).
 //
 // Rows too few for the machine: the length is split as in the forward pass,
-// with a first kernel that runs each chunk backwards from zero.
+// with a first kernel that walks the chunks backwards from zero, in shorter
+// runs, of which there are enough for all SMs.
 #pragma once
 #include "sc_ssm.cuh"
 
@@ -35,35 +45,76 @@ constexpr int kQuarter = 4;  // tokens kept in registers
 constexpr int kQuarters = kTile / kQuarter;
 constexpr int kBackWarps = 2;  // of a CTA of the first kernel
 
-// A warp's part of the shared memory, in floats.
+// The shared memory, in floats: the CTA's B and C, then each warp's part.
 template <class G>
 struct BwdShared {
     static constexpr int kRow = kTile * G::CH, kSums = G::TP * G::kSumRow, kStates = kTile * G::NP * 2;
     static constexpr int kHold = G::CPL * 4 * 32;                      // a warp's states
     static constexpr int d = 0, u = kRow, g = 2 * kRow;                // [kTile][CH]
     static constexpr int y = 3 * kRow, gu = y + kSums, ga = gu + kSums;  // [TP][kSumRow]
-    static constexpr int B = ga + kSums, C = B + kStates;              // [kTile][NP] pairs
-    static constexpr int h = C + kStates;                              // states before quarters 1 ..
-    static constexpr int bc = h + (kQuarters - 1) * kHold;             // [kQuarter][2][CL][S] fours of dB, dC
+    static constexpr int h = ga + kSums;                               // states before each quarter
+    static constexpr int bc = h + kQuarters * kHold;                   // [kQuarter][2][CL][S] fours of dB, dC
     static constexpr int sums = bc + kQuarter * 2 * 32 * 4;            // [kTile][2][NP]
-    static constexpr int kFloats = sums + kTile * 2 * G::NP;
-    static constexpr size_t kBytes = (size_t)kFloats * 4 * G::kBwdWarps;
+    static constexpr int ends = sums + kTile * 2 * G::NP;               // [dD, dbias][32] fours, the lanes' own
+    static constexpr int per = ends + 2 * 32 * 4;                      // [bias, D][CH]
+    static constexpr int kFloats = per + 2 * G::CH;
+    static constexpr int kWarp0 = 2 * kStates;                         // [B, C][kTile][NP] pairs before it
+    static constexpr size_t kBytes = (size_t)(kWarp0 + kFloats * G::kBwdWarps) * 4;
 };
 
-// dh of a chunk's first token, taken one token further back, with nothing
-// coming in from behind; and the chunk's sum of d.
+// A tile's B and C, fours of states (or one) a thread of the CTA's, to (v, v) pairs.
+template <class T, class G, bool kVec>
+struct CtaStates {
+    static constexpr int kNT = 32 * G::kBwdWarps, kPer = kVec ? 4 : 1;
+    static constexpr int kLine = G::NP / kPer, kAll = kTile * kLine, NA = (2 * kAll + kNT - 1) / kNT;
+    struct One {
+        T e;
+    };
+    typename std::conditional<kVec, Vec<T, kVec ? 4 : 2>, One>::type v[NA];
+    __device__ __forceinline__ void load(const T* B, const T* C, const SsmParams& p, long long t0, int nt) {
+#pragma unroll
+        for (int a = 0; a < NA; ++a) {
+            const int q = threadIdx.x + kNT * a, kind = q / kAll, t = q % kAll / kLine, n = q % kLine * kPer;
+            const T* from = kind ? C + (t0 + t) * p.C_token + n : B + (t0 + t) * p.B_token + n;
+            const bool in = (2 * kAll % kNT == 0 || q < 2 * kAll) && t < nt && n < p.states;
+            if constexpr (kVec) {
+                v[a].zero();
+                if (in) v[a].load(from);
+            } else {
+                v[a].e = in ? __ldg(from) : from_f32<T>(0.0f);
+            }
+        }
+    }
+    __device__ __forceinline__ void to_shared(float* s) const {
+#pragma unroll
+        for (int a = 0; a < NA; ++a) {
+            const int q = threadIdx.x + kNT * a;
+            if (2 * kAll % kNT != 0 && q >= 2 * kAll) break;
+            if constexpr (kVec) {
+                float4* o = reinterpret_cast<float4*>(s) + q * 2;
+                o[0] = make_float4(v[a].get(0), v[a].get(0), v[a].get(1), v[a].get(1));
+                o[1] = make_float4(v[a].get(2), v[a].get(2), v[a].get(3), v[a].get(3));
+            } else {
+                reinterpret_cast<float2*>(s)[q] = make_float2(to_f32(v[a].e), to_f32(v[a].e));
+            }
+        }
+    }
+};
+
+// dh of a run's first token, taken one token further back, with nothing
+// coming in from behind; and the run's sum of d.
 template <class T, class G, bool kVec>
 __global__ void __launch_bounds__(32 * kBackWarps) ssm_back_summary_kernel(SsmParams p, int blocks_per_group,
-                                                                             int grid_chunks) {
+                                                                             int grid_runs) {
     using Rows = TileRows<T, G, kVec, kTile>;
     using States = TileStates<T, G, kVec, kTile>;
     constexpr int kWarps = kBackWarps;
     __shared__ alignas(16) float s_d[kWarps][kTile * G::CH], s_g[kWarps][kTile * G::CH];
     __shared__ alignas(16) float2 s_C[kWarps][kTile * G::NP];
-    SsmPlace<G, kWarps> at(p, blocks_per_group, grid_chunks, threadIdx.x >> 5);
+    const SsmPlace<G, kWarps> at(p, blocks_per_group, grid_runs, threadIdx.x >> 5);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, left = at.left;
     if (left == 0) return;
-    at.chunk += 1;  // nobody waits for the first chunk's
+    const long long run = at.chunk + p.chunk_tiles / p.run_tiles;  // nobody waits for the first chunk's
     const int s = lane % G::S, c = lane / G::S;
     const long long b = at.b;
     float raw[G::CPL][4];
@@ -75,8 +126,8 @@ __global__ void __launch_bounds__(32 * kBackWarps) ssm_back_summary_kernel(SsmPa
     for (int q = 0; q < G::PC; ++q) dsum[q] = 0ull;
     Rows::per_channel(p.dt_bias ? p.dt_bias + at.ch0 : nullptr, left, lane, bias);
     const long long tiles = (p.length + kTile - 1) / kTile;
-    const long long tile0 = at.chunk * p.chunk_tiles;
-    const long long tile1 = tile0 + p.chunk_tiles < tiles ? tile0 + p.chunk_tiles : tiles;
+    const long long tile0 = run * p.run_tiles;
+    const long long tile1 = tile0 + p.run_tiles < tiles ? tile0 + p.run_tiles : tiles;
     const T* dtp = static_cast<const T*>(p.dt) + b * p.dt_batch + at.ch0;
     const T* zp = p.z ? static_cast<const T*>(p.z) + b * p.z_batch + at.ch0 : nullptr;
     const T* dyp = static_cast<const T*>(p.dy) + b * p.dy_batch + at.ch0;
@@ -146,8 +197,8 @@ __global__ void __launch_bounds__(32 * kBackWarps) ssm_back_summary_kernel(SsmPa
         else tokens(std::false_type{});
         __syncwarp();
     }
-    leave_chunk<G>(p, b, at.chunk, at.ch0, left, lane, dh, dsum);
-    if (at.cblock == 0 && threadIdx.x == 0) p.cut[b * p.chunks + at.chunk] = cut != 0;
+    leave_run<G>(p, b, run, at.ch0, left, lane, dh, dsum);
+    if (at.cblock == 0 && threadIdx.x == 0) p.cut[b * p.runs + run] = cut != 0;
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
@@ -173,7 +224,6 @@ __device__ __forceinline__ void run_quarter(const float* ld, const float* lu, co
 template <class T, class G, bool kVec>
 __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p, int blocks_per_group) {
     using Rows = TileRows<T, G, kVec, kTile>;
-    using States = TileStates<T, G, kVec, kTile>;
     using Sh = BwdShared<G>;
     constexpr int kWarps = G::kBwdWarps;
     extern __shared__ __align__(16) float s_all[];
@@ -182,10 +232,9 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
     const int left = at.left;  // a warp without channels still meets the CTA's barriers
     const int s = lane % G::S, c = lane / G::S;
     const long long b = at.b;
-    float* sm = s_all + warp * Sh::kFloats;
+    float* sm = s_all + Sh::kWarp0 + warp * Sh::kFloats;
     const float *ld = sm + Sh::d + G::CPL * c, *lu = sm + Sh::u + G::CPL * c, *lg = sm + Sh::g + G::CPL * c;
-    const float2 *lB = reinterpret_cast<const float2*>(sm + Sh::B) + 4 * s,
-                 *lC = reinterpret_cast<const float2*>(sm + Sh::C) + 4 * s;
+    const float2 *lB = reinterpret_cast<const float2*>(s_all) + 4 * s, *lC = lB + kTile * G::NP;
     ulonglong2* hold = reinterpret_cast<ulonglong2*>(sm + Sh::h) + lane;
     const long long tiles = (p.length + kTile - 1) / kTile;
     const long long tile0 = at.chunk * p.chunk_tiles;
@@ -199,11 +248,18 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
         load_lane_of<G>(p.dfinal ? p.dfinal + (b * p.channels + at.ch0) * p.states : nullptr, p.states, left, lane, raw);
         to_pairs<G>(raw, 1.0f, dh);
     }
-    for (long long j = p.chunks - 1; j > at.chunk; --j) fold_chunk<G>(p, A2, b, j, at.ch0, left, lane, dh);
+    for (long long j = p.runs - 1; j >= (at.chunk + 1) * (p.chunk_tiles / p.run_tiles); --j)
+        fold_run<G>(p, A2, b, j, at.ch0, left, lane, dh);
     clear<G>(dA);
-    f2 bias[2], D[2], dD[2] = {0ull, 0ull}, dbias[2] = {0ull, 0ull};
-    Rows::per_channel(p.dt_bias ? p.dt_bias + at.ch0 : nullptr, left, lane, bias);
-    Rows::per_channel(p.D ? p.D + at.ch0 : nullptr, left, lane, D);
+    // Registers are what this kernel has least of: the bias, D and their gradients'
+    // sums, used once a pass, stay in shared memory.
+    ulonglong2* ends = reinterpret_cast<ulonglong2*>(sm + Sh::ends) + lane;
+    ends[0] = ends[32] = make_ulonglong2(0ull, 0ull);
+    for (int i = lane; i < 2 * G::CH; i += 32) {
+        const float* from = i < G::CH ? p.dt_bias : p.D;
+        sm[Sh::per + i] = from && i % G::CH < left ? __ldg(from + at.ch0 + i % G::CH) : 0.0f;
+    }
+    __syncwarp();
     const T* xp = static_cast<const T*>(p.x) + b * p.x_batch + at.ch0;
     const T* dtp = static_cast<const T*>(p.dt) + b * p.dt_batch + at.ch0;
     const T* zp = p.z ? static_cast<const T*>(p.z) + b * p.z_batch + at.ch0 : nullptr;
@@ -214,6 +270,33 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
     const bool whole = left == G::CH;
     const uint8_t* heads = p.heads ? p.heads + b * p.length : nullptr;
 
+    auto held_states = [&](int q4, f2(&h)[G::PC][4]) {
+#pragma unroll
+        for (int q = 0; q < G::PC; ++q) {
+            const ulonglong2 v = hold[(q4 * G::CPL + 2 * q) * 32], w = hold[(q4 * G::CPL + 2 * q + 1) * 32];
+            h[q][0] = v.x;
+            h[q][1] = v.y;
+            h[q][2] = w.x;
+            h[q][3] = w.y;
+        }
+    };
+    auto hold_states = [&](int q4, const f2(&h)[G::PC][4]) {
+#pragma unroll
+        for (int q = 0; q < G::PC; ++q) {
+            hold[(q4 * G::CPL + 2 * q) * 32] = make_ulonglong2(h[q][0], h[q][1]);
+            hold[(q4 * G::CPL + 2 * q + 1) * 32] = make_ulonglong2(h[q][2], h[q][3]);
+        }
+    };
+    // a tile's B and C and the states at its start, asked for before the sums of
+    // the tile walked before it (its other elements too: 2.08 ms against 2.01 at
+    // 4 x 4096 x 4096, they do not fit in the registers)
+    CtaStates<T, G, kVec> BC;
+    float start[G::CPL][4];
+    auto fetch = [&](long long tile) {
+        BC.load(Bp, Cp, p, tile * kTile, tile_tokens<kTile>(p, tile * kTile));
+        load_lane<G>(p.saved + (b * tiles + tile) * p.channels * G::NP + at.ch0 * 4, p.channels, left, lane, start);
+    };
+    if (tile0 < tile1) fetch(tile1 - 1);
     for (long long tile = tile1 - 1; tile >= tile0; --tile) {
         const long long t0 = tile * kTile;
         const int nt = tile_tokens<kTile>(p, tile * kTile);
@@ -225,13 +308,12 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
         auto stage = [&](auto as_plain) {
             constexpr bool F = decltype(as_plain)::value;
             Rows x, dt, z, dy;
-            States B, C;
             dt.template load<F>(dtp + t0 * p.dt_token, p.dt_token, nt, left, lane);
             x.template load<F>(xp + t0 * p.x_token, p.x_token, nt, left, lane);
             dy.template load<F>(dyp + t0 * p.dy_token, p.dy_token, nt, left, lane);
             if (F || zp) z.template load<F>(zp + t0 * p.z_token, p.z_token, nt, left, lane);
-            B.template load<false>(Bp + t0 * p.B_token, p.B_token, nt, (int)p.states, lane);
-            C.template load<false>(Cp + t0 * p.C_token, p.C_token, nt, (int)p.states, lane);
+            f2 bias[2];
+            Rows::channel_values(sm + Sh::per, bias, lane);
             f2 d[Rows::NA][2], u[Rows::NA][2], g[Rows::NA][2];
 #pragma unroll
             for (int a = 0; a < Rows::NA; ++a) {
@@ -252,11 +334,13 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
                 Rows::put(sm + Sh::u + a * G::TP * G::CH, u[a], lane);
                 Rows::put(sm + Sh::g + a * G::TP * G::CH, g[a], lane);
             }
-            B.to_shared(reinterpret_cast<float2*>(sm + Sh::B), lane);
-            C.to_shared(reinterpret_cast<float2*>(sm + Sh::C), lane);
         };
         if (plain) stage(std::true_type{});
         else stage(std::false_type{});
+        BC.to_shared(s_all);
+        f2 h0[G::PC][4];
+        to_pairs<G>(start, 1.0f, h0);
+        hold_states(0, h0);
         if (tile > tile0 && left > 0) {  // the next tile and its states on their way into the L2
             const long long t = t0 - kTile + lane % kTile;  // lanes 0 .. 15: x and dy, 16 ..: dt and z
             prefetch_l2(lane < kTile ? xp + t * p.x_token : dtp + t * p.dt_token);
@@ -285,7 +369,10 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
         auto finish = [&](int pa, int tq, const Pass& e, auto as_plain) {
             constexpr bool F = decltype(as_plain)::value;
             const auto &rx = e.x, &rt = e.dt, &ry = e.dy, &rz = e.z;
-            f2 y[2], gu[2], ga[2], d[2], g[2], dd[2];
+            f2 y[2], gu[2], ga[2], d[2], g[2], dd[2], bias[2], D[2];
+            Rows::channel_values(sm + Sh::per, bias, lane);
+            Rows::channel_values(sm + Sh::per + G::CH, D, lane);
+            ulonglong2 dD = ends[0], db = ends[32];
             Rows::get_sums(sm + Sh::gu, gu, lane);
             Rows::get_sums(sm + Sh::ga, ga, lane);
             Rows::get_sums(sm + Sh::y, y, lane);
@@ -298,7 +385,7 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
                 dd[i] = fma2(gu[i], x, mul2(ga[i], both(kLn2)));
                 if (F || p.softplus) dd[i] = mul2(dd[i], sigmoid_2(add2(Rows::pair_of(rt, i), bias[i])));
                 gu[i] = fma2(gu[i], d[i], mul2(g[i], D[i]));  // dx
-                dD[i] = fma2(g[i], x, dD[i]);
+                (i ? dD.y : dD.x) = fma2(g[i], x, i ? dD.y : dD.x);
                 if (F || zp) {
                     const f2 z = Rows::pair_of(rz, i), sg = sigmoid_2(z);
                     const f2 slope = mul2(sg, fma2(z, fma2(sg, both(-1.0f), both(1.0f)), both(1.0f)));
@@ -309,27 +396,16 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
             Rows::template store<F>(static_cast<T*>(p.ddt) + o, p.channels, dd, pa, nt, left, lane);
             if (F || zp) Rows::template store<F>(static_cast<T*>(p.dz) + o, p.channels, y, pa, nt, left, lane);
             Rows::template mask<F>(dd, pa, nt, left, lane);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) dbias[i] = add2(dbias[i], dd[i]);
+            ends[0] = dD;
+            ends[32] = make_ulonglong2(add2(db.x, dd[0]), add2(db.y, dd[1]));
         };
-        const float* saved = p.saved + (b * tiles + tile) * p.channels * G::NP + at.ch0 * 4;
-        __syncwarp();
+        __syncthreads();
         auto work = [&](auto with_heads) {
             constexpr bool kHeads = decltype(with_heads)::value;
-            {   // the states before quarters 1, 2, ...
-                f2 h[G::PC][4];
-                float raw[G::CPL][4];
-                load_lane<G>(saved, p.channels, left, lane, raw);
-                to_pairs<G>(raw, 1.0f, h);
 #pragma unroll 1
-                for (int q4 = 0; q4 < kQuarters - 1; ++q4) {
-                    run_quarter<G, kHeads>(ld, lu, lB, q4 * kQuarter, hm, A2, h);
-#pragma unroll
-                    for (int q = 0; q < G::PC; ++q) {
-                        hold[(q4 * G::CPL + 2 * q) * 32] = make_ulonglong2(h[q][0], h[q][1]);
-                        hold[(q4 * G::CPL + 2 * q + 1) * 32] = make_ulonglong2(h[q][2], h[q][3]);
-                    }
-                }
+            for (int q4 = 1; q4 < kQuarters; ++q4) {  // the states before quarters 1, 2, ...
+                run_quarter<G, kHeads>(ld, lu, lB, (q4 - 1) * kQuarter, hm, A2, h0);
+                hold_states(q4, h0);
             }
 #pragma unroll 1
             for (int q4 = kQuarters - 1; q4 >= 0; --q4) {
@@ -337,21 +413,7 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
                 Pass raws;
                 if (tq % G::TP == 0) raws = plain ? again(tq / G::TP, std::true_type{}) : again(tq / G::TP, std::false_type{});
                 f2 a[kQuarter][G::PC][4], h[kQuarter + 1][G::PC][4];  // q, and h before each token
-                if (q4 == 0) {
-                    float raw[G::CPL][4];
-                    load_lane<G>(saved, p.channels, left, lane, raw);
-                    to_pairs<G>(raw, 1.0f, h[0]);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < G::PC; ++q) {
-                        const ulonglong2 v = hold[((q4 - 1) * G::CPL + 2 * q) * 32];
-                        const ulonglong2 w = hold[((q4 - 1) * G::CPL + 2 * q + 1) * 32];
-                        h[0][q][0] = v.x;
-                        h[0][q][1] = v.y;
-                        h[0][q][2] = w.x;
-                        h[0][q][3] = w.y;
-                    }
-                }
+                held_states(q4, h[0]);
 #pragma unroll
                 for (int j = 0; j < kQuarter; ++j) {
                     f2 d[G::PC], u[G::PC], Bv[4];
@@ -377,11 +439,12 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
                     read_channels<G>(lg + t * G::CH, g);
                     read_states(lB + t * G::NP, Bv);
                     read_states(lC + t * G::NP, Cv);
+                    if (j == 0) held_states(q4, h[0]);  // read again: not kept in registers meanwhile
                     f2 y[G::PC], gu[G::PC], ga[G::PC], dB[4], dC[4];
 #pragma unroll
-                    for (int q = 0; q < G::PC; ++q) {
+                    for (int k = 0; k < 4; ++k) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                        for (int q = 0; q < G::PC; ++q) {
                             const f2 ht = h[j + 1][q][k];
                             dh[q][k] = fma2(Cv[k], g[q], dh[q][k]);
                             y[q] = k ? fma2(Cv[k], ht, y[q]) : mul2(Cv[k], ht);
@@ -428,6 +491,7 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
         };
         if (hm) work(std::true_type{});
         else work(std::false_type{});
+        if (tile > tile0) fetch(tile - 1);
         // dA goes to its partial row every 128 tokens: one running sum over
         // thousands of tokens of either sign would lose a digit to rounding
         if ((tile - tile0) % 8 == 0 && left > 0) {
@@ -448,10 +512,10 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
         __syncthreads();
         float4* part = reinterpret_cast<float4*>(p.part_bc + ((at.cblock * p.batch + b) * p.length + t0) * 2 * G::NP);
         for (int i = threadIdx.x; i < nt * 2 * G::S; i += 32 * kWarps) {
-            float4 sum = reinterpret_cast<const float4*>(s_all + Sh::sums)[i];
+            float4 sum = reinterpret_cast<const float4*>(s_all + Sh::kWarp0 + Sh::sums)[i];
 #pragma unroll
             for (int w = 1; w < kWarps; ++w) {
-                const float4 v = reinterpret_cast<const float4*>(s_all + w * Sh::kFloats + Sh::sums)[i];
+                const float4 v = reinterpret_cast<const float4*>(s_all + Sh::kWarp0 + w * Sh::kFloats + Sh::sums)[i];
                 sum.x += v.x;
                 sum.y += v.y;
                 sum.z += v.z;
@@ -459,12 +523,14 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
             }
             part[i] = sum;
         }
-        __syncthreads();
     }
     if (left == 0) return;
     const long long row = b * p.chunks + at.chunk, rows = p.batch * p.chunks;
-    Rows::put_channel_sums(p.part_d + row * p.channels + at.ch0, dD, left, lane);
-    Rows::put_channel_sums(p.part_d + (rows + row) * p.channels + at.ch0, dbias, left, lane);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const f2 sum[2] = {ends[32 * i].x, ends[32 * i].y};
+        Rows::put_channel_sums(p.part_d + (i * rows + row) * p.channels + at.ch0, sum, left, lane);
+    }
     if (p.dstate && at.chunk == 0)
         store_lane_of<G>(p.dstate + (b * p.channels + at.ch0) * p.states, p.states, left, lane, dh);
 }
@@ -493,9 +559,9 @@ cudaError_t ssm_back_of(const SsmParams& p, const SsmPlan& plan, int* launches, 
     *launches = p.chunks > 1 ? 4 : 3;  // with the last sums, which the caller launches
     if (p.chunks > 1) {
         const long long block = kBackWarps * G::CH;
-        const int bpg = (int)((per + block - 1) / block);
+        const int bpg = (int)((per + block - 1) / block), runs = p.runs - (int)(p.chunk_tiles / p.run_tiles);
         ssm_back_summary_kernel<T, G, kVec>
-            <<<(unsigned)(bpg * p.groups * (p.chunks - 1) * p.batch), 32 * kBackWarps, 0, s>>>(p, bpg, p.chunks - 1);
+            <<<(unsigned)(bpg * p.groups * runs * p.batch), 32 * kBackWarps, 0, s>>>(p, bpg, runs);
     }
     auto kernel = ssm_back_kernel<T, G, kVec>;
     constexpr size_t bytes = BwdShared<G>::kBytes;
