@@ -183,6 +183,29 @@ cudaError_t step_of(const SsmParams& p, cudaStream_t s) {
     }
 }
 
+// Chunks of the backward pass, of `ctas` CTAs each where the machine holds
+// `slots`, by the least of what a token costs: the places that stay empty in the
+// last wave, a chunk's start (about a tile's time, and a twentieth for each chunk's
+// part that it folds), and the first kernel, which takes a quarter of the second's
+// time for all tokens but the first chunk's.  4 x 4096 x 4096, 128 CTAs, with the
+// forward pass: 2.87 ms whole, 1.98 in 2 chunks (256 of 304 places), 1.87 in 7
+// (896 in three waves of 304), 1.88 in 14.
+long long back_chunks(long long ctas, long long slots, long long tiles) {
+    long long best = 1;
+    double least = 0;
+    const long long most = ctas > 0 ? std::min(std::max(slots / ctas, 24ll), tiles / 2) : 1;
+    for (long long c = 1; c <= most; ++c) {
+        const long long per = ceil_div(tiles, c), n = ceil_div(tiles, per);
+        const double waves = (double)(ceil_div(ctas * n, slots) * slots) / (double)(ctas * n);
+        const double cost = waves * (1 + (1 + 0.05 * n) / per) + 0.25 * (n - 1) / n;
+        if (c == 1 || cost < least) {
+            least = cost;
+            best = n;
+        }
+    }
+    return best;
+}
+
 }  // namespace
 
 int ssm_lanes(long long states) { return states <= 8 ? 2 : states <= 16 ? 4 : states <= 32 ? 8 : 16; }
@@ -199,15 +222,13 @@ SsmPlan ssm_plan(long long batch, long long length, long long channels, long lon
     // recurrence nearly twice.  Below 1.7 pairs an SM it pays, and then into about
     // 7 pairs an SM (1 x 4096 x 4096, 128 pairs: 192 us in 4 chunks, 167 in 8 to 10;
     // 4 x 4096 x 4096, 512 pairs, with gradient: 2.17 ms whole, 2.29 in 2).
-    // Backward: one wave of the CTAs that the SMs hold (of 512 warps, 128 CTAs:
-    // 2.87 ms whole, 2.17 in 2 chunks = 256 CTAs, 2.38 in 3 = 384), whose chunks a
-    // first kernel walks in runs, about 4 warps' an SM (4 x 4096 x 4096, with the
-    // forward pass: 2.03 ms with a run a chunk, 1.98 so, and the same with 8 or 16;
-    // 2 x 1000 x 1002 with 24 states: 209 us, 206, 213 and 234).
+    // Backward: see back_chunks; a first kernel walks the chunks in runs, about 4
+    // warps' an SM (4 x 4096 x 4096 in 2 chunks, with the forward pass: 2.03 ms with
+    // a run a chunk, 1.98 so, and the same with 8 or 16; 2 x 1000 x 1002 with 24
+    // states: 209 us, 206, 213 and 234).
     long long chunks = 1;
     if (grad) {
-        const long long ctas = g.blocks_per_group * groups * batch, slots = (g.lanes == 16 ? 3 : 2) * kSms;
-        chunks = std::min(std::max(slots / ctas, 1ll), std::max(tiles / 2, 1ll));
+        chunks = back_chunks(g.blocks_per_group * groups * batch, (g.lanes == 16 ? 3 : 2) * kSms, tiles);
     } else if (10 * warps < 17 * kSms) {
         chunks = std::min(ceil_div(7 * kSms, warps), std::max(tiles / 4, 1ll));
     }

@@ -257,14 +257,12 @@ template <class T, class G, int kT>
 struct TileStates<T, G, true, kT> {  // states a multiple of 4
     static constexpr int NA = (kT * G::S + 31) / 32;  // fours per lane
     Vec<T, 4> v[NA];
-    template <bool kFull>  // all tokens and padded states are there
     __device__ __forceinline__ void load(const T* p, long long stride, int nt, int states, int lane) {
 #pragma unroll
         for (int a = 0; a < NA; ++a) {
             const int q = lane + 32 * a, t = q / G::S, n = (q % G::S) * 4;
-            constexpr bool kAll = kFull && kT * G::S % 32 == 0;
-            if constexpr (!kAll) v[a].zero();
-            if (kAll || (t < nt && n < states)) v[a].load(p + t * stride + n);
+            v[a].zero();
+            if (t < nt && n < states) v[a].load(p + t * stride + n);
         }
     }
     __device__ __forceinline__ void to_shared(float2* s, int lane) const {
@@ -282,13 +280,11 @@ template <class T, class G, int kT>
 struct TileStates<T, G, false, kT> {
     static constexpr int NA = kT * G::NP / 32;
     T v[NA];
-    template <bool kFull>
     __device__ __forceinline__ void load(const T* p, long long stride, int nt, int states, int lane) {
 #pragma unroll
         for (int a = 0; a < NA; ++a) {
             const int q = lane + 32 * a, t = q / G::NP, n = q % G::NP;
-            if constexpr (!kFull) v[a] = from_f32<T>(0.0f);
-            if (kFull || (t < nt && n < states)) v[a] = __ldg(p + t * stride + n);
+            v[a] = t < nt && n < states ? __ldg(p + t * stride + n) : from_f32<T>(0.0f);
         }
     }
     __device__ __forceinline__ void to_shared(float2* s, int lane) const {

@@ -23,15 +23,16 @@
 // of their own over the CTAs' partial rows.  Each in a fixed order.
 //
 // Per token and state 14 products and multiply-adds against 1.75 exponentials:
-// the multipliers' time, 0.63 ms at 4 x 4096 tokens, 4096 channels and 16 states
-// in bfloat16, is the nearest bound; the pass takes 1.35 ms (the whole step,
-// forward pass included, 1.98).  What keeps it from it is that an SM holds 8
+// the multipliers' time, 0.43 ms at 4 x 4096 tokens, 4096 channels and 16 states
+// in bfloat16, is the nearest bound; the pass takes 1.39 ms, 0.15 more in the
+// first kernel (the whole step, forward pass included, 1.98).  What keeps it
+// from the bound is that an SM holds 8
 // warps, 2 a quarter: 255 registers (A, dh and dA of 16 states a lane, q and h of
 // a quarter) and 27 KB of shared memory a warp.  The quarters' work takes 44 % of
 // a warp's time, the walk before it 8 %, the elements at both ends 22 %.  What
 // shared memory leaves of the L1 is too little for spilled registers to stay in
 // it, so what is used seldom (bias, D, their sums, a quarter's first state) lies
-// in shared memory (2.05 ms before, with spills).
+// in shared memory.
 //
 // Rows too few for the machine: the length is split as in the forward pass,
 // with a first kernel that walks the chunks backwards from zero, in shorter
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(32 * kBackWarps) ssm_back_summary_kernel(SsmPa
         dt.template load<false>(dtp + t0 * p.dt_token, p.dt_token, nt, left, lane);
         dy.template load<false>(dyp + t0 * p.dy_token, p.dy_token, nt, left, lane);
         if (zp) z.template load<false>(zp + t0 * p.z_token, p.z_token, nt, left, lane);
-        C.template load<false>(Cp + t0 * p.C_token, p.C_token, nt, (int)p.states, lane);
+        C.load(Cp + t0 * p.C_token, p.C_token, nt, (int)p.states, lane);
     };
     unsigned cut = 0;
     const float *ld = s_d[warp] + G::CPL * c, *lg = s_g[warp] + G::CPL * c;
