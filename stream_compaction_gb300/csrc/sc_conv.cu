@@ -18,6 +18,12 @@
 // value is ever multiplied.  The gradient recomputes pre, runs width - 1 tokens
 // past its end for dx, and leaves its sums over tokens as one partial row per
 // run, which a second kernel adds in order.
+//
+// 8 x 4096 tokens, 4096 channels, width 4, SiLU, bfloat16: forward 97 us (5.5 TB/s),
+// gradient 206 (3.9 TB/s), its sums 7.  The instruction issue bounds both now (60
+// and 56 % of the slots, the rest waits for results of few warps): conversions, the
+// taps and, of the two activations, an exponential and a reciprocal per element.
+// With two channels a thread and no loads ahead: 818 us for the three, 310 so.
 #include <algorithm>
 
 #include "sc_seq.cuh"

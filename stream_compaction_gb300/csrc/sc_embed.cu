@@ -17,6 +17,11 @@
 //   rows       each CTA takes up to kRowsPerCta rows of dweight: first it writes the
 //              zeros of those without a token, which wait for nothing, then the
 //              sums of at most kRun rows of dout, or of the row's pieces.
+// 16384 tokens of 4096 bfloat16 in a table of 131072: the lookup 44 us (6.1 TB/s),
+// the gradient 215: sort 17, long runs 15, rows 180 (1.2 GB, 6.7 TB/s); 5003 tokens
+// of 1000 float32 in 50021: 12, 10 and 38 us.  kRun 64 or 128 leaves a CTA's one
+// frequent id to the end of the launch (94 us for all of the second case, 78 so).
+//
 // Sums are taken in the order of t in float32, so a result is the same on
 // every run, whatever the schedule (no atomics on values).
 #include <algorithm>

@@ -24,12 +24,12 @@
 //
 // Per token and state 14 products and multiply-adds against 1.75 exponentials:
 // the multipliers' time, 0.43 ms at 4 x 4096 tokens, 4096 channels and 16 states
-// in bfloat16, is the nearest bound; the pass takes 1.39 ms, 0.15 more in the
-// first kernel (the whole step, forward pass included, 1.98).  What keeps it
-// from the bound is that an SM holds 8
-// warps, 2 a quarter: 255 registers (A, dh and dA of 16 states a lane, q and h of
-// a quarter) and 27 KB of shared memory a warp.  The quarters' work takes 44 % of
-// a warp's time, the walk before it 8 %, the elements at both ends 22 %.  What
+// in bfloat16, is the nearest bound; the pass takes 1.20 ms, and the first kernel
+// (below) 0.23 more; the whole step, forward pass included, 1.87.  What keeps it
+// from the bound is that an SM holds 8 warps, 2 a quarter, which issue in 40 % of
+// the clocks: 255 registers (A, dh and dA of 16 states a lane, q and h of a
+// quarter) and 28 KB of shared memory a warp.  The quarters' work takes 44 % of a
+// warp's time, the walk before it 8 %, the elements at both ends 22 %.  What
 // shared memory leaves of the L1 is too little for spilled registers to stay in
 // it, so what is used seldom (bias, D, their sums, a quarter's first state) lies
 // in shared memory.
@@ -289,8 +289,8 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
         }
     };
     // a tile's B and C and the states at its start, asked for before the sums of
-    // the tile walked before it (its other elements too: 2.08 ms against 2.01 at
-    // 4 x 4096 x 4096, they do not fit in the registers)
+    // the tile walked before it (its other elements too: 2.08 ms a training step
+    // against 2.01, 4 x 4096 x 4096; they do not fit in the registers)
     CtaStates<T, G, kVec> BC;
     float start[G::CPL][4];
     auto fetch = [&](long long tile) {
