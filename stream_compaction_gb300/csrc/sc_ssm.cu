@@ -59,8 +59,8 @@ __global__ void __launch_bounds__(256) ssm_sum_kernel(SsmParams p, int np) {
 // row and channel (softplus, gate) is done once: by lane r of the channel's
 // lanes for row r, the others get d and d x from it.  The loads' latency bounds it
 // (half of a warp's time).  256 x 4096 x 16 states, a tenth of the rows idle: 42 us
-// with one row a thread, whose S lanes all did that work; 25 to 30 so (4.1 to 4.9
-// TB/s); one sequence of 2048 channels: 5 us, a chain of loads.
+// with one row a thread, whose S lanes all did that work; 25 to 30 so (129 MB, 4.3
+// to 5.2 TB/s); one sequence of 2048 channels: 5 us, a chain of loads.
 template <class T, int S, bool kVec>
 __global__ void __launch_bounds__(kStepNT) ssm_step_kernel(SsmParams p, unsigned cblocks) {
     constexpr int R = S < 4 ? S : 4;
