@@ -8,7 +8,7 @@
 //              at most 10 bits a pass (so two passes below 2^20 ids).  Up to
 //              kClusterKeys tokens: one launch, one cluster of up to 8 CTAs whose
 //              digit counts meet in distributed shared memory (16384 tokens:
-//              17 us against 38 us of the four launches below).  Beyond: per
+//              15 us against 38 us of the four launches below).  Beyond: per
 //              tile digit counts, their sums over tiles, the placement.  Then
 //              where each id's run starts and ends.
 //   long runs  tokens of one id may be a large part of all (padding, a frequent
@@ -18,9 +18,9 @@
 //              zeros of those without a token, which wait for nothing, then the
 //              sums of at most kRun rows of dout, or of the row's pieces.
 // 16384 tokens of 4096 bfloat16 in a table of 131072: the lookup 44 us (6.1 TB/s),
-// the gradient 215: sort 17, long runs 15, rows 180 (1.2 GB, 6.7 TB/s); 5003 tokens
-// of 1000 float32 in 50021: 12, 10 and 38 us.  kRun 64 or 128 leaves a CTA's one
-// frequent id to the end of the launch (94 us for all of the second case, 78 so).
+// the gradient 210: sort 15, long runs 15, rows 180 (1.2 GB, 6.7 TB/s); 5003 tokens
+// of 1000 float32 in 50021: 10, 10 and 38 us.  kRun 64 or 128 leaves a CTA's one
+// frequent id to the end of the launch (94 us for all of the second case, 79 so).
 //
 // Sums are taken in the order of t in float32, so a result is the same on
 // every run, whatever the schedule (no atomics on values).
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kNT) sort_runs_kernel(const uint32_t* keys, lo
 template <int K>
 __global__ void __launch_bounds__(kClusterNT) sort_cluster_kernel(EmbedParams p, int passes, int bits, uint32_t* keys0,
                                                                   uint32_t* vals0, uint32_t* keys1, uint32_t* vals1,
-                                                                  Runs runs) {
+                                                                  Runs runs, bool zero_last) {
     namespace cg = cooperative_groups;
     extern __shared__ uint16_t s_cnt[];  // [kClusterWarps][digits]
     __shared__ uint32_t s_total[kMaxDigit], s_base[kMaxDigit], s_warp[kClusterWarps];
@@ -248,6 +248,9 @@ __global__ void __launch_bounds__(kClusterNT) sort_cluster_kernel(EmbedParams p,
     const uint32_t mask = (uint32_t)digits - 1;
     const long long base = (long long)rank * (kClusterNT * K) + warp * (32 * K);
     uint32_t *kin = nullptr, *vin = nullptr;
+    if (zero_last)  // the cluster's barriers stand between these and the marks below
+        for (long long i = (long long)rank * kClusterNT + tid; i < p.vocab; i += (long long)ctas * kClusterNT)
+            runs.last[i] = 0u;
     for (int pass = 0; pass < passes; ++pass) {
         const int shift = pass * bits;
         uint32_t *ko = pass & 1 ? keys1 : keys0, *vo = pass & 1 ? vals1 : vals0;
@@ -293,11 +296,16 @@ __global__ void __launch_bounds__(kClusterNT) sort_cluster_kernel(EmbedParams p,
         cluster.sync();
         uint32_t prev = 0, total = 0;
         if (tid < digits)
-            for (int r = 0; r < ctas; ++r) {
-                const uint32_t c = cluster.map_shared_rank(s_total, r)[tid];
-                prev += r < rank ? c : 0u;
-                total += c;
+        {
+            uint32_t c[kClusterCtas];  // all asked for at once
+#pragma unroll
+            for (int r = 0; r < kClusterCtas; ++r) c[r] = r < ctas ? cluster.map_shared_rank(s_total, r)[tid] : 0u;
+#pragma unroll
+            for (int r = 0; r < kClusterCtas; ++r) {
+                prev += r < rank ? c[r] : 0u;
+                total += c[r];
             }
+        }
         uint32_t incl = total;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -306,8 +314,7 @@ __global__ void __launch_bounds__(kClusterNT) sort_cluster_kernel(EmbedParams p,
         }
         if (lane == 31) s_warp[warp] = incl;
         __syncthreads();
-        uint32_t at = incl - total + prev;
-        for (int w = 0; w < warp; ++w) at += s_warp[w];
+        const uint32_t at = incl - total + prev + __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0u);
         if (tid < digits) s_base[tid] = at;
         __syncthreads();
 #pragma unroll
@@ -607,15 +614,20 @@ sc_status launch_embed_grad(int dtype, int wtype, const EmbedParams& p, const Em
     float* partials = reinterpret_cast<float*>(base + g.partials);
     const Runs runs{reinterpret_cast<uint32_t*>(base + g.first), reinterpret_cast<uint32_t*>(base + g.last)};
     const uint32_t *kin = nullptr, *vin = nullptr;
-    if (cudaMemsetAsync(runs.last, 0, (size_t)p.vocab * 4, s) != cudaSuccess) return SC_ERR_CUDA;
-    if (p.tokens > 0 && p.tokens <= kClusterKeys) {
-        auto go = [&](auto kernel, long long k) {
+    // The cluster clears `last` on its way while that is little work (16 words a
+    // thread): a launch less.
+    const long long each = ceil_div(p.tokens, (long long)kClusterNT * kClusterCtas);
+    const long long k = each <= 2 ? std::max(each, 1ll) : each <= 4 ? 4 : 8, ctas = ceil_div(p.tokens, kClusterNT * k);
+    const bool in_cluster = p.tokens > 0 && p.tokens <= kClusterKeys, zero_last = in_cluster && p.vocab <= 16 * kClusterNT * ctas;
+    if (!zero_last && cudaMemsetAsync(runs.last, 0, (size_t)p.vocab * 4, s) != cudaSuccess) return SC_ERR_CUDA;
+    if (in_cluster) {
+        auto go = [&](auto kernel) {
             const int bytes = kClusterWarps * (1 << g.digit_bits) * 2;
             cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
             if (e != cudaSuccess) return e;
             cudaLaunchAttribute attr{};
             attr.id = cudaLaunchAttributeClusterDimension;
-            attr.val.clusterDim = {(unsigned)ceil_div(p.tokens, kClusterNT * k), 1, 1};
+            attr.val.clusterDim = {(unsigned)ctas, 1, 1};
             cudaLaunchConfig_t cfg{};
             cfg.gridDim = dim3(attr.val.clusterDim.x);
             cfg.blockDim = dim3(kClusterNT);
@@ -623,13 +635,13 @@ sc_status launch_embed_grad(int dtype, int wtype, const EmbedParams& p, const Em
             cfg.stream = s;
             cfg.attrs = &attr;
             cfg.numAttrs = 1;
-            return cudaLaunchKernelEx(&cfg, kernel, p, g.passes, g.digit_bits, keys[0], vals[0], keys[1], vals[1], runs);
+            return cudaLaunchKernelEx(&cfg, kernel, p, g.passes, g.digit_bits, keys[0], vals[0], keys[1], vals[1], runs,
+                                      zero_last);
         };
-        const long long each = ceil_div(p.tokens, (long long)kClusterNT * kClusterCtas);
-        const cudaError_t e = each <= 1   ? go(sort_cluster_kernel<1>, 1)
-                              : each <= 2 ? go(sort_cluster_kernel<2>, 2)
-                              : each <= 4 ? go(sort_cluster_kernel<4>, 4)
-                                          : go(sort_cluster_kernel<8>, 8);
+        const cudaError_t e = k == 1   ? go(sort_cluster_kernel<1>)
+                              : k == 2 ? go(sort_cluster_kernel<2>)
+                              : k == 4 ? go(sort_cluster_kernel<4>)
+                                       : go(sort_cluster_kernel<8>);
         if (e != cudaSuccess) return SC_ERR_CUDA;
         count_launches(1);
         kin = keys[(g.passes - 1) & 1];
