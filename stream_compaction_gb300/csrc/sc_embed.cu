@@ -8,7 +8,7 @@
 //              at most 10 bits a pass (so two passes below 2^20 ids).  Up to
 //              kClusterKeys tokens: one launch, one cluster of up to 8 CTAs whose
 //              digit counts meet in distributed shared memory (16384 tokens:
-//              15 us against 38 us of the four launches below).  Beyond: per
+//              18 us against 38 us of the four launches below).  Beyond: per
 //              tile digit counts, their sums over tiles, the placement.  Then
 //              where each id's run starts and ends.
 //   long runs  tokens of one id may be a large part of all (padding, a frequent
@@ -18,8 +18,10 @@
 //              zeros of those without a token, which wait for nothing, then the
 //              sums of at most kRun rows of dout, or of the row's pieces.
 // 16384 tokens of 4096 bfloat16 in a table of 131072: the lookup 44 us (6.1 TB/s),
-// the gradient 210: sort 15, long runs 15, rows 180 (1.2 GB, 6.7 TB/s); 5003 tokens
-// of 1000 float32 in 50021: 10, 10 and 38 us.  kRun 64 or 128 leaves a CTA's one
+// the gradient 214: sort 18, long runs 16, rows 180 (1.2 GB, 6.7 TB/s); 5003 tokens
+// of 1000 float32 in 50021: 12, 10 and 38 us.  The rows begun while the long runs are
+// summed (a programmatic launch): 301 us for all of the first case, 266 one after the
+// other.  kRun 64 or 128 leaves a CTA's one
 // frequent id to the end of the launch (94 us for all of the second case, 79 so).
 //
 // Sums are taken in the order of t in float32, so a result is the same on
@@ -615,7 +617,8 @@ sc_status launch_embed_grad(int dtype, int wtype, const EmbedParams& p, const Em
     const Runs runs{reinterpret_cast<uint32_t*>(base + g.first), reinterpret_cast<uint32_t*>(base + g.last)};
     const uint32_t *kin = nullptr, *vin = nullptr;
     // The cluster clears `last` on its way while that is little work (16 words a
-    // thread): a launch less.
+    // thread): a launch less (300 tokens of 5000 ids: 26.8 us for lookup and
+    // gradient with it, 23.6 without).
     const long long each = ceil_div(p.tokens, (long long)kClusterNT * kClusterCtas);
     const long long k = each <= 2 ? std::max(each, 1ll) : each <= 4 ? 4 : 8, ctas = ceil_div(p.tokens, kClusterNT * k);
     const bool in_cluster = p.tokens > 0 && p.tokens <= kClusterKeys, zero_last = in_cluster && p.vocab <= 16 * kClusterNT * ctas;
