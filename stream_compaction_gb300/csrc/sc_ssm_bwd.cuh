@@ -136,18 +136,19 @@ __global__ void __launch_bounds__(32 * kBackWarps) ssm_back_summary_kernel(SsmPa
     const uint8_t* heads = p.heads ? p.heads + b * p.length : nullptr;
     Rows dt, z, dy;
     States C;
-    auto fetch = [&](long long tile) {
+    auto fetch = [&](long long tile, auto as_whole) {
+        constexpr bool F = decltype(as_whole)::value;
         const long long t0 = tile * kTile;
-        const int nt = tile_tokens<kTile>(p, tile * kTile);
-        dt.template load<false>(dtp + t0 * p.dt_token, p.dt_token, nt, left, lane);
-        dy.template load<false>(dyp + t0 * p.dy_token, p.dy_token, nt, left, lane);
-        if (zp) z.template load<false>(zp + t0 * p.z_token, p.z_token, nt, left, lane);
+        const int nt = F ? kTile : tile_tokens<kTile>(p, tile * kTile);
+        dt.template load<F>(dtp + t0 * p.dt_token, p.dt_token, nt, left, lane);
+        dy.template load<F>(dyp + t0 * p.dy_token, p.dy_token, nt, left, lane);
+        if (F || zp) z.template load<F>(zp + t0 * p.z_token, p.z_token, nt, left, lane);
         C.load(Cp + t0 * p.C_token, p.C_token, nt, (int)p.states, lane);
     };
     unsigned cut = 0;
     const float *ld = s_d[warp] + G::CPL * c, *lg = s_g[warp] + G::CPL * c;
     const float2* lC = s_C[warp] + 4 * s;
-    if (tile0 < tile1) fetch(tile1 - 1);
+    if (tile0 < tile1) fetch(tile1 - 1, std::false_type{});
     for (long long tile = tile1 - 1; tile >= tile0; --tile) {
         const int nt = tile_tokens<kTile>(p, tile * kTile);
         const unsigned hm = tile_heads(heads, tile * kTile, nt, lane);
@@ -176,7 +177,10 @@ __global__ void __launch_bounds__(32 * kBackWarps) ssm_back_summary_kernel(SsmPa
         else stage(std::false_type{});
         C.to_shared(s_C[warp], lane);
         __syncwarp();
-        if (tile > tile0) fetch(tile - 1);
+        if (tile > tile0) {  // only the last tile of a row may be short of tokens
+            if (left == G::CH && zp) fetch(tile - 1, std::true_type{});
+            else fetch(tile - 1, std::false_type{});
+        }
         auto tokens = [&](auto with_heads) {
 #pragma unroll
             for (int t = kTile - 1; t >= 0; --t) {
