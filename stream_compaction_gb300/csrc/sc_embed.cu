@@ -44,6 +44,10 @@ constexpr int kSortWarps = kNT / 32;
 constexpr int kMaxDigit = 1024;
 constexpr int kClusterNT = 1024, kClusterWarps = kClusterNT / 32, kClusterCtas = 8;
 constexpr long long kClusterKeys = 8ll * kClusterNT * kClusterCtas;  // 8 a thread: 65536
+// A launch asks for its digits' share of this.  The kernels' limit is always the
+// whole: it is one per device, and another host thread's call between a call's own
+// limit and its launch would have the launch refused.
+constexpr int kClusterShared = kClusterWarps * kMaxDigit * 2;
 constexpr int kRun = 32;
 constexpr int kRowsPerCta = 32;
 
@@ -626,7 +630,7 @@ sc_status launch_embed_grad(int dtype, int wtype, const EmbedParams& p, const Em
     if (in_cluster) {
         auto go = [&](auto kernel) {
             const int bytes = kClusterWarps * (1 << g.digit_bits) * 2;
-            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kClusterShared);
             if (e != cudaSuccess) return e;
             cudaLaunchAttribute attr{};
             attr.id = cudaLaunchAttributeClusterDimension;
