@@ -31,8 +31,9 @@
  * Layout.  Elements of a token are contiguous; batch and token strides
  * (*_batch, *_token, in elements, >= 0) are free, so the halves of a joint
  * projection's output need no copy.  weight, bias, A, D, dt_bias, states and
- * heads are contiguous.  Outputs must not overlap inputs or one another,
- * except that a step's state is updated in place.  Tensors whose pointers and
+ * heads are contiguous.  Outputs must not overlap inputs or one another
+ * (SC_ERR_INVALID; column slices of one joint buffer do not overlap), except
+ * that a step's state is updated in place.  Tensors whose pointers and
  * strides are multiples of 16 bytes take 16-byte accesses; others work, element
  * by element.
  *

@@ -28,9 +28,9 @@ int64_t product(int64_t a, int64_t b, int64_t c = 1, int64_t d = 1) {
 
 // A batch x tokens x channels tensor with free strides.
 struct Tensor {
-    const void* p;
-    int64_t batch, tokens, channels, sb, st;
-    int eb;
+    const void* p = nullptr;
+    int64_t batch = 0, tokens = 0, channels = 0, sb = 0, st = 0;
+    int eb = 1;
     int64_t span() const {  // elements from the first to behind the last
         if (!batch || !tokens || !channels) return 0;
         const __int128 n = (__int128)(batch - 1) * sb + (__int128)(tokens - 1) * st + channels;
@@ -64,6 +64,30 @@ bool share(const Tensor& a, const Tensor& b) {
         const int64_t col = ((diff % stride) + stride) % stride;   // its column in b's rows
         if (col >= b.channels && col + a.channels <= stride) return false;
     }
+    return true;
+}
+
+// Whether every output has its memory to itself: none shares it with an input or
+// with another output.  The ranges of addresses decide nearly always.
+template <int kOut, int kIn>
+bool apart(const Tensor (&out)[kOut], const Tensor (&in)[kIn]) {
+    const Tensor* all[kOut + kIn];
+    uintptr_t lo[kOut + kIn], hi[kOut + kIn];
+    int n = 0, outs = 0;
+    auto add = [&](const Tensor& t) {
+        const int64_t span = t.p ? t.span() : 0;
+        if (span <= 0) return;
+        all[n] = &t;
+        lo[n] = reinterpret_cast<uintptr_t>(t.p);
+        hi[n] = lo[n] + (uintptr_t)span * t.eb;
+        ++n;
+    };
+    for (const Tensor& t : out) add(t);
+    outs = n;
+    for (const Tensor& t : in) add(t);
+    for (int i = 0; i < outs; ++i)
+        for (int j = i + 1; j < n; ++j)
+            if (lo[i] < hi[j] && lo[j] < hi[i] && share(*all[i], *all[j])) return false;
     return true;
 }
 
@@ -118,6 +142,8 @@ sc_status conv_args(const sc_conv_desc* d, bool step, ConvParams* p) {
 Tensor conv_state(const void* p, const sc_conv_desc* d) {
     return flat(p, d->batch * (d->width - 1) * d->channels, bytes_of(d->dtype));
 }
+Tensor conv_weight(const sc_conv_desc* d) { return flat(d->weight, d->channels * d->width, bytes_of(d->dtype)); }
+Tensor conv_bias(const sc_conv_desc* d) { return flat(d->bias, d->channels, bytes_of(d->dtype)); }
 
 // ------------------------------------------------------ selective scan
 sc_status ssm_args(const sc_ssm_desc* d, bool step, SsmParams* p) {
@@ -189,6 +215,24 @@ sc_status ssm_args(const sc_ssm_desc* d, bool step, SsmParams* p) {
 
 Tensor ssm_x(const sc_ssm_desc* d, const void* p, int64_t sb, int64_t st) {
     return {p, d->batch, d->length, d->channels, sb, st, bytes_of(d->dtype)};
+}
+
+// B or C: a token's groups as one row, up to the last group's end (ssm_args checks it).
+Tensor ssm_bc(const sc_ssm_desc* d, const void* p, int64_t sb, int64_t st, int64_t group) {
+    return {p, d->batch, d->length, (d->groups - 1) * group + d->states, sb, st, bytes_of(d->dtype)};
+}
+// What every form of the scan reads, into in[0 .. 7] (a step's token strides are not used).
+constexpr int kSsmInputs = 8;
+void ssm_inputs(const sc_ssm_desc* d, bool step, Tensor* in) {
+    const int64_t f = step ? 0 : 1;
+    in[0] = ssm_x(d, d->x, d->x_batch, f * d->x_token);
+    in[1] = ssm_x(d, d->dt, d->dt_batch, f * d->dt_token);
+    in[2] = ssm_x(d, d->z, d->z_batch, f * d->z_token);
+    in[3] = ssm_bc(d, d->B, d->B_batch, f * d->B_token, d->B_group);
+    in[4] = ssm_bc(d, d->C, d->C_batch, f * d->C_token, d->C_group);
+    in[5] = flat(d->A, d->channels * d->states, 4);
+    in[6] = flat(d->D, d->channels, 4);
+    in[7] = flat(d->dt_bias, d->channels, 4);
 }
 
 // 16-byte accesses for every tensor that the tiled kernels read or write.
@@ -319,7 +363,8 @@ sc_status sc_causal_conv(const sc_conv_desc* d, void* y, int64_t y_batch, int64_
     if (final_state && final_state == d->state) return SC_ERR_INVALID;  // other runs of tokens still read it
     const Tensor x{d->x, d->batch, d->length, d->channels, d->x_batch, d->x_token, eb};
     const Tensor o{y, d->batch, d->length, d->channels, y_batch, y_token, eb};
-    if (!o.ok() || !o.distinct() || share(o, x) || share(o, is) || share(o, fs) || share(fs, x)) return SC_ERR_INVALID;
+    const Tensor in[] = {x, is, conv_weight(d), conv_bias(d), flat(d->heads, d->batch * d->length, 1)}, out[] = {o, fs};
+    if (!o.ok() || !o.distinct() || !apart(out, in)) return SC_ERR_INVALID;
     const int e = 4;  // channels of a thread
     p.y = y;
     p.y_batch = y_batch;
@@ -354,10 +399,11 @@ sc_status sc_causal_conv_grad(const sc_conv_desc* d, const void* dy, int64_t dy_
     const Tensor x{d->x, d->batch, d->length, d->channels, d->x_batch, d->x_token, eb};
     const Tensor g{dy, d->batch, d->length, d->channels, dy_batch, dy_token, eb};
     const Tensor o{dx, d->batch, d->length, d->channels, dx_batch, dx_token, eb};
-    const Tensor is = conv_state(d->state, d), ds = conv_state(dstate, d);
-    if (!g.ok() || (dx && (!o.ok() || !o.distinct())) || share(o, x) || share(o, g) || share(o, is) || share(ds, x) ||
-        share(ds, g) || share(ds, is) || share(ds, o))
-        return SC_ERR_INVALID;
+    const Tensor in[] = {x, g, conv_state(d->state, d), conv_weight(d), conv_bias(d),
+                         flat(d->heads, d->batch * d->length, 1)};
+    const Tensor out[] = {o, flat(dweight, d->channels * d->width, 4), flat(dbias, d->channels, 4),
+                          conv_state(dstate, d)};
+    if (!g.ok() || (dx && (!o.ok() || !o.distinct())) || !apart(out, in)) return SC_ERR_INVALID;
     const int e = 4;  // channels of a thread
     p.dy = dy;
     p.dy_batch = dy_batch;
@@ -390,8 +436,8 @@ sc_status sc_causal_conv_step(const sc_conv_desc* d, void* pool, int64_t pool_ro
     if (d->batch == 0 || d->channels == 0) return SC_OK;
     const Tensor x{d->x, d->batch, 1, d->channels, d->x_batch, 0, eb}, o{y, d->batch, 1, d->channels, y_batch, 0, eb};
     const Tensor ps = flat(pool, pool_rows * (d->width - 1) * d->channels, eb);
-    if (!o.ok() || !o.distinct() || (ps.channels > 0 && !ps.ok()) || share(o, x) || share(o, ps) || share(ps, x))
-        return SC_ERR_INVALID;
+    const Tensor in[] = {x, conv_weight(d), conv_bias(d), flat(slots, d->batch, 4)}, out[] = {o, ps};
+    if (!o.ok() || !o.distinct() || (ps.channels > 0 && !ps.ok()) || !apart(out, in)) return SC_ERR_INVALID;
     const int e = 4;  // channels of a thread
     p.y = y;
     p.y_batch = y_batch;
@@ -429,12 +475,12 @@ sc_status sc_selective_scan(const sc_ssm_desc* d, void* y, int64_t y_batch, int6
     if (d->length == 0) return copy_or_zero(final_state, d->state, (size_t)sn * 4, s);
     const Tensor o = ssm_x(d, y, y_batch, y_token);
     const Tensor sv = flat(saved, (int64_t)(sc_selective_scan_saved_bytes(d->batch, d->length, d->channels, d->states) / 4), 4);
-    if (!o.ok() || !o.distinct()) return SC_ERR_INVALID;
-    const Tensor in[] = {ssm_x(d, d->x, d->x_batch, d->x_token), ssm_x(d, d->dt, d->dt_batch, d->dt_token),
-                         ssm_x(d, d->z, d->z_batch, d->z_token), is};
-    for (const Tensor& t : in)
-        if (share(o, t) || share(fs, t) || share(sv, t)) return SC_ERR_INVALID;
-    if (share(o, fs) || share(o, sv) || share(fs, sv)) return SC_ERR_INVALID;
+    Tensor in[kSsmInputs + 2];
+    ssm_inputs(d, false, in);
+    in[kSsmInputs] = flat(d->heads, d->batch * d->length, 1);
+    in[kSsmInputs + 1] = is;
+    const Tensor out[] = {o, fs, sv};
+    if (!o.ok() || !o.distinct() || !apart(out, in)) return SC_ERR_INVALID;
     const SsmPlan plan = ssm_plan(d->batch, d->length, d->channels, d->states, d->groups, false);
     unsigned char* base = nullptr;
     if (plan.total) {
@@ -480,21 +526,22 @@ sc_status sc_selective_scan_grad(const sc_ssm_desc* d, const sc_ssm_grads* g, sc
     const int64_t row = d->length * d->channels, bcn = d->batch * d->length * d->groups * d->states;
     const Tensor dy = ssm_x(d, g->dy, g->dy_batch, g->dy_token);
     const Tensor out[] = {ssm_x(d, g->dx, row, d->channels), ssm_x(d, g->ddt, row, d->channels),
-                          ssm_x(d, g->dz, row, d->channels)};
-    const Tensor db = flat(g->dB, bcn, eb), dc = flat(g->dC, bcn, eb);
-    if (!dy.ok() || !out[0].ok() || !out[1].ok() || (d->z ? !out[2].ok() : g->dz != nullptr) || !db.ok() || !dc.ok() ||
-        !g->saved)
+                          ssm_x(d, g->dz, row, d->channels), flat(g->dB, bcn, eb), flat(g->dC, bcn, eb),
+                          flat(g->dA, d->channels * d->states, 4), flat(g->dD, d->channels, 4),
+                          flat(g->ddt_bias, d->channels, 4), dst};
+    if (!dy.ok() || !out[0].ok() || !out[1].ok() || (d->z ? !out[2].ok() : g->dz != nullptr) || !out[3].ok() ||
+        !out[4].ok() || !g->saved)
         return SC_ERR_INVALID;
-    const Tensor in[] = {ssm_x(d, d->x, d->x_batch, d->x_token), ssm_x(d, d->dt, d->dt_batch, d->dt_token),
-                         ssm_x(d, d->z, d->z_batch, d->z_token), dy};
-    for (int i = 0; i < 3; ++i) {
-        for (const Tensor& t : in)
-            if (share(out[i], t)) return SC_ERR_INVALID;
-        for (int j = 0; j < i; ++j)
-            if (share(out[i], out[j])) return SC_ERR_INVALID;
-        if (share(out[i], db) || share(out[i], dc)) return SC_ERR_INVALID;
-    }
-    if (share(db, dc)) return SC_ERR_INVALID;
+    const Tensor saved = flat(
+        g->saved, (int64_t)(sc_selective_scan_saved_bytes(d->batch, d->length, d->channels, d->states) / 4), 4);
+    Tensor in[kSsmInputs + 5];
+    ssm_inputs(d, false, in);
+    in[kSsmInputs] = flat(d->heads, d->batch * d->length, 1);
+    in[kSsmInputs + 1] = flat(d->state, sn, 4);
+    in[kSsmInputs + 2] = dy;
+    in[kSsmInputs + 3] = saved;
+    in[kSsmInputs + 4] = df;
+    if (!apart(out, in)) return SC_ERR_INVALID;
     const SsmPlan plan = ssm_plan(d->batch, d->length, d->channels, d->states, d->groups, true);
     unsigned char* base = nullptr;
     st = seq_scratch(s, plan.total, &base);
@@ -530,10 +577,11 @@ sc_status sc_selective_scan_step(const sc_ssm_desc* d, float* pool, int64_t pool
     if (d->batch == 0 || d->channels == 0) return SC_OK;
     const int eb = bytes_of(d->dtype);
     const Tensor o = ssm_x(d, y, y_batch, 0), ps = flat(pool, pool_rows * d->channels * d->states, 4);
-    if (!o.ok() || !o.distinct() || (ps.channels > 0 && !ps.ok()) || share(o, ps) ||
-        share(o, ssm_x(d, d->x, d->x_batch, 0)) || share(o, ssm_x(d, d->dt, d->dt_batch, 0)) ||
-        share(o, ssm_x(d, d->z, d->z_batch, 0)))
-        return SC_ERR_INVALID;
+    Tensor in[kSsmInputs + 1];
+    ssm_inputs(d, true, in);
+    in[kSsmInputs] = flat(slots, d->batch, 4);
+    const Tensor out[] = {o, ps};
+    if (!o.ok() || !o.distinct() || (ps.channels > 0 && !ps.ok()) || !apart(out, in)) return SC_ERR_INVALID;
     p.y = y;
     p.y_batch = y_batch;
     p.pool = pool;
