@@ -3,7 +3,9 @@ sequence operators to torch tensors with the host compiler.
 
 Each .cu translation unit is compiled in parallel into _build/, then linked
 into stream_compaction_gb300/libsc_gb300.so (CUDA runtime linked statically);
-sc_bind.cpp becomes stream_compaction_gb300/_seqbind.so on top of it.
+sc_bind.cpp becomes stream_compaction_gb300/_seqbind.so on top of it.  The
+library needs nvcc alone: it is linked whatever becomes of the binding, which
+is left out where torch is not installed and raises where it does not build.
 Run ``python -m stream_compaction_gb300.build`` or call ``build()``.
 """
 from __future__ import annotations
@@ -37,23 +39,36 @@ def sources():
     return sorted(f for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _deps_mtime():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+def _newest(names):
+    files = [os.path.join(CSRC, f) for f in names]
     files += [os.path.join(ROOT, "include", h) for h in ("sc_scan.h", "sc_seq.h")]
     files.append(os.path.abspath(__file__))
     return max(os.path.getmtime(f) for f in files)
 
 
-def up_to_date() -> bool:
-    newest = _deps_mtime()
-    return all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, BIND))
+def _library_up_to_date() -> bool:
+    return os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest(f for f in os.listdir(CSRC) if f != "sc_bind.cpp")
 
 
-def _bind_commands(cc: str):
-    """Compile and link commands of the binding (paths from the installed torch, without importing it)."""
+def _torch_dir():
+    """Folder of the installed torch (which is not imported), or None."""
     import importlib.util
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def _binding_up_to_date() -> bool:
+    return os.path.exists(BIND) and os.path.getmtime(BIND) >= _newest(["sc_bind.cpp"])
+
+
+def up_to_date() -> bool:
+    """Whether there is nothing to build: the library and, where torch is, the binding."""
+    return _library_up_to_date() and (_torch_dir() is None or _binding_up_to_date())
+
+
+def _bind_commands(cc: str, torch_dir: str):
+    """Compile and link commands of the binding."""
     import sysconfig
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(cc)))
     obj = os.path.join(BUILD, "sc_bind.o")
     include = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
@@ -75,6 +90,33 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
+    torch_dir = _torch_dir()
+    commands = _bind_commands(cc, torch_dir) if torch_dir and (force or not _binding_up_to_date()) else None
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:  # beside the library's compilation
+        binding = ex.submit(_run, commands[0], "the binding's compilation") if commands else None
+        if force or not _library_up_to_date():
+            _build_library(cc, verbose, extra_flags)
+        if binding:
+            binding.result()
+    if commands:
+        _run(commands[1], "the binding's link")
+        os.replace(commands[2], BIND)
+    elif not torch_dir:
+        sys.stderr.write("torch is not installed: the sequence operators' binding to its tensors is not built\n")
+    return LIB
+
+
+def _run(command, what: str) -> str:
+    try:
+        r = subprocess.run(command, capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError("%s failed: %s" % (what, e)) from e
+    if r.returncode != 0:
+        raise RuntimeError("%s failed:\n%s\n%s" % (what, r.stdout, r.stderr))
+    return r.stderr
+
+
+def _build_library(cc: str, verbose: bool, extra_flags) -> None:
     flags = list(NVCC_FLAGS) + list(extra_flags)
 
     def compile_one(src):
@@ -82,38 +124,19 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         cmd = [cc] + flags + ["-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError("nvcc failed on %s:\n%s\n%s" % (src, r.stdout, r.stderr))
-        return obj, r.stderr
-
-    bind_compile, bind_link, bind_tmp = _bind_commands(cc)
-
-    def compile_bind():
-        r = subprocess.run(bind_compile, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError("the binding's compilation failed:\n%s\n%s" % (r.stdout, r.stderr))
+        return obj, _run(cmd, "nvcc on %s" % src)
 
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
-        binding = ex.submit(compile_bind)
         results = list(ex.map(compile_one, srcs))
-        binding.result()
     if verbose:
         for (obj, log) in results:
             sys.stderr.write(log)
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [cc] + ARCH + ["-shared", "-o", tmp] + [o for o, _ in results] + ["-cudart", "static", "-Xlinker",
                                                                            "-soname=libsc_gb300.so"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
+    _run(cmd, "link")
     os.replace(tmp, LIB)
-    r = subprocess.run(bind_link, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("the binding's link failed:\n%s\n%s" % (r.stdout, r.stderr))
-    os.replace(bind_tmp, BIND)
-    return LIB
 
 
 if __name__ == "__main__":
