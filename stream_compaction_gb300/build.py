@@ -58,7 +58,12 @@ def _torch_dir():
 
 
 def _binding_up_to_date() -> bool:
-    return os.path.exists(BIND) and os.path.getmtime(BIND) >= _newest(["sc_bind.cpp"])
+    """Newer than its sources and than the installed torch, whose headers and libraries it is built on."""
+    if not os.path.exists(BIND):
+        return False
+    version = os.path.join(_torch_dir() or "", "version.py")
+    built = os.path.getmtime(BIND)
+    return built >= _newest(["sc_bind.cpp"]) and not (os.path.exists(version) and os.path.getmtime(version) > built)
 
 
 def up_to_date() -> bool:

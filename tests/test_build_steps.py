@@ -72,3 +72,17 @@ def test_a_host_without_a_compiler_for_the_binding(tree, monkeypatch):
     with pytest.raises(RuntimeError, match="binding"):
         build.build()
     assert os.path.exists(build.LIB)
+
+def test_another_torch_rebuilds_the_binding(tree, monkeypatch):
+    pytest.importorskip("torch")
+    build.build()
+    later = os.stat(build.BIND).st_mtime + 10
+    version = tree / "torch" / "version.py"
+    version.parent.mkdir()
+    version.write_text("")
+    (tree / "torch" / "__init__.py").write_text("")
+    os.utime(version, (later, later))
+    spec = importlib.util.spec_from_file_location("torch", tree / "torch" / "__init__.py")
+    found = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: spec if name == "torch" else found(name, *a))
+    assert not build.up_to_date()
