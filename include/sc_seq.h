@@ -45,7 +45,8 @@
  * (the two gradients that sum over tokens, and a scan whose rows are too few
  * for the machine, which splits the length) take it from the stream's
  * workspace of sc_scan.h, after its look-back part, under the same rules:
- * allocated on first use and grown, or bound by sc_set_workspace; such a call
+ * allocated on first use and grown, or bound by sc_set_workspace (the
+ * *_workspace_bytes are for the current device); such a call
  * on a capturing stream returns SC_ERR_UNSUPPORTED.  The others may be
  * captured: sc_embed, sc_causal_conv, both steps, and any call whose
  * *_workspace_bytes is 0.  Empty problems (no tokens, no rows, no channels)

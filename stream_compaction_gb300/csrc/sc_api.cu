@@ -1090,6 +1090,12 @@ sc_status seq_scratch(cudaStream_t s, size_t bytes, unsigned char** out) {
 }
 
 void count_launches(int n) { g_launches.fetch_add((uint64_t)n); }
+
+// Without a device (sizes asked for on a host that has none): a GB300's.
+long long seq_sms() {
+    const int n = num_sms();
+    return n > 0 ? n : 152;
+}
 }  // namespace scg
 
 // Tile sizes (host side).

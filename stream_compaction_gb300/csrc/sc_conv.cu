@@ -445,7 +445,7 @@ long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 // Tokens per thread: the longest run up to `most` that leaves eight warps per
 // SM, at least `least`.
 int run_length(long long batch, long long length, long long channels, int n, int least, int most) {
-    const long long warps = ceil_div(channels, 32ll * n) * std::max(batch, 1ll), want = 8ll * 152;
+    const long long warps = ceil_div(channels, 32ll * n) * std::max(batch, 1ll), want = 8 * seq_sms();
     int run = most;
     while (run > least && warps * ceil_div(length, run) < want) run /= 2;
     return run;

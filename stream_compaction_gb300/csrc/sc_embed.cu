@@ -567,7 +567,8 @@ cudaError_t sums_of(const EmbedParams& p, const uint32_t* keys, const uint32_t* 
     // fewer rows a CTA, down to one for each of its thread rows, where 32 would
     // leave SMs without a CTA
     int per_cta = kRowsPerCta;
-    while (per_cta > std::max(kNT / tpr / 2, 1) && ceil_div(p.vocab, per_cta) * slices < 8 * 152) per_cta /= 2;
+    const long long enough = 8 * seq_sms();
+    while (per_cta > std::max(kNT / tpr / 2, 1) && ceil_div(p.vocab, per_cta) * slices < enough) per_cta /= 2;
     const dim3 grid((unsigned)ceil_div(p.vocab, per_cta), slices);
     if (p.vec) embed_rows_kernel<T, O, W, true><<<grid, kNT, 0, s>>>(p, vals, runs, partials, tpr, per_cta);
     else embed_rows_kernel<T, O, W, false><<<grid, kNT, 0, s>>>(p, vals, runs, partials, tpr, per_cta);

@@ -13,6 +13,7 @@ namespace scg {
 sc_status seq_scratch(cudaStream_t s, size_t bytes, unsigned char** out);
 size_t seq_scratch_total(size_t bytes);  // workspace bytes that hold it
 void count_launches(int n);
+long long seq_sms();  // multiprocessors of the current device
 
 // ------------------------------------------------------------- embedding
 struct EmbedParams {

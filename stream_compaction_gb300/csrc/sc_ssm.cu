@@ -16,7 +16,6 @@ cudaError_t launch_ssm_grad_f32(const SsmParams&, const SsmPlan&, int*, cudaStre
 namespace {
 
 constexpr int kStepNT = 128;
-constexpr long long kSms = 152;
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
@@ -215,7 +214,7 @@ int ssm_lanes(long long states) { return states <= 8 ? 2 : states <= 16 ? 4 : st
 SsmPlan ssm_plan(long long batch, long long length, long long channels, long long states, long long groups, bool grad) {
     SsmPlan g{};
     g.lanes = ssm_lanes(states);
-    const long long per = channels / groups, ch = g.lanes <= 4 ? 32 : g.lanes == 8 ? 16 : 8;
+    const long long sms = seq_sms(), per = channels / groups, ch = g.lanes <= 4 ? 32 : g.lanes == 8 ? 16 : 8;
     const long long block = ch * (g.lanes == 16 ? 2 : 4), np = 4 * g.lanes;
     g.blocks_per_group = ceil_div(per, block);
     const long long warps = batch * groups * ceil_div(per, ch), tiles = ceil_div(length, kTile);
@@ -230,12 +229,12 @@ SsmPlan ssm_plan(long long batch, long long length, long long channels, long lon
     // states: 209 us, 206, 213 and 234).
     long long chunks = 1;
     if (grad) {
-        chunks = back_chunks(g.blocks_per_group * groups * batch, (g.lanes == 16 ? 3 : 2) * kSms, tiles);
-    } else if (10 * warps < 17 * kSms) {
-        chunks = std::min(ceil_div(7 * kSms, warps), std::max(tiles / 4, 1ll));
+        chunks = back_chunks(g.blocks_per_group * groups * batch, (g.lanes == 16 ? 3 : 2) * sms, tiles);
+    } else if (10 * warps < 17 * sms) {
+        chunks = std::min(ceil_div(7 * sms, warps), std::max(tiles / 4, 1ll));
     }
     g.chunk_tiles = ceil_div(tiles, chunks);
-    const long long split = grad && chunks > 1 ? std::min(ceil_div(4 * kSms, warps * (chunks - 1)), g.chunk_tiles) : 1;
+    const long long split = grad && chunks > 1 ? std::min(ceil_div(4 * sms, warps * (chunks - 1)), g.chunk_tiles) : 1;
     g.run_tiles = ceil_div(g.chunk_tiles, split);
     g.chunk_tiles = g.run_tiles * split;
     g.chunks = (int)ceil_div(tiles, g.chunk_tiles);
