@@ -19,46 +19,6 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import stream_compaction_gb300 as sc  # noqa: E402
 
 
-class Embed(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, ids, weight, scale):
-        ctx.save_for_backward(ids)
-        ctx.vocab, ctx.scale = weight.shape[0], scale
-        return sc.embed(ids, weight, scale)
-
-    @staticmethod
-    def backward(ctx, dy):
-        (ids,) = ctx.saved_tensors
-        return None, sc.embed_grad(ids, dy.contiguous(), ctx.vocab, ctx.scale), None
-
-
-class CausalConv(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, weight, bias, heads):
-        ctx.save_for_backward(x, weight, bias, heads)
-        return sc.causal_conv(x, weight, bias, heads=heads)
-
-    @staticmethod
-    def backward(ctx, dy):
-        x, weight, bias, heads = ctx.saved_tensors
-        g = sc.causal_conv_grad(dy.contiguous(), x, weight, bias, heads=heads)
-        return g["x"], g["weight"].to(weight.dtype), g["bias"].to(bias.dtype), None
-
-
-class SelectiveScan(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, dt, A, B, C, D, z, dt_bias, heads):
-        saved = sc.selective_scan_saved(x, A)
-        ctx.save_for_backward(x, dt, A, B, C, D, z, dt_bias, heads, saved)
-        return sc.selective_scan(x, dt, A, B, C, D, z, dt_bias, heads=heads, saved=saved)
-
-    @staticmethod
-    def backward(ctx, dy):
-        x, dt, A, B, C, D, z, dt_bias, heads, saved = ctx.saved_tensors
-        g = sc.selective_scan_grad(dy.contiguous(), x, dt, A, B, C, D, z, dt_bias, heads=heads, saved=saved)
-        return g["x"], g["dt"], g["A"], g["B"], g["C"], g["D"], g["z"], g["dt_bias"], None
-
-
 class Model:
     """The parameters, in float32, and the two ways through them."""
 
@@ -92,11 +52,11 @@ class Model:
     def logits(self, ids, heads):
         """A batch of rows, packed sequences starting where heads is set."""
         p = self.p
-        h = Embed.apply(ids, p["tokens"], math.sqrt(self.dim))
+        h = sc.embed(ids, p["tokens"], math.sqrt(self.dim))
         x, z = (h @ p["to_xz"]).chunk(2, -1)
-        u = CausalConv.apply(x, p["conv"], p["conv_bias"], heads)
+        u = sc.causal_conv(x, p["conv"], p["conv_bias"], heads=heads)
         dt, B, C = self._inner(u)
-        y = SelectiveScan.apply(u, dt, -torch.exp(p["log_A"]), B, C, p["D"], z, p["dt_bias"], heads)
+        y = sc.selective_scan(u, dt, -torch.exp(p["log_A"]), B, C, p["D"], z, p["dt_bias"], heads=heads)
         return (h + y @ p["out"]) @ p["tokens"].T
 
     @torch.no_grad()

@@ -94,6 +94,15 @@ const int32_t* slots_of(const Maybe& slots, const Tensor& x) {
     return static_cast<const int32_t*>(whole(slots, "slots", {x.size(0)}, at::kInt, x.device()));
 }
 
+// A tensor of the caller's that the call writes to: autograd learns of it, as of any
+// operation in place, and refuses a gradient that would read the old values.
+void written(const Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(const Maybe& t) {
+    if (t) written(*t);
+}
+
 Tensor make(at::IntArrayRef shape, const Tensor& like_this) { return at::empty(shape, like_this.options()); }
 Tensor make_f32(at::IntArrayRef shape, const Tensor& like_this) {
     return at::empty(shape, like_this.options().dtype(at::kFloat));
@@ -125,6 +134,7 @@ Tensor embed(const Tensor& ids, const Tensor& weight, double scale, const Maybe&
     check(sc_embed(ids.data_ptr(), wide, ids.numel(), (sc_dtype)type, weight.data_ptr(), vocab, dim,
                    vocab > 1 ? weight.stride(0) : dim, (float)scale, to, dim, stream()),
           "sc_embed");
+    written(out);
     return y;
 }
 
@@ -148,6 +158,7 @@ Tensor embed_grad(const Tensor& ids, const Tensor& dout, int64_t vocab, double s
                         (float)scale, (sc_dtype)code(dw, "out"), dw.data_ptr(), vocab > 1 ? dw.stride(0) : dim,
                         accumulate, stream()),
           "sc_embed_grad");
+    written(out);
     return dw;
 }
 
@@ -190,6 +201,8 @@ Tensor causal_conv(const Tensor& x, const Tensor& weight, const Maybe& bias,
     void* fs = whole(final_state, "final_state", shape, x.scalar_type(), x.device());
     Tensor y = out_like(out, x);
     check(sc_causal_conv(&d, y.data_ptr(), y.stride(0), y.stride(1), fs, stream()), "sc_causal_conv");
+    written(final_state);
+    written(out);
     return y;
 }
 
@@ -221,6 +234,8 @@ Tensor causal_conv_step(const Tensor& x, const Tensor& state, const Tensor& weig
     Tensor y = out_like(out, x);
     check(sc_causal_conv_step(&d, pool, state.size(0), sl, y.data_ptr(), y.stride(0), stream()),
           "sc_causal_conv_step");
+    written(state);
+    written(out);
     return y;
 }
 
@@ -305,6 +320,9 @@ Tensor selective_scan(const Tensor& x, const Tensor& dt, const Tensor& A, const 
     float* sv = saved_of(saved, d, x);
     Tensor y = out_like(out, x);
     check(sc_selective_scan(&d, y.data_ptr(), y.stride(0), y.stride(1), fs, sv, stream()), "sc_selective_scan");
+    written(final_state);
+    written(saved);
+    written(out);
     return y;
 }
 
@@ -351,6 +369,8 @@ Tensor selective_scan_step(const Tensor& x, const Tensor& dt, const Tensor& A, c
     check(sc_selective_scan_step(&d, static_cast<float*>(pool), state.size(0), sl, y.data_ptr(), y.stride(0),
                                  stream()),
           "sc_selective_scan_step");
+    written(state);
+    written(out);
     return y;
 }
 

@@ -6,6 +6,12 @@ The functions take torch CUDA tensors and run on the current torch stream (or
 (on that stream), and leave every step of the computation to the library's
 kernels.  Definitions, layouts and limits: the header.
 
+embed, causal_conv and selective_scan are differentiable: where torch records
+gradients and an input requires one, their results carry it (seq_autograd.py), by the
+`_grad` functions below, which may also be called by themselves.  `out` cannot be given
+then, and nothing goes back through `final_state`.  The `_step` forms have no gradient;
+asking for one raises.
+
     ids, weight                 y = embed(ids, weight, scale)
                                 dweight = embed_grad(ids, dy, vocab, scale)
     x (batch, length, channels) y = causal_conv(x, weight, bias)
@@ -98,9 +104,39 @@ def _call(name, stream, *args):
         return getattr(_native(), name)(*args)
 
 
+def _requires_grad(*tensors) -> bool:
+    for t in tensors:
+        if t is not None and getattr(t, "requires_grad", False):
+            import torch
+            return torch.is_grad_enabled()
+    return False
+
+
+def _record(function, stream, out, *args):
+    """The call through an autograd function; `out` has no place in it."""
+    if out is not None:
+        raise ValueError("out cannot be given where an input requires a gradient")
+    from . import seq_autograd
+    native, apply = _native(), getattr(seq_autograd, function).apply
+    if stream is None:
+        return apply(native, *args)
+    import torch
+    with torch.cuda.stream(stream):  # the gradient runs there, too
+        return apply(native, *args)
+
+
+def _step(name, stream, inputs, *args):
+    if not _requires_grad(*inputs):
+        return _call(name, stream, *args)
+    from . import seq_autograd
+    return seq_autograd.Step.apply(name, lambda *a: _call(name, stream, *a), *args)
+
+
 def embed(ids, weight, scale: float = 1.0, out=None, stream=None):
     """scale * weight[ids]: ids (int32 or int64) of any shape, weight (vocab, dim);
     a row of zeros where an id is outside [0, vocab)."""
+    if _requires_grad(weight):
+        return _record("Embed", stream, out, ids, weight, scale)
     return _call("embed", stream, ids, weight, scale, out)
 
 
@@ -117,6 +153,8 @@ def causal_conv(x, weight, bias=None, activation="silu", heads=None, state=None,
     uint8/bool flag per token, nonzero where a segment starts.  state: the width - 1
     inputs before x, oldest first (batch, width - 1, channels); final_state:
     receives those after x."""
+    if _requires_grad(x, weight, bias, state):
+        return _record("CausalConv", stream, out, x, weight, bias, activation, heads, state, final_state)
     return _call("causal_conv", stream, x, weight, bias, activation, heads, state, final_state, out)
 
 
@@ -130,7 +168,7 @@ def causal_conv_step(x, state, weight, bias=None, activation="silu", slots=None,
     """One token for each row of x (batch, channels); state (rows, width - 1,
     channels) is moved on in place.  slots (int32): the state row of each x row,
     no row twice; outside [0, rows): the x row sits out, its y is 0."""
-    return _call("causal_conv_step", stream, x, state, weight, bias, activation, slots, out)
+    return _step("causal_conv_step", stream, (x, weight, bias, state), x, state, weight, bias, activation, slots, out)
 
 
 def selective_scan_saved(x, A, stream=None):
@@ -144,7 +182,10 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool 
     (channels, states) float32, B and C (batch, length, groups, states), D and
     dt_bias (channels) float32, z like x.  heads as in causal_conv; state /
     final_state: (batch, channels, states) float32.  saved: from
-    selective_scan_saved, for the gradient."""
+    selective_scan_saved, for selective_scan_grad."""
+    if _requires_grad(x, dt, A, B, C, D, z, dt_bias, state):
+        return _record("SelectiveScan", stream, out, x, dt, A, B, C, D, z, dt_bias, softplus, heads, state, final_state,
+                       saved)
     return _call("selective_scan", stream, x, dt, A, B, C, D, z, dt_bias, softplus, heads, state, final_state, saved,
                  out)
 
@@ -162,4 +203,5 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, sof
     """One token for each row of x (batch, channels), B and C (batch, groups,
     states); state (rows, channels, states) float32 is moved on in place.  slots
     as in causal_conv_step."""
-    return _call("selective_scan_step", stream, x, dt, A, B, C, state, D, z, dt_bias, softplus, slots, out)
+    return _step("selective_scan_step", stream, (x, dt, A, B, C, D, z, dt_bias, state), x, dt, A, B, C, state, D, z,
+                 dt_bias, softplus, slots, out)
