@@ -174,8 +174,8 @@ __global__ void __launch_bounds__(kNT, WD == 4 && kVec && !kHeads ? 8 : 4) conv_
         }
         f.apply(x, lim, pre);
         if (p.silu) {
-            pre[0] = mul2(pre[0], sigmoid_2(pre[0]));
-            pre[1] = mul2(pre[1], sigmoid_2(pre[1]));
+            pre[0] = mul2(pre[0], sigmoid_2<T>(pre[0]));
+            pre[1] = mul2(pre[1], sigmoid_2<T>(pre[1]));
         }
         Four<T, kVec>::store(out, left, pre);
         out += p.y_token;
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kNT) conv_grad_kernel(ConvParams p, int run, u
             f.apply(x, lim, pre);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const f2 sg = sigmoid_2(pre[i]);
+                const f2 sg = sigmoid_2<T>(pre[i]);
                 g[i] = mul2(mul2(g[i], sg), fma2(pre[i], fma2(sg, both(-1.0f), both(1.0f)), both(1.0f)));
             }
         }
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kNT) conv_step_kernel(ConvParams p, unsigned c
 #pragma unroll
         for (int k = 0; k < WD; ++k)
             if (k >= pad) pre[i] = fma2(pack2(w[2 * i][k], w[2 * i + 1][k]), win[k].pair(i), pre[i]);
-        if (p.silu) pre[i] = mul2(pre[i], sigmoid_2(pre[i]));
+        if (p.silu) pre[i] = mul2(pre[i], sigmoid_2<T>(pre[i]));
     }
     Four<T, kVec>::store(out, left, pre);
 #pragma unroll

@@ -166,26 +166,75 @@ __device__ __forceinline__ float rcp(float v) {
 __device__ __forceinline__ f2 rcp_2(f2 v) { return pack2(rcp(lo2(v)), rcp(hi2(v))); }
 __device__ __forceinline__ f2 both(float v) { return pack2(v, v); }
 
-// 1 / (1 + exp(-v)); exp(-v) = infinity gives 0.
-__device__ __forceinline__ float sigmoid(float v) { return rcp(1.0f + ex2(v * -kLog2e)); }
+// exp(-a) for a >= 0 (NaN: NaN), 0 beyond 87.3.  2^t takes t = -a log2(e) rounded
+// to float32, an error of up to |t| 2^-25 in the exponent.  kFine takes it out:
+// exp(-a) = 2^t exp(r), r = -a - t ln 2, with ln 2 in two parts (the argument
+// reduction of Cody and Waite), exp(r) = 1 + r.
+constexpr float kLn2Low = -1.9046542e-9f;  // ln 2 - kLn2
+__device__ __forceinline__ float capped(float a) {  // beyond 104 nothing changes, and an infinity would give r = NaN
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(104.0f));
+    return r;
+}
+template <bool kFine>
+__device__ __forceinline__ float exp_minus(float a) {
+    if constexpr (!kFine) {
+        return ex2(a * -kLog2e);
+    } else {
+        a = capped(a);
+        const float t = a * -kLog2e, e = ex2(t);
+        return fmaf(e, fmaf(t, -kLn2Low, fmaf(t, -kLn2, -a)), e);
+    }
+}
+template <bool kFine>
+__device__ __forceinline__ f2 exp_minus_2(f2 a) {
+    if constexpr (!kFine) {
+        return ex2_2(mul2(a, both(-kLog2e)));
+    } else {
+        a = pack2(capped(lo2(a)), capped(hi2(a)));
+        const f2 t = mul2(a, both(-kLog2e)), e = ex2_2(t);
+        const f2 r = fma2(t, both(-kLn2Low), fma2(t, both(-kLn2), a ^ 0x8000000080000000ull));
+        return fma2(e, r, e);
+    }
+}
+
+// The activations for elements of T.  In 16 bits an element's own rounding hides
+// the exponent's error ((4 + |v|) 2^-24 of exp(-|v|)); in float32 it would be the
+// largest of all, so it is taken out, for two to four more instructions.
+template <class T> constexpr bool kFine = sizeof(T) == 4;
+
+// 1 / (1 + exp(-v)).  float32: exp(-|v|) / (1 + exp(-|v|)) below 0, within 9 x 2^-24
+// of the result; 16 bits: exp(-v) = infinity gives 0.
+template <class T>
+__device__ __forceinline__ float sigmoid(float v) {
+    if constexpr (!kFine<T>) return rcp(1.0f + ex2(v * -kLog2e));
+    const float e = exp_minus<true>(fabsf(v)), r = rcp(1.0f + e);
+    return v < 0.0f ? e * r : r;
+}
+template <class T>
 __device__ __forceinline__ f2 sigmoid_2(f2 v) {
-    return rcp_2(add2(both(1.0f), ex2_2(mul2(v, both(-kLog2e)))));
+    if constexpr (!kFine<T>) return rcp_2(add2(both(1.0f), ex2_2(mul2(v, both(-kLog2e)))));
+    const f2 e = exp_minus_2<true>(v & 0x7fffffff7fffffffull), r = rcp_2(add2(both(1.0f), e)), below = mul2(e, r);
+    return pack2(lo2(v) < 0.0f ? lo2(below) : lo2(r), hi2(v) < 0.0f ? hi2(below) : hi2(r));
 }
 
 // log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1], and
 // log1p(e) = 2 artanh(s), s = e / (2 + e) <= 1/3; artanh(s) = s + s^3 P(s^2)
 // with the cubic P fitted to (artanh(s) / s - 1) / s^2 at Chebyshev points of
 // s^2 in [0, 1/9] (relative error of the sum below 2e-8).  No branch and no
-// cancellation: relative error of a few 2^-24 for every v.
+// cancellation.  Relative error: within 11 x 2^-24 in float32, (9 + |v|) 2^-24 in 16
+// bits (v < 0); 0 below -87.3.
 constexpr float kP0 = 0.3333332f, kP1 = 0.20003836f, kP2 = 0.14116974f, kP3 = 0.13433797f;
+template <class T>
 __device__ __forceinline__ float softplus(float v) {
-    const float e = ex2(fabsf(v) * -kLog2e);
+    const float e = exp_minus<kFine<T>>(fabsf(v));
     const float s = e * rcp(2.0f + e), q = s * s;
     const float p = fmaf(fmaf(fmaf(kP3, q, kP2), q, kP1), q, kP0);
     return fmaf(2.0f, fmaf(p * q, s, s), fmaxf(v, 0.0f));  // NaN: e is NaN
 }
+template <class T>
 __device__ __forceinline__ f2 softplus_2(f2 v) {
-    const f2 e = ex2_2(mul2(v & 0x7fffffff7fffffffull, both(-kLog2e)));
+    const f2 e = exp_minus_2<kFine<T>>(v & 0x7fffffff7fffffffull);
     const f2 s = mul2(e, rcp_2(add2(both(2.0f), e))), q = mul2(s, s);
     const f2 p = fma2(fma2(fma2(both(kP3), q, both(kP2)), q, both(kP1)), q, both(kP0));
     return fma2(both(2.0f), fma2(mul2(p, q), s, s), pack2(fmaxf(lo2(v), 0.0f), fmaxf(hi2(v), 0.0f)));

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kStepNT) ssm_step_kernel(SsmParams p, unsigned
         }
     }
     d += bias;
-    if (p.softplus) d = softplus(d);
+    if (p.softplus) d = softplus<T>(d);
     const float u = d * x;
     float sum[R];
 #pragma unroll
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kStepNT) ssm_step_kernel(SsmParams p, unsigned
     }
     if (live && s < R && b < p.batch) {
         y = fmaf(D, x, y);
-        if (p.z) y *= z * sigmoid(z);
+        if (p.z) y *= z * sigmoid<T>(z);
         static_cast<T*>(p.y)[b * p.y_batch + e] = from_f32<T>(run ? y : 0.0f);  // a row that sits out: 0
     }
 }

@@ -161,9 +161,9 @@ __global__ void __launch_bounds__(32 * kBackWarps) ssm_back_summary_kernel(SsmPa
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     d[a][i] = add2(dt.pair(a, i), bias[i]);
-                    if (F || p.softplus) d[a][i] = softplus_2(d[a][i]);
+                    if (F || p.softplus) d[a][i] = softplus_2<T>(d[a][i]);
                     g[a][i] = dy.pair(a, i);
-                    if (F || zp) g[a][i] = mul2(g[a][i], mul2(z.pair(a, i), sigmoid_2(z.pair(a, i))));
+                    if (F || zp) g[a][i] = mul2(g[a][i], mul2(z.pair(a, i), sigmoid_2<T>(z.pair(a, i))));
                 }
                 Rows::template mask<F>(d[a], a, nt, left, lane);
             }
@@ -325,9 +325,9 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     d[a][i] = add2(dt.pair(a, i), bias[i]);
-                    if (F || p.softplus) d[a][i] = softplus_2(d[a][i]);
+                    if (F || p.softplus) d[a][i] = softplus_2<T>(d[a][i]);
                     g[a][i] = dy.pair(a, i);
-                    if (F || zp) g[a][i] = mul2(g[a][i], mul2(z.pair(a, i), sigmoid_2(z.pair(a, i))));
+                    if (F || zp) g[a][i] = mul2(g[a][i], mul2(z.pair(a, i), sigmoid_2<T>(z.pair(a, i))));
                 }
                 Rows::template mask<F>(d[a], a, nt, left, lane);
 #pragma unroll
@@ -388,11 +388,11 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
             for (int i = 0; i < 2; ++i) {
                 const f2 x = Rows::pair_of(rx, i);
                 dd[i] = fma2(gu[i], x, mul2(ga[i], both(kLn2)));
-                if (F || p.softplus) dd[i] = mul2(dd[i], sigmoid_2(add2(Rows::pair_of(rt, i), bias[i])));
+                if (F || p.softplus) dd[i] = mul2(dd[i], sigmoid_2<T>(add2(Rows::pair_of(rt, i), bias[i])));
                 gu[i] = fma2(gu[i], d[i], mul2(g[i], D[i]));  // dx
                 (i ? dD.y : dD.x) = fma2(g[i], x, i ? dD.y : dD.x);
                 if (F || zp) {
-                    const f2 z = Rows::pair_of(rz, i), sg = sigmoid_2(z);
+                    const f2 z = Rows::pair_of(rz, i), sg = sigmoid_2<T>(z);
                     const f2 slope = mul2(sg, fma2(z, fma2(sg, both(-1.0f), both(1.0f)), both(1.0f)));
                     y[i] = mul2(mul2(Rows::pair_of(ry, i), fma2(D[i], x, y[i])), slope);
                 }

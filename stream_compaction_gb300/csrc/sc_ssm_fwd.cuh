@@ -214,14 +214,14 @@ __global__ void __launch_bounds__(64) ssm_kernel(SsmParams p, int blocks_per_gro
                 for (int i = 0; i < 2; ++i) {
                     if constexpr (kStage) {
                         d[a][i] = add2(d[a][i], bias[i]);
-                        if constexpr (decltype(with_softplus)::value) d[a][i] = softplus_2(d[a][i]);
+                        if constexpr (decltype(with_softplus)::value) d[a][i] = softplus_2<T>(d[a][i]);
                         // past the end d = 0, whatever the bias
                         if constexpr (!kFull) d[a][i] = Elems::tok(a, lane) < nts ? d[a][i] : 0ull;
                         x[a][i] = mul2(d[a][i], x[a][i]);
                     }
                     if constexpr (kFinish) {
                         y[a][i] = fma2(D[i], xe[a][i], y[a][i]);
-                        if constexpr (kGate) y[a][i] = mul2(y[a][i], mul2(z[a][i], sigmoid_2(z[a][i])));
+                        if constexpr (kGate) y[a][i] = mul2(y[a][i], mul2(z[a][i], sigmoid_2<T>(z[a][i])));
                     }
                 }
             if constexpr (kStage) {
