@@ -259,6 +259,7 @@ void ssm_place(SsmParams* p, const SsmPlan& g, unsigned char* base) {
     p->part_bc = reinterpret_cast<float*>(base + g.part_bc);
     p->part_a = reinterpret_cast<float*>(base + g.part_a);
     p->part_d = reinterpret_cast<float*>(base + g.part_d);
+    p->odd = base + g.odd;
 }
 
 sc_status zero(void* p, size_t bytes, cudaStream_t s) {

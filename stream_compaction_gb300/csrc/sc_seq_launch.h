@@ -105,6 +105,7 @@ struct SsmParams {
     float* part_bc;  // [channel blocks][batch][length][2][padded states]
     float* part_a;   // [batch][chunks][channels][padded states]
     float* part_d;   // [2][batch][chunks][channels]
+    uint8_t* odd;    // by CTA, padded states: it met an infinity or NaN and left
     // step
     float* pool;
     long long pool_rows;
@@ -115,7 +116,7 @@ int ssm_lanes(long long states);
 struct SsmPlan {
     int lanes, chunks, runs;
     long long chunk_tiles, run_tiles, blocks_per_group;  // channel blocks of one CTA
-    size_t carry, sum_d, cut, part_bc, part_a, part_d, total;
+    size_t carry, sum_d, cut, part_bc, part_a, part_d, odd, total;
 };
 SsmPlan ssm_plan(long long batch, long long length, long long channels, long long states, long long groups, bool grad);
 cudaError_t launch_ssm(int dtype, const SsmParams& p, const SsmPlan& plan, cudaStream_t s);

@@ -136,7 +136,8 @@ __global__ void __launch_bounds__(kStepNT) ssm_step_kernel(SsmParams p, unsigned
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             h[r][k] = fmaf(decay(dr, A[k]), h[r][k], ur * B[r][k]);
-            sum[r] = fmaf(C[r][k], h[r][k], sum[r]);
+            // (a state past the last would be infinity times 0 where d or d x is infinite)
+            sum[r] = n0 + k < p.states ? fmaf(C[r][k], h[r][k], sum[r]) : sum[r];
         }
         if constexpr (kVec) {
             if (hp[r]) *reinterpret_cast<float4*>(hp[r]) = make_float4(h[r][0], h[r][1], h[r][2], h[r][3]);
@@ -255,6 +256,7 @@ SsmPlan ssm_plan(long long batch, long long length, long long channels, long lon
         g.part_bc = take((size_t)(g.blocks_per_group * groups) * batch * length * 2 * np * 4);
         g.part_a = take(rows * channels * np * 4);
         g.part_d = take(2 * rows * channels * 4);
+        if (states != np) g.odd = take(rows * (size_t)(g.blocks_per_group * groups));
     }
     g.total = at;
     return g;

@@ -15,8 +15,9 @@
 // Channels go in pairs through the two-lane float32 instructions (one issue
 // slot for two multiply-adds; measured: two clocks each, so they relieve the
 // issue, not the multipliers); B and C lie in shared memory as (v, v) pairs for
-// them.  States beyond `states` have A = B = C = 0 and stay 0.  Tokens beyond
-// the length have d = d*x = 0: the state passes them unchanged.
+// them.  States beyond `states` have A = B = C = 0 and stay 0; tiles with an infinity
+// or NaN, whose products with those zeros would be NaN, set them to 0 instead.  Tokens
+// beyond the length have d = d*x = 0: the state passes them unchanged.
 //
 // The elements of a tile (token, channel) are worked on in passes of 128, four
 // a lane: four channels of one token (kVec: 8 or 16-byte accesses, channels
@@ -455,6 +456,22 @@ __device__ __forceinline__ void to_pairs(const float (&v)[G::CPL][4], float scal
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[q][k] = pack2(v[2 * q][k] * scale, v[2 * q + 1][k] * scale);
 }
+// The lane, asked for anew: what is made of it, seldom used, is not kept in registers.
+__device__ __forceinline__ int lane_anew() {
+    int lane;
+    asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));
+    return lane;
+}
+// Zeros for a lane's states beyond `states`.
+template <class G>
+__device__ __forceinline__ void drop_padding(long long states, f2 (&v)[G::PC][4]) {
+    const int real = (int)states - lane_anew() % G::S * 4;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int q = 0; q < G::PC; ++q)
+            if (k >= real) v[q][k] = 0ull;
+}
 template <class G>
 __device__ __forceinline__ void clear(f2 (&v)[G::PC][4]) {
 #pragma unroll
@@ -470,7 +487,7 @@ __device__ __forceinline__ unsigned tile_heads(const uint8_t* row, long long t0,
 }
 
 // carry = decay of run j over its whole length * carry + what the run adds.
-template <class G>
+template <class G, bool kPadded>
 __device__ __forceinline__ void fold_run(const SsmParams& p, const f2 (&A2)[G::PC][4], long long b, long long j,
                                          long long ch0, int left, int lane, f2 (&carry)[G::PC][4]) {
     const long long row = b * p.runs + j;
@@ -489,6 +506,7 @@ __device__ __forceinline__ void fold_run(const SsmParams& p, const f2 (&A2)[G::P
             const f2 a = ex2_2(mul2(pack2(d[2 * q], d[2 * q + 1]), A2[q][k]));
             carry[q][k] = cut ? add : fma2(a, carry[q][k], add);
         }
+    if constexpr (kPadded) drop_padding<G>(p.states, carry);
 }
 // The run's own part, left for the others to fold.
 template <class G>

@@ -34,6 +34,13 @@
 // it, so what is used seldom (bias, D, their sums, a quarter's first state) lies
 // in shared memory.
 //
+// States past `states`, where their number is none of 8, 16, 32 and 64, have A = B =
+// C = 0 and take no part, as long as d, d x and g are finite; an infinity times their
+// zeros would be NaN in every sum over states.  A CTA that meets one leaves, and a
+// second launch of the kernel, whose CTAs return at once where that did not happen,
+// sets those states to 0 token by token.  (Both in one kernel: 4 % more time in every
+// call, by other registers in the loops that never meet one.)
+//
 // Rows too few for the machine: the length is split as in the forward pass,
 // with a first kernel that walks the chunks backwards from zero, in shorter
 // runs, of which there are enough for all SMs.
@@ -102,9 +109,28 @@ struct CtaStates {
     }
 };
 
+// Whether any of kN floats of this warp's in shared memory is an infinity or NaN;
+// after a barrier of the warp.  (Read again: in registers they would have to be kept
+// for it, where the kernels have none to spare.)
+template <int kN>
+__device__ __forceinline__ bool not_finite(const float* s, int lane) {
+    static_assert(kN % 128 == 0, "whole passes");
+    f2 zero = 0ull;  // times 0: 0, or NaN
+#pragma unroll
+    for (int i = 0; i < kN / 128; ++i) {
+        const ulonglong2 v = reinterpret_cast<const ulonglong2*>(s)[lane + 32 * i];
+        zero = fma2(v.x, 0ull, fma2(v.y, 0ull, zero));
+    }
+    return __any_sync(0xffffffffu, lo2(zero) + hi2(zero) != 0.0f);
+}
+
+// Padding: no states past `states`; some, and CTAs that meet an infinity or NaN leave;
+// some, for those CTAs.
+enum Pad { kNoPad, kLeaveOdd, kOnlyOdd };
+
 // dh of a run's first token, taken one token further back, with nothing
 // coming in from behind; and the run's sum of d.
-template <class T, class G, bool kVec>
+template <class T, class G, bool kVec, bool kPadded>
 __global__ void __launch_bounds__(32 * kBackWarps) ssm_back_summary_kernel(SsmParams p, int blocks_per_group,
                                                                              int grid_runs) {
     using Rows = TileRows<T, G, kVec, kTile>;
@@ -177,11 +203,13 @@ __global__ void __launch_bounds__(32 * kBackWarps) ssm_back_summary_kernel(SsmPa
         else stage(std::false_type{});
         C.to_shared(s_C[warp], lane);
         __syncwarp();
+        // states past `states` that would not stay 0 (infinity times 0)
+        const bool odd = kPadded && (not_finite<kTile * G::CH>(s_d[warp], lane) || not_finite<kTile * G::CH>(s_g[warp], lane));
         if (tile > tile0) {  // only the last tile of a row may be short of tokens
             if (left == G::CH && zp) fetch(tile - 1, std::true_type{});
             else fetch(tile - 1, std::false_type{});
         }
-        auto tokens = [&](auto with_heads) {
+        auto tokens = [&](auto with_care) {  // segment starts, or states to be kept at 0
 #pragma unroll
             for (int t = kTile - 1; t >= 0; --t) {
                 f2 d[G::PC], g[G::PC], Cv[4];
@@ -195,10 +223,11 @@ __global__ void __launch_bounds__(32 * kBackWarps) ssm_back_summary_kernel(SsmPa
                     for (int k = 0; k < 4; ++k)
                         dh[q][k] = mul2(decay_2(d[q], A2[q][k]), fma2(Cv[k], g[q], dh[q][k]));
                 }
-                if (decltype(with_heads)::value && (hm >> t & 1u)) clear<G>(dh);
+                if constexpr (decltype(with_care)::value && kPadded) drop_padding<G>(p.states, dh);
+                if (decltype(with_care)::value && (hm >> t & 1u)) clear<G>(dh);
             }
         };
-        if (hm) tokens(std::true_type{});
+        if (odd || hm) tokens(std::true_type{});
         else tokens(std::false_type{});
         __syncwarp();
     }
@@ -209,9 +238,9 @@ __global__ void __launch_bounds__(32 * kBackWarps) ssm_back_summary_kernel(SsmPa
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // h = q h[t-1] + d x B over the tokens of a quarter.
-template <class G, bool kHeads>
+template <class G, bool kHeads, bool kMask>
 __device__ __forceinline__ void run_quarter(const float* ld, const float* lu, const float2* lB, int t0, unsigned hm,
-                                            const f2 (&A2)[G::PC][4], f2 (&h)[G::PC][4]) {
+                                            long long states, const f2 (&A2)[G::PC][4], f2 (&h)[G::PC][4]) {
 #pragma unroll
     for (int j = 0; j < kQuarter; ++j) {
         f2 d[G::PC], u[G::PC], Bv[4];
@@ -223,11 +252,14 @@ __device__ __forceinline__ void run_quarter(const float* ld, const float* lu, co
         for (int q = 0; q < G::PC; ++q)
 #pragma unroll
             for (int k = 0; k < 4; ++k) h[q][k] = fma2(decay_2(d[q], A2[q][k]), h[q][k], mul2(u[q], Bv[k]));
+        if constexpr (kMask) drop_padding<G>(states, h);
     }
 }
 
-template <class T, class G, bool kVec>
+template <class T, class G, bool kVec, Pad kPad>
 __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p, int blocks_per_group) {
+    if (kPad == kOnlyOdd && p.odd[blockIdx.x] == 0) return;
+    if (kPad == kLeaveOdd && threadIdx.x == 0) p.odd[blockIdx.x] = 0;
     using Rows = TileRows<T, G, kVec, kTile>;
     using Sh = BwdShared<G>;
     constexpr int kWarps = G::kBwdWarps;
@@ -254,7 +286,7 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
         to_pairs<G>(raw, 1.0f, dh);
     }
     for (long long j = p.runs - 1; j >= (at.chunk + 1) * (p.chunk_tiles / p.run_tiles); --j)
-        fold_run<G>(p, A2, b, j, at.ch0, left, lane, dh);
+        fold_run<G, kPad != kNoPad>(p, A2, b, j, at.ch0, left, lane, dh);
     clear<G>(dA);
     // Registers are what this kernel has least of: the bias, D and their gradients'
     // sums, used once a pass, stay in shared memory.
@@ -404,12 +436,20 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
             ends[0] = dD;
             ends[32] = make_ulonglong2(add2(db.x, dd[0]), add2(db.y, dd[1]));
         };
-        __syncthreads();
+        if constexpr (kPad == kLeaveOdd) {  // d, u and g lie together
+            __syncwarp();
+            if (__syncthreads_or(not_finite<3 * Sh::kRow>(sm + Sh::d, lane))) {
+                if (threadIdx.x == 0) p.odd[blockIdx.x] = 1;
+                return;
+            }
+        } else {
+            __syncthreads();
+        }
         auto work = [&](auto with_heads) {
             constexpr bool kHeads = decltype(with_heads)::value;
 #pragma unroll 1
             for (int q4 = 1; q4 < kQuarters; ++q4) {  // the states before quarters 1, 2, ...
-                run_quarter<G, kHeads>(ld, lu, lB, (q4 - 1) * kQuarter, hm, A2, h0);
+                run_quarter<G, kHeads, kPad == kOnlyOdd>(ld, lu, lB, (q4 - 1) * kQuarter, hm, p.states, A2, h0);
                 hold_states(q4, h0);
             }
 #pragma unroll 1
@@ -433,11 +473,13 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
                             a[j][q][k] = decay_2(d[q], A2[q][k]);
                             h[j + 1][q][k] = fma2(a[j][q][k], head ? 0ull : h[j][q][k], mul2(u[q], Bv[k]));
                         }
+                    if constexpr (kPad == kOnlyOdd) drop_padding<G>(p.states, h[j + 1]);
                 }
 #pragma unroll
                 for (int j = kQuarter - 1; j >= 0; --j) {
                     const int t = tq + j;
                     const bool head = kHeads && (hm >> t & 1u);
+                    const int real = kPad == kOnlyOdd ? (int)p.states - lane_anew() % G::S * 4 : 4;
                     f2 d[G::PC], u[G::PC], g[G::PC], Bv[4], Cv[4];
                     read_channels<G>(ld + t * G::CH, d);
                     read_channels<G>(lu + t * G::CH, u);
@@ -452,11 +494,13 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
                         for (int q = 0; q < G::PC; ++q) {
                             const f2 ht = h[j + 1][q][k];
                             dh[q][k] = fma2(Cv[k], g[q], dh[q][k]);
+                            if (kPad == kOnlyOdd && k >= real) dh[q][k] = 0ull;
                             y[q] = k ? fma2(Cv[k], ht, y[q]) : mul2(Cv[k], ht);
                             dC[k] = q ? fma2(g[q], ht, dC[k]) : mul2(g[q], ht);
                             gu[q] = k ? fma2(dh[q][k], Bv[k], gu[q]) : mul2(dh[q][k], Bv[k]);
                             dB[k] = q ? fma2(dh[q][k], u[q], dB[k]) : mul2(dh[q][k], u[q]);
                             dh[q][k] = head ? 0ull : mul2(dh[q][k], a[j][q][k]);
+                            if (kPad == kOnlyOdd && k >= real) dh[q][k] = 0ull;
                             const f2 r = mul2(dh[q][k], head ? 0ull : h[j][q][k]);
                             ga[q] = k ? fma2(r, A2[q][k], ga[q]) : mul2(r, A2[q][k]);
                             dA[q][k] = fma2(r, d[q], dA[q][k]);
@@ -558,22 +602,28 @@ __global__ void __launch_bounds__(256) ssm_back_bc_kernel(SsmParams p, long long
     static_cast<T*>(p.dC)[i] = from_f32<T>(sc);
 }
 
-template <class T, class G, bool kVec>
+template <class T, class G, bool kVec, bool kPadded>
 cudaError_t ssm_back_of(const SsmParams& p, const SsmPlan& plan, int* launches, cudaStream_t s) {
     const long long per = p.channels / p.groups;
-    *launches = p.chunks > 1 ? 4 : 3;  // with the last sums, which the caller launches
+    *launches = (p.chunks > 1 ? 4 : 3) + (kPadded ? 1 : 0);  // with the last sums, which the caller launches
     if (p.chunks > 1) {
         const long long block = kBackWarps * G::CH;
         const int bpg = (int)((per + block - 1) / block), runs = p.runs - (int)(p.chunk_tiles / p.run_tiles);
-        ssm_back_summary_kernel<T, G, kVec>
-            <<<(unsigned)(bpg * p.groups * runs * p.batch), 32 * kBackWarps, 0, s>>>(p, bpg, runs);
+        auto first = ssm_back_summary_kernel<T, G, kVec, kPadded>;
+        first<<<(unsigned)(bpg * p.groups * runs * p.batch), 32 * kBackWarps, 0, s>>>(p, bpg, runs);
     }
-    auto kernel = ssm_back_kernel<T, G, kVec>;
-    constexpr size_t bytes = BwdShared<G>::kBytes;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != cudaSuccess) return e;
     const int bpg = (int)plan.blocks_per_group;
-    kernel<<<(unsigned)(bpg * p.groups * p.chunks * p.batch), 32 * G::kBwdWarps, bytes, s>>>(p, bpg);
+    auto go = [&](auto kernel) {
+        constexpr size_t bytes = BwdShared<G>::kBytes;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e == cudaSuccess)
+            kernel<<<(unsigned)(bpg * p.groups * p.chunks * p.batch), 32 * G::kBwdWarps, bytes, s>>>(p, bpg);
+        return e;
+    };
+    cudaError_t e = go(ssm_back_kernel<T, G, kVec, kPadded ? kLeaveOdd : kNoPad>);
+    if constexpr (kPadded)
+        if (e == cudaSuccess) e = go(ssm_back_kernel<T, G, false, kOnlyOdd>);
+    if (e != cudaSuccess) return e;
     const long long n = p.batch * p.length * p.groups * p.states;
     ssm_back_bc_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, plan.blocks_per_group, G::NP);
     return cudaGetLastError();
@@ -581,19 +631,19 @@ cudaError_t ssm_back_of(const SsmParams& p, const SsmPlan& plan, int* launches, 
 
 template <class T>
 cudaError_t ssm_back_type(const SsmParams& p, const SsmPlan& plan, int* launches, cudaStream_t s) {
+    auto go = [&](auto g) {
+        using G = decltype(g);
+        if (p.states == G::NP)
+            return p.vec ? ssm_back_of<T, G, true, false>(p, plan, launches, s)
+                         : ssm_back_of<T, G, false, false>(p, plan, launches, s);
+        return p.vec ? ssm_back_of<T, G, true, true>(p, plan, launches, s)
+                     : ssm_back_of<T, G, false, true>(p, plan, launches, s);
+    };
     switch (plan.lanes) {
-    case 2:
-        return p.vec ? ssm_back_of<T, Geo<2>, true>(p, plan, launches, s)
-                     : ssm_back_of<T, Geo<2>, false>(p, plan, launches, s);
-    case 4:
-        return p.vec ? ssm_back_of<T, Geo<4>, true>(p, plan, launches, s)
-                     : ssm_back_of<T, Geo<4>, false>(p, plan, launches, s);
-    case 8:
-        return p.vec ? ssm_back_of<T, Geo<8>, true>(p, plan, launches, s)
-                     : ssm_back_of<T, Geo<8>, false>(p, plan, launches, s);
-    case 16:
-        return p.vec ? ssm_back_of<T, Geo<16>, true>(p, plan, launches, s)
-                     : ssm_back_of<T, Geo<16>, false>(p, plan, launches, s);
+    case 2: return go(Geo<2>{});
+    case 4: return go(Geo<4>{});
+    case 8: return go(Geo<8>{});
+    case 16: return go(Geo<16>{});
     default: return cudaErrorInvalidValue;
     }
 }

@@ -112,7 +112,22 @@ struct RowCopy {
     }
 };
 
-template <class T, class G, bool kVec, bool kSummary>
+// Whether any of a warp's values is an infinity or NaN.
+template <int kN>
+__device__ __forceinline__ bool not_finite(const f2 (&v)[kN][2], const f2 (&w)[kN][2]) {
+    f2 zero = 0ull;  // times 0: 0, or NaN
+#pragma unroll
+    for (int a = 0; a < kN; ++a)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) zero = fma2(v[a][i], 0ull, fma2(w[a][i], 0ull, zero));
+    return __any_sync(0xffffffffu, lo2(zero) + hi2(zero) != 0.0f);
+}
+
+// Beside a tile's segment starts (bits 0 .. kT - 1): an infinity or NaN, and padding.
+constexpr unsigned kOdd = 1u << 31;
+
+// kPadded: fewer states than the padded number.
+template <class T, class G, bool kVec, bool kSummary, bool kPadded>
 __global__ void __launch_bounds__(64) ssm_kernel(SsmParams p, int blocks_per_group, int grid_chunks) {
     using Sh = FwdShared<T, G, kSummary>;
     constexpr int kT = Sh::kT, kRing = Sh::kRing;
@@ -152,6 +167,7 @@ __global__ void __launch_bounds__(64) ssm_kernel(SsmParams p, int blocks_per_gro
         T* yp = kSummary ? nullptr : static_cast<T*>(p.y) + b * p.y_batch + t_begin * p.y_token + at.ch0;
         const uint8_t* heads = p.heads ? p.heads + b * p.length + t_begin : nullptr;
         const long long tokens = t_end - t_begin;
+        bool odd = false;  // the staged tile has a d or d x that is not finite
         auto tile_len = [&](int k) { return (int)min((long long)kT, tokens - (long long)k * kT); };
         auto raw = [&](int k, int what) { return reinterpret_cast<T*>(s_all + (k % kRing) * Sh::kRaw + what); };
         // The copies of one tile, addresses as far as possible made beforehand: a
@@ -225,6 +241,7 @@ __global__ void __launch_bounds__(64) ssm_kernel(SsmParams p, int blocks_per_gro
                     }
                 }
             if constexpr (kStage) {
+                if constexpr (kPadded) odd = not_finite(d, x);
                 ulonglong2* out = s_du + ks * Sh::kRow;
 #pragma unroll
                 for (int a = 0; a < Elems::NA; ++a)
@@ -257,7 +274,7 @@ __global__ void __launch_bounds__(64) ssm_kernel(SsmParams p, int blocks_per_gro
         };
         auto put_heads = [&](int k, bool head) {
             const unsigned mask = __ballot_sync(0xffffffffu, head);
-            if (lane == 0) s_heads[k & 1] = mask;
+            if (lane == 0) s_heads[k & 1] = kPadded && odd ? mask | kOdd : mask;
         };
         auto head_at = [&](int k) {
             const long long t = (long long)k * kT + lane;
@@ -265,8 +282,8 @@ __global__ void __launch_bounds__(64) ssm_kernel(SsmParams p, int blocks_per_gro
         };
 #pragma unroll
         for (int k = 0; k < kRing - 2; ++k) fetch(k);
-        put_heads(0, head_at(0));
         any_step(-1, No{}, Yes{}, No{});  // stages tile 0
+        put_heads(0, head_at(0));
         __syncthreads();
         for (int k = 0; k < n; ++k) {  // the token warp is at tile k
             const bool head = head_at(k + 1);
@@ -308,6 +325,14 @@ __global__ void __launch_bounds__(64) ssm_kernel(SsmParams p, int blocks_per_gro
     auto own = [&](float* base, long long row) {
         return reinterpret_cast<ulonglong2*>(base) + (row * (G::NP / 4) + s * (G::SP / 4)) * p.channels + e;
     };
+    // States past `states` have A = B = C = 0 and stay 0 by themselves while d and d x
+    // are finite.  An infinity times their zeros would be NaN, and reach y: where a tile
+    // has one they are set to 0, token by token.
+    auto drop_padding = [&]() {
+        const int real = (int)p.states - lane_anew() / G::CH * G::SP;  // the lane's states before the padding
+#pragma unroll
+        for (int i = 0; i < G::P; ++i) h[i] = pack2(2 * i < real ? lo2(h[i]) : 0.0f, 2 * i + 1 < real ? hi2(h[i]) : 0.0f);
+    };
     if constexpr (!kSummary) {
         for (long long j = 0; j < at.chunk; ++j) {  // the chunks before this one
             const long long row = b * p.chunks + j;
@@ -320,6 +345,7 @@ __global__ void __launch_bounds__(64) ssm_kernel(SsmParams p, int blocks_per_gro
                 h[2 * i] = cut ? v.x : fma2(ex2_2(mul2(d, A2[2 * i])), h[2 * i], v.x);
                 h[2 * i + 1] = cut ? v.y : fma2(ex2_2(mul2(d, A2[2 * i + 1])), h[2 * i + 1], v.y);
             }
+            if constexpr (kPadded) drop_padding();
         }
     }
     const long long saves = (p.length + kTile - 1) / kTile;
@@ -331,7 +357,7 @@ __global__ void __launch_bounds__(64) ssm_kernel(SsmParams p, int blocks_per_gro
         const ulonglong2* lC = reinterpret_cast<const ulonglong2*>(s_C + (k & 1) * Sh::kStates + s * G::SP);
         float* ly = s_y + (k & 1) * Sh::kRow + c;
         const unsigned hm = s_heads[k & 1];
-        cut |= hm;
+        cut |= hm & ~kOdd;
         if (!kSummary && p.saved && k % (kTile / kT) == 0 && mine) {
             ulonglong2* sp = own(p.saved, b * saves + at.chunk * p.chunk_tiles + k / (kTile / kT));
 #pragma unroll
@@ -340,7 +366,7 @@ __global__ void __launch_bounds__(64) ssm_kernel(SsmParams p, int blocks_per_gro
         // One token ahead: the decays and inputs of token t + 1 are on their way
         // while token t is applied, so that neither the exponentials nor the
         // multipliers wait for the other.
-        auto tokens = [&](auto with_heads) {
+        auto tokens = [&](auto with_care) {  // segment starts, or states to be kept at 0
             f2 a[G::P], ub[G::P];
             auto ahead = [&](int t) {
                 const ulonglong2 du = ldu[t * G::CH];
@@ -364,12 +390,13 @@ __global__ void __launch_bounds__(64) ssm_kernel(SsmParams p, int blocks_per_gro
                     in[i] = ub[i];
                 }
                 if (t + 1 < kT) ahead(t + 1);
-                if (decltype(with_heads)::value && (hm >> t & 1u)) {
+                if (decltype(with_care)::value && (hm >> t & 1u)) {
 #pragma unroll
                     for (int i = 0; i < G::P; ++i) h[i] = 0ull;
                 }
 #pragma unroll
                 for (int i = 0; i < G::P; ++i) h[i] = fma2(now[i], h[i], in[i]);
+                if (decltype(with_care)::value && kPadded && hm >= kOdd) drop_padding();
                 if constexpr (!kSummary) {
                     f2 y0 = 0ull, y1 = 0ull;
 #pragma unroll
@@ -418,12 +445,17 @@ cudaError_t ssm_of(const SsmParams& p, const SsmPlan& plan, int* launches, cudaS
         if (e == cudaSuccess) kernel<<<(unsigned)(ncb * chunks * p.batch), 64, bytes, s>>>(p, bpg, chunks);
         return e;
     };
+    const bool padded = p.states != G::NP;
     if (p.chunks > 1) {  // nobody waits for the last chunk's summary
-        const cudaError_t e = go(ssm_kernel<T, G, kVec, true>, FwdShared<T, G, true>::kBytes, p.chunks - 1);
+        const int bytes = FwdShared<T, G, true>::kBytes;
+        const cudaError_t e = padded ? go(ssm_kernel<T, G, kVec, true, true>, bytes, p.chunks - 1)
+                                     : go(ssm_kernel<T, G, kVec, true, false>, bytes, p.chunks - 1);
         if (e != cudaSuccess) return e;
         *launches = 2;
     }
-    const cudaError_t e = go(ssm_kernel<T, G, kVec, false>, FwdShared<T, G, false>::kBytes, p.chunks);
+    const int bytes = FwdShared<T, G, false>::kBytes;
+    const cudaError_t e = padded ? go(ssm_kernel<T, G, kVec, false, true>, bytes, p.chunks)
+                                 : go(ssm_kernel<T, G, kVec, false, false>, bytes, p.chunks);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }

@@ -76,3 +76,14 @@ def test_sigmoid(lo, hi):
     # the gradient by dt: dd = 1, times the softplus's slope
     sc.selective_scan(x, z, -one, bc, bc, saved=saved)
     _within(sc.selective_scan_grad(x, x, z, -one, bc, bc, saved=saved)["dt"][:, 0], _sigmoid(v), 9)
+
+def test_ends_and_what_is_no_number():
+    inf, nan = float("inf"), float("nan")
+    v = torch.tensor([[inf, 1e38, 3.4e38, 200.0, -200.0, -3.4e38, -inf, nan]], device="cuda")
+    one, bc = _ones(8, 1), _ones(1, 1, 1)
+    y = sc.selective_scan_step(_ones(1, 8), v, -one, bc, bc, torch.zeros(1, 8, 1, device="cuda"))[0]
+    y2 = sc.selective_scan(_ones(1, 1, 8), v[:, None], -one, bc[None], bc[None])[0, 0]
+    for got in (y, y2):
+        assert got[0] == inf and torch.equal(got[1:4], v[0, 1:4]) and (got[4:7] == 0).all() and got[7].isnan()
+    y = sc.causal_conv(v[None], one)[0, 0]
+    assert y[0] == inf and torch.equal(y[1:4], v[0, 1:4]) and (y[4:6] == 0).all() and y[7].isnan()
