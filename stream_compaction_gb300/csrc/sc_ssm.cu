@@ -86,12 +86,12 @@ __global__ void __launch_bounds__(kStepNT) ssm_step_kernel(SsmParams p, unsigned
     if constexpr (kVec) {  // states a multiple of 4
         if (on) {
             const float4 av = __ldg(reinterpret_cast<const float4*>(Ap));
-            A[0] = av.x * kLog2e; A[1] = av.y * kLog2e; A[2] = av.z * kLog2e; A[3] = av.w * kLog2e;
+            A[0] = rate(av.x); A[1] = rate(av.y); A[2] = rate(av.z); A[3] = rate(av.w);
         }
     } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (live && n0 + k < p.states) A[k] = __ldg(Ap + k) * kLog2e;
+            if (live && n0 + k < p.states) A[k] = rate(__ldg(Ap + k));
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {

@@ -450,11 +450,18 @@ __device__ __forceinline__ void store_lane_of(float* p, long long states, int le
                 p[(G::CPL * c + j) * states + 4 * s + k] = j & 1 ? hi2(v[j / 2][k]) : lo2(v[j / 2][k]);
 }
 template <class G>
-__device__ __forceinline__ void to_pairs(const float (&v)[G::CPL][4], float scale, f2 (&o)[G::PC][4]) {
+__device__ __forceinline__ void to_pairs(const float (&v)[G::CPL][4], f2 (&o)[G::PC][4]) {
 #pragma unroll
     for (int q = 0; q < G::PC; ++q)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[q][k] = pack2(v[2 * q][k] * scale, v[2 * q + 1][k] * scale);
+        for (int k = 0; k < 4; ++k) o[q][k] = pack2(v[2 * q][k], v[2 * q + 1][k]);
+}
+template <class G>
+__device__ __forceinline__ void to_rates(const float (&A)[G::CPL][4], f2 (&o)[G::PC][4]) {
+#pragma unroll
+    for (int q = 0; q < G::PC; ++q)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[q][k] = pack2(rate(A[2 * q][k]), rate(A[2 * q + 1][k]));
 }
 // The lane, asked for anew: what is made of it, seldom used, is not kept in registers.
 __device__ __forceinline__ int lane_anew() {

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(32 * kBackWarps) ssm_back_summary_kernel(SsmPa
     float raw[G::CPL][4];
     f2 A2[G::PC][4], dh[G::PC][4], dsum[G::PC], bias[2];
     load_lane_of<G>(p.A + at.ch0 * p.states, p.states, left, lane, raw);
-    to_pairs<G>(raw, kLog2e, A2);
+    to_rates<G>(raw, A2);
     clear<G>(dh);
 #pragma unroll
     for (int q = 0; q < G::PC; ++q) dsum[q] = 0ull;
@@ -281,9 +281,9 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
     {
         float raw[G::CPL][4];
         load_lane_of<G>(p.A + at.ch0 * p.states, p.states, left, lane, raw);
-        to_pairs<G>(raw, kLog2e, A2);
+        to_rates<G>(raw, A2);
         load_lane_of<G>(p.dfinal ? p.dfinal + (b * p.channels + at.ch0) * p.states : nullptr, p.states, left, lane, raw);
-        to_pairs<G>(raw, 1.0f, dh);
+        to_pairs<G>(raw, dh);
     }
     for (long long j = p.runs - 1; j >= (at.chunk + 1) * (p.chunk_tiles / p.run_tiles); --j)
         fold_run<G, kPad != kNoPad>(p, A2, b, j, at.ch0, left, lane, dh);
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
         else stage(std::false_type{});
         BC.to_shared(s_all);
         f2 h0[G::PC][4];
-        to_pairs<G>(start, 1.0f, h0);
+        to_pairs<G>(start, h0);
         hold_states(0, h0);
         if (tile > tile0 && left > 0) {  // the next tile and its states on their way into the L2
             const long long t = t0 - kTile + lane % kTile;  // lanes 0 .. 15: x and dy, 16 ..: dt and z
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(32 * G::kBwdWarps) ssm_back_kernel(SsmParams p
                 float raw[G::CPL][4];
                 f2 old[G::PC][4];
                 load_lane<G>(pa, p.channels, left, lane, raw);
-                to_pairs<G>(raw, 1.0f, old);
+                to_pairs<G>(raw, old);
 #pragma unroll
                 for (int q = 0; q < G::PC; ++q)
 #pragma unroll

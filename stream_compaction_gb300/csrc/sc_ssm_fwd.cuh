@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(64) ssm_kernel(SsmParams p, int blocks_per_gro
         const float* Ap = p.A + e * p.states + n0;
         const float* hp = p.state ? p.state + (b * p.channels + e) * p.states + n0 : nullptr;
         const bool in0 = mine && n0 < p.states, in1 = mine && n0 + 1 < p.states;
-        A2[i] = pack2(in0 ? Ap[0] * kLog2e : 0.0f, in1 ? Ap[1] * kLog2e : 0.0f);
+        A2[i] = pack2(in0 ? rate(Ap[0]) : 0.0f, in1 ? rate(Ap[1]) : 0.0f);
         h[i] = kSummary || !hp ? 0ull : pack2(in0 ? hp[0] : 0.0f, in1 ? hp[1] : 0.0f);
     }
     // states of this lane in the library's own arrays: [fours of states][channels][4]
