@@ -147,9 +147,17 @@ struct Filter {
     }
 };
 
+// CTAs an SM that the forward kernel's registers leave room for, where rows are
+// aligned and not packed and the taps at most four.  16 bits: 8 (64 registers; the
+// bfloat16 training case 312 us with its gradient, 320 with 4).  float32, whose elements
+// ahead take twice the registers: 5 (94); 8 x 4096 x 4096, forward: 184 us with 5, 188
+// with 4, 192 with 6, 238 with 8, which spills.
+template <class T> constexpr int kFastCtas = sizeof(T) == 2 ? 8 : 5;
+
 // Thread: channels c .. c + 3, one run of tokens of one row.
 template <class T, int WD, bool kVec, bool kHeads>
-__global__ void __launch_bounds__(kNT, WD == 4 && kVec && !kHeads ? 8 : 4) conv_kernel(ConvParams p, int run, unsigned cblocks, unsigned runs) {
+__global__ void __launch_bounds__(kNT, WD == 4 && kVec && !kHeads ? kFastCtas<T> : 4)
+    conv_kernel(ConvParams p, int run, unsigned cblocks, unsigned runs) {
     const Place at(cblocks, runs, kCh);
     const long long c = at.c, b = at.b, left = p.channels - c;
     if (left <= 0) return;

@@ -18,3 +18,16 @@ def test_the_device_is_asked_for_its_multiprocessors():
     for name in FILES:
         assert not re.search(r"\b152(ll)?\b", code(name)), name
     assert any("seq_sms()" in code(name) for name in FILES)
+
+
+def test_the_common_convolutions_do_not_spill():
+    """Registers of the forward kernel for aligned rows of up to four taps, as the
+    assembler reports them: a bound that one element type can live with made another
+    keep its elements in memory (152 bytes a thread)."""
+    import subprocess
+    from stream_compaction_gb300 import build
+    cmd = [build.nvcc()] + build.NVCC_FLAGS + ["-Xptxas", "-v", "-c", os.path.join(CSRC, "sc_conv.cu"), "-o", os.devnull]
+    log = subprocess.run(cmd, capture_output=True, text=True, check=True).stderr
+    found = re.findall(r"Compiling entry function '(\w*conv_kernelI\w*?Li4ELb1ELb0E\w*)'.*?(\d+) bytes spill stores", log, re.S)
+    assert len(found) == 3, found
+    assert all(int(spilled) <= 16 for _, spilled in found), found
