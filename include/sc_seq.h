@@ -127,7 +127,7 @@ typedef struct {
     int64_t batch, length, channels, states, groups;
     const void *x, *dt;        /* batch x length x channels */
     int64_t x_batch, x_token, dt_batch, dt_token;
-    const float *A;            /* channels x states; an infinity acts as the largest finite value */
+    const float *A;            /* channels x states; -infinity acts as the lowest finite value */
     const void *B, *C;         /* batch x length x groups x states, a group's states contiguous */
     int64_t B_batch, B_token, B_group, C_batch, C_token, C_group;
     const float *D;            /* channels; NULL: zeros */

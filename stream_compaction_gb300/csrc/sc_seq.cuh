@@ -158,13 +158,13 @@ constexpr float kNudge = 2.4e-8f;
 __device__ __forceinline__ f2 decay_2(f2 d, f2 A2) { return ex2_2(fma2(d, A2, pack2(kNudge, kNudge))); }
 __device__ __forceinline__ float decay(float d, float A2) { return ex2(fmaf(d, A2, kNudge)); }
 
-// A, as the decays take it: times log2(e), and an infinity as the largest finite value.
-// A step then multiplies a state by 0 (or by infinity) all the same, and d = 0, which
-// fills the kernels' tiles behind a row's end, keeps it: 0 times infinity would not.
-constexpr float kMostRate = 3.4028235e38f;
+// A, as the decays take it: times log2(e), and -infinity as the lowest finite value.  A
+// step then multiplies a state by 0 all the same, and d = 0, which fills the kernels'
+// tiles behind a row's end, keeps it: 0 times infinity would not.
 __device__ __forceinline__ float rate(float A) {
-    const float v = A * kLog2e;
-    return v < -kMostRate ? -kMostRate : v > kMostRate ? kMostRate : v;  // NaN: itself
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(A * kLog2e), "f"(-3.4028235e38f));
+    return r;
 }
 
 __device__ __forceinline__ float rcp(float v) {

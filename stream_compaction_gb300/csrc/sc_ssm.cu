@@ -137,9 +137,10 @@ __global__ void __launch_bounds__(kStepNT) ssm_step_kernel(SsmParams p, unsigned
         for (int k = 0; k < 4; ++k) {
             h[r][k] = fmaf(decay(dr, A[k]), h[r][k], ur * B[r][k]);
             // (a state past the last would be infinity times 0 where d or d x is infinite)
-            sum[r] = n0 + k < p.states ? fmaf(C[r][k], h[r][k], sum[r]) : sum[r];
+            sum[r] = kVec || n0 + k < p.states ? fmaf(C[r][k], h[r][k], sum[r]) : sum[r];
         }
         if constexpr (kVec) {
+            if (!on) sum[r] = 0.0f;
             if (hp[r]) *reinterpret_cast<float4*>(hp[r]) = make_float4(h[r][0], h[r][1], h[r][2], h[r][3]);
         } else {
 #pragma unroll
