@@ -11,7 +11,9 @@
  *   embedding    out[t] = scale * weight[ids[t]]; an id outside [0, vocab)
  *                gives a row of zeros (as the histogram skips such entries)
  *                dweight[v] = scale * sum of dout[t] over the t with ids[t] == v,
- *                summed in the order of t: bitwise the same on every run
+ *                in a fixed order of parts: bitwise the same on every run of
+ *                the same ids (where the parts of a long sum are cut depends on
+ *                the other ids)
  *   convolution  pre[t,e] = bias[e] + sum_k weight[e,k] * x[t-W+1+k, e]
  *                y = pre * sigmoid(pre), or pre (silu == 0)
  *   scan         d[t,e] = softplus(dt[t,e] + dt_bias[e])  (softplus == 0: the sum)
@@ -162,6 +164,10 @@ typedef struct {
 /* Every sum over tokens, rows or channels is taken in a fixed order: bitwise
  * the same on every run. */
 sc_status sc_selective_scan_grad(const sc_ssm_desc *p, const sc_ssm_grads *g, sc_stream_t stream);
+/* Mostly partial rows of dB and dC: 0.5, 1, 4 or 32 bytes for each token and
+ * channel with up to 8, 16, 32 or 64 states (at 4 x 4096 tokens of 4096 channels
+ * 2.1 GB with 64 states).  The stream keeps it until a larger call or
+ * sc_release_stream. */
 size_t sc_selective_scan_grad_workspace_bytes(int64_t batch, int64_t length, int64_t channels, int64_t states,
                                               int64_t groups);
 

@@ -19,11 +19,12 @@
 // past its end for dx, and leaves its sums over tokens as one partial row per
 // run, which a second kernel adds in order.
 //
-// 8 x 4096 tokens, 4096 channels, width 4, SiLU, bfloat16: forward 97 us (5.5 TB/s),
-// gradient 206 (3.9 TB/s), its sums 7.  The instruction issue bounds both now (60
-// and 56 % of the slots, the rest waits for results of few warps): conversions, the
-// taps and, of the two activations, an exponential and a reciprocal per element.
-// With two channels a thread and no loads ahead: 818 us for the three, 310 so.
+// 8 x 4096 tokens, 4096 channels, width 4, SiLU, bfloat16: forward 97 us (5.5 TB/s, 81 %
+// of a copy's rate), gradient 206 (3.9 TB/s), its sums 7; float32 forward 184 (5.8
+// TB/s).  No unit is full in the gradient: it issues in 56 % of its slots with 10 warps
+// an SM (144 registers allow 12), and DRAM is a third busy: too few warps to hide one
+// another's waits.  The forward kernel issues in 60 % with 20 warps.  With two channels
+// a thread and no loads ahead: 818 us for the three, 310 so.
 #include <algorithm>
 
 #include "sc_seq.cuh"

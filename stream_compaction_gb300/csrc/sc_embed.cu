@@ -24,8 +24,11 @@
 // other.  kRun 64 or 128 leaves a CTA's one
 // frequent id to the end of the launch (94 us for all of the second case, 79 so).
 //
-// Sums are taken in the order of t in float32, so a result is the same on
-// every run, whatever the schedule (no atomics on values).
+// Sums are float32 in a fixed order, so a result is the same on every run, whatever
+// the schedule (no atomics on values): a short run in the order of t, a long one piece
+// by piece (with few columns a piece's rows in shares of their own, then the shares).
+// Pieces are cut by position in the sorted order, so the rounding of a long run also
+// depends on how many tokens smaller ids have.
 #include <algorithm>
 
 #include <cooperative_groups.h>

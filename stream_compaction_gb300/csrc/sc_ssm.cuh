@@ -493,7 +493,8 @@ __device__ __forceinline__ unsigned tile_heads(const uint8_t* row, long long t0,
     return __ballot_sync(0xffffffffu, lane < nt && row[t0 + (lane < nt ? lane : 0)] != 0);
 }
 
-// carry = decay of run j over its whole length * carry + what the run adds.
+// carry = decay of run j over its whole length * carry + what the run adds.  (One
+// exponential for the run: without the nudge that makes up for hundreds of them.)
 template <class G, bool kPadded>
 __device__ __forceinline__ void fold_run(const SsmParams& p, const f2 (&A2)[G::PC][4], long long b, long long j,
                                          long long ch0, int left, int lane, f2 (&carry)[G::PC][4]) {

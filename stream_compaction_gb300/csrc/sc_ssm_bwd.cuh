@@ -25,7 +25,7 @@
 // Per token and state 14 products and multiply-adds against 1.75 exponentials:
 // the multipliers' time, 0.43 ms at 4 x 4096 tokens, 4096 channels and 16 states
 // in bfloat16, is the nearest bound; the pass takes 1.20 ms, and the first kernel
-// (below) 0.22 more; the whole step, forward pass included, 1.86.  What keeps it
+// (below) 0.22 more; the whole step, forward pass included, 1.87.  What keeps it
 // from the bound is that an SM holds 8 warps, 2 a quarter, which issue in 40 % of
 // the clocks: 255 registers (A, dh and dA of 16 states a lane, q and h of a
 // quarter) and 28 KB of shared memory a warp.  The quarters' work takes 44 % of a

@@ -15,7 +15,7 @@
 // raw elements are copied asynchronously, several tiles ahead, so that enough
 // bytes are under way.
 //
-// 8 x 4096 tokens, 4096 channels, 16 states, float16: 757 us, where the
+// 8 x 4096 tokens, 4096 channels, 16 states, float16: 761 us, where the
 // exponentials alone take 230 (and the 1.1 GB 159): an SM's quarter issues in 57 %
 // of its clocks, 122 instructions a token and 32 channels (the token warp 78), its
 // multipliers work in 43 %, its exponentials in 35 %; the rest is what a token
