@@ -7,8 +7,8 @@ Thin Python binding over the C ABI of ``libsc_gb300.so`` (declared in
   device pointers, element counts, a raw ``cudaStream_t``);
 * tensor helpers (``scan_inclusive``, ``scan_exclusive``, ``scan_batched``,
   ``compact_if``, ``scan_hierarchical``, ``scan_host``, and from ``seq.py``
-  ``embed``, ``causal_conv``, ``selective_scan`` with their gradients and
-  single-token forms) that take torch CUDA tensors and the current torch stream.
+  ``embed``, ``causal_conv``, ``selective_scan``, ``gated_scan``, ``layer_norm``
+  and the ``expert_`` functions with their gradients and single-token forms) that take torch CUDA tensors and the current torch stream.
 
 Every step of the computation runs in the library's CUDA kernels.  There is no
 CPU fallback: if the library has not been built (``python -m
@@ -21,9 +21,11 @@ import os
 import threading
 
 from . import seq as _seq
-from .seq import (SC_BF16, SC_CONV_MAX_WIDTH, SC_F16, SC_SSM_MAX_STATES, SC_SSM_SAVE, causal_conv, causal_conv_grad,
-                  causal_conv_step, embed, embed_grad, selective_scan, selective_scan_grad, selective_scan_saved,
-                  selective_scan_step)
+from .seq import (SC_BF16, SC_CONV_MAX_WIDTH, SC_EXPERT_MAX, SC_F16, SC_GATED_SAVE, SC_SSM_MAX_STATES, SC_SSM_SAVE,
+                  ExpertOrder, causal_conv, causal_conv_grad, causal_conv_step, embed, embed_grad, expert_combine,
+                  expert_combine_grad, expert_gather, expert_gather_grad, expert_sort, gated_scan, gated_scan_grad,
+                  gated_scan_saved, gated_scan_step, layer_norm, layer_norm_grad, layer_norm_saved, selective_scan,
+                  selective_scan_grad, selective_scan_saved, selective_scan_step)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsc_gb300.so")

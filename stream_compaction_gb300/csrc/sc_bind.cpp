@@ -10,6 +10,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
 
+#include <algorithm>
 #include <optional>
 #include <string>
 #include <vector>
@@ -374,6 +375,314 @@ Tensor selective_scan_step(const Tensor& x, const Tensor& dt, const Tensor& A, c
     return y;
 }
 
+// ------------------------------------------------------------ gated scan
+sc_gated_desc gated_desc(const Tensor& x, const Tensor& gate, const std::optional<std::string>& activation, bool step) {
+    on_device(x, "x");
+    sc_gated_desc d{};
+    d.dtype = code(x, "x");
+    need(x.dim() == (step ? 2 : 3), step ? "x must have shape (batch, channels)"
+                                         : "x must have shape (batch, length, channels)");
+    like(x, "x", x.sizes(), x.scalar_type(), x.device());
+    like(gate, "gate", x.sizes(), x.scalar_type(), x.device());
+    need(!activation || *activation == "sigmoid", "activation must be 'sigmoid' or None");
+    d.sigmoid = activation.has_value();
+    d.batch = x.size(0);
+    d.length = step ? 1 : x.size(1);
+    d.channels = x.size(-1);
+    d.x = x.data_ptr();
+    d.gate = gate.data_ptr();
+    d.x_batch = x.stride(0);
+    d.gate_batch = gate.stride(0);
+    if (!step) {
+        d.x_token = x.stride(1);
+        d.gate_token = gate.stride(1);
+    }
+    return d;
+}
+const float* gated_state(const Maybe& t, const char* what, const Tensor& x) {
+    return static_cast<const float*>(whole(t, what, {x.size(0), x.size(-1)}, at::kFloat, x.device()));
+}
+Shape gated_saved_shape(const Tensor& x) {
+    return {x.size(0), (x.size(1) + SC_GATED_SAVE - 1) / SC_GATED_SAVE, x.size(2)};
+}
+Tensor gated_scan_saved(const Tensor& x) {
+    on_device(x, "x");
+    need(x.dim() == 3, "x must have shape (batch, length, channels)");
+    return make_f32(gated_saved_shape(x), x);
+}
+
+Tensor gated_scan(const Tensor& x, const Tensor& gate, const std::optional<std::string>& activation,
+                  const Maybe& heads, const Maybe& state, const Maybe& final_state, const Maybe& saved,
+                  const Maybe& out) {
+    sc_gated_desc d = gated_desc(x, gate, activation, false);
+    d.heads = heads_of(heads, x);
+    d.state = gated_state(state, "state", x);
+    float* fs = const_cast<float*>(gated_state(final_state, "final_state", x));
+    float* sv = static_cast<float*>(whole(saved, "saved", gated_saved_shape(x), at::kFloat, x.device()));
+    Tensor y = out_like(out, x);
+    check(sc_gated_scan(&d, y.data_ptr(), y.stride(0), y.stride(1), fs, sv, stream()), "sc_gated_scan");
+    written(final_state);
+    written(saved);
+    written(out);
+    return y;
+}
+
+py::dict gated_scan_grad(const Tensor& dy, const Tensor& x, const Tensor& gate,
+                         const std::optional<std::string>& activation, const Maybe& heads, const Maybe& state,
+                         const Maybe& saved, const Maybe& dfinal_state) {
+    sc_gated_desc d = gated_desc(x, gate, activation, false);
+    d.heads = heads_of(heads, x);
+    d.state = gated_state(state, "state", x);
+    like(dy, "dy", x.sizes(), x.scalar_type(), x.device());
+    need(saved.has_value(), "saved: the buffer that gated_scan filled is needed");
+    const float* sv = static_cast<const float*>(whole(saved, "saved", gated_saved_shape(x), at::kFloat, x.device()));
+    const float* df = gated_state(dfinal_state, "dfinal_state", x);
+    Tensor dx = make(x.sizes(), x), dg = make(x.sizes(), x), ds;
+    if (state) ds = make_f32(state->sizes(), x);
+    check(sc_gated_scan_grad(&d, dy.data_ptr(), dy.stride(0), dy.stride(1), sv, df, dx.data_ptr(), dg.data_ptr(),
+                             state ? ds.data_ptr<float>() : nullptr, stream()),
+          "sc_gated_scan_grad");
+    py::dict g;
+    g["x"] = dx;
+    g["gate"] = dg;
+    if (state) g["state"] = ds;
+    return g;
+}
+
+Tensor gated_scan_step(const Tensor& x, const Tensor& gate, const Tensor& state,
+                       const std::optional<std::string>& activation, const Maybe& slots, const Maybe& out) {
+    const sc_gated_desc d = gated_desc(x, gate, activation, true);
+    need(state.dim() == 2, "state must have shape (rows, channels)");
+    void* pool = whole(state, "state", {state.size(0), d.channels}, at::kFloat, x.device());
+    const int32_t* sl = slots_of(slots, x);
+    Tensor y = out_like(out, x);
+    check(sc_gated_scan_step(&d, static_cast<float*>(pool), state.size(0), sl, y.data_ptr(), y.stride(0), stream()),
+          "sc_gated_scan_step");
+    written(state);
+    written(out);
+    return y;
+}
+
+// ------------------------------------------------------------------ norm
+// A tensor of any number of dimensions as batch x length rows: the dimensions before
+// `cut` are the batch, those from there to the last but one the length, each run of
+// them with one stride.
+struct Rows {
+    int64_t batch = 1, length = 1, sb = 0, st = 0;
+};
+Rows rows_of(const Tensor& t, const char* what, int64_t cut) {
+    Rows r;
+    auto run = [&](int64_t from, int64_t to, int64_t& n, int64_t& stride) {
+        for (int64_t i = to - 1; i >= from; --i) {
+            if (t.size(i) == 1) continue;
+            if (n == 1) stride = t.stride(i);
+            else need(t.stride(i) == n * stride, what, ": its leading dimensions have more than two strides");
+            n *= t.size(i);
+        }
+    };
+    run(0, cut, r.batch, r.sb);
+    run(cut, t.dim() - 1, r.length, r.st);
+    if (t.numel() == 0) r = Rows{0, 0, 0, 0};
+    return r;
+}
+// The first dimension from which on a tensor's rows have one stride.
+int64_t cut_of(const Tensor& t) {
+    int64_t n = 1, stride = 0, i = t.dim() - 2;
+    for (; i >= 0; --i) {
+        if (t.size(i) == 1) continue;
+        if (n == 1) stride = t.stride(i);
+        else if (t.stride(i) != n * stride) break;
+        n *= t.size(i);
+    }
+    return i + 1;
+}
+
+sc_norm_desc norm_desc(const Tensor& x, const Maybe& weight, const Maybe& bias, bool rms) {
+    on_device(x, "x");
+    sc_norm_desc d{};
+    d.dtype = d.wtype = code(x, "x");
+    need(x.dim() >= 1, "x must have shape (..., channels)");
+    like(x, "x", x.sizes(), x.scalar_type(), x.device());
+    d.rms = rms;
+    d.channels = x.size(-1);
+    d.x = x.data_ptr();
+    const Maybe& one = weight ? weight : bias;
+    if (one) {
+        const auto type = one->scalar_type();
+        need(type == x.scalar_type() || type == at::kFloat, "weight and bias must be of x's type or float32");
+        d.wtype = code(*one, "weight");
+        d.weight = whole(weight, "weight", {d.channels}, type, x.device());
+        d.bias = whole(bias, "bias", {d.channels}, type, x.device());
+    }
+    return d;
+}
+Shape norm_saved_shape(const Tensor& x) {
+    Shape s = x.sizes().vec();
+    s.back() = 2;
+    return s;
+}
+Tensor layer_norm_saved(const Tensor& x) {
+    on_device(x, "x");
+    need(x.dim() >= 1, "x must have shape (..., channels)");
+    return make_f32(norm_saved_shape(x), x);
+}
+
+py::object layer_norm(const Tensor& x, const Maybe& weight, const Maybe& bias, double eps, bool rms,
+                      const Maybe& residual, const Maybe& saved, const Maybe& out) {
+    sc_norm_desc d = norm_desc(x, weight, bias, rms);
+    need(eps >= 0, "eps must not be negative");
+    d.eps = (float)eps;
+    float* sv = static_cast<float*>(whole(saved, "saved", norm_saved_shape(x), at::kFloat, x.device()));
+    Tensor y = out_like(out, x), sum;
+    int64_t cut = std::max(cut_of(x), cut_of(y));
+    if (residual) {
+        like(*residual, "residual", x.sizes(), x.scalar_type(), x.device());
+        sum = at::empty(x.sizes(), x.options());
+        cut = std::max(cut, cut_of(*residual));
+    }
+    const Rows rx = rows_of(x, "x", cut), ry = rows_of(y, "out", cut);
+    d.batch = rx.batch;
+    d.length = rx.length;
+    d.x_batch = rx.sb;
+    d.x_token = rx.st;
+    Rows rs;
+    if (residual) {
+        const Rows rr = rows_of(*residual, "residual", cut);
+        d.residual = residual->data_ptr();
+        d.residual_batch = rr.sb;
+        d.residual_token = rr.st;
+        rs = rows_of(sum, "sum", cut);
+    }
+    check(sc_layer_norm(&d, y.data_ptr(), ry.sb, ry.st, residual ? sum.data_ptr() : nullptr, rs.sb, rs.st, sv, stream()),
+          "sc_layer_norm");
+    written(saved);
+    written(out);
+    if (!residual) return py::cast(y);
+    return py::make_tuple(y, sum);
+}
+
+py::dict layer_norm_grad(const Tensor& dy, const Tensor& x, const Maybe& weight, const Maybe& bias, bool rms,
+                         const Maybe& saved, const Maybe& dsum, bool by_weight, bool by_bias) {
+    sc_norm_desc d = norm_desc(x, weight, bias, rms);
+    like(dy, "dy", x.sizes(), x.scalar_type(), x.device());
+    need(saved.has_value(), "saved: the buffer that layer_norm filled is needed");
+    const float* sv = static_cast<const float*>(whole(saved, "saved", norm_saved_shape(x), at::kFloat, x.device()));
+    int64_t cut = std::max(cut_of(x), cut_of(dy));
+    if (dsum) {
+        like(*dsum, "dsum", x.sizes(), x.scalar_type(), x.device());
+        cut = std::max(cut, cut_of(*dsum));
+    }
+    const Rows rx = rows_of(x, "x", cut), re = rows_of(dy, "dy", cut);
+    d.batch = rx.batch;
+    d.length = rx.length;
+    d.x_batch = rx.sb;
+    d.x_token = rx.st;
+    const Rows rs = dsum ? rows_of(*dsum, "dsum", cut) : Rows{};
+    Tensor dx = make(x.sizes(), x), dw, db;
+    by_weight = by_weight && weight.has_value();
+    by_bias = by_bias && bias.has_value();
+    if (by_weight) dw = make_f32({d.channels}, x);
+    if (by_bias) db = make_f32({d.channels}, x);
+    check(sc_layer_norm_grad(&d, dy.data_ptr(), re.sb, re.st, dsum ? dsum->data_ptr() : nullptr, rs.sb, rs.st, sv,
+                             dx.data_ptr(), by_weight ? dw.data_ptr<float>() : nullptr,
+                             by_bias ? db.data_ptr<float>() : nullptr, stream()),
+          "sc_layer_norm_grad");
+    py::dict g;
+    g["x"] = dx;
+    if (by_weight) g["weight"] = dw;
+    if (by_bias) g["bias"] = db;
+    return g;
+}
+
+// --------------------------------------------------------------- experts
+py::tuple expert_sort(const Tensor& experts, int64_t n_experts) {
+    on_device(experts, "experts");
+    need(experts.scalar_type() == at::kInt || experts.scalar_type() == at::kLong, "experts must be int32 or int64");
+    need(experts.dim() == 2, "experts must have shape (tokens, choices)");
+    need(experts.is_contiguous(), "experts must be contiguous");
+    need(n_experts >= 1 && n_experts <= SC_EXPERT_MAX, "the number of experts must be 1 to 1024");
+    const auto i32 = experts.options().dtype(at::kInt);
+    Tensor offsets = at::empty({n_experts + 1}, experts.options().dtype(at::kLong));
+    Tensor order = at::empty({experts.numel()}, i32), place = at::empty(experts.sizes(), i32);
+    check(sc_expert_sort(experts.data_ptr(), experts.scalar_type() == at::kLong, experts.numel(), n_experts,
+                         order.data_ptr<int32_t>(), place.data_ptr<int32_t>(), offsets.data_ptr<int64_t>(), stream()),
+          "sc_expert_sort");
+    return py::make_tuple(offsets, order, place);
+}
+
+// The entries' side of a call, from what expert_sort returned, for rows like `rows`.
+sc_expert_desc expert_desc(const Tensor& offsets, const Tensor& place, const Tensor& rows, const char* what) {
+    on_device(rows, what);
+    sc_expert_desc d{};
+    d.dtype = d.wtype = code(rows, what);
+    need(rows.dim() == 2, what, " must have two dimensions");
+    like(rows, what, rows.sizes(), rows.scalar_type(), rows.device());
+    need(place.dim() == 2 && offsets.dim() == 1 && offsets.size(0) >= 2, "the order must be what expert_sort returned");
+    d.tokens = place.size(0);
+    d.choices = place.size(1);
+    d.dim = rows.size(1);
+    d.experts = offsets.size(0) - 1;
+    d.place = static_cast<const int32_t*>(whole(place, "order.place", place.sizes(), at::kInt, rows.device()));
+    d.offsets = static_cast<const int64_t*>(whole(offsets, "order.offsets", offsets.sizes(), at::kLong, rows.device()));
+    return d;
+}
+void expert_weights(sc_expert_desc& d, const Maybe& weights, const Tensor& rows) {
+    if (!weights) return;
+    need(weights->scalar_type() == rows.scalar_type() || weights->scalar_type() == at::kFloat,
+         "weights must be of the rows' type or float32");
+    d.wtype = code(*weights, "weights");
+    d.weights = whole(weights, "weights", {d.tokens, d.choices}, weights->scalar_type(), rows.device());
+}
+int64_t ld(const Tensor& t) { return t.size(0) > 1 ? t.stride(0) : t.size(1); }
+Tensor rows_out(const Maybe& out, int64_t rows, const Tensor& like_this) {
+    const int64_t shape[] = {rows, like_this.size(1)};
+    if (!out) return make(shape, like_this);
+    return like(*out, "out", shape, like_this.scalar_type(), like_this.device());
+}
+
+Tensor expert_gather(const Tensor& x, const Tensor& offsets, const Tensor& place, const Maybe& out) {
+    const sc_expert_desc d = expert_desc(offsets, place, x, "x");
+    need(x.size(0) == d.tokens, "x must have a row for each token");
+    Tensor rows = rows_out(out, d.tokens * d.choices, x);
+    check(sc_expert_gather(&d, x.data_ptr(), ld(x), rows.data_ptr(), ld(rows), stream()), "sc_expert_gather");
+    written(out);
+    return rows;
+}
+Tensor expert_gather_grad(const Tensor& drows, const Tensor& offsets, const Tensor& place, const Maybe& out) {
+    const sc_expert_desc d = expert_desc(offsets, place, drows, "drows");
+    need(drows.size(0) == d.tokens * d.choices, "drows must have a row for each entry");
+    Tensor dx = rows_out(out, d.tokens, drows);
+    check(sc_expert_gather_grad(&d, drows.data_ptr(), ld(drows), dx.data_ptr(), ld(dx), stream()), "sc_expert_gather_grad");
+    written(out);
+    return dx;
+}
+Tensor expert_combine(const Tensor& rows, const Tensor& offsets, const Tensor& place, const Maybe& weights,
+                      const Maybe& out) {
+    sc_expert_desc d = expert_desc(offsets, place, rows, "rows");
+    need(rows.size(0) == d.tokens * d.choices, "rows must have a row for each entry");
+    expert_weights(d, weights, rows);
+    Tensor y = rows_out(out, d.tokens, rows);
+    check(sc_expert_combine(&d, rows.data_ptr(), ld(rows), y.data_ptr(), ld(y), stream()), "sc_expert_combine");
+    written(out);
+    return y;
+}
+py::dict expert_combine_grad(const Tensor& dout, const Tensor& rows, const Tensor& offsets, const Tensor& place,
+                             const Maybe& weights) {
+    sc_expert_desc d = expert_desc(offsets, place, rows, "rows");
+    need(rows.size(0) == d.tokens * d.choices, "rows must have a row for each entry");
+    like(dout, "dout", {d.tokens, d.dim}, rows.scalar_type(), rows.device());
+    expert_weights(d, weights, rows);
+    Tensor dr = make(rows.sizes(), rows), dw;
+    if (weights) dw = at::empty(weights->sizes(), weights->options());
+    check(sc_expert_combine_grad(&d, dout.data_ptr(), ld(dout), rows.data_ptr(), ld(rows), dr.data_ptr(), ld(dr),
+                                 weights ? dw.data_ptr() : nullptr, stream()),
+          "sc_expert_combine_grad");
+    py::dict g;
+    g["y"] = dr;
+    if (weights) g["weights"] = dw;
+    return g;
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_seqbind, m) {
@@ -386,4 +695,16 @@ PYBIND11_MODULE(_seqbind, m) {
     m.def("selective_scan", &selective_scan);
     m.def("selective_scan_grad", &selective_scan_grad);
     m.def("selective_scan_step", &selective_scan_step);
+    m.def("gated_scan", &gated_scan);
+    m.def("gated_scan_saved", &gated_scan_saved);
+    m.def("gated_scan_grad", &gated_scan_grad);
+    m.def("gated_scan_step", &gated_scan_step);
+    m.def("layer_norm", &layer_norm);
+    m.def("layer_norm_saved", &layer_norm_saved);
+    m.def("layer_norm_grad", &layer_norm_grad);
+    m.def("expert_sort", &expert_sort);
+    m.def("expert_gather", &expert_gather);
+    m.def("expert_gather_grad", &expert_gather_grad);
+    m.def("expert_combine", &expert_combine);
+    m.def("expert_combine_grad", &expert_combine_grad);
 }

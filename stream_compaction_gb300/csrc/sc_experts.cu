@@ -1,0 +1,411 @@
+// Tokens to their experts and back: the stable sort of the entries (token, choice) by
+// expert, rows moved into that order and summed back with weights, and the gradients.
+//
+// The sort is one counting pass, since there is one digit: the expert.  One cluster of
+// up to 8 CTAs, without scratch memory:
+//   count   a warp counts its run of consecutive entries by expert (shared memory);
+//   scan    per expert over the CTA's warps, over the CTAs (distributed shared
+//           memory), then over the experts;
+//   place   a warp goes through its run again, 32 entries at a time: an entry's row is
+//           its expert's start + those before it in other warps and rounds + the lanes
+//           below with the same expert.
+// Entries of no expert are one more bin behind the others, so order and place are
+// permutations and every row of an output has exactly one writer.
+//
+// The rows: bytes alone.  All four kernels go by tokens, through place: a token's row
+// is read (or written) once, and its entries' rows wherever they lie; 16 bytes a lane,
+// up to kAhead entries under way.  No atomics; a token's sum goes in the order of its
+// choices.
+#include <algorithm>
+
+#include <cooperative_groups.h>
+
+#include "sc_seq.cuh"
+#include "sc_seq_launch.h"
+
+namespace scg {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+// ------------------------------------------------------------------ sort
+constexpr int kSortMaxWarps = 32, kSortMaxCtas = 8;
+constexpr int kRounds = 4;  // of 32 entries, loaded together
+constexpr int kMaxBins = SC_EXPERT_MAX + 1;
+
+struct SortParams {
+    const void* ids;
+    int ids64, experts;
+    long long entries, run;  // of a warp, a multiple of 32
+    int32_t *order, *place;
+    int64_t* offsets;
+};
+
+__device__ __forceinline__ int bin_of(const SortParams& p, long long i) {
+    const long long id = p.ids64 ? __ldg(static_cast<const long long*>(p.ids) + i)
+                                 : (long long)__ldg(static_cast<const int*>(p.ids) + i);
+    return id >= 0 && id < p.experts ? (int)id : p.experts;
+}
+
+// Shared memory: [warps][bins] counts, then starts.
+__global__ void __launch_bounds__(32 * kSortMaxWarps) expert_sort_kernel(SortParams p) {
+    extern __shared__ uint32_t s_count[];
+    __shared__ uint32_t s_total[kMaxBins], s_before[kMaxBins], s_all[kMaxBins], s_warp[kSortMaxWarps];
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+    const int threads = blockDim.x, warps = threads / 32, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int bins = p.experts + 1;
+    uint32_t* mine = s_count + warp * bins;
+    for (int d = lane; d < bins; d += 32) mine[d] = 0u;
+    __syncwarp();
+    const long long first = ((long long)rank * warps + warp) * p.run, last = min(p.entries, first + p.run);
+    for (long long i0 = first; i0 < last; i0 += 32 * kRounds) {
+        int d[kRounds];
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const long long i = i0 + r * 32 + lane;
+            d[r] = i < last ? bin_of(p, i) : -1;
+        }
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r)
+            if (d[r] >= 0) atomicAdd(&mine[d[r]], 1u);
+    }
+    __syncthreads();
+    // per bin: the entries of earlier warps, and the CTA's
+    for (int d = tid; d < bins; d += threads) {
+        uint32_t sum = 0;
+        for (int w0 = 0; w0 < warps; w0 += 8) {
+            uint32_t c[8];
+#pragma unroll
+            for (int w = 0; w < 8; ++w) c[w] = w0 + w < warps ? s_count[(w0 + w) * bins + d] : 0u;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                if (w0 + w < warps) s_count[(w0 + w) * bins + d] = sum;
+                sum += c[w];
+            }
+        }
+        s_total[d] = sum;
+    }
+    cluster.sync();
+    // per bin: the entries in earlier CTAs, and in all
+    for (int d = tid; d < bins; d += threads) {
+        uint32_t before = 0, all = 0;
+        for (int r = 0; r < ranks; ++r) {
+            const uint32_t c = *cluster.map_shared_rank(&s_total[d], r);
+            if (r < rank) before += c;
+            all += c;
+        }
+        s_before[d] = before;
+        s_all[d] = all;
+    }
+    cluster.sync();  // nobody reads totals any more
+    // a thread's bins, side by side, over the threads
+    const int per = (bins + threads - 1) / threads, d0 = min(bins, tid * per), d1 = min(bins, d0 + per);
+    uint32_t sum = 0;
+    for (int d = d0; d < d1; ++d) sum += s_all[d];
+    uint32_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    uint32_t start = incl - sum;
+    for (int w = 0; w < warp; ++w) start += s_warp[w];
+    for (int d = d0; d < d1; ++d) {
+        s_total[d] = start + s_before[d];
+        if (rank == 0) p.offsets[d] = start;
+        start += s_all[d];
+    }
+    __syncthreads();
+    for (int d = lane; d < bins; d += 32) mine[d] += s_total[d];
+    __syncwarp();
+    for (long long i0 = first; i0 < last; i0 += 32 * kRounds) {
+        int d[kRounds];
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const long long i = i0 + r * 32 + lane;
+            d[r] = i < last ? bin_of(p, i) : -1;
+        }
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const uint32_t same = __match_any_sync(0xffffffffu, d[r]);
+            const bool live = d[r] >= 0;
+            const uint32_t begin = live ? mine[d[r]] : 0u;
+            __syncwarp();
+            if (live) {
+                const uint32_t row = begin + __popc(same & ((1u << lane) - 1u));
+                const long long i = i0 + r * 32 + lane;
+                p.place[i] = (int32_t)row;
+                p.order[row] = (int32_t)i;
+                if (lane == __ffs(same) - 1) mine[d[r]] = begin + __popc(same);
+            }
+            __syncwarp();
+        }
+    }
+}
+
+// ------------------------------------------------------------------ rows
+constexpr int kNT = 256, kAhead = 4;
+
+// A lane's elements of a row: 16 bytes, or one element where rows are not aligned.
+template <class T, bool kVec>
+struct Part {
+    static constexpr int W = kVec ? 16 / (int)sizeof(T) : 1;
+    uint4 v;
+    T e;
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (kVec) v = __ldg(reinterpret_cast<const uint4*>(p));
+        else e = __ldg(p);
+    }
+    __device__ __forceinline__ void store(T* p) const {
+        if constexpr (kVec) *reinterpret_cast<uint4*>(p) = v;
+        else *p = e;
+    }
+    __device__ __forceinline__ void zero() {
+        v = make_uint4(0u, 0u, 0u, 0u);
+        e = from_f32<T>(0.0f);
+    }
+    __device__ __forceinline__ void get(float (&f)[W]) const {
+        if constexpr (kVec) {
+            Vec<T, W> r;
+            memcpy(r.w, &v, 16);
+#pragma unroll
+            for (int i = 0; i < W; ++i) f[i] = r.get(i);
+        } else {
+            f[0] = to_f32(e);
+        }
+    }
+    __device__ __forceinline__ void set(const float (&f)[W]) {
+        if constexpr (kVec) {
+            Vec<T, W> r;
+            r.set(f);
+            memcpy(&v, r.w, 16);
+        } else {
+            e = from_f32<T>(f[0]);
+        }
+    }
+};
+
+// `lanes` threads a token, the token's group within the CTA.
+struct Where {
+    long long token;
+    int lane;
+};
+__device__ __forceinline__ Where where(int lanes) {
+    const int group = threadIdx.x / lanes;
+    return {(long long)blockIdx.x * (kNT / lanes) + group, (int)threadIdx.x - group * lanes};
+}
+// Entries that have an expert; their rows come first.
+__device__ __forceinline__ long long kept_of(const ExpertParams& p) {
+    return min((long long)__ldg(reinterpret_cast<const long long*>(p.kept)), p.entries);
+}
+template <class T>
+__device__ __forceinline__ float weight_of(const ExpertParams& p, long long entry) {
+    if (!p.weights) return 1.0f;
+    return p.weights_f32 ? __ldg(static_cast<const float*>(p.weights) + entry) : to_f32(__ldg(static_cast<const T*>(p.weights) + entry));
+}
+
+template <class T, bool kVec>
+__global__ void __launch_bounds__(kNT) expert_gather_kernel(ExpertParams p, int lanes) {
+    const Where at = where(lanes);
+    if (at.token >= p.tokens) return;
+    const long long kept = kept_of(p);
+    const T* x = static_cast<const T*>(p.in) + at.token * p.ld_in;
+    const int32_t* place = p.place + at.token * p.choices;
+    constexpr int W = Part<T, kVec>::W;
+    for (long long c = (long long)at.lane * W; c < p.dim; c += lanes * W) {
+        Part<T, kVec> v, none;
+        v.load(x + c);
+        none.zero();
+        for (long long j = 0; j < p.choices; ++j) {
+            const long long row = __ldg(place + j);
+            if (row < 0 || row >= p.entries) continue;
+            (row < kept ? v : none).store(static_cast<T*>(p.out) + row * p.ld_out + c);
+        }
+    }
+}
+
+// out[t] = sum over j of weights[t,j] rows[place[t,j]]
+template <class T, bool kVec>
+__global__ void __launch_bounds__(kNT) expert_combine_kernel(ExpertParams p, int lanes) {
+    const Where at = where(lanes);
+    if (at.token >= p.tokens) return;
+    const long long kept = kept_of(p);
+    const long long entry = at.token * p.choices;
+    const T* rows = static_cast<const T*>(p.in);
+    constexpr int W = Part<T, kVec>::W;
+    for (long long c = (long long)at.lane * W; c < p.dim; c += lanes * W) {
+        float sum[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) sum[i] = 0.0f;
+        for (long long j0 = 0; j0 < p.choices; j0 += kAhead) {
+            Part<T, kVec> v[kAhead];
+            bool live[kAhead];
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) {
+                const long long row = j0 + a < p.choices ? __ldg(p.place + entry + j0 + a) : -1;
+                live[a] = row >= 0 && row < kept;
+                if (live[a]) v[a].load(rows + row * p.ld_in + c);
+            }
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) {
+                if (!live[a]) continue;
+                const float w = weight_of<T>(p, entry + j0 + a);
+                float f[W];
+                v[a].get(f);
+#pragma unroll
+                for (int i = 0; i < W; ++i) sum[i] = fmaf(w, f[i], sum[i]);
+            }
+        }
+        Part<T, kVec> o;
+        o.set(sum);
+        o.store(static_cast<T*>(p.out) + at.token * p.ld_out + c);
+    }
+}
+
+// drows[place[t,j]] = weights[t,j] dout[t];  dweights[t,j] = dout[t] . rows[place[t,j]]
+template <class T, bool kVec>
+__global__ void __launch_bounds__(kNT) expert_combine_grad_kernel(ExpertParams p, int lanes) {
+    __shared__ float s_dot[kNT / 32][kAhead];
+    const Where at = where(lanes);
+    const bool here = at.token < p.tokens;  // all stay for the sums over threads
+    const long long kept = kept_of(p), entry = (here ? at.token : 0) * p.choices;
+    const T* dout = static_cast<const T*>(p.in) + (here ? at.token : 0) * p.ld_in;
+    const T* rows = static_cast<const T*>(p.rows);
+    T* drows = static_cast<T*>(p.out);
+    constexpr int W = Part<T, kVec>::W;
+    for (long long j0 = 0; j0 < p.choices; j0 += kAhead) {
+        long long row[kAhead];
+        float w[kAhead], dot[kAhead];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            row[a] = here && j0 + a < p.choices ? __ldg(p.place + entry + j0 + a) : -1;
+            if (row[a] >= p.entries) row[a] = -1;
+            w[a] = row[a] >= 0 && row[a] < kept ? weight_of<T>(p, entry + j0 + a) : 0.0f;
+            dot[a] = 0.0f;
+        }
+        for (long long c = (long long)at.lane * W; here && c < p.dim; c += lanes * W) {
+            Part<T, kVec> g, v[kAhead];
+            g.load(dout + c);
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a)
+                if (rows && row[a] >= 0 && row[a] < kept) v[a].load(rows + row[a] * p.ld_rows + c);
+            float d[W];
+            g.get(d);
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) {
+                if (row[a] < 0) continue;
+                const bool live = row[a] < kept;
+                float f[W];
+                if (rows && live) {
+                    v[a].get(f);
+#pragma unroll
+                    for (int i = 0; i < W; ++i) dot[a] = fmaf(d[i], f[i], dot[a]);
+                }
+                Part<T, kVec> o;
+#pragma unroll
+                for (int i = 0; i < W; ++i) f[i] = w[a] * d[i];
+                o.set(f);
+                if (!live) o.zero();
+                o.store(drows + row[a] * p.ld_out + c);
+            }
+        }
+        if (!p.dweights) continue;
+        for (int o = 1; o < min(lanes, 32); o <<= 1)
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) dot[a] += __shfl_xor_sync(0xffffffffu, dot[a], o);
+        if (lanes > 32) {
+            __syncthreads();  // the sums of the choices before are read
+            if (threadIdx.x % 32 == 0) {
+#pragma unroll
+                for (int a = 0; a < kAhead; ++a) s_dot[threadIdx.x / 32][a] = dot[a];
+            }
+            __syncthreads();
+        }
+        if (here && at.lane < kAhead && j0 + at.lane < p.choices) {
+            float v = 0.0f;
+            if (lanes > 32) {
+                const int w0 = ((int)threadIdx.x - at.lane) / 32;
+                for (int i = 0; i < lanes / 32; ++i) v += s_dot[w0 + i][at.lane];
+            } else {
+#pragma unroll
+                for (int a = 0; a < kAhead; ++a)
+                    if (a == at.lane) v = dot[a];
+            }
+            const long long e = entry + j0 + at.lane;
+            if (p.weights_f32) static_cast<float*>(p.dweights)[e] = v;
+            else static_cast<T*>(p.dweights)[e] = from_f32<T>(v);
+        }
+    }
+}
+
+// Threads a token: one or two vectors each, up to a whole CTA.
+template <class T, bool kVec>
+int lanes_of(long long dim) {
+    const long long n = (dim + Part<T, kVec>::W - 1) / Part<T, kVec>::W;
+    int lanes = 8;
+    while (lanes < kNT && lanes < n) lanes *= 2;
+    return lanes;
+}
+enum { kGather, kCombine, kCombineGrad };
+template <class T, bool kVec>
+cudaError_t rows_as(int what, const ExpertParams& p, cudaStream_t s) {
+    const int lanes = lanes_of<T, kVec>(p.dim);
+    const unsigned grid = (unsigned)((p.tokens + kNT / lanes - 1) / (kNT / lanes));
+    if (what == kGather) expert_gather_kernel<T, kVec><<<grid, kNT, 0, s>>>(p, lanes);
+    else if (what == kCombine) expert_combine_kernel<T, kVec><<<grid, kNT, 0, s>>>(p, lanes);
+    else expert_combine_grad_kernel<T, kVec><<<grid, kNT, 0, s>>>(p, lanes);
+    count_launches(1);
+    return cudaGetLastError();
+}
+template <class T>
+cudaError_t rows_of(int what, const ExpertParams& p, cudaStream_t s) {
+    return p.vec ? rows_as<T, true>(what, p, s) : rows_as<T, false>(what, p, s);
+}
+cudaError_t rows(int dtype, int what, const ExpertParams& p, cudaStream_t s) {
+    return dtype == SC_F32 ? rows_of<float>(what, p, s) : dtype == SC_F16 ? rows_of<f16>(what, p, s) : rows_of<bf16>(what, p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_expert_sort(const void* ids, int ids64, long long entries, int experts, int32_t* order, int32_t* place,
+                               int64_t* offsets, cudaStream_t s) {
+    // a warp per 32 entries up to 8 CTAs of 32 warps, then longer runs
+    const long long least = (entries + 31) / 32;
+    int ctas = 1;
+    while (ctas < kSortMaxCtas && (long long)ctas * kSortMaxWarps < least) ctas *= 2;
+    // (a thread has two bins at most where a CTA can have as many threads)
+    const int warps = (int)std::clamp<long long>(std::max<long long>((least + ctas - 1) / ctas, experts / 64 + 1), 1, kSortMaxWarps);
+    SortParams p{ids, ids64, experts, entries, 0, order, place, offsets};
+    p.run = ((entries + (long long)ctas * warps - 1) / ((long long)ctas * warps) + 31) / 32 * 32;
+    const size_t bytes = (size_t)warps * (experts + 1) * sizeof(uint32_t);
+    // the limit is one per device: always the whole, whatever this call needs
+    cudaError_t e = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSortMaxWarps * kMaxBins * (int)sizeof(uint32_t));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(32 * warps);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute a{};
+    a.id = cudaLaunchAttributeClusterDimension;
+    a.val.clusterDim.x = (unsigned)ctas;
+    a.val.clusterDim.y = a.val.clusterDim.z = 1;
+    cfg.attrs = &a;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, expert_sort_kernel, p);
+    count_launches(1);
+    return e;
+}
+
+cudaError_t launch_expert_gather(int dtype, const ExpertParams& p, cudaStream_t s) { return rows(dtype, kGather, p, s); }
+cudaError_t launch_expert_combine(int dtype, const ExpertParams& p, cudaStream_t s) { return rows(dtype, kCombine, p, s); }
+cudaError_t launch_expert_combine_grad(int dtype, const ExpertParams& p, cudaStream_t s) {
+    return rows(dtype, kCombineGrad, p, s);
+}
+
+}  // namespace scg

@@ -123,4 +123,82 @@ cudaError_t launch_ssm(int dtype, const SsmParams& p, const SsmPlan& plan, cudaS
 cudaError_t launch_ssm_grad(int dtype, const SsmParams& p, const SsmPlan& plan, cudaStream_t s);
 cudaError_t launch_ssm_step(int dtype, const SsmParams& p, cudaStream_t s);
 
+// ---------------------------------------------------------- gated scan
+struct GatedParams {
+    int sigmoid;
+    long long batch, length, channels;
+    const void *x, *gate;
+    long long x_batch, x_token, gate_batch, gate_token;
+    const uint8_t* heads;
+    const float* state;
+    void* y;
+    long long y_batch, y_token;
+    float* final_state;
+    float* saved;
+    int pairs;  // elements two by two: aligned, channels even
+    // gradient
+    const void* dy;
+    long long dy_batch, dy_token;
+    const float* dfinal;
+    void *dx, *dgate;
+    float* dstate;
+    // step
+    float* pool;
+    long long pool_rows;
+    const int32_t* slots;
+    int vec;  // four channels at a time
+};
+cudaError_t launch_gated(int dtype, const GatedParams& p, cudaStream_t s);
+cudaError_t launch_gated_grad(int dtype, const GatedParams& p, cudaStream_t s);
+cudaError_t launch_gated_step(int dtype, const GatedParams& p, cudaStream_t s);
+
+// ---------------------------------------------------------------- norm
+struct NormParams {
+    int rms, params_f32, vec;
+    float eps;
+    uint32_t rows, length;  // rows = batch * length
+    long long channels;
+    const void *x, *residual, *weight, *bias;
+    long long x_batch, x_token, residual_batch, residual_token;
+    void *y, *sum;
+    long long y_batch, y_token, sum_batch, sum_token;
+    float* saved;
+    // gradient
+    const void *dy, *dsum;
+    long long dy_batch, dy_token, dsum_batch, dsum_token;
+    void* dx;
+    float *dweight, *dbias;
+    float* partials;  // [parts][2][channels]: dweight, dbias
+    long long parts;
+};
+cudaError_t launch_norm(int dtype, const NormParams& p, cudaStream_t s);
+struct NormGradPlan {
+    long long parts;
+    size_t partials, total;  // offset, then the size
+};
+NormGradPlan norm_grad_plan(int dtype, long long rows, long long channels);
+cudaError_t launch_norm_grad(int dtype, const NormParams& p, cudaStream_t s);
+
+// -------------------------------------------------------------- experts
+cudaError_t launch_expert_sort(const void* ids, int ids64, long long entries, int experts, int32_t* order, int32_t* place,
+                               int64_t* offsets, cudaStream_t s);
+struct ExpertParams {
+    long long tokens, choices, dim, entries;
+    const int32_t* place;
+    const int64_t* kept;  // offsets + experts
+    const void* weights;
+    int weights_f32, vec;
+    const void* in;  // rows of tokens, or of entries
+    long long ld_in;
+    void* out;
+    long long ld_out;
+    // combine's gradient
+    const void* rows;
+    long long ld_rows;
+    void* dweights;
+};
+cudaError_t launch_expert_gather(int dtype, const ExpertParams& p, cudaStream_t s);
+cudaError_t launch_expert_combine(int dtype, const ExpertParams& p, cudaStream_t s);  // weights NULL: the plain sum
+cudaError_t launch_expert_combine_grad(int dtype, const ExpertParams& p, cudaStream_t s);
+
 }  // namespace scg

@@ -1,15 +1,17 @@
-"""Sequence-model operators: token embedding, short causal convolution and
-selective state space scan (binding over ``include/sc_seq.h``).
+"""Sequence-model operators: token embedding, short causal convolution, selective
+state space scan, gated recurrence, norm, and the way of tokens to their experts and
+back (binding over ``include/sc_seq.h``).
 
 The functions take torch CUDA tensors and run on the current torch stream (or
 ``stream``); they check shapes and types (ValueError), allocate what they return
 (on that stream), and leave every step of the computation to the library's
 kernels.  Definitions, layouts and limits: the header.
 
-embed, causal_conv and selective_scan are differentiable: where torch records
-gradients and an input requires one, their results carry it (seq_autograd.py), by the
-`_grad` functions below, which may also be called by themselves.  `out` cannot be given
-then, and nothing goes back through `final_state`.  The `_step` forms have no gradient;
+embed, causal_conv, selective_scan, gated_scan, layer_norm, expert_gather and
+expert_combine are differentiable: where torch records gradients and an input requires
+one, their results carry it (seq_autograd.py), by the `_grad` functions below, which may
+also be called by themselves.  `out` cannot be given then, and nothing goes back through
+`final_state`.  The `_step` forms have no gradient;
 asking for one raises.
 
     ids, weight                 y = embed(ids, weight, scale)
@@ -20,13 +22,23 @@ asking for one raises.
     x, dt, A, B, C              y = selective_scan(x, dt, A, B, C, D, z, dt_bias)
                                 grads = selective_scan_grad(dy, x, ..., saved=saved)
                                 y = selective_scan_step(x1, dt1, A, B1, C1, state)
+    x, gate                     y = gated_scan(x, gate)
+                                grads = gated_scan_grad(dy, x, gate, saved=saved)
+                                y = gated_scan_step(x1, gate1, state)
+    x (..., channels), residual y, sum = layer_norm(x, weight, bias, residual=residual)
+                                grads = layer_norm_grad(dy, sum, weight, bias, saved=saved, dsum=dsum)
+    experts (tokens, choices)   order = expert_sort(experts, n_experts)
+    x (tokens, dim)             rows = expert_gather(x, order)
+                                y = expert_combine(rows, order, weights)
 """
 from __future__ import annotations
 
 import ctypes
+from typing import Any, NamedTuple
 
 SC_F16, SC_BF16 = 8, 9
 SC_CONV_MAX_WIDTH, SC_SSM_MAX_STATES, SC_SSM_SAVE = 8, 64, 16
+SC_GATED_SAVE, SC_EXPERT_MAX = 16, 1024
 
 _P, _I64, _I32, _INT, _SZ, _F = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int, ctypes.c_size_t,
                                 ctypes.c_float)
@@ -56,7 +68,28 @@ class SsmGrads(ctypes.Structure):
                 ("dstate", _P)]
 
 
+class GatedDesc(ctypes.Structure):
+    """sc_gated_desc."""
+    _fields_ = [("dtype", _I32), ("sigmoid", _I32), ("batch", _I64), ("length", _I64), ("channels", _I64), ("x", _P),
+                ("gate", _P), ("x_batch", _I64), ("x_token", _I64), ("gate_batch", _I64), ("gate_token", _I64),
+                ("heads", _P), ("state", _P)]
+
+
+class NormDesc(ctypes.Structure):
+    """sc_norm_desc."""
+    _fields_ = [("dtype", _I32), ("wtype", _I32), ("rms", _I32), ("eps", _F), ("batch", _I64), ("length", _I64),
+                ("channels", _I64), ("x", _P), ("x_batch", _I64), ("x_token", _I64), ("residual", _P),
+                ("residual_batch", _I64), ("residual_token", _I64), ("weight", _P), ("bias", _P)]
+
+
+class ExpertDesc(ctypes.Structure):
+    """sc_expert_desc."""
+    _fields_ = [("dtype", _I32), ("wtype", _I32), ("tokens", _I64), ("choices", _I64), ("dim", _I64),
+                ("experts", _I64), ("place", _P), ("offsets", _P), ("weights", _P)]
+
+
 _CONV, _SSM, _GRADS = ctypes.POINTER(ConvDesc), ctypes.POINTER(SsmDesc), ctypes.POINTER(SsmGrads)
+_GATED, _NORM, _EXPERT = ctypes.POINTER(GatedDesc), ctypes.POINTER(NormDesc), ctypes.POINTER(ExpertDesc)
 
 SIGNATURES = {
     "sc_embed": ([_P, _INT, _I64, _INT, _P, _I64, _I64, _I64, _F, _P, _I64, _P], _INT),
@@ -72,6 +105,18 @@ SIGNATURES = {
     "sc_selective_scan_grad": ([_SSM, _GRADS, _P], _INT),
     "sc_selective_scan_grad_workspace_bytes": ([_I64, _I64, _I64, _I64, _I64], _SZ),
     "sc_selective_scan_step": ([_SSM, _P, _I64, _P, _P, _I64, _P], _INT),
+    "sc_gated_scan": ([_GATED, _P, _I64, _I64, _P, _P, _P], _INT),
+    "sc_gated_scan_saved_bytes": ([_I64, _I64, _I64], _SZ),
+    "sc_gated_scan_grad": ([_GATED, _P, _I64, _I64, _P, _P, _P, _P, _P, _P], _INT),
+    "sc_gated_scan_step": ([_GATED, _P, _I64, _P, _P, _I64, _P], _INT),
+    "sc_layer_norm": ([_NORM, _P, _I64, _I64, _P, _I64, _I64, _P, _P], _INT),
+    "sc_layer_norm_grad": ([_NORM, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _P, _P], _INT),
+    "sc_layer_norm_grad_workspace_bytes": ([_I64, _I64, _I64, _INT], _SZ),
+    "sc_expert_sort": ([_P, _INT, _I64, _I64, _P, _P, _P, _P], _INT),
+    "sc_expert_gather": ([_EXPERT, _P, _I64, _P, _I64, _P], _INT),
+    "sc_expert_gather_grad": ([_EXPERT, _P, _I64, _P, _I64, _P], _INT),
+    "sc_expert_combine": ([_EXPERT, _P, _I64, _P, _I64, _P], _INT),
+    "sc_expert_combine_grad": ([_EXPERT, _P, _I64, _P, _I64, _P, _I64, _P, _P], _INT),
 }
 
 
@@ -205,3 +250,102 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, sof
     as in causal_conv_step."""
     return _step("selective_scan_step", stream, (x, dt, A, B, C, D, z, dt_bias, state), x, dt, A, B, C, state, D, z,
                  dt_bias, softplus, slots, out)
+
+
+def gated_scan_saved(x, stream=None):
+    """The buffer that a gated_scan of x fills for gated_scan_grad."""
+    return _call("gated_scan_saved", stream, x)
+
+
+def gated_scan(x, gate, activation="sigmoid", heads=None, state=None, final_state=None, saved=None, out=None,
+               stream=None):
+    """Gated recurrence of x (batch, length, channels), gate like x: h = f * h + (1 - f) * x
+    with f = sigmoid(gate), or with activation None h = gate * h + x.  heads as in
+    causal_conv; state / final_state: (batch, channels) float32.  saved: from
+    gated_scan_saved, for gated_scan_grad."""
+    if _requires_grad(x, gate, state):
+        return _record("GatedScan", stream, out, x, gate, activation, heads, state, final_state, saved)
+    return _call("gated_scan", stream, x, gate, activation, heads, state, final_state, saved, out)
+
+
+def gated_scan_grad(dy, x, gate, activation="sigmoid", heads=None, state=None, saved=None, dfinal_state=None,
+                    stream=None):
+    """Gradients of gated_scan, given what it saved: a dict with x and gate (their type)
+    and, where `state` is given, state (float32)."""
+    return _call("gated_scan_grad", stream, dy, x, gate, activation, heads, state, saved, dfinal_state)
+
+
+def gated_scan_step(x, gate, state, activation="sigmoid", slots=None, out=None, stream=None):
+    """One token for each row of x (batch, channels); state (rows, channels) float32 is
+    moved on in place.  slots as in causal_conv_step."""
+    return _step("gated_scan_step", stream, (x, gate, state), x, gate, state, activation, slots, out)
+
+
+def layer_norm_saved(x, stream=None):
+    """The buffer that a layer_norm of x fills for layer_norm_grad: a row's mean and
+    1 / deviation."""
+    return _call("layer_norm_saved", stream, x)
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, rms: bool = False, residual=None, saved=None, out=None,
+               stream=None):
+    """The norm of x (..., channels) over its channels, times weight, plus bias (each
+    (channels), of x's type or float32); rms: without the mean.  residual (like x): the
+    norm of x + residual, and the result is the pair (y, x + residual), the sum rounded
+    to x's type.  saved: from layer_norm_saved, for layer_norm_grad."""
+    if _requires_grad(x, weight, bias, residual):
+        return _record("LayerNorm", stream, out, x, weight, bias, eps, rms, residual, saved)
+    return _call("layer_norm", stream, x, weight, bias, eps, rms, residual, saved, out)
+
+
+def layer_norm_grad(dy, x, weight=None, bias=None, rms: bool = False, saved=None, dsum=None, stream=None):
+    """Gradients of layer_norm at x (the sum, where there was a residual), given what it
+    saved: a dict with x (x's type; dsum, what reaches the sum by itself, is added to
+    it, and it is the residual's gradient too), and weight and bias (float32) where they
+    are given."""
+    return _call("layer_norm_grad", stream, dy, x, weight, bias, rms, saved, dsum, True, True)
+
+
+class ExpertOrder(NamedTuple):
+    """What expert_sort returns.  The rows of expert e are offsets[e] to offsets[e + 1]
+    (int64, n_experts + 1); order[row] is the entry of a row, token * choices + choice,
+    and place[token, choice] the row of an entry (both int32).  Entries of no expert
+    are behind offsets[n_experts]."""
+    offsets: Any
+    order: Any
+    place: Any
+
+
+def expert_sort(experts, n_experts: int, stream=None):
+    """The entries of experts (tokens, choices; int32 or int64) in the order of their
+    experts, stable; ids outside [0, n_experts) have no expert and come last.
+    n_experts: 1 to 1024."""
+    return ExpertOrder(*_call("expert_sort", stream, experts, n_experts))
+
+
+def expert_gather(x, order, out=None, stream=None):
+    """A row of x (tokens, dim) for each entry, in the order of the experts (tokens *
+    choices, dim); zeros for entries of no expert."""
+    if _requires_grad(x):
+        return _record("ExpertGather", stream, out, x, order.offsets, order.place)
+    return _call("expert_gather", stream, x, order.offsets, order.place, out)
+
+
+def expert_gather_grad(drows, order, out=None, stream=None):
+    """Gradient of expert_gather by x: the sum of a token's rows of drows."""
+    return _call("expert_gather_grad", stream, drows, order.offsets, order.place, out)
+
+
+def expert_combine(y, order, weights=None, out=None, stream=None):
+    """The way back: the sum of a token's rows of y (tokens * choices, dim, in the order
+    of the experts), times weights (tokens, choices; of y's type or float32) where they
+    are given; entries of no expert add nothing."""
+    if _requires_grad(y, weights):
+        return _record("ExpertCombine", stream, out, y, order.offsets, order.place, weights)
+    return _call("expert_combine", stream, y, order.offsets, order.place, weights, out)
+
+
+def expert_combine_grad(dout, y, order, weights=None, stream=None):
+    """Gradients of expert_combine: a dict with y (y's type, zeros for entries of no
+    expert) and, where they are given, weights (their type)."""
+    return _call("expert_combine_grad", stream, dout, y, order.offsets, order.place, weights)
