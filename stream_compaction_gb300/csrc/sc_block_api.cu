@@ -22,7 +22,8 @@ sc_status gated_args(const sc_gated_desc* d, bool step, GatedParams* p) {
     const sc_status st = types(d->dtype);
     if (st != SC_OK) return st;
     const int eb = bytes_of(d->dtype);
-    if (d->batch < 0 || d->length < 0 || d->channels < 0 || (step && d->length != 1)) return SC_ERR_INVALID;
+    if (d->batch < 0 || d->length < 0 || d->length > kMaxGrid / 2 || d->channels < 0 || (step && d->length != 1))
+        return SC_ERR_INVALID;
     if (product(d->batch, std::max<int64_t>(d->length, 1), d->channels, 64) < 0) return SC_ERR_INVALID;
     // the smallest channel block, the largest cluster
     const int64_t grid = product(d->batch, (d->channels + 31) / 32, 8);
@@ -185,6 +186,8 @@ sc_status sc_gated_scan(const sc_gated_desc* d, void* y, int64_t y_batch, int64_
     p.final_state = final_state;
     p.saved = saved;
     p.pairs = d->channels % 2 == 0 && x.vec(2) && g.vec(2) && o.vec(2);
+    const int e = 16 / bytes_of(d->dtype);
+    p.wide = d->channels % e == 0 && x.vec(e) && g.vec(e);
     return status_of(launch_gated(d->dtype, p, cu(stream)));
 }
 
@@ -215,6 +218,8 @@ sc_status sc_gated_scan_grad(const sc_gated_desc* d, const void* dy, int64_t dy_
     p.dgate = dgate;
     p.dstate = dstate;
     p.pairs = d->channels % 2 == 0 && x.vec(2) && g.vec(2) && e.vec(2) && out[0].vec(2) && out[1].vec(2);
+    const int wide = 16 / bytes_of(d->dtype);
+    p.wide = d->channels % wide == 0 && x.vec(wide) && g.vec(wide) && e.vec(wide);
     return status_of(launch_gated_grad(d->dtype, p, cu(stream)));
 }
 

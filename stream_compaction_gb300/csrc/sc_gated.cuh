@@ -40,149 +40,268 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kTokens = SC_GATED_SAVE;
+constexpr int kStages = 3, kGradStages = 2;
 constexpr int kMaxCluster = 8;
 
-// A lane's K channels of a token.
-template <class T, int K> struct Raw;
+template <int kBytes>
+__device__ __forceinline__ void copy_async(unsigned char* to, const void* from) {
+    const uint32_t s = (uint32_t)__cvta_generic_to_shared(to);
+    if constexpr (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kAhead>  // all but the last kAhead groups of copies have arrived, for the whole warp
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+    __syncwarp();
+}
+
+// A lane's K channels of a token: as they lie in memory, and as one operand.
+template <class T, int K> struct Raw { using type = unsigned short; };
 template <> struct Raw<float, 1> { using type = float; };
-template <> struct Raw<f16, 1> { using type = unsigned short; };
-template <> struct Raw<bf16, 1> { using type = unsigned short; };
 template <> struct Raw<f16, 2> { using type = uint32_t; };
 template <> struct Raw<bf16, 2> { using type = uint32_t; };
 
-template <class T, int K>
-struct Cell {
-    typename Raw<T, K>::type r;
-    __device__ __forceinline__ void load(const T* p) { r = __ldg(reinterpret_cast<const typename Raw<T, K>::type*>(p)); }
-    __device__ __forceinline__ void zero() { memset(&r, 0, sizeof(r)); }
-    __device__ __forceinline__ float get(int k) const {
-        T e[K];
-        memcpy(e, &r, sizeof(r));
-        return to_f32(e[k]);
-    }
-    __device__ __forceinline__ static void store(T* p, const float (&v)[K]) {
-        T e[K];
-#pragma unroll
-        for (int k = 0; k < K; ++k) e[k] = from_f32<T>(v[k]);
-        typename Raw<T, K>::type w;
-        memcpy(&w, e, sizeof(w));
-        *reinterpret_cast<typename Raw<T, K>::type*>(p) = w;
+template <int K> struct Lane;
+template <> struct Lane<1> {
+    using V = float;
+    static __device__ __forceinline__ V all(float v) { return v; }
+    static __device__ __forceinline__ V mul(V a, V b) { return a * b; }
+    static __device__ __forceinline__ V add(V a, V b) { return a + b; }
+    static __device__ __forceinline__ V fma(V a, V b, V c) { return fmaf(a, b, c); }
+    static __device__ __forceinline__ V load(const float* p) { return __ldg(p); }
+    static __device__ __forceinline__ void store(float* p, V v) { *p = v; }
+};
+template <> struct Lane<2> {
+    using V = f2;
+    static __device__ __forceinline__ V all(float v) { return both(v); }
+    static __device__ __forceinline__ V mul(V a, V b) { return mul2(a, b); }
+    static __device__ __forceinline__ V add(V a, V b) { return add2(a, b); }
+    static __device__ __forceinline__ V fma(V a, V b, V c) { return fma2(a, b, c); }
+    static __device__ __forceinline__ V load(const float* p) { return pack2(__ldg(p), __ldg(p + 1)); }
+    static __device__ __forceinline__ void store(float* p, V v) {
+        p[0] = lo2(v);
+        p[1] = hi2(v);
     }
 };
 
-// f = sigmoid(g) and 1 - f, each without cancellation: the smaller of the two is
-// e / (1 + e), e = exp(-|g|), and the other 1 minus it.  So a decay close to 1 is off
-// by its own rounding alone, however many of them are multiplied.
+// A lane's tile: kTokens tokens of K channels in pairs, for two-lane arithmetic: a
+// token's two channels, or two tokens of one channel.
+template <int K> constexpr int kPairs = kTokens * K / 2;
+template <int K>
+__device__ __forceinline__ typename Lane<K>::V token(const f2 (&v)[kPairs<K>], int j) {
+    if constexpr (K == 2) return v[j];
+    else return j % 2 ? hi2(v[j / 2]) : lo2(v[j / 2]);
+}
+template <int K>
+__device__ __forceinline__ void set_token(f2 (&v)[kPairs<K>], int j, typename Lane<K>::V t) {
+    if constexpr (K == 2) v[j] = t;
+    else v[j / 2] = j % 2 ? pack2(lo2(v[j / 2]), t) : pack2(t, hi2(v[j / 2]));
+}
+
+// A warp's tiles of one tensor lie in shared memory, 32 K channels a token, filled by
+// asynchronous copies kStages - 1 rounds ahead: loads into registers left a third of
+// that under way and doubled the registers (measured).
+template <class T, int K>
+struct Tile {
+    using R = typename Raw<T, K>::type;
+    static constexpr int kBytes = kTokens * 32 * (int)sizeof(R);
+    const R* at;  // the lane's channels of the first token
+    __device__ __forceinline__ Tile(const unsigned char* tile, int lane) : at(reinterpret_cast<const R*>(tile) + lane) {}
+
+    static __device__ __forceinline__ float one(R v) {
+        if constexpr (sizeof(T) == 4) {
+            return v;
+        } else {
+            T e;
+            memcpy(&e, &v, 2);
+            return to_f32(e);
+        }
+    }
+    __device__ __forceinline__ f2 pair(int i) const {
+        if constexpr (K == 2) {
+            Vec<T, 2> v;
+            v.w[0] = at[i * 32];
+            return v.pair(0);
+        } else {
+            return pack2(one(at[2 * i * 32]), one(at[(2 * i + 1) * 32]));
+        }
+    }
+    __device__ __forceinline__ typename Lane<K>::V get(int j) const {
+        if constexpr (K == 2) return pair(j);
+        else return one(at[j * 32]);
+    }
+    static __device__ __forceinline__ void store(T* p, typename Lane<K>::V v) {
+        if constexpr (K == 2) {
+            const float f[2] = {lo2(v), hi2(v)};
+            Vec<T, 2> o;
+            o.set(f);
+            o.store(p);
+        } else {
+            *p = from_f32<T>(v);
+        }
+    }
+};
+
+// Where a warp's tiles of a tensor come from.  Rows that are aligned to 16 bytes go by
+// chunks of 16 (8 or 4 lanes a token), others by a lane's own channels; single 16-bit
+// elements are too small for an asynchronous copy and go through registers.
+template <class T, int K>
+struct Source {
+    using R = typename Raw<T, K>::type;
+    static constexpr int kChunks = 32 * (int)sizeof(R) / 16, kRows = 32 / kChunks;
+    const T* p;         // the lane's part of the next tile's first token (or first of kRows)
+    long long stride;   // of a token
+    long long advance;  // from a tile to the warp's next
+    bool wide, mine;
+    __device__ __forceinline__ Source(const void* base, long long row, long long token, long long tile, long long step,
+                                      long long ch0, long long channels, int lane, bool wide_)
+        : stride(token), advance(step * kTokens * token), wide(wide_ && K * sizeof(T) > 2) {
+        const int first = wide ? lane / kChunks : 0, ch = wide ? lane % kChunks * (16 / (int)sizeof(T)) : lane * K;
+        p = static_cast<const T*>(base) + row + (tile * kTokens + first) * token + ch0 + ch;
+        mine = ch0 + ch < channels;
+    }
+    // The next tile, of which the row has `left` tokens (zeros for the others), to `tile`.
+    __device__ __forceinline__ void next(unsigned char* tile, int left, int lane) {
+        const T* q = p;
+        p += advance;
+        if (!mine) return;
+        if constexpr (K * sizeof(T) == 2) {
+            unsigned short v[kTokens];
+#pragma unroll
+            for (int j = 0; j < kTokens; ++j) v[j] = j < left ? __ldg(reinterpret_cast<const unsigned short*>(q + j * stride)) : 0;
+#pragma unroll
+            for (int j = 0; j < kTokens; ++j) reinterpret_cast<unsigned short*>(tile)[j * 32 + lane] = v[j];
+        } else if (wide) {
+            unsigned char* to = tile + lane * 16;  // the lanes' chunks follow one another, kRows tokens at a time
+            if (left >= kTokens) {
+#pragma unroll
+                for (int j = 0; j < kTokens / kRows; ++j) copy_async<16>(to + j * 512, q + j * kRows * stride);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kTokens / kRows; ++j) {
+                    if (j * kRows + lane / kChunks < left) copy_async<16>(to + j * 512, q + j * kRows * stride);
+                    else *reinterpret_cast<uint4*>(to + j * 512) = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+        } else {
+            unsigned char* to = tile + lane * 4;
+#pragma unroll
+            for (int j = 0; j < kTokens; ++j) {
+                if (j < left) copy_async<4>(to + j * 128, q + j * stride);
+                else *reinterpret_cast<uint32_t*>(to + j * 128) = 0u;
+            }
+        }
+    }
+};
+
+// rest = 1 - f = e / (1 + e), e = exp(-g), and f = 1 - rest, for a pair.  rest has its
+// relative error (4 + |g| units of 2^-24 in 16 bits, 8 in float32) however small it
+// is, and so has what x enters with; f is off by as much absolutely, times rest: decays
+// close to 1 are as good as rounded ones, however many are multiplied.  e ends at 2^126
+// (its reciprocal is a normal number; f is 0 to float32 then).
 template <class T>
-__device__ __forceinline__ void gate_of(float g, float& f, float& rest) {
-    const float e = exp_minus<kFine<T>>(fabsf(g));
-    const float small = e * rcp(1.0f + e), large = 1.0f - small;
-    f = g < 0.0f ? small : large;  // NaN: both are NaN
-    rest = g < 0.0f ? large : small;
+__device__ __forceinline__ void gates(f2 g, f2& f, f2& rest) {
+    f2 e;
+    if constexpr (kFine<T>) {
+        e = exp_minus_2<true>(pack2(at_least(lo2(g), -87.0f), at_least(hi2(g), -87.0f)));
+    } else {
+        const f2 t = mul2(g, both(kLog2e));
+        e = pack2(ex2(-at_least(lo2(t), -126.0f)), ex2(-at_least(hi2(t), -126.0f)));
+    }
+    rest = mul2(e, rcp_2(add2(e, both(1.0f))));
+    f = fma2(rest, both(-1.0f), both(1.0f));
 }
 
-// Tokens of a tile where a segment starts, one bit each.
-__device__ __forceinline__ uint32_t cuts_of(const uint8_t* heads, long long row, long long t0, long long length, int lane) {
-    if (!heads) return 0u;
+// A lane's flag of a tile's tokens, and the tokens where a segment starts, one bit each.
+__device__ __forceinline__ uint8_t head_of(const uint8_t* heads, long long row, long long t0, long long length, int lane) {
     const long long t = t0 + lane;
-    return __ballot_sync(0xffffffffu, lane < kTokens && t < length && heads[row * length + t] != 0);
+    return lane < kTokens && t >= 0 && t < length ? __ldg(heads + row * length + t) : 0;
 }
+__device__ __forceinline__ uint32_t cuts_of(uint8_t head) { return __ballot_sync(0xffffffffu, head != 0); }
 
-// The map of a run of tokens on the state before it: h -> A h + B, or B alone where a
+// The map of a run of tokens on the value before it: h -> A h + B, or B alone where a
 // segment starts inside (whatever h is, infinities too).
-__device__ __forceinline__ float through(float A, float B, bool cut, float h) { return cut ? B : fmaf(A, h, B); }
+template <int K>
+struct Map {
+    typename Lane<K>::V A, B;
+    __device__ __forceinline__ typename Lane<K>::V of(typename Lane<K>::V h) const { return Lane<K>::fma(A, h, B); }
+    __device__ __forceinline__ typename Lane<K>::V of(typename Lane<K>::V h, bool cut) const { return cut ? B : of(h); }
+};
 
 // What the warps and CTAs of a round exchange.
 template <int K, int kWarps>
 struct Exchange {
-    float A[2][kWarps][K][32], B[2][kWarps][K][32];
-    float rank_A[2][kMaxCluster][K][32], rank_B[2][kMaxCluster][K][32];
+    Map<K> warp[2][kWarps][32];
     int cut[2][kWarps], rank_cut[2][kMaxCluster];
+    Map<K> rank[1][32];  // [2][CTAs] of them; a CTA by itself needs none
+    static __host__ __device__ constexpr size_t bytes(int ctas) { return sizeof(Exchange) + (ctas > 1 ? (2 * ctas - 1) * sizeof(Map<K>[32]) : 0); }
 };
 
-// One round: takes this warp's map, returns the value before its tile in `in` and
-// moves `carry`, the value before the round, to behind it (the same in all warps).
-// Warps and CTAs count in the direction of the recurrence.  Buffers alternate: a warp
-// writes for the next round while others still read this one's, and two rounds on a
-// barrier lies between.
-template <int K, int kWarps>
-__device__ __forceinline__ void exchange(Exchange<K, kWarps>& x, int turn, int warp, int lane, int rank, int ranks,
-                                         const float (&A)[K], const float (&B)[K], bool cut, float (&carry)[K],
-                                         float (&in)[K]) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        x.A[turn][warp][k][lane] = A[k];
-        x.B[turn][warp][k][lane] = B[k];
-    }
-    if (lane == 0) x.cut[turn][warp] = cut;
+// One round: takes this warp's map, returns the value before its tile and moves
+// `carry`, the value before the round, to behind it (the same in all warps).  Warps and
+// CTAs count in the direction of the recurrence.  Buffers alternate: a warp writes for
+// the next round while others still read this one's, and two rounds on a barrier lies
+// between.  kCuts: segments may start anywhere.
+template <int K, int kWarps, bool kCuts>
+__device__ __forceinline__ typename Lane<K>::V exchange(Exchange<K, kWarps>& x, int turn, int warp, int lane, int rank,
+                                                        int ranks, const Map<K>& map, bool cut,
+                                                        typename Lane<K>::V& carry) {
+    using V = typename Lane<K>::V;
+    x.warp[turn][warp][lane] = map;
+    if (kCuts && lane == 0) x.cut[turn][warp] = cut;
     __syncthreads();
+    V in = carry;
     if (ranks > 1) {
-        if (warp == 0) {
-            float a[K], b[K];
-            bool any = false;
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                a[k] = 1.0f;
-                b[k] = 0.0f;
-            }
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const bool c = x.cut[turn][w] != 0;
-                any |= c;
-#pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    b[k] = through(x.A[turn][w][k][lane], x.B[turn][w][k][lane], c, b[k]);
-                    a[k] *= x.A[turn][w][k][lane];
-                }
-            }
+        // One warp writes to the other CTAs, so only its arrival has to wait for what it has
+        // written before; the others' stores of results need not be waited for.
+        if (warp != 0) {
+            asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+        } else {
             const cg::cluster_group cluster = cg::this_cluster();
+            Map<K> all = x.warp[turn][0][lane];
+            bool any = kCuts && x.cut[turn][0] != 0;
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) {
+                const Map<K> m = x.warp[turn][w][lane];
+                const bool c = kCuts && x.cut[turn][w] != 0;
+                all.B = m.of(all.B, c);
+                all.A = Lane<K>::mul(m.A, all.A);
+                any |= c;
+            }
             for (int r = 0; r < ranks; ++r) {
                 Exchange<K, kWarps>* other = cluster.map_shared_rank(&x, r);
-#pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    other->rank_A[turn][rank][k][lane] = a[k];
-                    other->rank_B[turn][rank][k][lane] = b[k];
-                }
-                if (lane == 0) other->rank_cut[turn][rank] = any;
+                other->rank[turn * ranks + rank][lane] = all;
+                if (kCuts && lane == 0) other->rank_cut[turn][rank] = any;
             }
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
         }
-        cg::this_cluster().sync();
-    }
-#pragma unroll
-    for (int k = 0; k < K; ++k) in[k] = carry[k];
-    if (ranks > 1) {
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         for (int r = 0; r < ranks; ++r) {
-            if (r == rank) {
-#pragma unroll
-                for (int k = 0; k < K; ++k) in[k] = carry[k];
-            }
-            const bool c = x.rank_cut[turn][r] != 0;
-#pragma unroll
-            for (int k = 0; k < K; ++k) carry[k] = through(x.rank_A[turn][r][k][lane], x.rank_B[turn][r][k][lane], c, carry[k]);
-        }
-    }
-    float h[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) h[k] = in[k];
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        const bool c = x.cut[turn][w] != 0;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (w == warp) in[k] = h[k];
-            h[k] = through(x.A[turn][w][k][lane], x.B[turn][w][k][lane], c, h[k]);
+            if (r == rank) in = carry;
+            carry = x.rank[turn * ranks + r][lane].of(carry, kCuts && x.rank_cut[turn][r] != 0);
         }
     }
     if (ranks == 1) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) carry[k] = h[k];
+        for (int w = 0; w < kWarps; ++w) {
+            const Map<K> m = x.warp[turn][w][lane];
+            const bool c = kCuts && x.cut[turn][w] != 0;
+            if (w < warp) in = m.of(in, c);
+            carry = m.of(carry, c);
+        }
+    } else {
+#pragma unroll
+        for (int w = 0; w + 1 < kWarps; ++w)
+            if (w < warp) in = x.warp[turn][w][lane].of(in, kCuts && x.cut[turn][w] != 0);
     }
+    return in;
 }
 
 // Where a CTA works: row b, the lane's first channel, the rounds.
 struct Place {
-    long long b, ch, rounds, tiles;
-    int rank, ranks, warp, lane;
+    long long b, ch0, ch;  // ch0: the warp's first channel, ch: the lane's
+    int rounds, tiles, rank, ranks, warp, lane;
     bool live;
 };
 template <int K, int kWarps>
@@ -194,242 +313,235 @@ __device__ __forceinline__ Place place_of(const GatedParams& p) {
     c.b = group / blocks;
     c.warp = threadIdx.x / 32;
     c.lane = threadIdx.x % 32;
-    c.ch = ((group - c.b * blocks) * 32 + c.lane) * K;
+    c.ch0 = (group - c.b * blocks) * 32 * K;
+    c.ch = c.ch0 + c.lane * K;
     c.live = c.ch < p.channels;
-    c.tiles = (p.length + kTokens - 1) / kTokens;
+    c.tiles = (int)((p.length + kTokens - 1) / kTokens);
     c.rounds = (c.tiles + c.ranks * kWarps - 1) / (c.ranks * kWarps);
     return c;
 }
 
-template <class T, int K>
-__device__ __forceinline__ void load_tile(const T* p, long long stride, int valid, Cell<T, K> (&v)[kTokens]) {
-    if (valid == kTokens) {
-#pragma unroll
-        for (int j = 0; j < kTokens; ++j) v[j].load(p + j * stride);
-    } else {
-#pragma unroll
-        for (int j = 0; j < kTokens; ++j) {
-            if (j < valid) v[j].load(p + j * stride);
-            else v[j].zero();
-        }
-    }
-}
-
 // ---------------------------------------------------------------- forward
-template <class T, int K, bool kSigmoid, int kWarps>
+template <class T, int K, bool kSigmoid, int kWarps, bool kCuts>
 __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) gated_kernel(GatedParams p) {
-    __shared__ Exchange<K, kWarps> s_ex;
+    using L = Lane<K>;
+    using V = typename L::V;
+    using Tl = Tile<T, K>;
+    extern __shared__ __align__(16) unsigned char s_mem[];
+    Exchange<K, kWarps>& s_ex = *reinterpret_cast<Exchange<K, kWarps>*>(s_mem);
     const Place c = place_of<K, kWarps>(p);
-    const T* x = static_cast<const T*>(p.x) + c.b * p.x_batch + c.ch;
-    const T* g = static_cast<const T*>(p.gate) + c.b * p.gate_batch + c.ch;
-    T* y = static_cast<T*>(p.y) + c.b * p.y_batch + c.ch;
-    Cell<T, K> xr[kTokens], gr[kTokens];
-    uint32_t cuts;
-    auto tokens = [&](long long tile) { return (int)max(0ll, min((long long)kTokens, p.length - tile * kTokens)); };
-    auto fetch = [&](long long tile) {
-        const long long t0 = tile * kTokens;
-        const int valid = c.live ? tokens(tile) : 0;
-        load_tile<T, K>(x + t0 * p.x_token, p.x_token, valid, xr);
-        load_tile<T, K>(g + t0 * p.gate_token, p.gate_token, valid, gr);
-        cuts = cuts_of(p.heads, c.b, t0, p.length, c.lane);
+    unsigned char* ring = s_mem + Exchange<K, kWarps>::bytes(c.ranks) + c.warp * (kStages * 2 * Tl::kBytes);
+    const int step = c.ranks * kWarps;
+    int tile = c.rank * kWarps + c.warp;
+    Source<T, K> x(p.x, c.b * p.x_batch, p.x_token, tile, step, c.ch0, p.channels, c.lane, p.wide);
+    Source<T, K> g(p.gate, c.b * p.gate_batch, p.gate_token, tile, step, c.ch0, p.channels, c.lane, p.wide);
+    T* y = static_cast<T*>(p.y) + c.b * p.y_batch + (long long)tile * kTokens * p.y_token + c.ch;
+    float* saved = p.saved ? p.saved + (c.b * c.tiles + tile) * p.channels + c.ch : nullptr;
+    int left = (int)p.length - tile * kTokens, left_ahead = left;  // tokens from a tile's start to the row's end
+    unsigned char *fill = ring, *take = ring, *const end = ring + kStages * 2 * Tl::kBytes;
+    uint8_t head = 0;
+    auto fetch = [&] {
+        x.next(fill, left_ahead, c.lane);
+        g.next(fill + Tl::kBytes, left_ahead, c.lane);
+        copies_end();
+        left_ahead -= step * kTokens;
+        fill += 2 * Tl::kBytes;
+        if (fill == end) fill = ring;
     };
-    float carry[K], h[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) carry[k] = p.state && c.live ? __ldg(p.state + c.b * p.channels + c.ch + k) : 0.0f;
-    long long tile = (long long)c.rank * kWarps + c.warp;
-    const long long step = (long long)c.ranks * kWarps;
-    fetch(tile);
+    for (int r = 0; r < kStages - 1; ++r) fetch();
+    if (kCuts) head = head_of(p.heads, c.b, tile * kTokens, p.length, c.lane);
+    V carry = p.state && c.live ? L::load(p.state + c.b * p.channels + c.ch) : L::all(0.0f);
     if (c.ranks > 1) cg::this_cluster().sync();  // every CTA has begun before one writes to its shared memory
-    for (long long round = 0; round < c.rounds; ++round, tile += step) {
-        float f[kTokens][K], b[kTokens][K];
-        const uint32_t cut = cuts;
-        const int valid = tokens(tile);
+    for (int round = 0; round < c.rounds; ++round) {
+        fetch();
+        copies_wait<kStages - 1>();
+        const Tl xr(take, c.lane), gr(take + Tl::kBytes, c.lane);
+        take += 2 * Tl::kBytes;
+        if (take == end) take = ring;
+        f2 f[kPairs<K>], b[kPairs<K>];
+        const uint32_t cut = kCuts ? cuts_of(head) : 0u;
+        if (kCuts) head = head_of(p.heads, c.b, (long long)(tile + step) * kTokens, p.length, c.lane);
+        const int valid = min(left, kTokens);
 #pragma unroll
-        for (int j = 0; j < kTokens; ++j)
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const float xv = xr[j].get(k), gv = gr[j].get(k);
-                if constexpr (kSigmoid) {
-                    gate_of<T>(gv, f[j][k], b[j][k]);
-                    b[j][k] *= xv;
-                } else {
-                    f[j][k] = gv;
-                    b[j][k] = xv;
-                }
+        for (int i = 0; i < kPairs<K>; ++i) {
+            if constexpr (kSigmoid) {
+                gates<T>(gr.pair(i), f[i], b[i]);
+                b[i] = mul2(b[i], xr.pair(i));
+            } else {
+                f[i] = gr.pair(i);
+                b[i] = xr.pair(i);
             }
+        }
         if (valid < kTokens) {  // behind the row's end: the state stays
 #pragma unroll
             for (int j = 0; j < kTokens; ++j)
-#pragma unroll
-                for (int k = 0; k < K; ++k)
-                    if (j >= valid) {
-                        f[j][k] = 1.0f;
-                        b[j][k] = 0.0f;
-                    }
-        }
-        if (cut) {
-#pragma unroll
-            for (int j = 0; j < kTokens; ++j)
-                if (cut >> j & 1u)
-#pragma unroll
-                    for (int k = 0; k < K; ++k) f[j][k] = 0.0f;
-        }
-        if (round + 1 < c.rounds) fetch(tile + step);
-        float A[K], B[K];
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            A[k] = f[0][k];
-            B[k] = b[0][k];
-        }
-        if (!cut) {
-#pragma unroll
-            for (int j = 1; j < kTokens; ++j)
-#pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    A[k] *= f[j][k];
-                    B[k] = fmaf(f[j][k], B[k], b[j][k]);
+                if (j >= valid) {
+                    set_token<K>(f, j, L::all(1.0f));
+                    set_token<K>(b, j, L::all(0.0f));
                 }
+        }
+        __syncwarp();  // the tile is read: the next round's copies may take its place
+        Map<K> map{token<K>(f, 0), token<K>(b, 0)};
+        if (!kCuts || cut == 0) {
+#pragma unroll
+            for (int j = 1; j < kTokens; ++j) {
+                map.A = L::mul(map.A, token<K>(f, j));
+                map.B = L::fma(token<K>(f, j), map.B, token<K>(b, j));
+            }
         } else {
+            map.A = L::all(0.0f);
 #pragma unroll
             for (int j = 1; j < kTokens; ++j)
-#pragma unroll
-                for (int k = 0; k < K; ++k) B[k] = cut >> j & 1u ? b[j][k] : fmaf(f[j][k], B[k], b[j][k]);
-#pragma unroll
-            for (int k = 0; k < K; ++k) A[k] = 0.0f;
+                map.B = cut >> j & 1u ? token<K>(b, j) : L::fma(token<K>(f, j), map.B, token<K>(b, j));
         }
-        exchange<K, kWarps>(s_ex, (int)(round & 1), c.warp, c.lane, c.rank, c.ranks, A, B, cut != 0, carry, h);
+        V h = exchange<K, kWarps, kCuts>(s_ex, round & 1, c.warp, c.lane, c.rank, c.ranks, map, cut != 0, carry);
         if (c.live && valid > 0) {
-            if (p.saved) {
-                float* to = p.saved + (c.b * c.tiles + tile) * p.channels + c.ch;
+            if (saved) L::store(saved, h);
+            T* to = y;
+            if (valid == kTokens && cut == 0) {
 #pragma unroll
-                for (int k = 0; k < K; ++k) to[k] = h[k];
-            }
-            T* to = y + tile * kTokens * p.y_token;
+                for (int j = 0; j < kTokens; ++j, to += p.y_token) {
+                    h = L::fma(token<K>(f, j), h, token<K>(b, j));
+                    Tl::store(to, h);
+                }
+            } else {
 #pragma unroll
-            for (int j = 0; j < kTokens; ++j) {
-#pragma unroll
-                for (int k = 0; k < K; ++k) h[k] = through(f[j][k], b[j][k], cut >> j & 1u, h[k]);
-                if (j < valid) Cell<T, K>::store(to + j * p.y_token, h);
+                for (int j = 0; j < kTokens; ++j, to += p.y_token) {
+                    h = cut >> j & 1u ? token<K>(b, j) : L::fma(token<K>(f, j), h, token<K>(b, j));
+                    if (j < valid) Tl::store(to, h);
+                }
             }
         }
+        if (saved) saved += step * p.channels;
+        y += (long long)step * kTokens * p.y_token;
+        tile += step;
+        left -= step * kTokens;
     }
-    if (p.final_state && c.live && c.rank == 0 && c.warp == 0) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) p.final_state[c.b * p.channels + c.ch + k] = carry[k];
-    }
+    if (p.final_state && c.live && c.rank == 0 && c.warp == 0) L::store(p.final_state + c.b * p.channels + c.ch, carry);
     if (c.ranks > 1) cg::this_cluster().sync();  // no CTA leaves while another writes to its shared memory
 }
 
 // --------------------------------------------------------------- gradient
 // Warps, CTAs and rounds count from the end of the row.
-template <class T, int K, bool kSigmoid, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, (K == 2 ? 12 : 16) / kWarps) gated_grad_kernel(GatedParams p) {
-    __shared__ Exchange<K, kWarps> s_ex;
+template <class T, int K, bool kSigmoid, int kWarps, bool kCuts>
+__global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) gated_grad_kernel(GatedParams p) {
+    using L = Lane<K>;
+    using V = typename L::V;
+    using Tl = Tile<T, K>;
+    extern __shared__ __align__(16) unsigned char s_mem[];
+    Exchange<K, kWarps>& s_ex = *reinterpret_cast<Exchange<K, kWarps>*>(s_mem);
     const Place c = place_of<K, kWarps>(p);
-    const T* x = static_cast<const T*>(p.x) + c.b * p.x_batch + c.ch;
-    const T* g = static_cast<const T*>(p.gate) + c.b * p.gate_batch + c.ch;
-    const T* dy = static_cast<const T*>(p.dy) + c.b * p.dy_batch + c.ch;
-    Cell<T, K> xr[kTokens], gr[kTokens], dr[kTokens];
-    float start[K];
-    uint32_t cuts;
-    auto tokens = [&](long long tile) {
-        return tile < 0 ? 0 : (int)max(0ll, min((long long)kTokens, p.length - tile * kTokens));
+    unsigned char* ring = s_mem + Exchange<K, kWarps>::bytes(c.ranks) + c.warp * (kGradStages * 3 * Tl::kBytes);
+    const int step = c.ranks * kWarps;
+    int tile = c.tiles - 1 - (c.rank * kWarps + c.warp);
+    Source<T, K> x(p.x, c.b * p.x_batch, p.x_token, tile, -step, c.ch0, p.channels, c.lane, p.wide);
+    Source<T, K> g(p.gate, c.b * p.gate_batch, p.gate_token, tile, -step, c.ch0, p.channels, c.lane, p.wide);
+    Source<T, K> dy(p.dy, c.b * p.dy_batch, p.dy_token, tile, -step, c.ch0, p.channels, c.lane, p.wide);
+    const long long to = (c.b * p.length + (long long)tile * kTokens) * p.channels + c.ch;
+    T *dx = static_cast<T*>(p.dx) + to, *dg = static_cast<T*>(p.dgate) + to;
+    // a warp's first tile ends with the row, those before the row's first are none
+    int ahead = tile;
+    auto tokens_of = [&](int t) { return t < 0 ? 0 : min(kTokens, (int)p.length - t * kTokens); };
+    unsigned char *fill = ring, *take = ring, *const end = ring + kGradStages * 3 * Tl::kBytes;
+    uint8_t head = 0;
+    V start = L::all(0.0f);
+    auto fetch = [&] {
+        const int left = tokens_of(ahead);
+        x.next(fill, left, c.lane);
+        g.next(fill + Tl::kBytes, left, c.lane);
+        dy.next(fill + 2 * Tl::kBytes, left, c.lane);
+        copies_end();
+        ahead -= step;
+        fill += 3 * Tl::kBytes;
+        if (fill == end) fill = ring;
     };
-    auto fetch = [&](long long tile) {
-        const long long t0 = tile * kTokens;
-        const int valid = c.live ? tokens(tile) : 0;
-        load_tile<T, K>(x + t0 * p.x_token, p.x_token, valid, xr);
-        load_tile<T, K>(g + t0 * p.gate_token, p.gate_token, valid, gr);
-        load_tile<T, K>(dy + t0 * p.dy_token, p.dy_token, valid, dr);
-        const float* from = p.saved + (c.b * c.tiles + tile) * p.channels + c.ch;
-#pragma unroll
-        for (int k = 0; k < K; ++k) start[k] = valid ? __ldg(from + k) : 0.0f;
-        cuts = tile < 0 ? 0u : cuts_of(p.heads, c.b, t0, p.length, c.lane);
+    const float* saved = p.saved + (c.b * c.tiles + tile) * p.channels + c.ch;
+    auto fetch_small = [&](int t) {  // a round ahead, in registers
+        if (c.live && t >= 0) start = L::load(saved);
+        saved -= step * p.channels;
+        if (kCuts) head = head_of(p.heads, c.b, (long long)t * kTokens, p.length, c.lane);
     };
-    float carry[K], q[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) carry[k] = p.dfinal && c.live ? __ldg(p.dfinal + c.b * p.channels + c.ch + k) : 0.0f;
-    const long long step = (long long)c.ranks * kWarps;
-    long long tile = c.tiles - 1 - ((long long)c.rank * kWarps + c.warp);
-    fetch(tile);
-    if (c.ranks > 1) cg::this_cluster().sync();  // every CTA has begun before one writes to its shared memory
-    for (long long round = 0; round < c.rounds; ++round, tile -= step) {
+    for (int r = 0; r < kGradStages - 1; ++r) fetch();
+    fetch_small(tile);
+    V carry = p.dfinal && c.live ? L::load(p.dfinal + c.b * p.channels + c.ch) : L::all(0.0f);
+    if (c.ranks > 1) cg::this_cluster().sync();
+    const V one = L::all(1.0f), minus = L::all(-1.0f), none = L::all(0.0f);
+    for (int round = 0; round < c.rounds; ++round) {
         // u: what dh is multiplied with for dgate; w: for dx (sigmoid), or f itself
-        float u[kTokens][K], w[kTokens][K], h[K];
-        Cell<T, K> d[kTokens];
-        const uint32_t cut = cuts;
-        const int valid = tokens(tile);
+        f2 u[kPairs<K>], w[kPairs<K>];
+        fetch();
+        copies_wait<kGradStages - 1>();
+        const Tl xr(take, c.lane), gr(take + Tl::kBytes, c.lane), d(take + 2 * Tl::kBytes, c.lane);
+        take += 3 * Tl::kBytes;
+        if (take == end) take = ring;
+        const uint32_t cut = kCuts ? cuts_of(head) : 0u;
+        const int valid = tokens_of(tile);
+        V h = start;
+        fetch_small(tile - step);
+        if constexpr (kSigmoid) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) h[k] = start[k];
-#pragma unroll
-        for (int j = 0; j < kTokens; ++j) {
-            d[j] = dr[j];
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const float xv = xr[j].get(k), gv = gr[j].get(k);
-                if (cut >> j & 1u) h[k] = 0.0f;
-                if constexpr (kSigmoid) {
-                    float f;
-                    gate_of<T>(gv, f, w[j][k]);
-                    u[j][k] = (h[k] - xv) * (f * w[j][k]);
-                    h[k] = fmaf(f, h[k], w[j][k] * xv);
-                } else {
-                    w[j][k] = gv;
-                    u[j][k] = h[k];
-                    h[k] = cut >> j & 1u ? xv : fmaf(gv, h[k], xv);
-                }
+            for (int i = 0; i < kPairs<K>; ++i) {
+                f2 f;
+                gates<T>(gr.pair(i), f, w[i]);
+                u[i] = f;
             }
         }
-        if (round + 1 < c.rounds) fetch(tile - step);
+#pragma unroll
+        for (int j = 0; j < kTokens; ++j) {
+            const V xv = xr.get(j);
+            if (kCuts && (cut >> j & 1u)) h = none;
+            if constexpr (kSigmoid) {
+                const V f = token<K>(u, j), r = token<K>(w, j);
+                set_token<K>(u, j, L::mul(L::fma(xv, minus, h), L::mul(f, r)));
+                h = L::fma(f, h, L::mul(r, xv));
+            } else {
+                const V f = gr.get(j);
+                set_token<K>(w, j, f);
+                set_token<K>(u, j, h);
+                h = kCuts && (cut >> j & 1u) ? xv : L::fma(f, h, xv);
+            }
+        }
         if (valid < kTokens) {  // behind the row's end: q stays
 #pragma unroll
             for (int j = 0; j < kTokens; ++j)
-#pragma unroll
-                for (int k = 0; k < K; ++k)
-                    if (j >= valid) w[j][k] = kSigmoid ? 0.0f : 1.0f;
+                if (j >= valid) set_token<K>(w, j, kSigmoid ? none : one);
         }
-        // f from 1 - f: it adds to q with its absolute error, 2^-25
-        auto decay_at = [&](int j, int k) { return kSigmoid ? 1.0f - w[j][k] : w[j][k]; };
-        float A[K], B[K];
+        // f from 1 - f: it enters with its absolute error
+        auto decay_of = [&](int j) { return kSigmoid ? L::fma(token<K>(w, j), minus, one) : token<K>(w, j); };
+        Map<K> map{one, none};
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            A[k] = 1.0f;
-            B[k] = 0.0f;
+        for (int j = kTokens - 1; j >= 0; --j) {
+            const V f = decay_of(j);
+            map.A = L::mul(map.A, f);
+            map.B = L::mul(f, L::add(d.get(j), map.B));
+            if (kCuts && (cut >> j & 1u)) map.B = none;
         }
-#pragma unroll
-        for (int j = kTokens - 1; j >= 0; --j)
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const float f = decay_at(j, k);
-                A[k] *= f;
-                B[k] = cut >> j & 1u ? 0.0f : f * (d[j].get(k) + B[k]);
-            }
-        exchange<K, kWarps>(s_ex, (int)(round & 1), c.warp, c.lane, c.rank, c.ranks, A, B, cut != 0, carry, q);
+        V q = exchange<K, kWarps, kCuts>(s_ex, round & 1, c.warp, c.lane, c.rank, c.ranks, map, cut != 0, carry);
         if (c.live && valid > 0) {
-            const long long to = (c.b * p.length + tile * kTokens) * p.channels + c.ch;
-            T* dx = static_cast<T*>(p.dx) + to;
-            T* dg = static_cast<T*>(p.dgate) + to;
+            T *tx = dx + (kTokens - 1) * p.channels, *tg = dg + (kTokens - 1) * p.channels;
 #pragma unroll
-            for (int j = kTokens - 1; j >= 0; --j) {
-                float ox[K], og[K];
-#pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    const float dh = d[j].get(k) + q[k];
-                    ox[k] = kSigmoid ? dh * w[j][k] : dh;
-                    og[k] = !kSigmoid && (cut >> j & 1u) ? 0.0f : dh * u[j][k];
-                    q[k] = cut >> j & 1u ? 0.0f : decay_at(j, k) * dh;
+            for (int j = kTokens - 1; j >= 0; --j, tx -= p.channels, tg -= p.channels) {
+                const V dh = L::add(d.get(j), q);
+                V og = L::mul(dh, token<K>(u, j));
+                q = L::mul(decay_of(j), dh);
+                if (kCuts && (cut >> j & 1u)) {
+                    q = none;
+                    if (!kSigmoid) og = none;
                 }
                 if (j < valid) {
-                    Cell<T, K>::store(dx + j * p.channels, ox);
-                    Cell<T, K>::store(dg + j * p.channels, og);
+                    Tl::store(tx, kSigmoid ? L::mul(dh, token<K>(w, j)) : dh);
+                    Tl::store(tg, og);
                 }
             }
         }
+        __syncwarp();  // the tile is read: the next round's copies may take its place
+        tile -= step;
+        dx -= (long long)step * kTokens * p.channels;
+        dg -= (long long)step * kTokens * p.channels;
     }
-    if (p.dstate && c.live && c.rank == 0 && c.warp == 0) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) p.dstate[c.b * p.channels + c.ch + k] = carry[k];
-    }
+    if (p.dstate && c.live && c.rank == 0 && c.warp == 0) L::store(p.dstate + c.b * p.channels + c.ch, carry);
     if (c.ranks > 1) cg::this_cluster().sync();
 }
 
@@ -468,9 +580,9 @@ __global__ void __launch_bounds__(kStepNT) gated_step_kernel(GatedParams p) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         if constexpr (kSigmoid) {
-            float f, rest;
-            gate_of<T>(g[k], f, rest);
-            h[k] = fmaf(f, h[k], rest * x[k]);
+            f2 f, rest;
+            gates<T>(both(g[k]), f, rest);
+            h[k] = fmaf(lo2(f), h[k], lo2(rest) * x[k]);
         } else {
             h[k] = fmaf(g[k], h[k], x[k]);
         }
@@ -492,40 +604,64 @@ __global__ void __launch_bounds__(kStepNT) gated_step_kernel(GatedParams p) {
 }
 
 // ---------------------------------------------------------------- launch
-// CTAs in a cluster: enough that the machine has about two CTAs an SM, but no more
-// than the length has rounds for.
-inline int cluster_of(long long groups, long long tiles, int warps) {
-    int n = 1;
-    while (n < kMaxCluster && groups * n < 2 * seq_sms() && (long long)n * warps < tiles) n *= 2;
-    return n;
+// The machine holds 16 warps an SM (128 registers a thread).  CTAs of 4 warps where the
+// rows and channels alone make enough of them (a round's fold is half as long, and they
+// fill the SMs more evenly), else of 8.  CTAs in a cluster: until there are 12 warps an
+// SM or the length has no more tiles; and while the last wave of CTAs is mostly empty,
+// up to 4.
+struct Split {
+    int warps, ctas;
+};
+inline Split split_of(long long groups, long long tiles) {
+    const long long sms = seq_sms();
+    Split s{groups * 4 >= 12 * sms || tiles <= 4 ? 4 : 8, 1};
+    const long long slots = 16 / s.warps * sms;
+    auto more = [&] {
+        if ((long long)s.ctas * s.warps >= tiles) return false;
+        const long long n = groups * s.ctas;
+        if (n * s.warps < 12 * sms) return s.ctas < kMaxCluster;
+        return n > slots && s.ctas < 4 && n * 5 < (n + slots - 1) / slots * slots * 4;
+    };
+    while (more()) s.ctas *= 2;
+    return s;
 }
 
-template <class T, int K, bool kSigmoid, int kWarps>
-cudaError_t go(const GatedParams& p, bool grad, cudaStream_t s) {
-    const long long tiles = (p.length + kTokens - 1) / kTokens, groups = p.batch * ((p.channels + 32 * K - 1) / (32 * K));
-    const int n = cluster_of(groups, tiles, kWarps);
+template <class T, int K, bool kSigmoid, int kWarps, bool kCuts>
+cudaError_t go(const GatedParams& p, bool grad, long long groups, int ctas, cudaStream_t s) {
+    const void* kernel = grad ? (const void*)gated_grad_kernel<T, K, kSigmoid, kWarps, kCuts>
+                              : (const void*)gated_kernel<T, K, kSigmoid, kWarps, kCuts>;
+    const int bytes = (int)Exchange<K, kWarps>::bytes(ctas) + kWarps * Tile<T, K>::kBytes * (grad ? 3 * kGradStages : 2 * kStages);
+    // the limit is one per device: always the largest, whatever this call needs
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         bytes - (int)Exchange<K, kWarps>::bytes(ctas) + (int)Exchange<K, kWarps>::bytes(kMaxCluster));
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(groups * n));
+    cfg.gridDim = dim3((unsigned)(groups * ctas));
     cfg.blockDim = dim3(32 * kWarps);
+    cfg.dynamicSmemBytes = (size_t)bytes;
     cfg.stream = s;
     cudaLaunchAttribute a{};
     a.id = cudaLaunchAttributeClusterDimension;
-    a.val.clusterDim.x = (unsigned)n;
+    a.val.clusterDim.x = (unsigned)ctas;
     a.val.clusterDim.y = a.val.clusterDim.z = 1;
     cfg.attrs = &a;
     cfg.numAttrs = 1;
-    const cudaError_t e = grad ? cudaLaunchKernelEx(&cfg, gated_grad_kernel<T, K, kSigmoid, kWarps>, p)
-                               : cudaLaunchKernelEx(&cfg, gated_kernel<T, K, kSigmoid, kWarps>, p);
+    GatedParams args = p;
+    void* argv[] = {&args};
+    e = cudaLaunchKernelExC(&cfg, kernel, argv);
     count_launches(1);
     return e;
 }
 
 template <class T, int K, bool kSigmoid>
 cudaError_t by_length(const GatedParams& p, bool grad, cudaStream_t s) {
-    const long long tiles = (p.length + kTokens - 1) / kTokens;
-    if (tiles <= 1) return go<T, K, kSigmoid, 1>(p, grad, s);
-    if (tiles <= 4) return go<T, K, kSigmoid, 4>(p, grad, s);
-    return go<T, K, kSigmoid, 8>(p, grad, s);
+    const long long tiles = (p.length + kTokens - 1) / kTokens, groups = p.batch * ((p.channels + 32 * K - 1) / (32 * K));
+    const Split split = split_of(groups, tiles);
+    if (split.warps == 4)
+        return p.heads ? go<T, K, kSigmoid, 4, true>(p, grad, groups, split.ctas, s)
+                       : go<T, K, kSigmoid, 4, false>(p, grad, groups, split.ctas, s);
+    return p.heads ? go<T, K, kSigmoid, 8, true>(p, grad, groups, split.ctas, s)
+                   : go<T, K, kSigmoid, 8, false>(p, grad, groups, split.ctas, s);
 }
 
 template <class T, int K>

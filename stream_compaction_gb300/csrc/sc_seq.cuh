@@ -191,6 +191,11 @@ __device__ __forceinline__ float capped(float a) {  // beyond 104 nothing change
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(104.0f));
     return r;
 }
+__device__ __forceinline__ float at_least(float v, float least) {  // NaN stays
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(least));
+    return r;
+}
 template <bool kFine>
 __device__ __forceinline__ float exp_minus(float a) {
     if constexpr (!kFine) {

@@ -136,6 +136,7 @@ struct GatedParams {
     float* final_state;
     float* saved;
     int pairs;  // elements two by two: aligned, channels even
+    int wide;   // rows of what is read in 16-byte chunks
     // gradient
     const void* dy;
     long long dy_batch, dy_token;

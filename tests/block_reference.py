@@ -18,16 +18,16 @@ Gradient, with dn as above (m and r are those that were saved), g = dy w:
   dx: r (da + |n| db + |b| dn + 6 EPS (|g| + |a| + |n b|)) + dr |dx| + EPS |dsum|
   dweight: sum |dy| dn + rows EPS sum |dy n|;  dbias: rows EPS sum |dy|.
 
-Gated recurrence.  s = e / (1 + e), e = exp(-|g|): the exponential's own error of 4 EPS
-and, with 16-bit elements, |g| EPS of its argument; sum, reciprocal and product 4: s is
-off by C = 8 + |g| <= 24 relative, 1 - s by C min(f, 1 - f) + 1 absolute, in EPS.
-Without the sigmoid C = 0.  With m the recurrence over absolute values:
-  eh[t] = f eh[t-1] + (C + 8) EPS (f m[t-1] + |b[t]|),
+Gated recurrence.  rest = 1 - f = e / (1 + e), e = exp(-g): the exponential's own error
+of 4 EPS and, with 16-bit elements, |g| EPS of its argument; sum, reciprocal and product
+4: rest is off by C = 8 + |g| <= 24 relative, and f = 1 - rest by C rest + 1 absolute, in
+EPS.  Without the sigmoid both are exact.  With m the recurrence over absolute values
+and F = C rest + 1 (0 without the sigmoid):
+  eh[t] = f eh[t-1] + (F + 8 f) EPS m[t-1] + (C + 8) EPS |b[t]|,
 where 8 covers the product and sum of a step and a step's share of the maps of whole
 tiles (16 products and the like a tile); a tile's fold over warps and CTAs adds at most
-2 EPS for each of up to 16 of them: 32 EPS m once.  Backwards, where f is taken as 1 -
-(1 - f) and so is off by (C min(f, 1 - f) + 2) EPS absolute:
-  ed[t] = f ed[t+1] + ((C + 8) f + 4) EPS md[t+1], + 32 EPS md once.
+2 EPS for each of up to 16 of them: 32 EPS m once.  Backwards the same:
+  ed[t] = f ed[t+1] + (F + 8 f) EPS md[t+1], + 32 EPS md once.
 
 Experts.  A token's sum of k terms: (k + 1) EPS sum |w y|; a product of dim elements:
 (dim + 2) EPS sum |dout y|; products: EPS.
@@ -116,7 +116,8 @@ def gated(x, gate, activation="sigmoid", heads=None, state=None, dy=None, dfinal
         eb.append(e)
         b = rest[:, t] * x[:, t]
         ft = torch.where(keep[:, t], f[:, t], 0.0)
-        e = ft.abs() * e + (C + 8) * EPS * (ft.abs() * m + b.abs())
+        off = torch.where(keep[:, t], (C * rest[:, t] + 1 if C else 0.0) + 8 * ft.abs(), 0.0)  # of f, and a step's roundings
+        e = ft.abs() * e + EPS * (off * m + (C + 8) * b.abs())
         h = ft * h + b
         m = ft.abs() * m + b.abs()
         y.append(h)
@@ -142,10 +143,13 @@ def gated(x, gate, activation="sigmoid", heads=None, state=None, dy=None, dfinal
             u, scale, mu = before[t] - x[:, t], f[:, t] * w, mb[t] + x[:, t].abs()
             eu = eb[t] + EPS * mu
         dg.append(dh * u * scale)
-        edg.append((eh * u.abs() + dh.abs() * (eu + 32 * EPS * mu) + (2 * C + 8) * EPS * (dh * u).abs()) * scale)
+        # f and rest in dgate: rest's error relative, f's absolute
+        edg.append((eh * u.abs() + dh.abs() * (eu + 32 * EPS * mu) + (C + 8) * EPS * (dh * u).abs()) * scale
+                   + ((C * w + 1) * w * EPS * (dh * u).abs() if C else 0.0))
         ft = torch.where(keep[:, t], f[:, t], 0.0).abs()
         live = keep[:, t]
-        eq = ft * (eq + EPS * mh) + torch.where(live, ((C + 8) * ft + 4) * EPS * mh, 0.0)
+        off = torch.where(live, (C * w + 1 if C else 0.0) + 8 * ft, 0.0)
+        eq = ft * (eq + EPS * mh) + off * EPS * mh
         q, mq = torch.where(live, f[:, t], 0.0) * dh, ft * mh
     rev = lambda v: stack(v[::-1])  # noqa: E731
     return out | {"dx": (rev(dx), rev(edx)), "dgate": (rev(dg), rev(edg)), "dstate": (q, eq + 32 * EPS * mq)}
