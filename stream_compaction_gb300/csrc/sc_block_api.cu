@@ -57,6 +57,17 @@ Tensor gated_state(const sc_gated_desc* d, const float* p) { return flat(p, d->b
 Tensor gated_saved(const sc_gated_desc* d, const float* p) {
     return flat(p, d->batch * ((d->length + SC_GATED_SAVE - 1) / SC_GATED_SAVE) * d->channels, 4);
 }
+// Whether the copy engine takes every tensor: rows aligned to 16 bytes, strides below
+// 2^40 bytes and not 0, indices of 32 bits.
+bool gated_wide(const sc_gated_desc* d, std::initializer_list<Tensor> all) {
+    const int eb = bytes_of(d->dtype), e = 16 / eb;
+    if (d->channels % e != 0 || d->channels > kMaxGrid || d->batch > kMaxGrid) return false;
+    for (const Tensor& t : all) {
+        const int64_t most = (((int64_t)1 << 40) - 1) / eb;
+        if (!t.vec(e) || (t.tokens > 1 && (t.st == 0 || t.st > most)) || (t.batch > 1 && (t.sb == 0 || t.sb > most))) return false;
+    }
+    return true;
+}
 
 // ---------------------------------------------------------------- norm
 // A tensor's rows follow one another with one stride.
@@ -186,8 +197,7 @@ sc_status sc_gated_scan(const sc_gated_desc* d, void* y, int64_t y_batch, int64_
     p.final_state = final_state;
     p.saved = saved;
     p.pairs = d->channels % 2 == 0 && x.vec(2) && g.vec(2) && o.vec(2);
-    const int e = 16 / bytes_of(d->dtype);
-    p.wide = d->channels % e == 0 && x.vec(e) && g.vec(e);
+    p.wide = gated_wide(d, {x, g, o});
     return status_of(launch_gated(d->dtype, p, cu(stream)));
 }
 
@@ -218,8 +228,7 @@ sc_status sc_gated_scan_grad(const sc_gated_desc* d, const void* dy, int64_t dy_
     p.dgate = dgate;
     p.dstate = dstate;
     p.pairs = d->channels % 2 == 0 && x.vec(2) && g.vec(2) && e.vec(2) && out[0].vec(2) && out[1].vec(2);
-    const int wide = 16 / bytes_of(d->dtype);
-    p.wide = d->channels % wide == 0 && x.vec(wide) && g.vec(wide) && e.vec(wide);
+    p.wide = gated_wide(d, {x, g, e, out[0], out[1]});
     return status_of(launch_gated_grad(d->dtype, p, cu(stream)));
 }
 

@@ -32,6 +32,8 @@
 
 #include "sc_seq.cuh"
 #include "sc_seq_launch.h"
+#include "sc_tensor_map.h"
+#include "sc_tma.cuh"
 
 namespace scg {
 
@@ -40,20 +42,39 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kTokens = SC_GATED_SAVE;
-constexpr int kStages = 3, kGradStages = 2;
 constexpr int kMaxCluster = 8;
 
-template <int kBytes>
-__device__ __forceinline__ void copy_async(unsigned char* to, const void* from) {
-    const uint32_t s = (uint32_t)__cvta_generic_to_shared(to);
-    if constexpr (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(from) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s), "l"(from) : "memory");
+__device__ __forceinline__ void copy_async(void* to, const void* from) {  // 4 bytes
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
 }
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kAhead>  // all but the last kAhead groups of copies have arrived, for the whole warp
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
     __syncwarp();
+}
+
+// Tensor maps of a call: forward x, gate and y; backward x, gate, dy, dx and dgate.
+struct GatedMaps {
+    CUtensorMap map[5];
+};
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c, int t, int b, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(t), "r"(b), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int c, int t, int b, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(t), "r"(b), "r"(src)
+                 : "memory");
+}
+// The end of a tile's copies, for the whole warp.  They end by themselves; a wait that
+// should run out all the same (a second or so) gives up, and the tile counts as NaN.
+__device__ __forceinline__ bool arrived(uint32_t bar, uint32_t parity) {
+    for (int i = 0; i < (1 << 20); ++i)
+        if (mbar_try_wait_sleep(bar, parity, 1000)) return true;
+    return false;
 }
 
 // A lane's K channels of a token: as they lie in memory, and as one operand.
@@ -131,6 +152,10 @@ struct Tile {
         if constexpr (K == 2) return pair(j);
         else return one(at[j * 32]);
     }
+    // The result of token j in place of what was read there.
+    __device__ __forceinline__ void put(int j, typename Lane<K>::V v) const {
+        store(reinterpret_cast<T*>(const_cast<R*>(at)) + j * 32 * K, v);
+    }
     static __device__ __forceinline__ void store(T* p, typename Lane<K>::V v) {
         if constexpr (K == 2) {
             const float f[2] = {lo2(v), hi2(v)};
@@ -143,53 +168,37 @@ struct Tile {
     }
 };
 
-// Where a warp's tiles of a tensor come from.  Rows that are aligned to 16 bytes go by
-// chunks of 16 (8 or 4 lanes a token), others by a lane's own channels; single 16-bit
-// elements are too small for an asynchronous copy and go through registers.
+// Where a warp's tiles of a tensor come from whose rows are not aligned to 16 bytes: a
+// lane's channels by asynchronous copies of 4 bytes; single 16-bit elements are too
+// small for those and go through registers.
 template <class T, int K>
 struct Source {
     using R = typename Raw<T, K>::type;
-    static constexpr int kChunks = 32 * (int)sizeof(R) / 16, kRows = 32 / kChunks;
-    const T* p;         // the lane's part of the next tile's first token (or first of kRows)
+    const T* p;         // the lane's channels of the next tile's first token
     long long stride;   // of a token
     long long advance;  // from a tile to the warp's next
-    bool wide, mine;
-    __device__ __forceinline__ Source(const void* base, long long row, long long token, long long tile, long long step,
-                                      long long ch0, long long channels, int lane, bool wide_)
-        : stride(token), advance(step * kTokens * token), wide(wide_ && K * sizeof(T) > 2) {
-        const int first = wide ? lane / kChunks : 0, ch = wide ? lane % kChunks * (16 / (int)sizeof(T)) : lane * K;
-        p = static_cast<const T*>(base) + row + (tile * kTokens + first) * token + ch0 + ch;
-        mine = ch0 + ch < channels;
-    }
+    bool mine;
+    __device__ __forceinline__ Source(const void* base, long long row, long long token, int tile, int step, long long ch0,
+                                      long long channels, int lane)
+        : p(static_cast<const T*>(base) + row + (long long)tile * kTokens * token + ch0 + lane * K), stride(token),
+          advance((long long)step * kTokens * token), mine(ch0 + lane * K < channels) {}
     // The next tile, of which the row has `left` tokens (zeros for the others), to `tile`.
     __device__ __forceinline__ void next(unsigned char* tile, int left, int lane) {
         const T* q = p;
         p += advance;
         if (!mine) return;
-        if constexpr (K * sizeof(T) == 2) {
-            unsigned short v[kTokens];
+        R* to = reinterpret_cast<R*>(tile) + lane;
+        if constexpr (sizeof(R) == 2) {
+            R v[kTokens];
 #pragma unroll
-            for (int j = 0; j < kTokens; ++j) v[j] = j < left ? __ldg(reinterpret_cast<const unsigned short*>(q + j * stride)) : 0;
+            for (int j = 0; j < kTokens; ++j) v[j] = j < left ? __ldg(reinterpret_cast<const R*>(q + j * stride)) : R(0);
 #pragma unroll
-            for (int j = 0; j < kTokens; ++j) reinterpret_cast<unsigned short*>(tile)[j * 32 + lane] = v[j];
-        } else if (wide) {
-            unsigned char* to = tile + lane * 16;  // the lanes' chunks follow one another, kRows tokens at a time
-            if (left >= kTokens) {
-#pragma unroll
-                for (int j = 0; j < kTokens / kRows; ++j) copy_async<16>(to + j * 512, q + j * kRows * stride);
-            } else {
-#pragma unroll
-                for (int j = 0; j < kTokens / kRows; ++j) {
-                    if (j * kRows + lane / kChunks < left) copy_async<16>(to + j * 512, q + j * kRows * stride);
-                    else *reinterpret_cast<uint4*>(to + j * 512) = make_uint4(0u, 0u, 0u, 0u);
-                }
-            }
+            for (int j = 0; j < kTokens; ++j) to[j * 32] = v[j];
         } else {
-            unsigned char* to = tile + lane * 4;
 #pragma unroll
             for (int j = 0; j < kTokens; ++j) {
-                if (j < left) copy_async<4>(to + j * 128, q + j * stride);
-                else *reinterpret_cast<uint32_t*>(to + j * 128) = 0u;
+                if (j < left) copy_async(to + j * 32, q + j * stride);
+                else to[j * 32] = R(0);
             }
         }
     }
@@ -321,44 +330,96 @@ __device__ __forceinline__ Place place_of(const GatedParams& p) {
     return c;
 }
 
+// A warp's ring of rounds, kTensors tiles each.  kTma: whole tiles by the copy engine,
+// one instruction of one lane, results back the same way from where the elements lay.
+template <class T, int K, int kTensors, int kStages, bool kTma>
+struct Ring {
+    using Tl = Tile<T, K>;
+    static constexpr int kRound = kTensors * Tl::kBytes, kBytes = kStages * kRound;
+    unsigned char *base, *fill, *take;
+    uint32_t bar, phase = 0;  // kTma: the stages' barriers, the parity of the round to take
+    __device__ __forceinline__ Ring(unsigned char* mem, uint64_t* bars, int lane) : base(mem), fill(mem), take(mem), bar(smem_u32(bars)) {
+        if constexpr (kTma) {
+            if (lane == 0) {
+#pragma unroll
+                for (int i = 0; i < kStages; ++i) mbar_init(bar + 8 * i, 1);
+                fence_mbar_init();
+            }
+            __syncwarp();
+        }
+    }
+    __device__ __forceinline__ void next(unsigned char*& at) {
+        at += kRound;
+        if (at == base + kBytes) at = base;
+    }
+    // The tiles of tokens t0 .. of row b (kTma), by one lane; what the stage held has
+    // been read, by the copies of results out of it, too.
+    __device__ __forceinline__ void load(const GatedMaps& m, int ch0, int t0, int b) {
+        bulk_wait_read_all();
+        const uint32_t full = bar + (uint32_t)(fill - base) / kRound * 8, to = smem_u32(fill);
+        mbar_arrive_expect_tx(full, kRound);
+#pragma unroll
+        for (int i = 0; i < kTensors; ++i) tma_load_3d(to + i * Tl::kBytes, &m.map[i], ch0, t0, b, full);
+    }
+    __device__ __forceinline__ bool wait() {
+        const uint32_t full = bar + (uint32_t)(take - base) / kRound * 8;
+        const bool ok = arrived(full, phase);
+        if (take + kRound == base + kBytes) phase ^= 1;
+        return ok;
+    }
+};
+template <int K, int kWarps, class Ring> struct Shared {
+    unsigned char ring[kWarps][Ring::kBytes];  // first: the copy engine wants 128 bytes' alignment
+    uint64_t bars[kWarps][4];
+    Exchange<K, kWarps> ex;  // last: its size goes by the cluster
+    static __host__ __device__ constexpr size_t bytes(int ctas) {
+        return sizeof(Shared) - sizeof(Exchange<K, kWarps>) + Exchange<K, kWarps>::bytes(ctas);
+    }
+};
+
 // ---------------------------------------------------------------- forward
-template <class T, int K, bool kSigmoid, int kWarps, bool kCuts>
-__global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) gated_kernel(GatedParams p) {
+template <class T, int K, bool kTma> using ForwardRing = Ring<T, K, 2, 3, kTma>;
+
+template <class T, int K, bool kTma, bool kSigmoid, int kWarps, bool kCuts>
+__global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
+    gated_kernel(GatedParams p, const __grid_constant__ GatedMaps maps) {
     using L = Lane<K>;
     using V = typename L::V;
     using Tl = Tile<T, K>;
-    extern __shared__ __align__(16) unsigned char s_mem[];
-    Exchange<K, kWarps>& s_ex = *reinterpret_cast<Exchange<K, kWarps>*>(s_mem);
+    using Rg = ForwardRing<T, K, kTma>;
+    extern __shared__ __align__(128) unsigned char s_mem[];
+    Shared<K, kWarps, Rg>& s = *reinterpret_cast<Shared<K, kWarps, Rg>*>(s_mem);
     const Place c = place_of<K, kWarps>(p);
-    unsigned char* ring = s_mem + Exchange<K, kWarps>::bytes(c.ranks) + c.warp * (kStages * 2 * Tl::kBytes);
     const int step = c.ranks * kWarps;
     int tile = c.rank * kWarps + c.warp;
-    Source<T, K> x(p.x, c.b * p.x_batch, p.x_token, tile, step, c.ch0, p.channels, c.lane, p.wide);
-    Source<T, K> g(p.gate, c.b * p.gate_batch, p.gate_token, tile, step, c.ch0, p.channels, c.lane, p.wide);
+    Rg ring(s.ring[c.warp], s.bars[c.warp], c.lane);
+    Source<T, K> x(p.x, c.b * p.x_batch, p.x_token, tile, step, c.ch0, p.channels, c.lane);
+    Source<T, K> g(p.gate, c.b * p.gate_batch, p.gate_token, tile, step, c.ch0, p.channels, c.lane);
     T* y = static_cast<T*>(p.y) + c.b * p.y_batch + (long long)tile * kTokens * p.y_token + c.ch;
     float* saved = p.saved ? p.saved + (c.b * c.tiles + tile) * p.channels + c.ch : nullptr;
     int left = (int)p.length - tile * kTokens, left_ahead = left;  // tokens from a tile's start to the row's end
-    unsigned char *fill = ring, *take = ring, *const end = ring + kStages * 2 * Tl::kBytes;
     uint8_t head = 0;
     auto fetch = [&] {
-        x.next(fill, left_ahead, c.lane);
-        g.next(fill + Tl::kBytes, left_ahead, c.lane);
-        copies_end();
+        if constexpr (kTma) {
+            if (c.lane == 0 && left_ahead > 0) ring.load(maps, (int)c.ch0, (int)p.length - left_ahead, (int)c.b);
+        } else {
+            x.next(ring.fill, left_ahead, c.lane);
+            g.next(ring.fill + Tl::kBytes, left_ahead, c.lane);
+            copies_end();
+        }
         left_ahead -= step * kTokens;
-        fill += 2 * Tl::kBytes;
-        if (fill == end) fill = ring;
+        ring.next(ring.fill);
     };
-#pragma unroll
-    for (int r = 0; r < kStages - 1; ++r) fetch();
+    fetch();
+    fetch();
     if (kCuts) head = head_of(p.heads, c.b, tile * kTokens, p.length, c.lane);
     V carry = p.state && c.live ? L::load(p.state + c.b * p.channels + c.ch) : L::all(0.0f);
     if (c.ranks > 1) cg::this_cluster().sync();  // every CTA has begun before one writes to its shared memory
     for (int round = 0; round < c.rounds; ++round) {
-        fetch();
-        copies_wait<kStages - 1>();
-        const Tl xr(take, c.lane), gr(take + Tl::kBytes, c.lane);
-        take += 2 * Tl::kBytes;
-        if (take == end) take = ring;
+        bool ok = true;
+        if constexpr (kTma) ok = left <= 0 || ring.wait();
+        else copies_wait<1>();
+        const Tl xr(ring.take, c.lane), gr(ring.take + Tl::kBytes, c.lane);
         f2 f[kPairs<K>], b[kPairs<K>];
         const uint32_t cut = kCuts ? cuts_of(head) : 0u;
         if (kCuts) head = head_of(p.heads, c.b, (long long)(tile + step) * kTokens, p.length, c.lane);
@@ -381,7 +442,9 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) gated_kernel(GatedPa
                     set_token<K>(b, j, L::all(0.0f));
                 }
         }
-        __syncwarp();  // the tile is read: the next round's copies may take its place
+        if (!ok) set_token<K>(b, 0, L::all(__int_as_float(0x7fffffff)));
+        __syncwarp();  // every lane has read
+        fetch();
         Map<K> map{token<K>(f, 0), token<K>(b, 0)};
         if (!kCuts || cut == 0) {
 #pragma unroll
@@ -395,66 +458,77 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) gated_kernel(GatedPa
             for (int j = 1; j < kTokens; ++j)
                 map.B = cut >> j & 1u ? token<K>(b, j) : L::fma(token<K>(f, j), map.B, token<K>(b, j));
         }
-        V h = exchange<K, kWarps, kCuts>(s_ex, round & 1, c.warp, c.lane, c.rank, c.ranks, map, cut != 0, carry);
-        if (c.live && valid > 0) {
-            if (saved) L::store(saved, h);
-            T* to = y;
-            if (valid == kTokens && cut == 0) {
+        V h = exchange<K, kWarps, kCuts>(s.ex, round & 1, c.warp, c.lane, c.rank, c.ranks, map, cut != 0, carry);
+        if (saved && c.live && valid > 0) L::store(saved, h);
+        T* to = y;
 #pragma unroll
-                for (int j = 0; j < kTokens; ++j, to += p.y_token) {
-                    h = L::fma(token<K>(f, j), h, token<K>(b, j));
-                    Tl::store(to, h);
-                }
+        for (int j = 0; j < kTokens; ++j) {
+            h = kCuts && (cut >> j & 1u) ? token<K>(b, j) : L::fma(token<K>(f, j), h, token<K>(b, j));
+            if constexpr (kTma) {
+                xr.put(j, h);
             } else {
-#pragma unroll
-                for (int j = 0; j < kTokens; ++j, to += p.y_token) {
-                    h = cut >> j & 1u ? token<K>(b, j) : L::fma(token<K>(f, j), h, token<K>(b, j));
-                    if (j < valid) Tl::store(to, h);
-                }
+                if (c.live && j < valid) Tl::store(to, h);
+                to += p.y_token;
             }
         }
+        if constexpr (kTma) {
+            fence_proxy_async();
+            __syncwarp();
+            if (c.lane == 0 && valid > 0) {
+                tma_store_3d(&maps.map[2], (int)c.ch0, tile * kTokens, (int)c.b, smem_u32(ring.take));
+                bulk_commit();
+            }
+        }
+        ring.next(ring.take);
         if (saved) saved += step * p.channels;
         y += (long long)step * kTokens * p.y_token;
         tile += step;
         left -= step * kTokens;
     }
     if (p.final_state && c.live && c.rank == 0 && c.warp == 0) L::store(p.final_state + c.b * p.channels + c.ch, carry);
+    if (kTma && c.lane == 0) bulk_wait_read_all();
     if (c.ranks > 1) cg::this_cluster().sync();  // no CTA leaves while another writes to its shared memory
 }
 
 // --------------------------------------------------------------- gradient
+template <class T, int K, bool kTma> using BackwardRing = Ring<T, K, 3, 2, kTma>;
+
 // Warps, CTAs and rounds count from the end of the row.
-template <class T, int K, bool kSigmoid, int kWarps, bool kCuts>
-__global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) gated_grad_kernel(GatedParams p) {
+template <class T, int K, bool kTma, bool kSigmoid, int kWarps, bool kCuts>
+__global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
+    gated_grad_kernel(GatedParams p, const __grid_constant__ GatedMaps maps) {
     using L = Lane<K>;
     using V = typename L::V;
     using Tl = Tile<T, K>;
-    extern __shared__ __align__(16) unsigned char s_mem[];
-    Exchange<K, kWarps>& s_ex = *reinterpret_cast<Exchange<K, kWarps>*>(s_mem);
+    using Rg = BackwardRing<T, K, kTma>;
+    extern __shared__ __align__(128) unsigned char s_mem[];
+    Shared<K, kWarps, Rg>& s = *reinterpret_cast<Shared<K, kWarps, Rg>*>(s_mem);
     const Place c = place_of<K, kWarps>(p);
-    unsigned char* ring = s_mem + Exchange<K, kWarps>::bytes(c.ranks) + c.warp * (kGradStages * 3 * Tl::kBytes);
     const int step = c.ranks * kWarps;
     int tile = c.tiles - 1 - (c.rank * kWarps + c.warp);
-    Source<T, K> x(p.x, c.b * p.x_batch, p.x_token, tile, -step, c.ch0, p.channels, c.lane, p.wide);
-    Source<T, K> g(p.gate, c.b * p.gate_batch, p.gate_token, tile, -step, c.ch0, p.channels, c.lane, p.wide);
-    Source<T, K> dy(p.dy, c.b * p.dy_batch, p.dy_token, tile, -step, c.ch0, p.channels, c.lane, p.wide);
+    Rg ring(s.ring[c.warp], s.bars[c.warp], c.lane);
+    Source<T, K> x(p.x, c.b * p.x_batch, p.x_token, tile, -step, c.ch0, p.channels, c.lane);
+    Source<T, K> g(p.gate, c.b * p.gate_batch, p.gate_token, tile, -step, c.ch0, p.channels, c.lane);
+    Source<T, K> dy(p.dy, c.b * p.dy_batch, p.dy_token, tile, -step, c.ch0, p.channels, c.lane);
     const long long to = (c.b * p.length + (long long)tile * kTokens) * p.channels + c.ch;
     T *dx = static_cast<T*>(p.dx) + to, *dg = static_cast<T*>(p.dgate) + to;
     // a warp's first tile ends with the row, those before the row's first are none
     int ahead = tile;
     auto tokens_of = [&](int t) { return t < 0 ? 0 : min(kTokens, (int)p.length - t * kTokens); };
-    unsigned char *fill = ring, *take = ring, *const end = ring + kGradStages * 3 * Tl::kBytes;
     uint8_t head = 0;
     V start = L::all(0.0f);
     auto fetch = [&] {
-        const int left = tokens_of(ahead);
-        x.next(fill, left, c.lane);
-        g.next(fill + Tl::kBytes, left, c.lane);
-        dy.next(fill + 2 * Tl::kBytes, left, c.lane);
-        copies_end();
+        if constexpr (kTma) {
+            if (c.lane == 0 && ahead >= 0) ring.load(maps, (int)c.ch0, ahead * kTokens, (int)c.b);
+        } else {
+            const int n = tokens_of(ahead);
+            x.next(ring.fill, n, c.lane);
+            g.next(ring.fill + Tl::kBytes, n, c.lane);
+            dy.next(ring.fill + 2 * Tl::kBytes, n, c.lane);
+            copies_end();
+        }
         ahead -= step;
-        fill += 3 * Tl::kBytes;
-        if (fill == end) fill = ring;
+        ring.next(ring.fill);
     };
     const float* saved = p.saved + (c.b * c.tiles + tile) * p.channels + c.ch;
     auto fetch_small = [&](int t) {  // a round ahead, in registers
@@ -462,20 +536,19 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) gated_grad_kernel(Ga
         saved -= step * p.channels;
         if (kCuts) head = head_of(p.heads, c.b, (long long)t * kTokens, p.length, c.lane);
     };
-#pragma unroll
-    for (int r = 0; r < kGradStages - 1; ++r) fetch();
+    fetch();
     fetch_small(tile);
     V carry = p.dfinal && c.live ? L::load(p.dfinal + c.b * p.channels + c.ch) : L::all(0.0f);
     if (c.ranks > 1) cg::this_cluster().sync();
     const V one = L::all(1.0f), minus = L::all(-1.0f), none = L::all(0.0f);
     for (int round = 0; round < c.rounds; ++round) {
+        bool ok = true;
+        fetch();
+        if constexpr (kTma) ok = tile < 0 || ring.wait();
+        else copies_wait<1>();
+        const Tl xr(ring.take, c.lane), gr(ring.take + Tl::kBytes, c.lane), d(ring.take + 2 * Tl::kBytes, c.lane);
         // u: what dh is multiplied with for dgate; w: for dx (sigmoid), or f itself
         f2 u[kPairs<K>], w[kPairs<K>];
-        fetch();
-        copies_wait<kGradStages - 1>();
-        const Tl xr(take, c.lane), gr(take + Tl::kBytes, c.lane), d(take + 2 * Tl::kBytes, c.lane);
-        take += 3 * Tl::kBytes;
-        if (take == end) take = ring;
         const uint32_t cut = kCuts ? cuts_of(head) : 0u;
         const int valid = tokens_of(tile);
         V h = start;
@@ -508,40 +581,61 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) gated_grad_kernel(Ga
             for (int j = 0; j < kTokens; ++j)
                 if (j >= valid) set_token<K>(w, j, kSigmoid ? none : one);
         }
+        if (!ok) set_token<K>(w, 0, L::all(__int_as_float(0x7fffffff)));
         // f from 1 - f: it enters with its absolute error
         auto decay_of = [&](int j) { return kSigmoid ? L::fma(token<K>(w, j), minus, one) : token<K>(w, j); };
         Map<K> map{one, none};
+        if (valid > 0) {
 #pragma unroll
-        for (int j = kTokens - 1; j >= 0; --j) {
-            const V f = decay_of(j);
-            map.A = L::mul(map.A, f);
-            map.B = L::mul(f, L::add(d.get(j), map.B));
-            if (kCuts && (cut >> j & 1u)) map.B = none;
-        }
-        V q = exchange<K, kWarps, kCuts>(s_ex, round & 1, c.warp, c.lane, c.rank, c.ranks, map, cut != 0, carry);
-        if (c.live && valid > 0) {
-            T *tx = dx + (kTokens - 1) * p.channels, *tg = dg + (kTokens - 1) * p.channels;
-#pragma unroll
-            for (int j = kTokens - 1; j >= 0; --j, tx -= p.channels, tg -= p.channels) {
-                const V dh = L::add(d.get(j), q);
-                V og = L::mul(dh, token<K>(u, j));
-                q = L::mul(decay_of(j), dh);
-                if (kCuts && (cut >> j & 1u)) {
-                    q = none;
-                    if (!kSigmoid) og = none;
-                }
-                if (j < valid) {
-                    Tl::store(tx, kSigmoid ? L::mul(dh, token<K>(w, j)) : dh);
-                    Tl::store(tg, og);
-                }
+            for (int j = kTokens - 1; j >= 0; --j) {
+                const V f = decay_of(j);
+                map.A = L::mul(map.A, f);
+                map.B = L::mul(f, L::add(d.get(j), map.B));
+                if (kCuts && (cut >> j & 1u)) map.B = none;
             }
         }
-        __syncwarp();  // the tile is read: the next round's copies may take its place
+        V q = exchange<K, kWarps, kCuts>(s.ex, round & 1, c.warp, c.lane, c.rank, c.ranks, map, cut != 0, carry);
+        T *tx = dx + (kTokens - 1) * p.channels, *tg = dg + (kTokens - 1) * p.channels;
+#pragma unroll
+        for (int j = kTokens - 1; j >= 0; --j) {
+            const V dh = L::add(d.get(j), q);
+            V og = L::mul(dh, token<K>(u, j));
+            const V ox = kSigmoid ? L::mul(dh, token<K>(w, j)) : dh;
+            q = L::mul(decay_of(j), dh);
+            if (kCuts && (cut >> j & 1u)) {
+                q = none;
+                if (!kSigmoid) og = none;
+            }
+            if constexpr (kTma) {
+                xr.put(j, ox);
+                gr.put(j, og);
+            } else {
+                if (c.live && j < valid) {
+                    Tl::store(tx, ox);
+                    Tl::store(tg, og);
+                }
+                tx -= p.channels;
+                tg -= p.channels;
+            }
+        }
+        if constexpr (kTma) {
+            fence_proxy_async();
+            __syncwarp();
+            if (c.lane == 0 && valid > 0) {
+                tma_store_3d(&maps.map[3], (int)c.ch0, tile * kTokens, (int)c.b, smem_u32(ring.take));
+                tma_store_3d(&maps.map[4], (int)c.ch0, tile * kTokens, (int)c.b, smem_u32(ring.take + Tl::kBytes));
+                bulk_commit();
+            }
+        } else {
+            __syncwarp();  // every lane has read
+        }
+        ring.next(ring.take);
         tile -= step;
         dx -= (long long)step * kTokens * p.channels;
         dg -= (long long)step * kTokens * p.channels;
     }
     if (p.dstate && c.live && c.rank == 0 && c.warp == 0) L::store(p.dstate + c.b * p.channels + c.ch, carry);
+    if (kTma && c.lane == 0) bulk_wait_read_all();
     if (c.ranks > 1) cg::this_cluster().sync();
 }
 
@@ -626,19 +720,45 @@ inline Split split_of(long long groups, long long tiles) {
     return s;
 }
 
-template <class T, int K, bool kSigmoid, int kWarps, bool kCuts>
-cudaError_t go(const GatedParams& p, bool grad, long long groups, int ctas, cudaStream_t s) {
-    const void* kernel = grad ? (const void*)gated_grad_kernel<T, K, kSigmoid, kWarps, kCuts>
-                              : (const void*)gated_kernel<T, K, kSigmoid, kWarps, kCuts>;
-    const int bytes = (int)Exchange<K, kWarps>::bytes(ctas) + kWarps * Tile<T, K>::kBytes * (grad ? 3 * kGradStages : 2 * kStages);
+// Channels x tokens x rows, in boxes of a tile.
+template <class T, int K>
+bool map_of(CUtensorMap* m, const void* base, const GatedParams& p, long long batch, long long token) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = persist::tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)p.channels, (cuuint64_t)p.length, (cuuint64_t)p.batch};
+    // a stride that is not used (one row, one token) may be anything that the engine takes
+    const cuuint64_t row = (cuuint64_t)p.channels * sizeof(T);
+    const cuuint64_t strides[2] = {p.length > 1 ? (cuuint64_t)token * sizeof(T) : row,
+                                   p.batch > 1 ? (cuuint64_t)batch * sizeof(T) : row};
+    const cuuint32_t box[3] = {32 * K, kTokens, 1}, each[3] = {1, 1, 1};
+    const CUtensorMapDataType type = sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+    return enc(m, type, 3, const_cast<void*>(base), dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+template <class T, int K>
+bool maps_of(GatedMaps* m, const GatedParams& p, bool grad) {
+    if (!map_of<T, K>(&m->map[0], p.x, p, p.x_batch, p.x_token) || !map_of<T, K>(&m->map[1], p.gate, p, p.gate_batch, p.gate_token))
+        return false;
+    if (!grad) return map_of<T, K>(&m->map[2], p.y, p, p.y_batch, p.y_token);
+    const long long row = p.length * p.channels;
+    return map_of<T, K>(&m->map[2], p.dy, p, p.dy_batch, p.dy_token) && map_of<T, K>(&m->map[3], p.dx, p, row, p.channels) &&
+           map_of<T, K>(&m->map[4], p.dgate, p, row, p.channels);
+}
+
+template <class T, int K, bool kTma, bool kSigmoid, int kWarps, bool kCuts>
+cudaError_t go(const GatedParams& p, const GatedMaps& maps, bool grad, long long groups, int ctas, cudaStream_t s) {
+    const void* kernel = grad ? (const void*)gated_grad_kernel<T, K, kTma, kSigmoid, kWarps, kCuts>
+                              : (const void*)gated_kernel<T, K, kTma, kSigmoid, kWarps, kCuts>;
+    auto bytes = [&](int n) {
+        return (int)(grad ? Shared<K, kWarps, BackwardRing<T, K, kTma>>::bytes(n) : Shared<K, kWarps, ForwardRing<T, K, kTma>>::bytes(n));
+    };
     // the limit is one per device: always the largest, whatever this call needs
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         bytes - (int)Exchange<K, kWarps>::bytes(ctas) + (int)Exchange<K, kWarps>::bytes(kMaxCluster));
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(kMaxCluster));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(groups * ctas));
     cfg.blockDim = dim3(32 * kWarps);
-    cfg.dynamicSmemBytes = (size_t)bytes;
+    cfg.dynamicSmemBytes = (size_t)bytes(ctas);
     cfg.stream = s;
     cudaLaunchAttribute a{};
     a.id = cudaLaunchAttributeClusterDimension;
@@ -646,35 +766,38 @@ cudaError_t go(const GatedParams& p, bool grad, long long groups, int ctas, cuda
     a.val.clusterDim.y = a.val.clusterDim.z = 1;
     cfg.attrs = &a;
     cfg.numAttrs = 1;
-    GatedParams args = p;
-    void* argv[] = {&args};
-    e = cudaLaunchKernelExC(&cfg, kernel, argv);
+    void* args[] = {const_cast<GatedParams*>(&p), const_cast<GatedMaps*>(&maps)};
+    e = cudaLaunchKernelExC(&cfg, kernel, args);
     count_launches(1);
     return e;
 }
 
-template <class T, int K, bool kSigmoid>
+template <class T, int K, bool kTma, bool kSigmoid>
 cudaError_t by_length(const GatedParams& p, bool grad, cudaStream_t s) {
+    GatedMaps maps{};
+    if (kTma && !maps_of<T, K>(&maps, p, grad)) return cudaErrorInvalidValue;
     const long long tiles = (p.length + kTokens - 1) / kTokens, groups = p.batch * ((p.channels + 32 * K - 1) / (32 * K));
     const Split split = split_of(groups, tiles);
     if (split.warps == 4)
-        return p.heads ? go<T, K, kSigmoid, 4, true>(p, grad, groups, split.ctas, s)
-                       : go<T, K, kSigmoid, 4, false>(p, grad, groups, split.ctas, s);
-    return p.heads ? go<T, K, kSigmoid, 8, true>(p, grad, groups, split.ctas, s)
-                   : go<T, K, kSigmoid, 8, false>(p, grad, groups, split.ctas, s);
+        return p.heads ? go<T, K, kTma, kSigmoid, 4, true>(p, maps, grad, groups, split.ctas, s)
+                       : go<T, K, kTma, kSigmoid, 4, false>(p, maps, grad, groups, split.ctas, s);
+    return p.heads ? go<T, K, kTma, kSigmoid, 8, true>(p, maps, grad, groups, split.ctas, s)
+                   : go<T, K, kTma, kSigmoid, 8, false>(p, maps, grad, groups, split.ctas, s);
 }
 
-template <class T, int K>
+template <class T, int K, bool kTma>
 cudaError_t by_gate(const GatedParams& p, bool grad, cudaStream_t s) {
-    return p.sigmoid ? by_length<T, K, true>(p, grad, s) : by_length<T, K, false>(p, grad, s);
+    return p.sigmoid ? by_length<T, K, kTma, true>(p, grad, s) : by_length<T, K, kTma, false>(p, grad, s);
 }
 
 template <class T>
 cudaError_t launch_gated_as(const GatedParams& p, bool grad, cudaStream_t s) {
-    if constexpr (sizeof(T) == 2) {
-        if (p.pairs) return by_gate<T, 2>(p, grad, s);
+    constexpr int K = 4 / (int)sizeof(T);  // 4 bytes a lane
+    if (p.wide) return by_gate<T, K, true>(p, grad, s);
+    if constexpr (K == 2) {
+        if (!p.pairs) return by_gate<T, 1, false>(p, grad, s);
     }
-    return by_gate<T, 1>(p, grad, s);
+    return by_gate<T, K, false>(p, grad, s);
 }
 
 template <class T, int K>

@@ -1,15 +1,13 @@
 // Shared pieces of the persistent (TMA-pipelined) kernels: bounded mbarrier
-// waits, bit packing of carries into shared-memory slots, and the host-side
-// tensor-map encoder.
+// waits, bit packing of carries into shared-memory slots, and their tensor maps.
 #pragma once
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
-#include <mutex>
 
 #include "sc_device.cuh"
+#include "sc_tensor_map.h"
 #include "sc_tma.cuh"
 
 namespace scg {
@@ -64,22 +62,6 @@ __device__ __forceinline__ int vload(const int* p) { return *reinterpret_cast<co
 __device__ __forceinline__ void vstore(int* p, int v) { *reinterpret_cast<volatile int*>(p) = v; }
 
 // ------------------------------------------------------------- host side
-inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn_ptr = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* fn = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn_ptr = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-        else
-            cudaGetLastError();
-    });
-    return fn_ptr;
-}
-
 // The first `rows` rows of 128 bytes at `base`, boxes of `box_rows` rows,
 // 128-byte swizzle.  `base` must be 16-byte aligned.
 inline bool make_map(CUtensorMap* m, const void* base, unsigned long long rows, unsigned box_rows) {

@@ -136,7 +136,7 @@ struct GatedParams {
     float* final_state;
     float* saved;
     int pairs;  // elements two by two: aligned, channels even
-    int wide;   // rows of what is read in 16-byte chunks
+    int wide;   // rows aligned for the copy engine
     // gradient
     const void* dy;
     long long dy_batch, dy_token;
