@@ -241,56 +241,64 @@ struct Map {
 // What the warps and CTAs of a round exchange.
 template <int K, int kWarps>
 struct Exchange {
-    Map<K> warp[2][kWarps][32];
+    uint64_t bar[2];  // the other CTAs' maps have arrived
     int cut[2][kWarps], rank_cut[2][kMaxCluster];
+    Map<K> warp[2][kWarps][32];
     Map<K> rank[1][32];  // [2][CTAs] of them; a CTA by itself needs none
-    static __host__ __device__ constexpr size_t bytes(int ctas) { return sizeof(Exchange) + (ctas > 1 ? (2 * ctas - 1) * sizeof(Map<K>[32]) : 0); }
+    static __host__ __device__ constexpr size_t bytes(int ctas) {
+        return sizeof(Exchange) + (ctas > 1 ? (2 * ctas - 1) * sizeof(Map<K>[32]) : 0);
+    }
 };
+
+// Remote writes that are counted on a barrier of the CTA that they go to, so nothing has
+// to be waited for but the data themselves (a cluster barrier's release waits for all
+// that the CTA has written, results too: 8192 tokens of 2048 channels 41 us).
+__device__ __forceinline__ uint32_t at_rank(uint32_t address, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(address), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void send(uint32_t to, uint32_t bar, const Map<1>& m) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];"
+                 ::"r"(to), "r"(__float_as_uint(m.A)), "r"(__float_as_uint(m.B)), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void send(uint32_t to, uint32_t bar, const Map<2>& m) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];"
+                 ::"r"(to), "l"(m.A), "l"(m.B), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void send(uint32_t to, uint32_t bar, int v) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(to), "r"(v), "r"(bar) : "memory");
+}
+__device__ __forceinline__ bool arrived_from_cluster(uint32_t bar, uint32_t parity) {
+    for (int i = 0; i < (1 << 20); ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+        if (ok) return true;
+    }
+    return false;
+}
 
 // One round: takes this warp's map, returns the value before its tile and moves
 // `carry`, the value before the round, to behind it (the same in all warps).  Warps and
 // CTAs count in the direction of the recurrence.  Buffers alternate: a warp writes for
 // the next round while others still read this one's, and two rounds on a barrier lies
-// between.  kCuts: segments may start anywhere.
+// between (in a cluster: a CTA sends for a round when all its warps are through with
+// the one before, and gets no further until every other has).
+// kCuts: segments may start anywhere.
 template <int K, int kWarps, bool kCuts>
-__device__ __forceinline__ typename Lane<K>::V exchange(Exchange<K, kWarps>& x, int turn, int warp, int lane, int rank,
+__device__ __forceinline__ typename Lane<K>::V exchange(Exchange<K, kWarps>& x, int round, int warp, int lane, int rank,
                                                         int ranks, const Map<K>& map, bool cut,
                                                         typename Lane<K>::V& carry) {
     using V = typename Lane<K>::V;
+    const int turn = round & 1;
     x.warp[turn][warp][lane] = map;
     if (kCuts && lane == 0) x.cut[turn][warp] = cut;
     __syncthreads();
     V in = carry;
-    if (ranks > 1) {
-        // One warp writes to the other CTAs, so only its arrival has to wait for what it has
-        // written before; the others' stores of results need not be waited for.
-        if (warp != 0) {
-            asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-        } else {
-            const cg::cluster_group cluster = cg::this_cluster();
-            Map<K> all = x.warp[turn][0][lane];
-            bool any = kCuts && x.cut[turn][0] != 0;
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) {
-                const Map<K> m = x.warp[turn][w][lane];
-                const bool c = kCuts && x.cut[turn][w] != 0;
-                all.B = m.of(all.B, c);
-                all.A = Lane<K>::mul(m.A, all.A);
-                any |= c;
-            }
-            for (int r = 0; r < ranks; ++r) {
-                Exchange<K, kWarps>* other = cluster.map_shared_rank(&x, r);
-                other->rank[turn * ranks + rank][lane] = all;
-                if (kCuts && lane == 0) other->rank_cut[turn][rank] = any;
-            }
-            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-        }
-        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-        for (int r = 0; r < ranks; ++r) {
-            if (r == rank) in = carry;
-            carry = x.rank[turn * ranks + r][lane].of(carry, kCuts && x.rank_cut[turn][r] != 0);
-        }
-    }
     if (ranks == 1) {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
@@ -299,12 +307,52 @@ __device__ __forceinline__ typename Lane<K>::V exchange(Exchange<K, kWarps>& x, 
             if (w < warp) in = m.of(in, c);
             carry = m.of(carry, c);
         }
-    } else {
-#pragma unroll
-        for (int w = 0; w + 1 < kWarps; ++w)
-            if (w < warp) in = x.warp[turn][w][lane].of(in, kCuts && x.cut[turn][w] != 0);
+        return in;
     }
-    return in;
+    // the maps of the warps before this one, and of the CTA
+    Map<K> before{Lane<K>::all(1.0f), Lane<K>::all(0.0f)}, all = before;
+    bool before_cut = false, all_cut = false;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w == warp) {
+            before = all;
+            before_cut = all_cut;
+        }
+        const Map<K> m = x.warp[turn][w][lane];
+        const bool c = kCuts && x.cut[turn][w] != 0;
+        all.B = m.of(all.B, c);
+        all.A = Lane<K>::mul(m.A, all.A);
+        all_cut |= c;
+    }
+    const uint32_t bar = smem_u32(&x.bar[turn]), to = smem_u32(&x.rank[turn * ranks + rank][lane]);
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, (uint32_t)ranks * (32 * sizeof(Map<K>) + (kCuts ? 4 : 0)));
+    for (int r = warp; r < ranks; r += kWarps) {
+        send(at_rank(to, r), at_rank(bar, r), all);
+        if (kCuts && lane == 0) send(at_rank(smem_u32(&x.rank_cut[turn][rank]), r), at_rank(bar, r), (int)all_cut);
+    }
+    if (!arrived_from_cluster(bar, (uint32_t)(round >> 1) & 1u)) carry = Lane<K>::all(__int_as_float(0x7fffffff));
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+        if (r >= ranks) break;
+        if (r == rank) in = carry;
+        carry = x.rank[turn * ranks + r][lane].of(carry, kCuts && x.rank_cut[turn][r] != 0);
+    }
+    return before.of(in, kCuts && before_cut);
+}
+// Before the first round: every CTA's barriers stand before another writes to it.
+template <class E>
+__device__ __forceinline__ void exchange_begin(E& x, int ranks) {
+    if (ranks == 1) return;
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&x.bar[0]), 1);
+        mbar_init(smem_u32(&x.bar[1]), 1);
+        fence_mbar_init();
+    }
+    cg::this_cluster().sync();
+}
+// After the last: no CTA leaves while another writes to its shared memory.
+__device__ __forceinline__ void exchange_end(int ranks) {
+    if (ranks > 1) cg::this_cluster().sync();
 }
 
 // Where a CTA works: row b, the lane's first channel, the rounds.
@@ -414,7 +462,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
     fetch();
     if (kCuts) head = head_of(p.heads, c.b, tile * kTokens, p.length, c.lane);
     V carry = p.state && c.live ? L::load(p.state + c.b * p.channels + c.ch) : L::all(0.0f);
-    if (c.ranks > 1) cg::this_cluster().sync();  // every CTA has begun before one writes to its shared memory
+    exchange_begin(s.ex, c.ranks);
     for (int round = 0; round < c.rounds; ++round) {
         bool ok = true;
         if constexpr (kTma) ok = left <= 0 || ring.wait();
@@ -458,7 +506,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
             for (int j = 1; j < kTokens; ++j)
                 map.B = cut >> j & 1u ? token<K>(b, j) : L::fma(token<K>(f, j), map.B, token<K>(b, j));
         }
-        V h = exchange<K, kWarps, kCuts>(s.ex, round & 1, c.warp, c.lane, c.rank, c.ranks, map, cut != 0, carry);
+        V h = exchange<K, kWarps, kCuts>(s.ex, round, c.warp, c.lane, c.rank, c.ranks, map, cut != 0, carry);
         if (saved && c.live && valid > 0) L::store(saved, h);
         T* to = y;
 #pragma unroll
@@ -487,7 +535,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
     }
     if (p.final_state && c.live && c.rank == 0 && c.warp == 0) L::store(p.final_state + c.b * p.channels + c.ch, carry);
     if (kTma && c.lane == 0) bulk_wait_read_all();
-    if (c.ranks > 1) cg::this_cluster().sync();  // no CTA leaves while another writes to its shared memory
+    exchange_end(c.ranks);
 }
 
 // --------------------------------------------------------------- gradient
@@ -539,7 +587,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
     fetch();
     fetch_small(tile);
     V carry = p.dfinal && c.live ? L::load(p.dfinal + c.b * p.channels + c.ch) : L::all(0.0f);
-    if (c.ranks > 1) cg::this_cluster().sync();
+    exchange_begin(s.ex, c.ranks);
     const V one = L::all(1.0f), minus = L::all(-1.0f), none = L::all(0.0f);
     for (int round = 0; round < c.rounds; ++round) {
         bool ok = true;
@@ -594,7 +642,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
                 if (kCuts && (cut >> j & 1u)) map.B = none;
             }
         }
-        V q = exchange<K, kWarps, kCuts>(s.ex, round & 1, c.warp, c.lane, c.rank, c.ranks, map, cut != 0, carry);
+        V q = exchange<K, kWarps, kCuts>(s.ex, round, c.warp, c.lane, c.rank, c.ranks, map, cut != 0, carry);
         T *tx = dx + (kTokens - 1) * p.channels, *tg = dg + (kTokens - 1) * p.channels;
 #pragma unroll
         for (int j = kTokens - 1; j >= 0; --j) {
@@ -636,7 +684,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
     }
     if (p.dstate && c.live && c.rank == 0 && c.warp == 0) L::store(p.dstate + c.b * p.channels + c.ch, carry);
     if (kTma && c.lane == 0) bulk_wait_read_all();
-    if (c.ranks > 1) cg::this_cluster().sync();
+    exchange_end(c.ranks);
 }
 
 // -------------------------------------------------------------- one token
