@@ -44,16 +44,6 @@ namespace cg = cooperative_groups;
 constexpr int kTokens = SC_GATED_SAVE;
 constexpr int kMaxCluster = 8;
 
-__device__ __forceinline__ void copy_async(void* to, const void* from) {  // 4 bytes
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kAhead>  // all but the last kAhead groups of copies have arrived, for the whole warp
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
-    __syncwarp();
-}
-
 // Tensor maps of a call: forward x, gate and y; backward x, gate, dy, dx and dgate.
 struct GatedMaps {
     CUtensorMap map[5];
@@ -120,43 +110,32 @@ __device__ __forceinline__ void set_token(f2 (&v)[kPairs<K>], int j, typename La
     else v[j / 2] = j % 2 ? pack2(lo2(v[j / 2]), t) : pack2(t, hi2(v[j / 2]));
 }
 
-// A warp's tiles of one tensor lie in shared memory, 32 K channels a token, filled by
-// asynchronous copies kStages - 1 rounds ahead: loads into registers left a third of
-// that under way and doubled the registers (measured).
+// A lane's elements as they lie in memory, as an operand.
+template <class T, class R>
+__device__ __forceinline__ float one_of(R v) {
+    if constexpr (sizeof(T) == 4) {
+        return v;
+    } else {
+        T e;
+        memcpy(&e, &v, 2);
+        return to_f32(e);
+    }
+}
 template <class T, int K>
-struct Tile {
+struct Elements {
     using R = typename Raw<T, K>::type;
-    static constexpr int kBytes = kTokens * 32 * (int)sizeof(R);
-    const R* at;  // the lane's channels of the first token
-    __device__ __forceinline__ Tile(const unsigned char* tile, int lane) : at(reinterpret_cast<const R*>(tile) + lane) {}
-
-    static __device__ __forceinline__ float one(R v) {
-        if constexpr (sizeof(T) == 4) {
-            return v;
-        } else {
-            T e;
-            memcpy(&e, &v, 2);
-            return to_f32(e);
-        }
-    }
-    __device__ __forceinline__ f2 pair(int i) const {
+    using V = typename Lane<K>::V;
+    static __device__ __forceinline__ V of(R v) {
         if constexpr (K == 2) {
-            Vec<T, 2> v;
-            v.w[0] = at[i * 32];
-            return v.pair(0);
+            Vec<T, 2> e;
+            e.w[0] = v;
+            return e.pair(0);
         } else {
-            return pack2(one(at[2 * i * 32]), one(at[(2 * i + 1) * 32]));
+            return one_of<T>(v);
         }
     }
-    __device__ __forceinline__ typename Lane<K>::V get(int j) const {
-        if constexpr (K == 2) return pair(j);
-        else return one(at[j * 32]);
-    }
-    // The result of token j in place of what was read there.
-    __device__ __forceinline__ void put(int j, typename Lane<K>::V v) const {
-        store(reinterpret_cast<T*>(const_cast<R*>(at)) + j * 32 * K, v);
-    }
-    static __device__ __forceinline__ void store(T* p, typename Lane<K>::V v) {
+    static __device__ __forceinline__ f2 pair(R a, R b) { return pack2(one_of<T>(a), one_of<T>(b)); }
+    static __device__ __forceinline__ void store(T* p, V v) {
         if constexpr (K == 2) {
             const float f[2] = {lo2(v), hi2(v)};
             Vec<T, 2> o;
@@ -168,40 +147,55 @@ struct Tile {
     }
 };
 
-// Where a warp's tiles of a tensor come from whose rows are not aligned to 16 bytes: a
-// lane's channels by asynchronous copies of 4 bytes; single 16-bit elements are too
-// small for those and go through registers.
+// A warp's tile of one tensor in shared memory, 32 K channels a token: rounds ahead of
+// its use without a register, where loads into registers had a third of that under way
+// (8 x 4096 tokens of 4096 channels: 160 us, 141 so).
 template <class T, int K>
-struct Source {
-    using R = typename Raw<T, K>::type;
+struct Tile : Elements<T, K> {
+    using E = Elements<T, K>;
+    using R = typename E::R;
+    static constexpr int kBytes = kTokens * 32 * (int)sizeof(R);
+    R* at;  // the lane's channels of the first token
+    __device__ __forceinline__ Tile(unsigned char* tile, int lane) : at(reinterpret_cast<R*>(tile) + lane) {}
+    __device__ __forceinline__ f2 pair(int i) const {
+        if constexpr (K == 2) return E::of(at[i * 32]);
+        else return E::pair(at[2 * i * 32], at[(2 * i + 1) * 32]);
+    }
+    __device__ __forceinline__ typename E::V get(int j) const { return E::of(at[j * 32]); }
+    // The result of token j in place of what was read there.
+    __device__ __forceinline__ void put(int j, typename E::V v) const { E::store(reinterpret_cast<T*>(at + j * 32), v); }
+};
+
+// A warp's tile in registers, where rows are not aligned to 16 bytes; the next one is
+// loaded when this one has been used.
+template <class T, int K>
+struct Held : Elements<T, K> {
+    using E = Elements<T, K>;
+    using R = typename E::R;
+    R r[kTokens];
     const T* p;         // the lane's channels of the next tile's first token
     long long stride;   // of a token
     long long advance;  // from a tile to the warp's next
-    bool mine;
-    __device__ __forceinline__ Source(const void* base, long long row, long long token, int tile, int step, long long ch0,
-                                      long long channels, int lane)
-        : p(static_cast<const T*>(base) + row + (long long)tile * kTokens * token + ch0 + lane * K), stride(token),
-          advance((long long)step * kTokens * token), mine(ch0 + lane * K < channels) {}
-    // The next tile, of which the row has `left` tokens (zeros for the others), to `tile`.
-    __device__ __forceinline__ void next(unsigned char* tile, int left, int lane) {
-        const T* q = p;
-        p += advance;
-        if (!mine) return;
-        R* to = reinterpret_cast<R*>(tile) + lane;
-        if constexpr (sizeof(R) == 2) {
-            R v[kTokens];
+    __device__ __forceinline__ Held(const void* base, long long row, long long token, int tile, int step, long long ch)
+        : p(static_cast<const T*>(base) + row + (long long)tile * kTokens * token + ch), stride(token),
+          advance((long long)step * kTokens * token) {}
+    // The next tile, of which the row has `left` tokens (zeros for the others).
+    __device__ __forceinline__ void next(int left, bool live) {
+        if (left >= kTokens && live) {
 #pragma unroll
-            for (int j = 0; j < kTokens; ++j) v[j] = j < left ? __ldg(reinterpret_cast<const R*>(q + j * stride)) : R(0);
-#pragma unroll
-            for (int j = 0; j < kTokens; ++j) to[j * 32] = v[j];
+            for (int j = 0; j < kTokens; ++j) r[j] = __ldg(reinterpret_cast<const R*>(p + j * stride));
         } else {
 #pragma unroll
-            for (int j = 0; j < kTokens; ++j) {
-                if (j < left) copy_async(to + j * 32, q + j * stride);
-                else to[j * 32] = R(0);
-            }
+            for (int j = 0; j < kTokens; ++j) r[j] = live && j < left ? __ldg(reinterpret_cast<const R*>(p + j * stride)) : R(0);
         }
+        p += advance;
     }
+    __device__ __forceinline__ f2 pair(int i) const {
+        if constexpr (K == 2) return E::of(r[i]);
+        else return E::pair(r[2 * i], r[2 * i + 1]);
+    }
+    __device__ __forceinline__ typename E::V get(int j) const { return E::of(r[j]); }
+    __device__ __forceinline__ void put(int, typename E::V) const {}
 };
 
 // rest = 1 - f = e / (1 + e), e = exp(-g), and f = 1 - rest, for a pair.  rest has its
@@ -378,30 +372,28 @@ __device__ __forceinline__ Place place_of(const GatedParams& p) {
     return c;
 }
 
-// A warp's ring of rounds, kTensors tiles each.  kTma: whole tiles by the copy engine,
-// one instruction of one lane, results back the same way from where the elements lay.
-template <class T, int K, int kTensors, int kStages, bool kTma>
+// A warp's ring of rounds, kTensors tiles each: whole tiles by the copy engine, one
+// instruction of one lane, and results back the same way from where the elements lay.
+template <class T, int K, int kTensors, int kStages>
 struct Ring {
     using Tl = Tile<T, K>;
     static constexpr int kRound = kTensors * Tl::kBytes, kBytes = kStages * kRound;
     unsigned char *base, *fill, *take;
-    uint32_t bar, phase = 0;  // kTma: the stages' barriers, the parity of the round to take
+    uint32_t bar, phase = 0;  // the stages' barriers, the parity of the round to take
     __device__ __forceinline__ Ring(unsigned char* mem, uint64_t* bars, int lane) : base(mem), fill(mem), take(mem), bar(smem_u32(bars)) {
-        if constexpr (kTma) {
-            if (lane == 0) {
+        if (bars && lane == 0) {
 #pragma unroll
-                for (int i = 0; i < kStages; ++i) mbar_init(bar + 8 * i, 1);
-                fence_mbar_init();
-            }
-            __syncwarp();
+            for (int i = 0; i < kStages; ++i) mbar_init(bar + 8 * i, 1);
+            fence_mbar_init();
         }
+        __syncwarp();
     }
     __device__ __forceinline__ void next(unsigned char*& at) {
         at += kRound;
         if (at == base + kBytes) at = base;
     }
-    // The tiles of tokens t0 .. of row b (kTma), by one lane; what the stage held has
-    // been read, by the copies of results out of it, too.
+    // The tiles of the tokens from t0 of row b, by one lane; what the stage held has been
+    // read, by the copies of results out of it, too.
     __device__ __forceinline__ void load(const GatedMaps& m, int ch0, int t0, int b) {
         bulk_wait_read_all();
         const uint32_t full = bar + (uint32_t)(fill - base) / kRound * 8, to = smem_u32(fill);
@@ -415,9 +407,11 @@ struct Ring {
         if (take + kRound == base + kBytes) phase ^= 1;
         return ok;
     }
+    __device__ __forceinline__ Tl tile(int i, int lane) const { return Tl(take + i * Tl::kBytes, lane); }
 };
-template <int K, int kWarps, class Ring> struct Shared {
-    unsigned char ring[kWarps][Ring::kBytes];  // first: the copy engine wants 128 bytes' alignment
+// Rows that are not aligned have no ring.
+template <int K, int kWarps, class Ring, bool kTma> struct Shared {
+    unsigned char ring[kTma ? kWarps : 1][kTma ? Ring::kBytes : 16];  // first: the copy engine wants 128 bytes' alignment
     uint64_t bars[kWarps][4];
     Exchange<K, kWarps> ex;  // last: its size goes by the cluster
     static __host__ __device__ constexpr size_t bytes(int ctas) {
@@ -425,24 +419,29 @@ template <int K, int kWarps, class Ring> struct Shared {
     }
 };
 
+// The tensor's tile of this round: in the ring, or as it was loaded.
+template <bool kTma, class Ring, class Held>
+__device__ __forceinline__ auto tile_of(const Ring& ring, const Held& held, int i, int lane) {
+    if constexpr (kTma) return ring.tile(i, lane);
+    else return held;
+}
+
 // ---------------------------------------------------------------- forward
-template <class T, int K, bool kTma> using ForwardRing = Ring<T, K, 2, 3, kTma>;
+template <class T, int K> using ForwardRing = Ring<T, K, 2, 3>;
 
 template <class T, int K, bool kTma, bool kSigmoid, int kWarps, bool kCuts>
 __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
     gated_kernel(GatedParams p, const __grid_constant__ GatedMaps maps) {
     using L = Lane<K>;
     using V = typename L::V;
-    using Tl = Tile<T, K>;
-    using Rg = ForwardRing<T, K, kTma>;
+    using Sh = Shared<K, kWarps, ForwardRing<T, K>, kTma>;
     extern __shared__ __align__(128) unsigned char s_mem[];
-    Shared<K, kWarps, Rg>& s = *reinterpret_cast<Shared<K, kWarps, Rg>*>(s_mem);
+    Sh& s = *reinterpret_cast<Sh*>(s_mem);
     const Place c = place_of<K, kWarps>(p);
     const int step = c.ranks * kWarps;
     int tile = c.rank * kWarps + c.warp;
-    Rg ring(s.ring[c.warp], s.bars[c.warp], c.lane);
-    Source<T, K> x(p.x, c.b * p.x_batch, p.x_token, tile, step, c.ch0, p.channels, c.lane);
-    Source<T, K> g(p.gate, c.b * p.gate_batch, p.gate_token, tile, step, c.ch0, p.channels, c.lane);
+    ForwardRing<T, K> ring(s.ring[kTma ? c.warp : 0], kTma ? s.bars[c.warp] : nullptr, c.lane);
+    Held<T, K> x(p.x, c.b * p.x_batch, p.x_token, tile, step, c.ch), g(p.gate, c.b * p.gate_batch, p.gate_token, tile, step, c.ch);
     T* y = static_cast<T*>(p.y) + c.b * p.y_batch + (long long)tile * kTokens * p.y_token + c.ch;
     float* saved = p.saved ? p.saved + (c.b * c.tiles + tile) * p.channels + c.ch : nullptr;
     int left = (int)p.length - tile * kTokens, left_ahead = left;  // tokens from a tile's start to the row's end
@@ -450,24 +449,21 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
     auto fetch = [&] {
         if constexpr (kTma) {
             if (c.lane == 0 && left_ahead > 0) ring.load(maps, (int)c.ch0, (int)p.length - left_ahead, (int)c.b);
+            ring.next(ring.fill);
         } else {
-            x.next(ring.fill, left_ahead, c.lane);
-            g.next(ring.fill + Tl::kBytes, left_ahead, c.lane);
-            copies_end();
+            x.next(left_ahead, c.live);
+            g.next(left_ahead, c.live);
         }
         left_ahead -= step * kTokens;
-        ring.next(ring.fill);
     };
     fetch();
-    fetch();
+    if (kTma) fetch();
     if (kCuts) head = head_of(p.heads, c.b, tile * kTokens, p.length, c.lane);
     V carry = p.state && c.live ? L::load(p.state + c.b * p.channels + c.ch) : L::all(0.0f);
     exchange_begin(s.ex, c.ranks);
     for (int round = 0; round < c.rounds; ++round) {
-        bool ok = true;
-        if constexpr (kTma) ok = left <= 0 || ring.wait();
-        else copies_wait<1>();
-        const Tl xr(ring.take, c.lane), gr(ring.take + Tl::kBytes, c.lane);
+        const bool ok = !kTma || left <= 0 || ring.wait();
+        const auto xr = tile_of<kTma>(ring, x, 0, c.lane), gr = tile_of<kTma>(ring, g, 1, c.lane);
         f2 f[kPairs<K>], b[kPairs<K>];
         const uint32_t cut = kCuts ? cuts_of(head) : 0u;
         if (kCuts) head = head_of(p.heads, c.b, (long long)(tile + step) * kTokens, p.length, c.lane);
@@ -515,7 +511,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
             if constexpr (kTma) {
                 xr.put(j, h);
             } else {
-                if (c.live && j < valid) Tl::store(to, h);
+                if (c.live && j < valid) Elements<T, K>::store(to, h);
                 to += p.y_token;
             }
         }
@@ -526,8 +522,8 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
                 tma_store_3d(&maps.map[2], (int)c.ch0, tile * kTokens, (int)c.b, smem_u32(ring.take));
                 bulk_commit();
             }
+            ring.next(ring.take);
         }
-        ring.next(ring.take);
         if (saved) saved += step * p.channels;
         y += (long long)step * kTokens * p.y_token;
         tile += step;
@@ -539,7 +535,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
 }
 
 // --------------------------------------------------------------- gradient
-template <class T, int K, bool kTma> using BackwardRing = Ring<T, K, 3, 2, kTma>;
+template <class T, int K> using BackwardRing = Ring<T, K, 3, 2>;
 
 // Warps, CTAs and rounds count from the end of the row.
 template <class T, int K, bool kTma, bool kSigmoid, int kWarps, bool kCuts>
@@ -547,17 +543,15 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
     gated_grad_kernel(GatedParams p, const __grid_constant__ GatedMaps maps) {
     using L = Lane<K>;
     using V = typename L::V;
-    using Tl = Tile<T, K>;
-    using Rg = BackwardRing<T, K, kTma>;
+    using Sh = Shared<K, kWarps, BackwardRing<T, K>, kTma>;
     extern __shared__ __align__(128) unsigned char s_mem[];
-    Shared<K, kWarps, Rg>& s = *reinterpret_cast<Shared<K, kWarps, Rg>*>(s_mem);
+    Sh& s = *reinterpret_cast<Sh*>(s_mem);
     const Place c = place_of<K, kWarps>(p);
     const int step = c.ranks * kWarps;
     int tile = c.tiles - 1 - (c.rank * kWarps + c.warp);
-    Rg ring(s.ring[c.warp], s.bars[c.warp], c.lane);
-    Source<T, K> x(p.x, c.b * p.x_batch, p.x_token, tile, -step, c.ch0, p.channels, c.lane);
-    Source<T, K> g(p.gate, c.b * p.gate_batch, p.gate_token, tile, -step, c.ch0, p.channels, c.lane);
-    Source<T, K> dy(p.dy, c.b * p.dy_batch, p.dy_token, tile, -step, c.ch0, p.channels, c.lane);
+    BackwardRing<T, K> ring(s.ring[kTma ? c.warp : 0], kTma ? s.bars[c.warp] : nullptr, c.lane);
+    Held<T, K> x(p.x, c.b * p.x_batch, p.x_token, tile, -step, c.ch), g(p.gate, c.b * p.gate_batch, p.gate_token, tile, -step, c.ch),
+        dy(p.dy, c.b * p.dy_batch, p.dy_token, tile, -step, c.ch);
     const long long to = (c.b * p.length + (long long)tile * kTokens) * p.channels + c.ch;
     T *dx = static_cast<T*>(p.dx) + to, *dg = static_cast<T*>(p.dgate) + to;
     // a warp's first tile ends with the row, those before the row's first are none
@@ -568,15 +562,14 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
     auto fetch = [&] {
         if constexpr (kTma) {
             if (c.lane == 0 && ahead >= 0) ring.load(maps, (int)c.ch0, ahead * kTokens, (int)c.b);
+            ring.next(ring.fill);
         } else {
             const int n = tokens_of(ahead);
-            x.next(ring.fill, n, c.lane);
-            g.next(ring.fill + Tl::kBytes, n, c.lane);
-            dy.next(ring.fill + 2 * Tl::kBytes, n, c.lane);
-            copies_end();
+            x.next(n, c.live);
+            g.next(n, c.live);
+            dy.next(n, c.live);
         }
         ahead -= step;
-        ring.next(ring.fill);
     };
     const float* saved = p.saved + (c.b * c.tiles + tile) * p.channels + c.ch;
     auto fetch_small = [&](int t) {  // a round ahead, in registers
@@ -590,11 +583,9 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
     exchange_begin(s.ex, c.ranks);
     const V one = L::all(1.0f), minus = L::all(-1.0f), none = L::all(0.0f);
     for (int round = 0; round < c.rounds; ++round) {
-        bool ok = true;
-        fetch();
-        if constexpr (kTma) ok = tile < 0 || ring.wait();
-        else copies_wait<1>();
-        const Tl xr(ring.take, c.lane), gr(ring.take + Tl::kBytes, c.lane), d(ring.take + 2 * Tl::kBytes, c.lane);
+        if (kTma) fetch();
+        const bool ok = !kTma || tile < 0 || ring.wait();
+        const auto xr = tile_of<kTma>(ring, x, 0, c.lane), gr = tile_of<kTma>(ring, g, 1, c.lane), d = tile_of<kTma>(ring, dy, 2, c.lane);
         // u: what dh is multiplied with for dgate; w: for dx (sigmoid), or f itself
         f2 u[kPairs<K>], w[kPairs<K>];
         const uint32_t cut = kCuts ? cuts_of(head) : 0u;
@@ -630,6 +621,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
                 if (j >= valid) set_token<K>(w, j, kSigmoid ? none : one);
         }
         if (!ok) set_token<K>(w, 0, L::all(__int_as_float(0x7fffffff)));
+        if (!kTma) fetch();
         // f from 1 - f: it enters with its absolute error
         auto decay_of = [&](int j) { return kSigmoid ? L::fma(token<K>(w, j), minus, one) : token<K>(w, j); };
         Map<K> map{one, none};
@@ -659,8 +651,8 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
                 gr.put(j, og);
             } else {
                 if (c.live && j < valid) {
-                    Tl::store(tx, ox);
-                    Tl::store(tg, og);
+                    Elements<T, K>::store(tx, ox);
+                    Elements<T, K>::store(tg, og);
                 }
                 tx -= p.channels;
                 tg -= p.channels;
@@ -671,13 +663,11 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
             __syncwarp();
             if (c.lane == 0 && valid > 0) {
                 tma_store_3d(&maps.map[3], (int)c.ch0, tile * kTokens, (int)c.b, smem_u32(ring.take));
-                tma_store_3d(&maps.map[4], (int)c.ch0, tile * kTokens, (int)c.b, smem_u32(ring.take + Tl::kBytes));
+                tma_store_3d(&maps.map[4], (int)c.ch0, tile * kTokens, (int)c.b, smem_u32(ring.take + Tile<T, K>::kBytes));
                 bulk_commit();
             }
-        } else {
-            __syncwarp();  // every lane has read
+            ring.next(ring.take);
         }
-        ring.next(ring.take);
         tile -= step;
         dx -= (long long)step * kTokens * p.channels;
         dg -= (long long)step * kTokens * p.channels;
@@ -793,12 +783,20 @@ bool maps_of(GatedMaps* m, const GatedParams& p, bool grad) {
            map_of<T, K>(&m->map[4], p.dgate, p, row, p.channels);
 }
 
+// The kernel of a call (forward with K = 2 in registers has no gradient beside it).
+template <class T, int K, bool kTma, bool kSigmoid, int kWarps, bool kCuts>
+const void* kernel_of(bool grad) {
+    if constexpr (kTma || K == 1) {
+        if (grad) return (const void*)gated_grad_kernel<T, K, kTma, kSigmoid, kWarps, kCuts>;
+    }
+    return (const void*)gated_kernel<T, K, kTma, kSigmoid, kWarps, kCuts>;
+}
+
 template <class T, int K, bool kTma, bool kSigmoid, int kWarps, bool kCuts>
 cudaError_t go(const GatedParams& p, const GatedMaps& maps, bool grad, long long groups, int ctas, cudaStream_t s) {
-    const void* kernel = grad ? (const void*)gated_grad_kernel<T, K, kTma, kSigmoid, kWarps, kCuts>
-                              : (const void*)gated_kernel<T, K, kTma, kSigmoid, kWarps, kCuts>;
+    const void* kernel = kernel_of<T, K, kTma, kSigmoid, kWarps, kCuts>(grad);
     auto bytes = [&](int n) {
-        return (int)(grad ? Shared<K, kWarps, BackwardRing<T, K, kTma>>::bytes(n) : Shared<K, kWarps, ForwardRing<T, K, kTma>>::bytes(n));
+        return (int)(grad ? Shared<K, kWarps, BackwardRing<T, K>, kTma>::bytes(n) : Shared<K, kWarps, ForwardRing<T, K>, kTma>::bytes(n));
     };
     // the limit is one per device: always the largest, whatever this call needs
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(kMaxCluster));
@@ -843,9 +841,10 @@ cudaError_t launch_gated_as(const GatedParams& p, bool grad, cudaStream_t s) {
     constexpr int K = 4 / (int)sizeof(T);  // 4 bytes a lane
     if (p.wide) return by_gate<T, K, true>(p, grad, s);
     if constexpr (K == 2) {
-        if (!p.pairs) return by_gate<T, 1, false>(p, grad, s);
+        // (the gradient's three tensors in registers, with two channels a lane: 12 warps an SM)
+        if (p.pairs && !grad) return by_gate<T, 2, false>(p, grad, s);
     }
-    return by_gate<T, K, false>(p, grad, s);
+    return by_gate<T, 1, false>(p, grad, s);
 }
 
 template <class T, int K>
