@@ -105,15 +105,17 @@ Tensor norm_parameter(const sc_norm_desc* d, const void* p) { return flat(p, d->
 template <int N>
 void norm_rows(const sc_norm_desc* d, const Tensor (&t)[N], NormParams* p) {
     const int e = 16 / bytes_of(d->dtype);
-    bool one = true;
+    bool one = true, dense = true;
     p->vec = d->channels % e == 0;
     for (const Tensor& v : t) {
         if (!v.p) continue;
         p->vec = p->vec && v.vec(e);
         one = one && one_stride(v);
+        dense = dense && (v.tokens > 1 ? v.st : v.sb) == v.channels;
     }
     // length 1: the batch strides are the rows'
     if (one && d->length > 1) p->length = p->rows;
+    p->dense = one && dense;
 }
 
 // -------------------------------------------------------------- experts
@@ -289,7 +291,7 @@ size_t sc_layer_norm_grad_workspace_bytes(int64_t batch, int64_t length, int64_t
     if (types(dtype) != SC_OK || channels <= 0 || rows <= 0 || rows >= kMaxGrid || product(rows, channels, 8) < 0 ||
         channels >= kMaxGrid)
         return 0;
-    return seq_scratch_total(norm_grad_plan(dtype, rows, channels).total);
+    return seq_scratch_total(norm_grad_scratch(rows, channels));
 }
 
 sc_status sc_layer_norm_grad(const sc_norm_desc* d, const void* dy, int64_t dy_batch, int64_t dy_token,
@@ -324,13 +326,11 @@ sc_status sc_layer_norm_grad(const sc_norm_desc* d, const void* dy, int64_t dy_b
     p.dbias = dbias;
     const Tensor rows[] = {x, e, t, o};
     norm_rows(d, rows, &p);
-    const NormGradPlan plan = norm_grad_plan(d->dtype, p.rows, p.channels);
-    p.parts = plan.parts;
     if (dweight || dbias) {
         unsigned char* base = nullptr;
-        st = seq_scratch(s, plan.total, &base);
+        st = seq_scratch(s, norm_grad_scratch(p.rows, p.channels), &base);
         if (st != SC_OK) return st;
-        p.partials = reinterpret_cast<float*>(base + plan.partials);
+        p.partials = reinterpret_cast<float*>(base);
     }
     return status_of(launch_norm_grad(d->dtype, p, s));
 }

@@ -39,35 +39,23 @@ __global__ void __launch_bounds__(kSumCols* kSumRows) norm_parameters_kernel(Nor
     }
 }
 
+cudaError_t by_type(int dtype, NormParams& p, bool grad, cudaStream_t s) {
+    return dtype == SC_F32 ? launch_norm_f32(p, grad, s) : dtype == SC_F16 ? launch_norm_f16(p, grad, s)
+                                                                          : launch_norm_bf16(p, grad, s);
+}
+
 }  // namespace
 
-cudaError_t launch_norm(int dtype, const NormParams& p, cudaStream_t s) {
-    return dtype == SC_F32 ? launch_norm_f32(p, false, s) : dtype == SC_F16 ? launch_norm_f16(p, false, s)
-                                                                          : launch_norm_bf16(p, false, s);
+cudaError_t launch_norm(int dtype, NormParams p, cudaStream_t s) { return by_type(dtype, p, false, s); }
+
+// One row of partial sums for each CTA of the gradient's kernel: at most two an SM, and
+// a row each.
+size_t norm_grad_scratch(long long rows, long long channels) {
+    return (size_t)std::min(rows, std::max<long long>(2 * seq_sms(), kColumnParts)) * 2 * channels * sizeof(float);
 }
 
-// One row of partial sums for each CTA of the gradient's kernel: as many as the
-// machine holds at once (kResident), fewer where there are fewer rows.  Rows beyond
-// kRowMax are summed by columns, in 32 parts.
-NormGradPlan norm_grad_plan(int dtype, long long rows, long long channels) {
-    NormGradPlan g{};
-    if (channels > kRowMax) {
-        g.parts = std::min<long long>(rows, 32);
-    } else {
-        const long long n = (channels + (dtype == SC_F32 ? 4 : 8) - 1) / (dtype == SC_F32 ? 4 : 8);
-        // the kernel's groups of threads and CTAs an SM, by width as in by_width
-        const long long lanes = n <= 8 ? 8 : n <= 16 ? 16 : n <= 64 ? 32 : n <= 128 ? 64 : n <= 256 ? 128 : n <= 512 ? 256 : n <= 1024 ? 512 : 1024;
-        const long long threads = std::max<long long>(lanes, 256), groups = threads / lanes;
-        g.parts = std::min((rows + groups - 1) / groups, seq_sms() * (threads == 256 ? 2 : 1));
-    }
-    g.partials = 0;
-    g.total = (size_t)g.parts * 2 * channels * sizeof(float);
-    return g;
-}
-
-cudaError_t launch_norm_grad(int dtype, const NormParams& p, cudaStream_t s) {
-    const cudaError_t e = dtype == SC_F32 ? launch_norm_f32(p, true, s) : dtype == SC_F16 ? launch_norm_f16(p, true, s)
-                                                                                         : launch_norm_bf16(p, true, s);
+cudaError_t launch_norm_grad(int dtype, NormParams p, cudaStream_t s) {
+    const cudaError_t e = by_type(dtype, p, true, s);
     if (e != cudaSuccess || !p.partials) return e;
     const dim3 grid((unsigned)((p.channels + kSumCols - 1) / kSumCols), 2);
     norm_parameters_kernel<<<grid, kSumCols * kSumRows, 0, s>>>(p);

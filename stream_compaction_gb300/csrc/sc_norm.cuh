@@ -7,20 +7,27 @@
 // (rms: m = 0, and mean(dn) drops out.)
 //
 // A row lies in the registers of kLanes threads, N elements each, so each tensor is
-// read and written once: bytes are all that the operator costs (a third of the
-// issue slots at most).  The variance is of the centred row, a second sum over
-// registers, not a difference of moments.  Rows of up to 32 vectors of 16 bytes take
-// part of a warp or one, wider ones up to 1024 threads, which then meet in shared
-// memory.  Rows beyond kRowMax elements are read again for each of their sums.
+// read and written once: bytes are all that the operator costs.  The variance is of the
+// centred row, a second sum over registers, not a difference of moments.  Rows of up to
+// 32 vectors of 16 bytes take part of a warp or one, wider ones up to 1024 threads, which
+// then meet in shared memory.  Rows beyond kRowMax elements are read again for each of
+// their sums.
 //
-// The gradient's sums over tokens: a persistent CTA keeps its columns' sums in
-// registers over all its rows, writes one row of partial sums, and a second kernel
-// adds those in the order of the CTAs: the same bits on every run.
+// CTAs stay and take rows in turns, with the parameters (and the gradient's sums over
+// tokens) in registers.  A team, the threads of a wide row or a warp with several
+// narrow ones, has a ring of rows in shared memory that bulk copies fill some turns
+// ahead; rows that are not aligned to 16 bytes, and calls of one turn, are loaded into
+// registers, the next row's while this one is worked on.
+//
+// The gradient's sums over tokens: a CTA's columns' sums over all its rows become one row
+// of partial sums, and a second kernel adds those in the order of the CTAs: the same bits
+// on every run.
 #pragma once
 #include <algorithm>
 
 #include "sc_seq.cuh"
 #include "sc_seq_launch.h"
+#include "sc_tma.cuh"
 
 namespace scg {
 
@@ -61,6 +68,14 @@ struct Row {
                 }
                 memcpy(v[i].w, e, 16);
             }
+        }
+    }
+    __device__ __forceinline__ void load_shared(const unsigned char* row, int lane, int channels) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = column<T, true, kLanes>(i, 0, lane);
+            if (c < channels) v[i].load_rw(reinterpret_cast<const T*>(row) + c);
+            else v[i].zero();
         }
     }
     __device__ __forceinline__ float get(int i, int j) const { return v[i].get(j); }
@@ -118,82 +133,288 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* slot, int lane, in
 
 template <int kLanes> constexpr int kThreads = kLanes < 256 ? 256 : kLanes;
 
-// ---------------------------------------------------------------- forward
-template <class T, bool kVec, int kLanes, int NV>
-__global__ void __launch_bounds__(kThreads<kLanes>) norm_kernel(NormParams p) {
-    constexpr int W = kWidth<T>, N = NV * W, kGroups = kThreads<kLanes> / kLanes;
-    __shared__ float s_sum[kGroups][2][kLanes > 32 ? kLanes / 32 : 1];
-    const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes, channels = (int)p.channels;
-    const long long r0 = (long long)blockIdx.x * kGroups + group;
-    const bool live = r0 < p.rows;
-    if (kLanes >= 32 && !live) return;  // part of a warp stays for the shuffles
-    const uint32_t r = live ? (uint32_t)r0 : 0u;
-    const int some = live ? channels : 0;
-    using R = Row<T, kVec, kLanes, NV>;
-    R x;
-    x.load(static_cast<const T*>(p.x) + at(r, p.length, p.x_batch, p.x_token), lane, some);
-    float f[N];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < W; ++j) f[i * W + j] = x.get(i, j);
-    if (p.residual) {
-        R e;
-        e.load(static_cast<const T*>(p.residual) + at(r, p.length, p.residual_batch, p.residual_token), lane, some);
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < W; ++j) f[i * W + j] = to_f32(from_f32<T>(f[i * W + j] + e.get(i, j)));
-        R::store(static_cast<T*>(p.sum) + at(r, p.length, p.sum_batch, p.sum_token), lane, some, f);
-    }
-    const float per = 1.0f / (float)channels;
-    float mean = 0.0f;
-    if (!p.rms) {
-        float s[1] = {0.0f};
-#pragma unroll
-        for (int i = 0; i < N; ++i) s[0] += f[i];
-        row_sum<kLanes, 1>(s, s_sum[group][0], lane, group);
-        mean = s[0] * per;
-    }
-    float q[1] = {0.0f};
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-            float& c = f[i * W + j];
-            c = column<T, kVec, kLanes>(i, j, lane) < channels ? c - mean : 0.0f;
-            q[0] = fmaf(c, c, q[0]);
+// How rows come: element by element, by vectors, or by vectors through the ring.
+enum Way { kElements, kVectors, kRing };
+
+// A team: the threads of a row, or a warp with kSide rows side by side, and kDeep of
+// them one behind the other where they are short.
+template <class T, Way kWay, int kLanes, int NV> struct Team {
+    static constexpr int W = kWidth<T>, N = NV * W, NT = kThreads<kLanes>;
+    static constexpr int kSize = kLanes > 32 ? kLanes : 32, kTeams = NT / kSize;
+    static constexpr int kSide = kLanes < 32 ? 32 / kLanes : 1, kDeep = NV == 1 && kLanes <= 32 && kWay == kRing ? 2 : 1;
+    static constexpr int kRows = kSide * kDeep;  // of a turn
+    static constexpr int kGroups = NT / kLanes;
+};
+
+// A wait for bulk copies: they end by themselves; one that should run out all the same
+// (a second or so) gives up, and the rows count as NaN.
+__device__ __forceinline__ bool arrived(uint32_t bar, uint32_t parity) {
+    for (int i = 0; i < (1 << 20); ++i)
+        if (mbar_try_wait_sleep(bar, parity, 1000)) return true;
+    return false;
+}
+__device__ __forceinline__ void bulk_load(uint32_t to, const void* from, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(to), "l"(from), "r"(bytes), "r"(bar) : "memory");
+}
+
+// A team's ring: stages of kTensors x kRows rows.
+template <class T, int kTensors, int kRows>
+struct RowRing {
+    const T* from[kTensors];
+    long long sb[kTensors], st[kTensors];
+    uint32_t row_bytes, length;
+    unsigned char* base;
+    uint32_t bar;  // of stage 0
+    int stages, fill = 0, take = 0, tensors;
+    uint32_t phase = 0;
+    bool dense;  // all rows follow one another
+
+    __device__ __forceinline__ int bytes() const { return tensors * kRows * (int)row_bytes; }
+    __device__ __forceinline__ void begin(unsigned char* mem, uint64_t* bars, int n, int thread) {
+        base = mem;
+        bar = smem_u32(bars);
+        stages = n;
+        if (thread == 0) {
+            for (int i = 0; i < n; ++i) mbar_init(bar + 8 * i, 1);
+            fence_mbar_init();
         }
-    row_sum<kLanes, 1>(q, s_sum[group][1], lane, group);
-    const float rstd = 1.0f / sqrtf(fmaf(q[0], per, p.eps));
-    if (p.saved && lane == 0 && live) reinterpret_cast<float2*>(p.saved)[r] = make_float2(mean, rstd);
+    }
+    // The rows [r0, r0 + n) into the next stage; by the team's first warp, when the whole
+    // team has read what was there.
+    __device__ __forceinline__ void load(long long r0, int n, int lane) {
+        const uint32_t full = bar + 8 * fill, to = smem_u32(base) + fill * bytes();
+        if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(tensors * n) * row_bytes);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (kVec && column<T, kVec, kLanes>(i, 0, lane) >= channels) continue;
+        for (int i = 0; i < kTensors; ++i) {
+            if (i >= tensors) break;
+            const uint32_t dst = to + i * kRows * row_bytes;
+            if (kRows == 1 || dense) {
+                if (lane == 0) bulk_load(dst, from[i] + at((uint32_t)r0, length, sb[i], st[i]), n * row_bytes, full);
+            } else if (lane < n) {
+                bulk_load(dst + lane * row_bytes, from[i] + at((uint32_t)r0 + lane, length, sb[i], st[i]), row_bytes, full);
+            }
+        }
+        if (++fill == stages) fill = 0;
+    }
+    __device__ __forceinline__ bool wait() const { return arrived(bar + 8 * take, phase); }
+    __device__ __forceinline__ const unsigned char* row(int i, int r) const {
+        return base + take * bytes() + (i * kRows + r) * row_bytes;
+    }
+    __device__ __forceinline__ void taken() {
+        if (++take == stages) {
+            take = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// The rows of a team's turns.  `tensors` of p: 2 or 3.
+template <class T, Way kWay, int kLanes, int NV, int kTensors>
+struct Turns {
+    using G = Team<T, kWay, kLanes, NV>;
+    using R = Row<T, kWay != kElements, kLanes, NV>;
+    RowRing<T, kTensors, G::kRows> ring;
+    R next[kWay == kRing ? 1 : kTensors][kWay == kRing ? 1 : G::kDeep];
+    long long rows, step, ahead;
+    int thread, lane, side, channels;  // thread: of the team
+
+    __device__ __forceinline__ void begin(const NormParams& p, unsigned char* mem, const void* const (&from)[kTensors],
+                                          const long long (&sb)[kTensors], const long long (&st)[kTensors], int tensors) {
+        const int team = threadIdx.x / G::kSize;
+        thread = threadIdx.x % G::kSize;
+        lane = threadIdx.x % kLanes;
+        side = kLanes < 32 ? thread / kLanes : 0;
+        channels = (int)p.channels;
+        rows = p.rows;
+        ahead = first();
+        step = (long long)gridDim.x * G::kTeams * G::kRows;
+        ring.tensors = tensors;
+        ring.length = p.length;
+        ring.dense = p.dense;
+        ring.row_bytes = (uint32_t)(channels * sizeof(T));
+#pragma unroll
+        for (int i = 0; i < kTensors; ++i) {
+            ring.from[i] = static_cast<const T*>(from[i]);
+            ring.sb[i] = sb[i];
+            ring.st[i] = st[i];
+        }
+        if constexpr (kWay == kRing) {
+            uint64_t* bars = reinterpret_cast<uint64_t*>(mem + (long long)G::kTeams * p.stages * ring.bytes());
+            ring.begin(mem + (long long)team * p.stages * ring.bytes(), bars + team * p.stages, p.stages, thread);
+            __syncthreads();
+            for (int i = 0; i < p.stages; ++i) fetch();
+        } else {
+            fetch();
+        }
+    }
+    __device__ __forceinline__ long long first() const {
+        return ((long long)blockIdx.x * G::kTeams + threadIdx.x / G::kSize) * G::kRows;
+    }
+    // This thread's row d of the turn that begins with `base`.
+    __device__ __forceinline__ long long row(long long base, int d) const { return base + d * G::kSide + side; }
+    // The turn after those under way.
+    __device__ __forceinline__ void fetch() {
+        if (ahead >= rows) return;
+        if constexpr (kWay == kRing) {
+            if (thread < 32) ring.load(ahead, (int)min((long long)G::kRows, rows - ahead), thread);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kTensors; ++i) {
+                if (i >= ring.tensors) break;
+#pragma unroll
+                for (int d = 0; d < G::kDeep; ++d) {
+                    const long long r = row(ahead, d);
+                    const bool live = r < rows;
+                    next[i][d].load(ring.from[i] + at(live ? (uint32_t)r : 0u, ring.length, ring.sb[i], ring.st[i]), lane,
+                                    live ? channels : 0);
+                }
+            }
+        }
+        ahead += step;
+    }
+    // The turn's rows of tensor i, when wait() says that they are there.
+    __device__ __forceinline__ bool wait() const {
+        if constexpr (kWay == kRing) return ring.wait();
+        else return true;
+    }
+    __device__ __forceinline__ void take(int i, long long base, R (&to)[G::kDeep]) const {
+#pragma unroll
+        for (int d = 0; d < G::kDeep; ++d) {
+            if constexpr (kWay == kRing) to[d].load_shared(ring.row(i, d * G::kSide + side), lane, row(base, d) < rows ? channels : 0);
+            else to[d] = next[i][d];
+        }
+    }
+    // Every thread of the team has taken its rows (a barrier lies between): the next turn's
+    // may come.
+    __device__ __forceinline__ void done() {
+        if constexpr (kWay == kRing) {
+            if constexpr (kLanes <= 32) __syncwarp();
+            ring.taken();
+            fetch();
+        }
+    }
+};
+__device__ __forceinline__ float not_a_number() { return __int_as_float(0x7fffffff); }
+
+// ---------------------------------------------------------------- forward
+// CTAs that an SM holds: 65536 registers by 80 a thread, 128 with rows in registers.
+template <Way kWay, int kLanes> constexpr int kResident = kThreads<kLanes> == 256 ? (kWay == kRing ? 3 : 2) : 1;
+
+template <class T, Way kWay, int kLanes, int NV>
+__global__ void __launch_bounds__(kThreads<kLanes>, kResident<kWay, kLanes>) norm_kernel(NormParams p) {
+    using G = Team<T, kWay, kLanes, NV>;
+    using R = Row<T, kWay != kElements, kLanes, NV>;
+    constexpr int W = G::W, N = G::N, D = G::kDeep;
+    constexpr bool kVec = kWay != kElements;
+    __shared__ float s_sum[G::kGroups][2][2][kLanes > 32 ? kLanes / 32 : 1];
+    extern __shared__ __align__(128) unsigned char s_mem[];
+    const int group = threadIdx.x / kLanes, channels = (int)p.channels;
+    Turns<T, kWay, kLanes, NV, 2> turns;
+    {
+        const void* const from[2] = {p.x, p.residual};
+        const long long sb[2] = {p.x_batch, p.residual_batch}, st[2] = {p.x_token, p.residual_token};
+        turns.begin(p, s_mem, from, sb, st, p.residual ? 2 : 1);
+    }
+    const int lane = turns.lane;
+    float w[N], b[N];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < W; ++j) {
             const int c = column<T, kVec, kLanes>(i, j, lane);
-            float& o = f[i * W + j];
-            if (!kVec && c >= channels) continue;
-            o *= rstd;
-            const float w = p.weight ? parameter<T>(p.weight, p.params_f32, c) : 1.0f;
-            o = p.bias ? fmaf(o, w, parameter<T>(p.bias, p.params_f32, c)) : o * w;
+            w[i * W + j] = c < channels && p.weight ? parameter<T>(p.weight, p.params_f32, c) : 1.0f;
+            b[i * W + j] = c < channels && p.bias ? parameter<T>(p.bias, p.params_f32, c) : 0.0f;
+        }
+    const float per = 1.0f / (float)channels;
+    int turn = 0;
+    for (long long base = turns.first(); base < turns.rows; base += turns.step) {
+        const bool ok = turns.wait();
+        R x[D];
+        turns.take(0, base, x);
+        float f[D][N];
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < W; ++j) f[d][i * W + j] = x[d].get(i, j);
+        if (p.residual) {
+            R e[D];
+            turns.take(1, base, e);
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        f[d][i * W + j] = to_f32(from_f32<T>(f[d][i * W + j] + e[d].get(i, j)));
+                const long long r = turns.row(base, d);
+                if (r < turns.rows)
+                    R::store(static_cast<T*>(p.sum) + at((uint32_t)r, p.length, p.sum_batch, p.sum_token), lane, channels, f[d]);
+            }
+        }
+        if constexpr (kWay != kRing) turns.fetch();
+        float mean[D], q[D];
+#pragma unroll
+        for (int d = 0; d < D; ++d) mean[d] = 0.0f;
+        if (!p.rms) {
+#pragma unroll
+            for (int d = 0; d < D; ++d)
+#pragma unroll
+                for (int i = 0; i < N; ++i) mean[d] += f[d][i];
+            row_sum<kLanes, D>(mean, &s_sum[group][turn][0][0], lane, group);
+#pragma unroll
+            for (int d = 0; d < D; ++d) mean[d] *= per;
+        }
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            q[d] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    float& c = f[d][i * W + j];
+                    c = column<T, kVec, kLanes>(i, j, lane) < channels ? c - mean[d] : 0.0f;
+                    q[d] = fmaf(c, c, q[d]);
+                }
+        }
+        row_sum<kLanes, D>(q, &s_sum[group][turn][1][0], lane, group);
+        turn ^= 1;
+        turns.done();
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            const long long r = turns.row(base, d);
+            if (r >= turns.rows) continue;
+            const float rstd = ok ? 1.0f / sqrtf(fmaf(q[d], per, p.eps)) : not_a_number();
+            if (p.saved && lane == 0) reinterpret_cast<float2*>(p.saved)[r] = make_float2(mean[d], rstd);
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[d][i] = fmaf(f[d][i] * rstd, w[i], b[i]);
+            R::store(static_cast<T*>(p.y) + at((uint32_t)r, p.length, p.y_batch, p.y_token), lane, channels, f[d]);
         }
     }
-    R::store(static_cast<T*>(p.y) + at(r, p.length, p.y_batch, p.y_token), lane, some, f);
 }
 
 // --------------------------------------------------------------- gradient
-// CTAs that an SM holds: 65536 registers by 128 a thread (64 of 1024 threads).
-template <int kLanes> constexpr int kResident = kThreads<kLanes> == 256 ? 2 : 1;
+// 128 registers a thread (64 of 1024 threads).
+template <int kLanes> constexpr int kGradResident = kThreads<kLanes> == 256 ? 2 : 1;
 
-template <class T, bool kVec, int kLanes, int NV>
-__global__ void __launch_bounds__(kThreads<kLanes>, kResident<kLanes>) norm_grad_kernel(NormParams p) {
-    constexpr int W = kWidth<T>, N = NV * W, NT = kThreads<kLanes>, kGroups = NT / kLanes;
-    __shared__ float s_sum[kGroups][2][2 * (kLanes > 32 ? kLanes / 32 : 1)];
-    __shared__ float s_col[kGroups > 1 ? NT * N : 1];
-    const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes, channels = (int)p.channels;
-    using R = Row<T, kVec, kLanes, NV>;
+template <class T, Way kWay, int kLanes, int NV>
+__global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<kLanes>) norm_grad_kernel(NormParams p) {
+    using G = Team<T, kWay, kLanes, NV>;
+    using R = Row<T, kWay != kElements, kLanes, NV>;
+    constexpr int W = G::W, N = G::N, D = G::kDeep, NT = G::NT, kGroups = G::kGroups;
+    constexpr bool kVec = kWay != kElements;
+    __shared__ float s_sum[kGroups][2][2 * D * (kLanes > 32 ? kLanes / 32 : 1)];
+    extern __shared__ __align__(128) unsigned char s_mem[];
+    const int group = threadIdx.x / kLanes, channels = (int)p.channels;
+    Turns<T, kWay, kLanes, NV, 3> turns;
+    {
+        const void* const from[3] = {p.x, p.dy, p.dsum};
+        const long long sb[3] = {p.x_batch, p.dy_batch, p.dsum_batch}, st[3] = {p.x_token, p.dy_token, p.dsum_token};
+        turns.begin(p, s_mem, from, sb, st, p.dsum ? 3 : 2);
+    }
+    const int lane = turns.lane;
     float w[N], dw[N], db[N];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -204,59 +425,68 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kResident<kLanes>) norm_grad
             dw[i * W + j] = db[i * W + j] = 0.0f;
         }
     const float per = 1.0f / (float)channels;
-    const long long step = (long long)gridDim.x * kGroups;
-    // a warp's groups go round together, for the shuffles
-    const long long first = (long long)blockIdx.x * kGroups + (kLanes >= 32 ? group : threadIdx.x / 32 * (32 / kLanes));
-    const int mine = kLanes >= 32 ? 0 : group % (32 / (kLanes < 32 ? kLanes : 32));
-    R x, dy, ds;
-    float2 stat;
-    auto fetch = [&](long long base) {
-        const long long row = base + mine;
-        const bool live = row < p.rows;
-        const uint32_t r = live ? (uint32_t)row : 0u;
-        const int some = live ? channels : 0;
-        x.load(static_cast<const T*>(p.x) + at(r, p.length, p.x_batch, p.x_token), lane, some);
-        dy.load(static_cast<const T*>(p.dy) + at(r, p.length, p.dy_batch, p.dy_token), lane, some);
-        if (p.dsum) ds.load(static_cast<const T*>(p.dsum) + at(r, p.length, p.dsum_batch, p.dsum_token), lane, some);
-        stat = __ldg(reinterpret_cast<const float2*>(p.saved) + r);
+    float2 stat[D];
+    auto fetch_stat = [&](long long base) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            const long long r = turns.row(base, d);
+            stat[d] = r < turns.rows ? __ldg(reinterpret_cast<const float2*>(p.saved) + r) : make_float2(0.0f, 0.0f);
+        }
     };
     int turn = 0;
-    if (first < p.rows) fetch(first);
-    for (long long base = first; base < p.rows; base += step) {
-        const R x0 = x, dy0 = dy, ds0 = ds;
-        const float mean = stat.x, rstd = stat.y;
-        if (base + step < p.rows) fetch(base + step);  // under way during this row's sums
-        float s[2] = {0.0f, 0.0f};
+    fetch_stat(turns.first());
+    for (long long base = turns.first(); base < turns.rows; base += turns.step) {
+        const bool ok = turns.wait();
+        R x[D], dy[D], ds[D];
+        turns.take(0, base, x);
+        turns.take(1, base, dy);
+        if (p.dsum) turns.take(2, base, ds);
+        float mean[D], rstd[D], s[2 * D];
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int d = 0; d < D; ++d) {
+            mean[d] = stat[d].x;
+            rstd[d] = ok ? stat[d].y : not_a_number();
+            s[2 * d] = s[2 * d + 1] = 0.0f;
+        }
+        fetch_stat(base + turns.step);
+        if constexpr (kWay != kRing) turns.fetch();
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                const int k = i * W + j;
-                const float g = dy0.get(i, j), n = (x0.get(i, j) - mean) * rstd, dn = g * w[k];
-                s[0] += dn;
-                // w = 0 behind the row's end, where n is not 0
-                s[1] = fmaf(dn, n, s[1]);
-                db[k] += g;
-                dw[k] = fmaf(g, n, dw[k]);
-            }
-        row_sum<kLanes, 2>(s, s_sum[group][turn], lane, group);
+        for (int d = 0; d < D; ++d)
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    const int k = i * W + j;
+                    const float g = dy[d].get(i, j), n = (x[d].get(i, j) - mean[d]) * rstd[d], dn = g * w[k];
+                    s[2 * d] += dn;
+                    // w = 0 behind the row's end, where n is not 0
+                    s[2 * d + 1] = fmaf(dn, n, s[2 * d + 1]);
+                    db[k] += g;
+                    dw[k] = fmaf(g, n, dw[k]);
+                }
+        row_sum<kLanes, 2 * D>(s, s_sum[group][turn], lane, group);
         turn ^= 1;
-        const float a = p.rms ? 0.0f : s[0] * per, b = s[1] * per;
-        float o[N];
+        turns.done();
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int d = 0; d < D; ++d) {
+            const float a = p.rms ? 0.0f : s[2 * d] * per, b = s[2 * d + 1] * per;
+            float o[N];
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                const int k = i * W + j;
-                const float n = (x0.get(i, j) - mean) * rstd;
-                o[k] = fmaf(-n, b, dy0.get(i, j) * w[k] - a) * rstd;
-                if (p.dsum) o[k] += ds0.get(i, j);
-            }
-        if (base + mine < p.rows)
-            R::store(static_cast<T*>(p.dx) + (base + mine) * channels, lane, channels, o);
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    const int k = i * W + j;
+                    const float n = (x[d].get(i, j) - mean[d]) * rstd[d];
+                    o[k] = fmaf(-n, b, dy[d].get(i, j) * w[k] - a) * rstd[d];
+                    if (p.dsum) o[k] += ds[d].get(i, j);
+                }
+            const long long r = turns.row(base, d);
+            if (r < turns.rows) R::store(static_cast<T*>(p.dx) + r * channels, lane, channels, o);
+        }
     }
     if (!p.partials) return;
     // one row of partial sums a CTA: over its groups, in their order
+    float* s_col = reinterpret_cast<float*>(s_mem);
     auto put = [&](int which, const float (&v)[N]) {
         float* to = p.partials + ((long long)blockIdx.x * 2 + which) * channels;
         if constexpr (kGroups == 1) {
@@ -421,7 +651,7 @@ __global__ void __launch_bounds__(kWideNT) norm_grad_wide_kernel(NormParams p) {
 }
 
 // Columns' sums over the rows blockIdx.y, + parts, ...: into partials.
-constexpr int kColumnNT = 256;
+constexpr int kColumnNT = 256, kColumnParts = 32;
 template <class T>
 __global__ void __launch_bounds__(kColumnNT) norm_columns_kernel(NormParams p) {
     const long long c = (long long)blockIdx.x * kColumnNT + threadIdx.x;
@@ -441,33 +671,72 @@ __global__ void __launch_bounds__(kColumnNT) norm_columns_kernel(NormParams p) {
 }
 
 // ---------------------------------------------------------------- launch
-template <class T, bool kVec, int kLanes, int NV>
-cudaError_t go(const NormParams& p, bool grad, cudaStream_t s) {
-    constexpr int NT = kThreads<kLanes>, kGroups = NT / kLanes;
-    if (grad) norm_grad_kernel<T, kVec, kLanes, NV><<<(unsigned)p.parts, NT, 0, s>>>(p);
-    else norm_kernel<T, kVec, kLanes, NV><<<(unsigned)((p.rows + (long long)kGroups - 1) / kGroups), NT, 0, s>>>(p);
-    return cudaGetLastError();
+// Shared memory of an SM that its rings share, and of a CTA's ring at most.
+constexpr int kRingBytes = 200 * 1024;
+
+template <class T, Way kWay, int kLanes, int NV>
+cudaError_t go(NormParams& p, bool grad, cudaStream_t s) {
+    using G = Team<T, kWay, kLanes, NV>;
+    const long long turns = (p.rows + (long long)G::kTeams * G::kRows - 1) / (G::kTeams * G::kRows);
+    const int resident = grad ? kGradResident<kLanes> : kResident<kWay, kLanes>;
+    const int tensors = grad ? (p.dsum ? 3 : 2) : p.residual ? 2 : 1;
+    int bytes = grad && G::kGroups > 1 ? (int)sizeof(float) * G::NT * G::N : 0;  // the columns' sums
+    if (kWay == kRing) {
+        const int stage = G::kTeams * tensors * G::kRows * (int)(p.channels * sizeof(T));
+        p.stages = std::clamp(kRingBytes / resident / stage, 2, 8);
+        bytes = std::max(bytes, p.stages * (stage + G::kTeams * 8));
+    }
+    p.parts = std::min(turns, seq_sms() * resident);
+    const void* kernel = grad ? (const void*)norm_grad_kernel<T, kWay, kLanes, NV> : (const void*)norm_kernel<T, kWay, kLanes, NV>;
+    // the limit is one per device: always the largest, whatever this call needs
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes + 8192);
+    if (e != cudaSuccess) return e;
+    void* args[] = {&p};
+    e = cudaLaunchKernel(kernel, dim3((unsigned)p.parts), dim3(G::NT), args, (size_t)bytes, s);
+    return e;
 }
 
-template <class T, bool kVec>
-cudaError_t by_width(const NormParams& p, bool grad, cudaStream_t s) {
+// Through the ring where CTAs have several turns to take.
+template <class T, int kLanes, int NV>
+cudaError_t vectors(NormParams& p, bool grad, cudaStream_t s) {
+    using G = Team<T, kVectors, kLanes, NV>;
+    const long long held = seq_sms() * (grad ? kGradResident<kLanes> : kResident<kVectors, kLanes>) * G::kTeams * G::kRows;
+    if (p.rows <= held) return go<T, kVectors, kLanes, NV>(p, grad, s);
+    return go<T, kRing, kLanes, NV>(p, grad, s);
+}
+
+template <class T>
+cudaError_t by_width(NormParams& p, bool grad, cudaStream_t s) {
     const long long n = (p.channels + kWidth<T> - 1) / kWidth<T>;
-    if (n <= 8) return go<T, kVec, 8, 1>(p, grad, s);
-    if (n <= 16) return go<T, kVec, 16, 1>(p, grad, s);
-    if (n <= 32) return go<T, kVec, 32, 1>(p, grad, s);
-    if (n <= 64) return go<T, kVec, 32, 2>(p, grad, s);
-    if (n <= 128) return go<T, kVec, 64, 2>(p, grad, s);
-    if (n <= 256) return go<T, kVec, 128, 2>(p, grad, s);
-    if (n <= 512) return go<T, kVec, 256, 2>(p, grad, s);
-    if (n <= 1024) return go<T, kVec, 512, 2>(p, grad, s);
-    if constexpr (sizeof(T) == 4) return go<T, kVec, 1024, 2>(p, grad, s);
+    if (!p.vec) {
+        // 16-bit elements one by one: 8 a thread (with 16 the gradient's rows do not fit the registers)
+        constexpr int NV = sizeof(T) == 4 ? 2 : 1;
+        if (n <= 8) return go<T, kElements, 8, 1>(p, grad, s);
+        if (n <= 16) return go<T, kElements, 16, 1>(p, grad, s);
+        if (n <= 32) return go<T, kElements, 32, 1>(p, grad, s);
+        if (n <= 32 * NV) return go<T, kElements, 32, NV>(p, grad, s);
+        if (n <= 64 * NV) return go<T, kElements, 64, NV>(p, grad, s);
+        if (n <= 128 * NV) return go<T, kElements, 128, NV>(p, grad, s);
+        if (n <= 256 * NV) return go<T, kElements, 256, NV>(p, grad, s);
+        if (n <= 512 * NV) return go<T, kElements, 512, NV>(p, grad, s);
+        return go<T, kElements, 1024, NV>(p, grad, s);
+    }
+    if (n <= 8) return vectors<T, 8, 1>(p, grad, s);
+    if (n <= 16) return vectors<T, 16, 1>(p, grad, s);
+    if (n <= 32) return vectors<T, 32, 1>(p, grad, s);
+    if (n <= 64) return vectors<T, 32, 2>(p, grad, s);
+    if (n <= 128) return vectors<T, 64, 2>(p, grad, s);
+    if (n <= 256) return vectors<T, 128, 2>(p, grad, s);
+    if (n <= 512) return vectors<T, 256, 2>(p, grad, s);
+    if (n <= 1024) return vectors<T, 512, 2>(p, grad, s);
+    if constexpr (sizeof(T) == 4) return vectors<T, 1024, 2>(p, grad, s);
     return cudaErrorInvalidValue;
 }
 
 template <class T>
-cudaError_t launch_norm_as(const NormParams& p, bool grad, cudaStream_t s) {
+cudaError_t launch_norm_as(NormParams& p, bool grad, cudaStream_t s) {
     if (p.channels <= kRowMax) {
-        const cudaError_t e = p.vec ? by_width<T, true>(p, grad, s) : by_width<T, false>(p, grad, s);
+        const cudaError_t e = by_width<T>(p, grad, s);
         count_launches(1);
         return e;
     }
@@ -482,6 +751,7 @@ cudaError_t launch_norm_as(const NormParams& p, bool grad, cudaStream_t s) {
     count_launches(1);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !p.partials) return e;
+    p.parts = std::min<long long>(p.rows, kColumnParts);
     const dim3 grid((unsigned)((p.channels + kColumnNT - 1) / kColumnNT), (unsigned)p.parts);
     norm_columns_kernel<T><<<grid, kColumnNT, 0, s>>>(p);
     count_launches(1);
@@ -491,8 +761,8 @@ cudaError_t launch_norm_as(const NormParams& p, bool grad, cudaStream_t s) {
 }  // namespace
 
 // By element type, one translation unit each.
-cudaError_t launch_norm_f32(const NormParams& p, bool grad, cudaStream_t s);
-cudaError_t launch_norm_f16(const NormParams& p, bool grad, cudaStream_t s);
-cudaError_t launch_norm_bf16(const NormParams& p, bool grad, cudaStream_t s);
+cudaError_t launch_norm_f32(NormParams& p, bool grad, cudaStream_t s);
+cudaError_t launch_norm_f16(NormParams& p, bool grad, cudaStream_t s);
+cudaError_t launch_norm_bf16(NormParams& p, bool grad, cudaStream_t s);
 
 }  // namespace scg

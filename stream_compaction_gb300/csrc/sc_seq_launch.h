@@ -155,7 +155,7 @@ cudaError_t launch_gated_step(int dtype, const GatedParams& p, cudaStream_t s);
 
 // ---------------------------------------------------------------- norm
 struct NormParams {
-    int rms, params_f32, vec;
+    int rms, params_f32, vec, dense, stages;  // dense: all rows follow one another
     float eps;
     uint32_t rows, length;  // rows = batch * length
     long long channels;
@@ -170,15 +170,11 @@ struct NormParams {
     void* dx;
     float *dweight, *dbias;
     float* partials;  // [parts][2][channels]: dweight, dbias
-    long long parts;
+    long long parts;  // set by the launch
 };
-cudaError_t launch_norm(int dtype, const NormParams& p, cudaStream_t s);
-struct NormGradPlan {
-    long long parts;
-    size_t partials, total;  // offset, then the size
-};
-NormGradPlan norm_grad_plan(int dtype, long long rows, long long channels);
-cudaError_t launch_norm_grad(int dtype, const NormParams& p, cudaStream_t s);
+cudaError_t launch_norm(int dtype, NormParams p, cudaStream_t s);
+size_t norm_grad_scratch(long long rows, long long channels);  // bytes of partials
+cudaError_t launch_norm_grad(int dtype, NormParams p, cudaStream_t s);
 
 // -------------------------------------------------------------- experts
 cudaError_t launch_expert_sort(const void* ids, int ids64, long long entries, int experts, int32_t* order, int32_t* place,
