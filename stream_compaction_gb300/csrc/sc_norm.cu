@@ -7,27 +7,30 @@ namespace scg {
 namespace {
 
 // Column c of dweight (blockIdx.y == 0) or dbias: kSumRows threads take every
-// kSumRows-th row of partial sums, then their sums are added in order.
-constexpr int kSumCols = 32, kSumRows = 16;
+// kSumRows-th row of partial sums, then their sums are added in order.  Launched while
+// the kernel before it ends, it waits for that one's rows.
+constexpr int kSumCols = 32, kSumRows = 32, kSumAhead = 8;
 __global__ void __launch_bounds__(kSumCols* kSumRows) norm_parameters_kernel(NormParams p) {
     __shared__ float s_part[kSumRows][kSumCols];
     const int tx = threadIdx.x % kSumCols, ty = threadIdx.x / kSumCols;
     const long long c = (long long)blockIdx.x * kSumCols + tx;
     const int which = blockIdx.y;
     float* to = which ? p.dbias : p.dweight;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!to) return;
     float sum = 0.0f;
     if (c < p.channels) {
         const float* from = p.partials + which * p.channels + c;
-        long long i = ty;
-        for (; i + 3 * kSumRows < p.parts; i += 4 * kSumRows) {
-            float v[4];
+        for (long long i0 = ty; i0 < p.parts; i0 += kSumAhead * kSumRows) {
+            float v[kSumAhead];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = from[(i + k * kSumRows) * 2 * p.channels];
+            for (int k = 0; k < kSumAhead; ++k) {
+                const long long i = i0 + k * kSumRows;
+                v[k] = i < p.parts ? from[i * 2 * p.channels] : 0.0f;
+            }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) sum += v[k];
+            for (int k = 0; k < kSumAhead; ++k) sum += v[k];
         }
-        for (; i < p.parts; i += kSumRows) sum += from[i * 2 * p.channels];
     }
     s_part[ty][tx] = sum;
     __syncthreads();
@@ -57,10 +60,17 @@ size_t norm_grad_scratch(long long rows, long long channels) {
 cudaError_t launch_norm_grad(int dtype, NormParams p, cudaStream_t s) {
     const cudaError_t e = by_type(dtype, p, true, s);
     if (e != cudaSuccess || !p.partials) return e;
-    const dim3 grid((unsigned)((p.channels + kSumCols - 1) / kSumCols), 2);
-    norm_parameters_kernel<<<grid, kSumCols * kSumRows, 0, s>>>(p);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((p.channels + kSumCols - 1) / kSumCols), 2);
+    cfg.blockDim = dim3(kSumCols * kSumRows);
+    cfg.stream = s;
+    cudaLaunchAttribute a{};
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &a;
+    cfg.numAttrs = 1;
     count_launches(1);
-    return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, norm_parameters_kernel, p);
 }
 
 }  // namespace scg

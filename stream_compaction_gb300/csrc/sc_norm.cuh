@@ -37,7 +37,9 @@ constexpr long long kRowMax = 8192;
 
 template <class T> constexpr int kWidth = 16 / (int)sizeof(T);  // elements of a vector
 
+// A row's first element: rows of `length` tokens, or all in one stride (length >= rows).
 __device__ __forceinline__ long long at(uint32_t row, uint32_t length, long long sb, long long st) {
+    if (row < length) return (long long)row * st;
     const uint32_t b = row / length;
     return (long long)b * sb + (long long)(row - b * length) * st;
 }
@@ -78,27 +80,54 @@ struct Row {
             else v[i].zero();
         }
     }
-    __device__ __forceinline__ float get(int i, int j) const { return v[i].get(j); }
-    __device__ __forceinline__ static void store(T* p, int lane, int channels, const float (&f)[NV * W]) {
+    // Elements 2 j and 2 j + 1 of vector i.
+    __device__ __forceinline__ f2 pair(int i, int j) const { return v[i].pair(j); }
+    // The elements of f (as pairs, vector by vector) to a row, rounded; `rounded`: and back in f.
+    template <bool kRounded = false>
+    __device__ __forceinline__ static void store(T* p, int lane, int channels, f2 (&f)[NV * W / 2]) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if constexpr (kVec) {
                 const int c = column<T, kVec, kLanes>(i, 0, lane);
-                if (c < channels) {
-                    Vec<T, W> o;
-                    o.set(&f[i * W]);
-                    o.store(p + c);
-                }
+                Vec<T, W> o;
+#pragma unroll
+                for (int j = 0; j < W / 2; ++j) set_pair(o, j, f[i * W / 2 + j]);
+                if (kRounded)
+#pragma unroll
+                    for (int j = 0; j < W / 2; ++j) f[i * W / 2 + j] = o.pair(j);
+                if (c < channels) o.store(p + c);
             } else {
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
                     const int c = column<T, kVec, kLanes>(i, j, lane);
-                    if (c < channels) p[c] = from_f32<T>(f[i * W + j]);
+                    f2& v = f[(i * W + j) / 2];
+                    const T e = from_f32<T>(j % 2 ? hi2(v) : lo2(v));
+                    if (kRounded) v = j % 2 ? pack2(lo2(v), to_f32(e)) : pack2(to_f32(e), hi2(v));
+                    if (c < channels) p[c] = e;
                 }
             }
         }
     }
+    __device__ __forceinline__ static void set_pair(Vec<T, W>& o, int j, f2 v) {
+        if constexpr (sizeof(T) == 4) {
+            o.w[2 * j] = __float_as_uint(lo2(v));
+            o.w[2 * j + 1] = __float_as_uint(hi2(v));
+        } else if constexpr (std::is_same<T, bf16>::value) {
+            const __nv_bfloat162 e = __floats2bfloat162_rn(lo2(v), hi2(v));
+            memcpy(&o.w[j], &e, 4);
+        } else {
+            const __half2 e = __floats2half2_rn(lo2(v), hi2(v));
+            memcpy(&o.w[j], &e, 4);
+        }
+    }
 };
+__device__ __forceinline__ float sum2(f2 v) { return lo2(v) + hi2(v); }
+// 1 / sqrt(v): the instruction's result and a step of Newton's, which would make NaN of 0
+// and of infinity (rounding: within 1.5 units of 2^-23; the instruction's is 2).
+__device__ __forceinline__ float inverse_root(float v) {
+    const float r = rsqrtf(v), n = fmaf(0.5f * r, fmaf(-v * r, r, 1.0f), r);
+    return n == n ? n : r;
+}
 
 template <class T>
 __device__ __forceinline__ float parameter(const void* p, int f32, int c) {
@@ -123,10 +152,24 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* slot, int lane, in
         asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kLanes) : "memory");
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            float s = 0.0f;
+            float s[kWarps];
+            constexpr int kAtOnce = kWarps < 4 ? kWarps : 4;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) s += slot[k * kWarps + w];
-            v[k] = s;
+            for (int w = 0; w < kWarps; w += kAtOnce) {
+                if constexpr (kAtOnce == 4) {
+                    const float4 q = *reinterpret_cast<const float4*>(slot + k * kWarps + w);
+                    s[w] = q.x, s[w + 1] = q.y, s[w + 2] = q.z, s[w + 3] = q.w;
+                } else {
+                    const float2 q = *reinterpret_cast<const float2*>(slot + k * kWarps + w);
+                    s[w] = q.x, s[w + 1] = q.y;
+                }
+            }
+            // in pairs, then their sums, for a short chain
+#pragma unroll
+            for (int o = 1; o < kWarps; o *= 2)
+#pragma unroll
+                for (int w = 0; w < kWarps; w += 2 * o) s[w] += s[w + o];
+            v[k] = s[0];
         }
     }
 }
@@ -307,7 +350,7 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kResident<kWay, kLanes>) nor
     using R = Row<T, kWay != kElements, kLanes, NV>;
     constexpr int W = G::W, N = G::N, D = G::kDeep;
     constexpr bool kVec = kWay != kElements;
-    __shared__ float s_sum[G::kGroups][2][2][kLanes > 32 ? kLanes / 32 : 1];
+    __shared__ __align__(16) float s_sum[G::kGroups][2][2][kLanes > 32 ? kLanes / 32 : 1];
     extern __shared__ __align__(128) unsigned char s_mem[];
     const int group = threadIdx.x / kLanes, channels = (int)p.channels;
     Turns<T, kWay, kLanes, NV, 2> turns;
@@ -317,41 +360,47 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kResident<kWay, kLanes>) nor
         turns.begin(p, s_mem, from, sb, st, p.residual ? 2 : 1);
     }
     const int lane = turns.lane;
-    float w[N], b[N];
+    f2 w[N / 2], b[N / 2];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            const int c = column<T, kVec, kLanes>(i, j, lane);
-            w[i * W + j] = c < channels && p.weight ? parameter<T>(p.weight, p.params_f32, c) : 1.0f;
-            b[i * W + j] = c < channels && p.bias ? parameter<T>(p.bias, p.params_f32, c) : 0.0f;
+        for (int j = 0; j < W; j += 2) {
+            float v[2][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int c = column<T, kVec, kLanes>(i, j + h, lane);
+                v[0][h] = c < channels && p.weight ? parameter<T>(p.weight, p.params_f32, c) : 1.0f;
+                v[1][h] = c < channels && p.bias ? parameter<T>(p.bias, p.params_f32, c) : 0.0f;
+            }
+            w[(i * W + j) / 2] = pack2(v[0][0], v[0][1]);
+            b[(i * W + j) / 2] = pack2(v[1][0], v[1][1]);
         }
     const float per = 1.0f / (float)channels;
+    const bool full = channels == kLanes * N;
     int turn = 0;
     for (long long base = turns.first(); base < turns.rows; base += turns.step) {
         const bool ok = turns.wait();
         R x[D];
         turns.take(0, base, x);
-        float f[D][N];
+        f2 f[D][N / 2];
 #pragma unroll
         for (int d = 0; d < D; ++d)
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < W; ++j) f[d][i * W + j] = x[d].get(i, j);
+                for (int j = 0; j < W / 2; ++j) f[d][i * W / 2 + j] = x[d].pair(i, j);
         if (p.residual) {
-            R e[D];
-            turns.take(1, base, e);
+            turns.take(1, base, x);
 #pragma unroll
             for (int d = 0; d < D; ++d) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
-                    for (int j = 0; j < W; ++j)
-                        f[d][i * W + j] = to_f32(from_f32<T>(f[d][i * W + j] + e[d].get(i, j)));
+                    for (int j = 0; j < W / 2; ++j) f[d][i * W / 2 + j] = add2(f[d][i * W / 2 + j], x[d].pair(i, j));
                 const long long r = turns.row(base, d);
-                if (r < turns.rows)
-                    R::store(static_cast<T*>(p.sum) + at((uint32_t)r, p.length, p.sum_batch, p.sum_token), lane, channels, f[d]);
+                const bool live = r < turns.rows;
+                R::template store<true>(static_cast<T*>(p.sum) + at(live ? (uint32_t)r : 0u, p.length, p.sum_batch, p.sum_token),
+                                        lane, live ? channels : 0, f[d]);
             }
         }
         if constexpr (kWay != kRing) turns.fetch();
@@ -360,24 +409,39 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kResident<kWay, kLanes>) nor
         for (int d = 0; d < D; ++d) mean[d] = 0.0f;
         if (!p.rms) {
 #pragma unroll
-            for (int d = 0; d < D; ++d)
+            for (int d = 0; d < D; ++d) {
+                f2 sum = f[d][0];
 #pragma unroll
-                for (int i = 0; i < N; ++i) mean[d] += f[d][i];
+                for (int i = 1; i < N / 2; ++i) sum = add2(sum, f[d][i]);
+                mean[d] = sum2(sum);
+            }
             row_sum<kLanes, D>(mean, &s_sum[group][turn][0][0], lane, group);
 #pragma unroll
-            for (int d = 0; d < D; ++d) mean[d] *= per;
+            for (int d = 0; d < D; ++d) {
+                mean[d] *= per;
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) f[d][i] = add2(f[d][i], both(-mean[d]));
+            }
+            if (!full) {  // behind the row's end: not minus the mean
+#pragma unroll
+                for (int d = 0; d < D; ++d)
+#pragma unroll
+                    for (int i = 0; i < NV; ++i)
+#pragma unroll
+                        for (int j = 0; j < W / 2; ++j) {
+                            f2& v = f[d][i * W / 2 + j];
+                            if (kVec) v = column<T, kVec, kLanes>(i, 0, lane) < channels ? v : 0ull;
+                            else v = pack2(column<T, kVec, kLanes>(i, 2 * j, lane) < channels ? lo2(v) : 0.0f,
+                                           column<T, kVec, kLanes>(i, 2 * j + 1, lane) < channels ? hi2(v) : 0.0f);
+                        }
+            }
         }
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-            q[d] = 0.0f;
+            f2 sum = mul2(f[d][0], f[d][0]);
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    float& c = f[d][i * W + j];
-                    c = column<T, kVec, kLanes>(i, j, lane) < channels ? c - mean[d] : 0.0f;
-                    q[d] = fmaf(c, c, q[d]);
-                }
+            for (int i = 1; i < N / 2; ++i) sum = fma2(f[d][i], f[d][i], sum);
+            q[d] = sum2(sum);
         }
         row_sum<kLanes, D>(q, &s_sum[group][turn][1][0], lane, group);
         turn ^= 1;
@@ -385,12 +449,13 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kResident<kWay, kLanes>) nor
 #pragma unroll
         for (int d = 0; d < D; ++d) {
             const long long r = turns.row(base, d);
-            if (r >= turns.rows) continue;
-            const float rstd = ok ? 1.0f / sqrtf(fmaf(q[d], per, p.eps)) : not_a_number();
-            if (p.saved && lane == 0) reinterpret_cast<float2*>(p.saved)[r] = make_float2(mean[d], rstd);
+            const bool live = r < turns.rows;
+            const float rstd = ok ? inverse_root(fmaf(q[d], per, p.eps)) : not_a_number();
+            if (p.saved && lane == 0 && live) reinterpret_cast<float2*>(p.saved)[r] = make_float2(mean[d], rstd);
 #pragma unroll
-            for (int i = 0; i < N; ++i) f[d][i] = fmaf(f[d][i] * rstd, w[i], b[i]);
-            R::store(static_cast<T*>(p.y) + at((uint32_t)r, p.length, p.y_batch, p.y_token), lane, channels, f[d]);
+            for (int i = 0; i < N / 2; ++i) f[d][i] = fma2(mul2(f[d][i], both(rstd)), w[i], b[i]);
+            R::store(static_cast<T*>(p.y) + at(live ? (uint32_t)r : 0u, p.length, p.y_batch, p.y_token), lane, live ? channels : 0,
+                     f[d]);
         }
     }
 }
@@ -405,7 +470,7 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<kLanes>) norm_
     using R = Row<T, kWay != kElements, kLanes, NV>;
     constexpr int W = G::W, N = G::N, D = G::kDeep, NT = G::NT, kGroups = G::kGroups;
     constexpr bool kVec = kWay != kElements;
-    __shared__ float s_sum[kGroups][2][2 * D * (kLanes > 32 ? kLanes / 32 : 1)];
+    __shared__ __align__(16) float s_sum[kGroups][2][2 * D * (kLanes > 32 ? kLanes / 32 : 1)];
     extern __shared__ __align__(128) unsigned char s_mem[];
     const int group = threadIdx.x / kLanes, channels = (int)p.channels;
     Turns<T, kWay, kLanes, NV, 3> turns;
@@ -415,14 +480,19 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<kLanes>) norm_
         turns.begin(p, s_mem, from, sb, st, p.dsum ? 3 : 2);
     }
     const int lane = turns.lane;
-    float w[N], dw[N], db[N];
+    f2 w[N / 2], dw[N / 2], db[N / 2];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            const int c = column<T, kVec, kLanes>(i, j, lane);
-            w[i * W + j] = c >= channels ? 0.0f : p.weight ? parameter<T>(p.weight, p.params_f32, c) : 1.0f;
-            dw[i * W + j] = db[i * W + j] = 0.0f;
+        for (int j = 0; j < W; j += 2) {
+            float v[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int c = column<T, kVec, kLanes>(i, j + h, lane);
+                v[h] = c >= channels ? 0.0f : p.weight ? parameter<T>(p.weight, p.params_f32, c) : 1.0f;
+            }
+            w[(i * W + j) / 2] = pack2(v[0], v[1]);
+            dw[(i * W + j) / 2] = db[(i * W + j) / 2] = 0ull;
         }
     const float per = 1.0f / (float)channels;
     float2 stat[D];
@@ -446,48 +516,61 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<kLanes>) norm_
         for (int d = 0; d < D; ++d) {
             mean[d] = stat[d].x;
             rstd[d] = ok ? stat[d].y : not_a_number();
-            s[2 * d] = s[2 * d + 1] = 0.0f;
         }
         fetch_stat(base + turns.step);
         if constexpr (kWay != kRing) turns.fetch();
 #pragma unroll
-        for (int d = 0; d < D; ++d)
+        for (int d = 0; d < D; ++d) {
+            f2 a = 0ull, b = 0ull;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    const int k = i * W + j;
-                    const float g = dy[d].get(i, j), n = (x[d].get(i, j) - mean[d]) * rstd[d], dn = g * w[k];
-                    s[2 * d] += dn;
-                    // w = 0 behind the row's end, where n is not 0
-                    s[2 * d + 1] = fmaf(dn, n, s[2 * d + 1]);
-                    db[k] += g;
-                    dw[k] = fmaf(g, n, dw[k]);
+                for (int j = 0; j < W / 2; ++j) {
+                    const int k = i * W / 2 + j;
+                    const f2 g = dy[d].pair(i, j), n = mul2(add2(x[d].pair(i, j), both(-mean[d])), both(rstd[d])), dn = mul2(g, w[k]);
+                    a = add2(a, dn);
+                    b = fma2(dn, n, b);  // w = 0 behind the row's end, where n is not 0
+                    db[k] = add2(db[k], g);
+                    dw[k] = fma2(g, n, dw[k]);
                 }
+            s[2 * d] = sum2(a);
+            s[2 * d + 1] = sum2(b);
+        }
         row_sum<kLanes, 2 * D>(s, s_sum[group][turn], lane, group);
         turn ^= 1;
         turns.done();
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-            const float a = p.rms ? 0.0f : s[2 * d] * per, b = s[2 * d + 1] * per;
-            float o[N];
+            const f2 a = both(p.rms ? 0.0f : -s[2 * d] * per), b = both(-s[2 * d + 1] * per);
+            f2 o[N / 2];
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    const int k = i * W + j;
-                    const float n = (x[d].get(i, j) - mean[d]) * rstd[d];
-                    o[k] = fmaf(-n, b, dy[d].get(i, j) * w[k] - a) * rstd[d];
-                    if (p.dsum) o[k] += ds[d].get(i, j);
+                for (int j = 0; j < W / 2; ++j) {
+                    const int k = i * W / 2 + j;
+                    const f2 n = mul2(add2(x[d].pair(i, j), both(-mean[d])), both(rstd[d]));
+                    o[k] = fma2(n, b, fma2(dy[d].pair(i, j), w[k], a));
                 }
+            if (p.dsum) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int j = 0; j < W / 2; ++j) o[i * W / 2 + j] = fma2(o[i * W / 2 + j], both(rstd[d]), ds[d].pair(i, j));
+            } else {
+#pragma unroll
+                for (int k = 0; k < N / 2; ++k) o[k] = mul2(o[k], both(rstd[d]));
+            }
             const long long r = turns.row(base, d);
-            if (r < turns.rows) R::store(static_cast<T*>(p.dx) + r * channels, lane, channels, o);
+            const bool live = r < turns.rows;
+            R::store(static_cast<T*>(p.dx) + (live ? r : 0) * channels, lane, live ? channels : 0, o);
         }
     }
     if (!p.partials) return;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the kernel that adds the partial sums may get ready
     // one row of partial sums a CTA: over its groups, in their order
     float* s_col = reinterpret_cast<float*>(s_mem);
-    auto put = [&](int which, const float (&v)[N]) {
+    auto put = [&](int which, const f2 (&v)[N / 2]) {
+        auto element = [&](int k) { return k % 2 ? hi2(v[k / 2]) : lo2(v[k / 2]); };
         float* to = p.partials + ((long long)blockIdx.x * 2 + which) * channels;
         if constexpr (kGroups == 1) {
 #pragma unroll
@@ -495,14 +578,14 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<kLanes>) norm_
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
                     const int c = column<T, kVec, kLanes>(i, j, lane);
-                    if (c < channels) to[c] = v[i * W + j];
+                    if (c < channels) to[c] = element(i * W + j);
                 }
         } else {
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < W; ++j) s_col[group * (kLanes * N) + column<T, kVec, kLanes>(i, j, lane)] = v[i * W + j];
+                for (int j = 0; j < W; ++j) s_col[group * (kLanes * N) + column<T, kVec, kLanes>(i, j, lane)] = element(i * W + j);
             __syncthreads();
             for (int c = threadIdx.x; c < channels; c += NT) {
                 float sum = 0.0f;
@@ -557,7 +640,7 @@ __device__ __forceinline__ void give(T* p, const float (&f)[kEach<T, kVec>]) {
 template <class T, bool kVec>
 __global__ void __launch_bounds__(kWideNT) norm_wide_kernel(NormParams p) {
     constexpr int E = kEach<T, kVec>;
-    __shared__ float slot[2][kWideNT / 32];
+    __shared__ __align__(16) float slot[2][kWideNT / 32];
     const uint32_t r = blockIdx.x;
     const T* x = static_cast<const T*>(p.x) + at(r, p.length, p.x_batch, p.x_token);
     T* y = static_cast<T*>(p.y) + at(r, p.length, p.y_batch, p.y_token);
@@ -597,7 +680,7 @@ __global__ void __launch_bounds__(kWideNT) norm_wide_kernel(NormParams p) {
         for (int i = 0; i < E; ++i) q[0] = fmaf(f[i] - mean, f[i] - mean, q[0]);
     });
     cta_sum<1>(q, slot[1]);
-    const float rstd = 1.0f / sqrtf(fmaf(q[0], per, p.eps));
+    const float rstd = inverse_root(fmaf(q[0], per, p.eps));
     if (p.saved && threadIdx.x == 0) reinterpret_cast<float2*>(p.saved)[r] = make_float2(mean, rstd);
     each<T, kVec>(ch, [&](long long c) {
         float f[E];
@@ -614,7 +697,7 @@ __global__ void __launch_bounds__(kWideNT) norm_wide_kernel(NormParams p) {
 template <class T, bool kVec>
 __global__ void __launch_bounds__(kWideNT) norm_grad_wide_kernel(NormParams p) {
     constexpr int E = kEach<T, kVec>;
-    __shared__ float slot[2 * kWideNT / 32];
+    __shared__ __align__(16) float slot[2 * kWideNT / 32];
     const uint32_t r = blockIdx.x;
     const T* x = static_cast<const T*>(p.x) + at(r, p.length, p.x_batch, p.x_token);
     const T* dy = static_cast<const T*>(p.dy) + at(r, p.length, p.dy_batch, p.dy_token);
