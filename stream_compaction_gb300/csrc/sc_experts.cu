@@ -228,46 +228,75 @@ __global__ void __launch_bounds__(kNT) expert_gather_kernel(ExpertParams p, int 
     }
 }
 
-// out[t] = sum over j of weights[t,j] rows[place[t,j]]
-template <class T, bool kVec>
+// A batch of kAhead choices of a token: their rows (-1: none) and weights.
+struct Batch {
+    long long row[kAhead];
+    float weight[kAhead];
+};
+template <class T>
+__device__ __forceinline__ Batch batch_of(const ExpertParams& p, long long entry, long long left, long long kept) {
+    Batch b;
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+        const long long row = a < left ? __ldg(p.place + entry + a) : -1;
+        b.row[a] = row >= 0 && row < kept ? row : -1;
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) b.weight[a] = b.row[a] >= 0 ? weight_of<T>(p, entry + a) : 0.0f;
+    return b;
+}
+
+// out[t] = sum over j of weights[t,j] rows[place[t,j]].  A lane has kColumns vectors of
+// the token, kAhead rows of each: up to kAhead kColumns loads under way.
+template <class T, bool kVec, int kColumns>
 __global__ void __launch_bounds__(kNT) expert_combine_kernel(ExpertParams p, int lanes) {
     const Where at = where(lanes);
     if (at.token >= p.tokens) return;
     const long long kept = kept_of(p);
     const long long entry = at.token * p.choices;
     const T* rows = static_cast<const T*>(p.in);
+    T* out = static_cast<T*>(p.out) + at.token * p.ld_out;
     constexpr int W = Part<T, kVec>::W;
-    for (long long c = (long long)at.lane * W; c < p.dim; c += lanes * W) {
-        float sum[W];
+    const Batch first = batch_of<T>(p, entry, p.choices, kept);
+    for (long long c0 = (long long)at.lane * W; c0 < p.dim; c0 += (long long)lanes * W * kColumns) {
+        float sum[kColumns][W];
 #pragma unroll
-        for (int i = 0; i < W; ++i) sum[i] = 0.0f;
+        for (int k = 0; k < kColumns; ++k)
+#pragma unroll
+            for (int i = 0; i < W; ++i) sum[k][i] = 0.0f;
         for (long long j0 = 0; j0 < p.choices; j0 += kAhead) {
-            Part<T, kVec> v[kAhead];
-            bool live[kAhead];
+            const Batch b = j0 == 0 ? first : batch_of<T>(p, entry + j0, p.choices - j0, kept);
+            Part<T, kVec> v[kAhead][kColumns];
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a)
+#pragma unroll
+                for (int k = 0; k < kColumns; ++k)
+                    if (b.row[a] >= 0 && c0 + k * lanes * W < p.dim) v[a][k].load(rows + b.row[a] * p.ld_in + c0 + k * lanes * W);
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
-                const long long row = j0 + a < p.choices ? __ldg(p.place + entry + j0 + a) : -1;
-                live[a] = row >= 0 && row < kept;
-                if (live[a]) v[a].load(rows + row * p.ld_in + c);
-            }
+                if (b.row[a] < 0) continue;
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                if (!live[a]) continue;
-                const float w = weight_of<T>(p, entry + j0 + a);
-                float f[W];
-                v[a].get(f);
+                for (int k = 0; k < kColumns; ++k) {
+                    float f[W];
+                    v[a][k].get(f);
 #pragma unroll
-                for (int i = 0; i < W; ++i) sum[i] = fmaf(w, f[i], sum[i]);
+                    for (int i = 0; i < W; ++i) sum[k][i] = fmaf(b.weight[a], f[i], sum[k][i]);
+                }
             }
         }
-        Part<T, kVec> o;
-        o.set(sum);
-        o.store(static_cast<T*>(p.out) + at.token * p.ld_out + c);
+#pragma unroll
+        for (int k = 0; k < kColumns; ++k) {
+            const long long c = c0 + k * lanes * W;
+            if (c >= p.dim) break;
+            Part<T, kVec> o;
+            o.set(sum[k]);
+            o.store(out + c);
+        }
     }
 }
 
 // drows[place[t,j]] = weights[t,j] dout[t];  dweights[t,j] = dout[t] . rows[place[t,j]]
-template <class T, bool kVec>
+template <class T, bool kVec, int kColumns>
 __global__ void __launch_bounds__(kNT) expert_combine_grad_kernel(ExpertParams p, int lanes) {
     __shared__ float s_dot[kNT / 32][kAhead];
     const Where at = where(lanes);
@@ -284,33 +313,44 @@ __global__ void __launch_bounds__(kNT) expert_combine_grad_kernel(ExpertParams p
         for (int a = 0; a < kAhead; ++a) {
             row[a] = here && j0 + a < p.choices ? __ldg(p.place + entry + j0 + a) : -1;
             if (row[a] >= p.entries) row[a] = -1;
-            w[a] = row[a] >= 0 && row[a] < kept ? weight_of<T>(p, entry + j0 + a) : 0.0f;
             dot[a] = 0.0f;
         }
-        for (long long c = (long long)at.lane * W; here && c < p.dim; c += lanes * W) {
-            Part<T, kVec> g, v[kAhead];
-            g.load(dout + c);
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a)
-                if (rows && row[a] >= 0 && row[a] < kept) v[a].load(rows + row[a] * p.ld_rows + c);
-            float d[W];
-            g.get(d);
+        for (int a = 0; a < kAhead; ++a) w[a] = row[a] >= 0 && row[a] < kept ? weight_of<T>(p, entry + j0 + a) : 0.0f;
+        for (long long c0 = (long long)at.lane * W; here && c0 < p.dim; c0 += (long long)lanes * W * kColumns) {
+            Part<T, kVec> g[kColumns], v[kAhead][kColumns];
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                if (row[a] < 0) continue;
-                const bool live = row[a] < kept;
-                float f[W];
-                if (rows && live) {
-                    v[a].get(f);
+            for (int k = 0; k < kColumns; ++k) {
+                const long long c = c0 + k * lanes * W;
+                if (c >= p.dim) break;
+                g[k].load(dout + c);
 #pragma unroll
-                    for (int i = 0; i < W; ++i) dot[a] = fmaf(d[i], f[i], dot[a]);
+                for (int a = 0; a < kAhead; ++a)
+                    if (rows && row[a] >= 0 && row[a] < kept) v[a][k].load(rows + row[a] * p.ld_rows + c);
+            }
+#pragma unroll
+            for (int k = 0; k < kColumns; ++k) {
+                const long long c = c0 + k * lanes * W;
+                if (c >= p.dim) break;
+                float d[W];
+                g[k].get(d);
+#pragma unroll
+                for (int a = 0; a < kAhead; ++a) {
+                    if (row[a] < 0) continue;
+                    const bool live = row[a] < kept;
+                    float f[W];
+                    if (rows && live) {
+                        v[a][k].get(f);
+#pragma unroll
+                        for (int i = 0; i < W; ++i) dot[a] = fmaf(d[i], f[i], dot[a]);
+                    }
+                    Part<T, kVec> o;
+#pragma unroll
+                    for (int i = 0; i < W; ++i) f[i] = w[a] * d[i];
+                    o.set(f);
+                    if (!live) o.zero();
+                    o.store(drows + row[a] * p.ld_out + c);
                 }
-                Part<T, kVec> o;
-#pragma unroll
-                for (int i = 0; i < W; ++i) f[i] = w[a] * d[i];
-                o.set(f);
-                if (!live) o.zero();
-                o.store(drows + row[a] * p.ld_out + c);
             }
         }
         if (!p.dweights) continue;
@@ -342,12 +382,13 @@ __global__ void __launch_bounds__(kNT) expert_combine_grad_kernel(ExpertParams p
     }
 }
 
-// Threads a token: one or two vectors each, up to a whole CTA.
+// Threads a token: kColumns vectors each, up to a whole CTA.
+constexpr int kColumns = 2;
 template <class T, bool kVec>
 int lanes_of(long long dim) {
     const long long n = (dim + Part<T, kVec>::W - 1) / Part<T, kVec>::W;
     int lanes = 8;
-    while (lanes < kNT && lanes < n) lanes *= 2;
+    while (lanes < kNT && lanes * kColumns < n) lanes *= 2;
     return lanes;
 }
 enum { kGather, kCombine, kCombineGrad };
@@ -356,8 +397,8 @@ cudaError_t rows_as(int what, const ExpertParams& p, cudaStream_t s) {
     const int lanes = lanes_of<T, kVec>(p.dim);
     const unsigned grid = (unsigned)((p.tokens + kNT / lanes - 1) / (kNT / lanes));
     if (what == kGather) expert_gather_kernel<T, kVec><<<grid, kNT, 0, s>>>(p, lanes);
-    else if (what == kCombine) expert_combine_kernel<T, kVec><<<grid, kNT, 0, s>>>(p, lanes);
-    else expert_combine_grad_kernel<T, kVec><<<grid, kNT, 0, s>>>(p, lanes);
+    else if (what == kCombine) expert_combine_kernel<T, kVec, kColumns><<<grid, kNT, 0, s>>>(p, lanes);
+    else expert_combine_grad_kernel<T, kVec, kColumns><<<grid, kNT, 0, s>>>(p, lanes);
     count_launches(1);
     return cudaGetLastError();
 }

@@ -179,8 +179,9 @@ template <int kLanes> constexpr int kThreads = kLanes < 256 ? 256 : kLanes;
 // How rows come: element by element, by vectors, or by vectors through the ring.
 enum Way { kElements, kVectors, kRing };
 
-// A team: the threads of a row, or a warp with kSide rows side by side, and kDeep of
-// them one behind the other where they are short.
+// A team: the threads of a row, or a warp with kSide rows side by side, and two of them
+// one behind the other where they are short (four: 262144 rows of 128 16-bit channels 31 us
+// forward, 29 so, and the gradient spills).
 template <class T, Way kWay, int kLanes, int NV> struct Team {
     static constexpr int W = kWidth<T>, N = NV * W, NT = kThreads<kLanes>;
     static constexpr int kSize = kLanes > 32 ? kLanes : 32, kTeams = NT / kSize;
@@ -225,7 +226,7 @@ struct RowRing {
     }
     // The rows [r0, r0 + n) into the next stage; by the team's first warp, when the whole
     // team has read what was there.
-    __device__ __forceinline__ void load(long long r0, int n, int lane) {
+    __device__ __forceinline__ void load(uint32_t r0, int n, int lane) {
         const uint32_t full = bar + 8 * fill, to = smem_u32(base) + fill * bytes();
         if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(tensors * n) * row_bytes);
 #pragma unroll
@@ -233,9 +234,9 @@ struct RowRing {
             if (i >= tensors) break;
             const uint32_t dst = to + i * kRows * row_bytes;
             if (kRows == 1 || dense) {
-                if (lane == 0) bulk_load(dst, from[i] + at((uint32_t)r0, length, sb[i], st[i]), n * row_bytes, full);
+                if (lane == 0) bulk_load(dst, from[i] + at(r0, length, sb[i], st[i]), n * row_bytes, full);
             } else if (lane < n) {
-                bulk_load(dst + lane * row_bytes, from[i] + at((uint32_t)r0 + lane, length, sb[i], st[i]), row_bytes, full);
+                bulk_load(dst + lane * row_bytes, from[i] + at(r0 + lane, length, sb[i], st[i]), row_bytes, full);
             }
         }
         if (++fill == stages) fill = 0;
@@ -252,14 +253,15 @@ struct RowRing {
     }
 };
 
-// The rows of a team's turns.  `tensors` of p: 2 or 3.
-template <class T, Way kWay, int kLanes, int NV, int kTensors>
+// The rows of a team's turns, of 1 or 2 tensors forward, 2 or 3 backward.
+template <class T, Way kWay, int kLanes, int NV, bool kGrad>
 struct Turns {
+    static constexpr int kTensors = kGrad ? 3 : 2;
     using G = Team<T, kWay, kLanes, NV>;
     using R = Row<T, kWay != kElements, kLanes, NV>;
     RowRing<T, kTensors, G::kRows> ring;
     R next[kWay == kRing ? 1 : kTensors][kWay == kRing ? 1 : G::kDeep];
-    long long rows, step, ahead;
+    uint32_t rows, step, ahead;  // below 2^31; a turn behind the last stays below 2^32
     int thread, lane, side, channels;  // thread: of the team
 
     __device__ __forceinline__ void begin(const NormParams& p, unsigned char* mem, const void* const (&from)[kTensors],
@@ -271,7 +273,7 @@ struct Turns {
         channels = (int)p.channels;
         rows = p.rows;
         ahead = first();
-        step = (long long)gridDim.x * G::kTeams * G::kRows;
+        step = gridDim.x * (uint32_t)(G::kTeams * G::kRows);
         ring.tensors = tensors;
         ring.length = p.length;
         ring.dense = p.dense;
@@ -291,25 +293,25 @@ struct Turns {
             fetch();
         }
     }
-    __device__ __forceinline__ long long first() const {
-        return ((long long)blockIdx.x * G::kTeams + threadIdx.x / G::kSize) * G::kRows;
+    __device__ __forceinline__ uint32_t first() const {
+        return (blockIdx.x * G::kTeams + threadIdx.x / G::kSize) * (uint32_t)G::kRows;
     }
     // This thread's row d of the turn that begins with `base`.
-    __device__ __forceinline__ long long row(long long base, int d) const { return base + d * G::kSide + side; }
+    __device__ __forceinline__ uint32_t row(uint32_t base, int d) const { return base + d * G::kSide + side; }
     // The turn after those under way.
     __device__ __forceinline__ void fetch() {
         if (ahead >= rows) return;
         if constexpr (kWay == kRing) {
-            if (thread < 32) ring.load(ahead, (int)min((long long)G::kRows, rows - ahead), thread);
+            if (thread < 32) ring.load(ahead, (int)min((uint32_t)G::kRows, rows - ahead), thread);
         } else {
 #pragma unroll
             for (int i = 0; i < kTensors; ++i) {
                 if (i >= ring.tensors) break;
 #pragma unroll
                 for (int d = 0; d < G::kDeep; ++d) {
-                    const long long r = row(ahead, d);
+                    const uint32_t r = row(ahead, d);
                     const bool live = r < rows;
-                    next[i][d].load(ring.from[i] + at(live ? (uint32_t)r : 0u, ring.length, ring.sb[i], ring.st[i]), lane,
+                    next[i][d].load(ring.from[i] + at(live ? r : 0u, ring.length, ring.sb[i], ring.st[i]), lane,
                                     live ? channels : 0);
                 }
             }
@@ -321,7 +323,7 @@ struct Turns {
         if constexpr (kWay == kRing) return ring.wait();
         else return true;
     }
-    __device__ __forceinline__ void take(int i, long long base, R (&to)[G::kDeep]) const {
+    __device__ __forceinline__ void take(int i, uint32_t base, R (&to)[G::kDeep]) const {
 #pragma unroll
         for (int d = 0; d < G::kDeep; ++d) {
             if constexpr (kWay == kRing) to[d].load_shared(ring.row(i, d * G::kSide + side), lane, row(base, d) < rows ? channels : 0);
@@ -353,7 +355,7 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kResident<kWay, kLanes>) nor
     __shared__ __align__(16) float s_sum[G::kGroups][2][2][kLanes > 32 ? kLanes / 32 : 1];
     extern __shared__ __align__(128) unsigned char s_mem[];
     const int group = threadIdx.x / kLanes, channels = (int)p.channels;
-    Turns<T, kWay, kLanes, NV, 2> turns;
+    Turns<T, kWay, kLanes, NV, false> turns;
     {
         const void* const from[2] = {p.x, p.residual};
         const long long sb[2] = {p.x_batch, p.residual_batch}, st[2] = {p.x_token, p.residual_token};
@@ -378,7 +380,7 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kResident<kWay, kLanes>) nor
     const float per = 1.0f / (float)channels;
     const bool full = channels == kLanes * N;
     int turn = 0;
-    for (long long base = turns.first(); base < turns.rows; base += turns.step) {
+    for (uint32_t base = turns.first(); base < turns.rows; base += turns.step) {
         const bool ok = turns.wait();
         R x[D];
         turns.take(0, base, x);
@@ -397,9 +399,9 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kResident<kWay, kLanes>) nor
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
                     for (int j = 0; j < W / 2; ++j) f[d][i * W / 2 + j] = add2(f[d][i * W / 2 + j], x[d].pair(i, j));
-                const long long r = turns.row(base, d);
+                const uint32_t r = turns.row(base, d);
                 const bool live = r < turns.rows;
-                R::template store<true>(static_cast<T*>(p.sum) + at(live ? (uint32_t)r : 0u, p.length, p.sum_batch, p.sum_token),
+                R::template store<true>(static_cast<T*>(p.sum) + at(live ? r : 0u, p.length, p.sum_batch, p.sum_token),
                                         lane, live ? channels : 0, f[d]);
             }
         }
@@ -448,13 +450,13 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kResident<kWay, kLanes>) nor
         turns.done();
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-            const long long r = turns.row(base, d);
+            const uint32_t r = turns.row(base, d);
             const bool live = r < turns.rows;
             const float rstd = ok ? inverse_root(fmaf(q[d], per, p.eps)) : not_a_number();
             if (p.saved && lane == 0 && live) reinterpret_cast<float2*>(p.saved)[r] = make_float2(mean[d], rstd);
 #pragma unroll
             for (int i = 0; i < N / 2; ++i) f[d][i] = fma2(mul2(f[d][i], both(rstd)), w[i], b[i]);
-            R::store(static_cast<T*>(p.y) + at(live ? (uint32_t)r : 0u, p.length, p.y_batch, p.y_token), lane, live ? channels : 0,
+            R::store(static_cast<T*>(p.y) + at(live ? r : 0u, p.length, p.y_batch, p.y_token), lane, live ? channels : 0,
                      f[d]);
         }
     }
@@ -473,7 +475,7 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<kLanes>) norm_
     __shared__ __align__(16) float s_sum[kGroups][2][2 * D * (kLanes > 32 ? kLanes / 32 : 1)];
     extern __shared__ __align__(128) unsigned char s_mem[];
     const int group = threadIdx.x / kLanes, channels = (int)p.channels;
-    Turns<T, kWay, kLanes, NV, 3> turns;
+    Turns<T, kWay, kLanes, NV, true> turns;
     {
         const void* const from[3] = {p.x, p.dy, p.dsum};
         const long long sb[3] = {p.x_batch, p.dy_batch, p.dsum_batch}, st[3] = {p.x_token, p.dy_token, p.dsum_token};
@@ -496,16 +498,16 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<kLanes>) norm_
         }
     const float per = 1.0f / (float)channels;
     float2 stat[D];
-    auto fetch_stat = [&](long long base) {
+    auto fetch_stat = [&](uint32_t base) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-            const long long r = turns.row(base, d);
+            const uint32_t r = turns.row(base, d);
             stat[d] = r < turns.rows ? __ldg(reinterpret_cast<const float2*>(p.saved) + r) : make_float2(0.0f, 0.0f);
         }
     };
     int turn = 0;
     fetch_stat(turns.first());
-    for (long long base = turns.first(); base < turns.rows; base += turns.step) {
+    for (uint32_t base = turns.first(); base < turns.rows; base += turns.step) {
         const bool ok = turns.wait();
         R x[D], dy[D], ds[D];
         turns.take(0, base, x);
@@ -560,9 +562,9 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<kLanes>) norm_
 #pragma unroll
                 for (int k = 0; k < N / 2; ++k) o[k] = mul2(o[k], both(rstd[d]));
             }
-            const long long r = turns.row(base, d);
+            const uint32_t r = turns.row(base, d);
             const bool live = r < turns.rows;
-            R::store(static_cast<T*>(p.dx) + (live ? r : 0) * channels, lane, live ? channels : 0, o);
+            R::store(static_cast<T*>(p.dx) + (long long)(live ? r : 0u) * channels, lane, live ? channels : 0, o);
         }
     }
     if (!p.partials) return;
@@ -757,26 +759,31 @@ __global__ void __launch_bounds__(kColumnNT) norm_columns_kernel(NormParams p) {
 // Shared memory of an SM that its rings share, and of a CTA's ring at most.
 constexpr int kRingBytes = 200 * 1024;
 
-template <class T, Way kWay, int kLanes, int NV>
-cudaError_t go(NormParams& p, bool grad, cudaStream_t s) {
+template <class T, Way kWay, int kLanes, int NV, bool kGrad>
+cudaError_t launch_as(NormParams& p, cudaStream_t s) {
     using G = Team<T, kWay, kLanes, NV>;
     const long long turns = (p.rows + (long long)G::kTeams * G::kRows - 1) / (G::kTeams * G::kRows);
-    const int resident = grad ? kGradResident<kLanes> : kResident<kWay, kLanes>;
-    const int tensors = grad ? (p.dsum ? 3 : 2) : p.residual ? 2 : 1;
-    int bytes = grad && G::kGroups > 1 ? (int)sizeof(float) * G::NT * G::N : 0;  // the columns' sums
+    const int resident = kGrad ? kGradResident<kLanes> : kResident<kWay, kLanes>;
+    const int tensors = kGrad ? (p.dsum ? 3 : 2) : p.residual ? 2 : 1;
+    int bytes = kGrad && G::kGroups > 1 ? (int)sizeof(float) * G::NT * G::N : 0;  // the columns' sums
     if (kWay == kRing) {
         const int stage = G::kTeams * tensors * G::kRows * (int)(p.channels * sizeof(T));
         p.stages = std::clamp(kRingBytes / resident / stage, 2, 8);
         bytes = std::max(bytes, p.stages * (stage + G::kTeams * 8));
     }
     p.parts = std::min(turns, seq_sms() * resident);
-    const void* kernel = grad ? (const void*)norm_grad_kernel<T, kWay, kLanes, NV> : (const void*)norm_kernel<T, kWay, kLanes, NV>;
+    const void* kernel;
+    if constexpr (kGrad) kernel = (const void*)norm_grad_kernel<T, kWay, kLanes, NV>;
+    else kernel = (const void*)norm_kernel<T, kWay, kLanes, NV>;
     // the limit is one per device: always the largest, whatever this call needs
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes + 8192);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes + 8192);
     if (e != cudaSuccess) return e;
     void* args[] = {&p};
-    e = cudaLaunchKernel(kernel, dim3((unsigned)p.parts), dim3(G::NT), args, (size_t)bytes, s);
-    return e;
+    return cudaLaunchKernel(kernel, dim3((unsigned)p.parts), dim3(G::NT), args, (size_t)bytes, s);
+}
+template <class T, Way kWay, int kLanes, int NV>
+cudaError_t go(NormParams& p, bool grad, cudaStream_t s) {
+    return grad ? launch_as<T, kWay, kLanes, NV, true>(p, s) : launch_as<T, kWay, kLanes, NV, false>(p, s);
 }
 
 // Through the ring where CTAs have several turns to take.
