@@ -20,6 +20,7 @@
 
 #include <cooperative_groups.h>
 
+#include "sc_bulk.cuh"
 #include "sc_seq.cuh"
 #include "sc_seq_launch.h"
 
@@ -228,75 +229,46 @@ __global__ void __launch_bounds__(kNT) expert_gather_kernel(ExpertParams p, int 
     }
 }
 
-// A batch of kAhead choices of a token: their rows (-1: none) and weights.
-struct Batch {
-    long long row[kAhead];
-    float weight[kAhead];
-};
-template <class T>
-__device__ __forceinline__ Batch batch_of(const ExpertParams& p, long long entry, long long left, long long kept) {
-    Batch b;
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-        const long long row = a < left ? __ldg(p.place + entry + a) : -1;
-        b.row[a] = row >= 0 && row < kept ? row : -1;
-    }
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) b.weight[a] = b.row[a] >= 0 ? weight_of<T>(p, entry + a) : 0.0f;
-    return b;
-}
-
-// out[t] = sum over j of weights[t,j] rows[place[t,j]].  A lane has kColumns vectors of
-// the token, kAhead rows of each: up to kAhead kColumns loads under way.
-template <class T, bool kVec, int kColumns>
+// out[t] = sum over j of weights[t,j] rows[place[t,j]]
+template <class T, bool kVec>
 __global__ void __launch_bounds__(kNT) expert_combine_kernel(ExpertParams p, int lanes) {
     const Where at = where(lanes);
     if (at.token >= p.tokens) return;
     const long long kept = kept_of(p);
     const long long entry = at.token * p.choices;
     const T* rows = static_cast<const T*>(p.in);
-    T* out = static_cast<T*>(p.out) + at.token * p.ld_out;
     constexpr int W = Part<T, kVec>::W;
-    const Batch first = batch_of<T>(p, entry, p.choices, kept);
-    for (long long c0 = (long long)at.lane * W; c0 < p.dim; c0 += (long long)lanes * W * kColumns) {
-        float sum[kColumns][W];
+    for (long long c = (long long)at.lane * W; c < p.dim; c += lanes * W) {
+        float sum[W];
 #pragma unroll
-        for (int k = 0; k < kColumns; ++k)
-#pragma unroll
-            for (int i = 0; i < W; ++i) sum[k][i] = 0.0f;
+        for (int i = 0; i < W; ++i) sum[i] = 0.0f;
         for (long long j0 = 0; j0 < p.choices; j0 += kAhead) {
-            const Batch b = j0 == 0 ? first : batch_of<T>(p, entry + j0, p.choices - j0, kept);
-            Part<T, kVec> v[kAhead][kColumns];
-#pragma unroll
-            for (int a = 0; a < kAhead; ++a)
-#pragma unroll
-                for (int k = 0; k < kColumns; ++k)
-                    if (b.row[a] >= 0 && c0 + k * lanes * W < p.dim) v[a][k].load(rows + b.row[a] * p.ld_in + c0 + k * lanes * W);
+            Part<T, kVec> v[kAhead];
+            bool live[kAhead];
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
-                if (b.row[a] < 0) continue;
+                const long long row = j0 + a < p.choices ? __ldg(p.place + entry + j0 + a) : -1;
+                live[a] = row >= 0 && row < kept;
+                if (live[a]) v[a].load(rows + row * p.ld_in + c);
+            }
 #pragma unroll
-                for (int k = 0; k < kColumns; ++k) {
-                    float f[W];
-                    v[a][k].get(f);
+            for (int a = 0; a < kAhead; ++a) {
+                if (!live[a]) continue;
+                const float w = weight_of<T>(p, entry + j0 + a);
+                float f[W];
+                v[a].get(f);
 #pragma unroll
-                    for (int i = 0; i < W; ++i) sum[k][i] = fmaf(b.weight[a], f[i], sum[k][i]);
-                }
+                for (int i = 0; i < W; ++i) sum[i] = fmaf(w, f[i], sum[i]);
             }
         }
-#pragma unroll
-        for (int k = 0; k < kColumns; ++k) {
-            const long long c = c0 + k * lanes * W;
-            if (c >= p.dim) break;
-            Part<T, kVec> o;
-            o.set(sum[k]);
-            o.store(out + c);
-        }
+        Part<T, kVec> o;
+        o.set(sum);
+        o.store(static_cast<T*>(p.out) + at.token * p.ld_out + c);
     }
 }
 
 // drows[place[t,j]] = weights[t,j] dout[t];  dweights[t,j] = dout[t] . rows[place[t,j]]
-template <class T, bool kVec, int kColumns>
+template <class T, bool kVec>
 __global__ void __launch_bounds__(kNT) expert_combine_grad_kernel(ExpertParams p, int lanes) {
     __shared__ float s_dot[kNT / 32][kAhead];
     const Where at = where(lanes);
@@ -313,44 +285,33 @@ __global__ void __launch_bounds__(kNT) expert_combine_grad_kernel(ExpertParams p
         for (int a = 0; a < kAhead; ++a) {
             row[a] = here && j0 + a < p.choices ? __ldg(p.place + entry + j0 + a) : -1;
             if (row[a] >= p.entries) row[a] = -1;
+            w[a] = row[a] >= 0 && row[a] < kept ? weight_of<T>(p, entry + j0 + a) : 0.0f;
             dot[a] = 0.0f;
         }
+        for (long long c = (long long)at.lane * W; here && c < p.dim; c += lanes * W) {
+            Part<T, kVec> g, v[kAhead];
+            g.load(dout + c);
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) w[a] = row[a] >= 0 && row[a] < kept ? weight_of<T>(p, entry + j0 + a) : 0.0f;
-        for (long long c0 = (long long)at.lane * W; here && c0 < p.dim; c0 += (long long)lanes * W * kColumns) {
-            Part<T, kVec> g[kColumns], v[kAhead][kColumns];
+            for (int a = 0; a < kAhead; ++a)
+                if (rows && row[a] >= 0 && row[a] < kept) v[a].load(rows + row[a] * p.ld_rows + c);
+            float d[W];
+            g.get(d);
 #pragma unroll
-            for (int k = 0; k < kColumns; ++k) {
-                const long long c = c0 + k * lanes * W;
-                if (c >= p.dim) break;
-                g[k].load(dout + c);
+            for (int a = 0; a < kAhead; ++a) {
+                if (row[a] < 0) continue;
+                const bool live = row[a] < kept;
+                float f[W];
+                if (rows && live) {
+                    v[a].get(f);
 #pragma unroll
-                for (int a = 0; a < kAhead; ++a)
-                    if (rows && row[a] >= 0 && row[a] < kept) v[a][k].load(rows + row[a] * p.ld_rows + c);
-            }
-#pragma unroll
-            for (int k = 0; k < kColumns; ++k) {
-                const long long c = c0 + k * lanes * W;
-                if (c >= p.dim) break;
-                float d[W];
-                g[k].get(d);
-#pragma unroll
-                for (int a = 0; a < kAhead; ++a) {
-                    if (row[a] < 0) continue;
-                    const bool live = row[a] < kept;
-                    float f[W];
-                    if (rows && live) {
-                        v[a][k].get(f);
-#pragma unroll
-                        for (int i = 0; i < W; ++i) dot[a] = fmaf(d[i], f[i], dot[a]);
-                    }
-                    Part<T, kVec> o;
-#pragma unroll
-                    for (int i = 0; i < W; ++i) f[i] = w[a] * d[i];
-                    o.set(f);
-                    if (!live) o.zero();
-                    o.store(drows + row[a] * p.ld_out + c);
+                    for (int i = 0; i < W; ++i) dot[a] = fmaf(d[i], f[i], dot[a]);
                 }
+                Part<T, kVec> o;
+#pragma unroll
+                for (int i = 0; i < W; ++i) f[i] = w[a] * d[i];
+                o.set(f);
+                if (!live) o.zero();
+                o.store(drows + row[a] * p.ld_out + c);
             }
         }
         if (!p.dweights) continue;
@@ -382,23 +343,220 @@ __global__ void __launch_bounds__(kNT) expert_combine_grad_kernel(ExpertParams p
     }
 }
 
-// Threads a token: kColumns vectors each, up to a whole CTA.
-constexpr int kColumns = 2;
+// ------------------------------------------------- rows through a ring
+// The two kernels that read a token's entries' rows from wherever they lie, for aligned
+// rows: CTAs stay and teams of 32 to 256 threads take tokens in turns; the rows of the
+// next ones are under way, one bulk copy each, into a ring of stages in shared memory.
+// A stage: (the gradient: the token's row of dout,) the rows of its entries that have an
+// expert, and for each entry its row's number and its weight.
+struct Entry {
+    int row;  // of the sorted order; -1: passed over
+    float weight;
+};
+constexpr int kMaxChoices = 32;  // a lane of the filling warp each
+
+struct TeamRing {
+    unsigned char* stage0;
+    uint32_t bar, row_bytes, stage_bytes, phase = 0;
+    int stages, fill = 0, take = 0;
+    long long kept;
+    // of the token to fill next, loaded a turn ahead: this lane's entry
+    int row = -1;
+    float weight = 0.0f;
+
+    template <class T>
+    __device__ __forceinline__ void peek(const ExpertParams& p, long long token, int lane) {
+        row = -1;
+        weight = 0.0f;
+        if (token >= p.tokens || lane >= p.choices) return;
+        const long long r = __ldg(p.place + token * p.choices + lane);
+        row = r >= 0 && r < p.entries ? (int)r : -1;
+        weight = weight_of<T>(p, token * p.choices + lane);
+    }
+    __device__ __forceinline__ Entry* entries(int stage) const {
+        return reinterpret_cast<Entry*>(stage0 + (size_t)stage * stage_bytes);
+    }
+    __device__ __forceinline__ unsigned char* rows(int stage) const {
+        return stage0 + (size_t)stage * stage_bytes + sizeof(Entry) * kMaxChoices;
+    }
+    // The token's rows into the next stage, by the team's first warp.
+    template <class T, bool kGrad>
+    __device__ __forceinline__ void load(const ExpertParams& p, long long token, int lane) {
+        const uint32_t full = bar + 8 * fill;
+        const bool live = row >= 0 && row < kept && (!kGrad || p.rows);
+        if (lane < p.choices) entries(fill)[lane] = {row, weight};
+        const int copies = __popc(__ballot_sync(0xffffffffu, live)) + (kGrad ? 1 : 0);  // after the entries are written
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(full, copies * row_bytes);
+        const uint32_t to = smem_u32(rows(fill));
+        const T* from = static_cast<const T*>(kGrad ? p.rows : p.in);
+        if (live) bulk_load(to + (lane + (kGrad ? 1 : 0)) * row_bytes, from + row * (kGrad ? p.ld_rows : p.ld_in), row_bytes, full);
+        if (kGrad && lane == 0) bulk_load(to, static_cast<const T*>(p.in) + token * p.ld_in, row_bytes, full);
+        if (++fill == stages) fill = 0;
+    }
+    __device__ __forceinline__ bool wait() const { return arrived(bar + 8 * take, phase); }
+    __device__ __forceinline__ void taken() {
+        if (++take == stages) {
+            take = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+__device__ __forceinline__ void team_sync(int team, int size) {
+    if (size == 32) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(size) : "memory");
+}
+
+template <class T, bool kGrad>
+__global__ void __launch_bounds__(kNT) expert_ring_kernel(ExpertParams p, int size, int stages, uint32_t stage_bytes) {
+    extern __shared__ __align__(128) unsigned char s_mem[];
+    __shared__ float s_dot[kNT / 32][kMaxChoices];
+    constexpr int W = 16 / (int)sizeof(T);
+    using P = Part<T, true>;
+    const int teams = kNT / size, team = threadIdx.x / size, thread = threadIdx.x - team * size, lane = threadIdx.x % 32;
+    const int choices = (int)p.choices;
+    const long long step = (long long)gridDim.x * teams;
+    long long token = (long long)blockIdx.x * teams + team, ahead = token;
+    TeamRing ring;
+    ring.stage0 = s_mem + (size_t)team * stages * stage_bytes;
+    ring.bar = smem_u32(s_mem + (size_t)teams * stages * stage_bytes + team * stages * 8);
+    ring.row_bytes = (uint32_t)(p.dim * sizeof(T));
+    ring.stage_bytes = stage_bytes;
+    ring.stages = stages;
+    ring.kept = kept_of(p);
+    if (thread == 0) {
+        for (int i = 0; i < stages; ++i) mbar_init(ring.bar + 8 * i, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    auto fetch = [&] {  // the first warp of the team
+        if (ahead < p.tokens) ring.load<T, kGrad>(p, ahead, lane);
+        ahead += step;
+        ring.peek<T>(p, ahead, lane);
+    };
+    if (thread < 32) {
+        ring.peek<T>(p, ahead, lane);
+        for (int i = 0; i < stages; ++i) fetch();
+    }
+    for (; token < p.tokens; token += step) {
+        const bool ok = ring.wait();
+        const Entry* entry = ring.entries(ring.take);
+        const T* rows = reinterpret_cast<const T*>(ring.rows(ring.take));
+        if constexpr (!kGrad) {
+            for (long long c = (long long)thread * W; c < p.dim; c += size * W) {
+                float sum[W];
+#pragma unroll
+                for (int i = 0; i < W; ++i) sum[i] = ok ? 0.0f : not_a_number();
+#pragma unroll 4
+                for (int j = 0; j < choices; ++j) {
+                    const Entry e = entry[j];
+                    if (e.row < 0 || e.row >= ring.kept) continue;
+                    Vec<T, W> v;
+                    v.load_rw(rows + j * p.dim + c);
+#pragma unroll
+                    for (int i = 0; i < W; ++i) sum[i] = fmaf(e.weight, v.get(i), sum[i]);
+                }
+                P o;
+                o.set(sum);
+                o.store(static_cast<T*>(p.out) + token * p.ld_out + c);
+            }
+        } else {
+            for (int j = 0; j < choices; ++j) {
+                const Entry e = entry[j];
+                const bool live = e.row >= 0 && e.row < ring.kept;
+                float dot = 0.0f;
+                if (e.row >= 0) {
+                    T* to = static_cast<T*>(p.out) + e.row * p.ld_out;
+#pragma unroll 2
+                    for (long long c = (long long)thread * W; c < p.dim; c += size * W) {
+                        Vec<T, W> g, v;
+                        P o;
+                        o.zero();
+                        if (live) {
+                            g.load_rw(rows + c);
+                            if (p.rows) {
+                                v.load_rw(rows + (j + 1) * p.dim + c);
+#pragma unroll
+                                for (int i = 0; i < W; ++i) dot = fmaf(g.get(i), v.get(i), dot);
+                            }
+                            float f[W];
+                            const float w = ok ? e.weight : not_a_number();
+#pragma unroll
+                            for (int i = 0; i < W; ++i) f[i] = w * g.get(i);
+                            o.set(f);
+                        }
+                        o.store(to + c);
+                    }
+                }
+                if (p.dweights) {
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                    if (lane == 0) s_dot[threadIdx.x / 32][j] = ok ? dot : not_a_number();
+                }
+            }
+        }
+        team_sync(team, size);  // the stage is read, and the parts of the products are there
+        if (kGrad && p.dweights && thread < choices) {
+            float v = 0.0f;
+            for (int w = 0; w < size / 32; ++w) v += s_dot[team * (size / 32) + w][thread];
+            const long long at = token * p.choices + thread;
+            if (p.weights_f32) static_cast<float*>(p.dweights)[at] = v;
+            else static_cast<T*>(p.dweights)[at] = from_f32<T>(v);
+        }
+        ring.taken();
+        if (thread < 32) fetch();
+        if (kGrad && p.dweights) team_sync(team, size);  // the parts are read
+    }
+}
+
+// Threads a token: one or two vectors each, up to a whole CTA.
 template <class T, bool kVec>
 int lanes_of(long long dim) {
     const long long n = (dim + Part<T, kVec>::W - 1) / Part<T, kVec>::W;
     int lanes = 8;
-    while (lanes < kNT && lanes * kColumns < n) lanes *= 2;
+    while (lanes < kNT && lanes < n) lanes *= 2;
     return lanes;
 }
 enum { kGather, kCombine, kCombineGrad };
+// Through a ring where two stages fit a team's share of the shared memory and CTAs have
+// several turns.
+template <class T, bool kGrad>
+bool ring_as(const ExpertParams& p, cudaStream_t s, cudaError_t* e) {
+    constexpr int kShared = 200 * 1024;
+    const long long vectors = p.dim * (long long)sizeof(T) / 16, row = p.dim * (long long)sizeof(T);
+    if (p.choices < 1 || p.choices > kMaxChoices || row > kShared) return false;
+    int size = 32;
+    while (size < kNT && size < vectors) size *= 2;
+    const int teams = kNT / size;
+    const long long stage = (sizeof(Entry) * kMaxChoices + (p.choices + (kGrad ? 1 : 0)) * row + 127) / 128 * 128;
+    int resident = 4;
+    while (resident > 1 && stage * teams * 2 > kShared / resident) --resident;
+    const int stages = (int)std::min<long long>(kShared / resident / (stage * teams), 8);
+    if (stages < 2 || p.tokens <= seq_sms() * resident * teams) return false;
+    const int bytes = stages * teams * ((int)stage + 8);
+    auto kernel = expert_ring_kernel<T, kGrad>;
+    // the limit is one per device: always the largest, whatever this call needs
+    *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared + 1024);
+    if (*e != cudaSuccess) return true;
+    const unsigned grid = (unsigned)std::min<long long>((p.tokens + teams - 1) / teams, seq_sms() * resident);
+    kernel<<<grid, kNT, bytes, s>>>(p, size, stages, (uint32_t)stage);
+    count_launches(1);
+    *e = cudaGetLastError();
+    return true;
+}
+
 template <class T, bool kVec>
 cudaError_t rows_as(int what, const ExpertParams& p, cudaStream_t s) {
+    if constexpr (kVec) {
+        cudaError_t e;
+        if ((what == kCombine && ring_as<T, false>(p, s, &e)) || (what == kCombineGrad && ring_as<T, true>(p, s, &e))) return e;
+    }
     const int lanes = lanes_of<T, kVec>(p.dim);
     const unsigned grid = (unsigned)((p.tokens + kNT / lanes - 1) / (kNT / lanes));
     if (what == kGather) expert_gather_kernel<T, kVec><<<grid, kNT, 0, s>>>(p, lanes);
-    else if (what == kCombine) expert_combine_kernel<T, kVec, kColumns><<<grid, kNT, 0, s>>>(p, lanes);
-    else expert_combine_grad_kernel<T, kVec, kColumns><<<grid, kNT, 0, s>>>(p, lanes);
+    else if (what == kCombine) expert_combine_kernel<T, kVec><<<grid, kNT, 0, s>>>(p, lanes);
+    else expert_combine_grad_kernel<T, kVec><<<grid, kNT, 0, s>>>(p, lanes);
     count_launches(1);
     return cudaGetLastError();
 }

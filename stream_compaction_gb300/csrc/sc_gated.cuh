@@ -30,10 +30,10 @@
 
 #include <cooperative_groups.h>
 
+#include "sc_bulk.cuh"
 #include "sc_seq.cuh"
 #include "sc_seq_launch.h"
 #include "sc_tensor_map.h"
-#include "sc_tma.cuh"
 
 namespace scg {
 
@@ -59,14 +59,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int c, int 
                  ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(t), "r"(b), "r"(src)
                  : "memory");
 }
-// The end of a tile's copies, for the whole warp.  They end by themselves; a wait that
-// should run out all the same (a second or so) gives up, and the tile counts as NaN.
-__device__ __forceinline__ bool arrived(uint32_t bar, uint32_t parity) {
-    for (int i = 0; i < (1 << 20); ++i)
-        if (mbar_try_wait_sleep(bar, parity, 1000)) return true;
-    return false;
-}
-
 // A lane's K channels of a token: as they lie in memory, and as one operand.
 template <class T, int K> struct Raw { using type = unsigned short; };
 template <> struct Raw<float, 1> { using type = float; };
@@ -324,7 +316,7 @@ __device__ __forceinline__ typename Lane<K>::V exchange(Exchange<K, kWarps>& x, 
         send(at_rank(to, r), at_rank(bar, r), all);
         if (kCuts && lane == 0) send(at_rank(smem_u32(&x.rank_cut[turn][rank]), r), at_rank(bar, r), (int)all_cut);
     }
-    if (!arrived_from_cluster(bar, (uint32_t)(round >> 1) & 1u)) carry = Lane<K>::all(__int_as_float(0x7fffffff));
+    if (!arrived_from_cluster(bar, (uint32_t)(round >> 1) & 1u)) carry = Lane<K>::all(not_a_number());
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r) {
         if (r >= ranks) break;
@@ -486,7 +478,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
                     set_token<K>(b, j, L::all(0.0f));
                 }
         }
-        if (!ok) set_token<K>(b, 0, L::all(__int_as_float(0x7fffffff)));
+        if (!ok) set_token<K>(b, 0, L::all(not_a_number()));
         __syncwarp();  // every lane has read
         fetch();
         Map<K> map{token<K>(f, 0), token<K>(b, 0)};
@@ -620,7 +612,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
             for (int j = 0; j < kTokens; ++j)
                 if (j >= valid) set_token<K>(w, j, kSigmoid ? none : one);
         }
-        if (!ok) set_token<K>(w, 0, L::all(__int_as_float(0x7fffffff)));
+        if (!ok) set_token<K>(w, 0, L::all(not_a_number()));
         if (!kTma) fetch();
         // f from 1 - f: it enters with its absolute error
         auto decay_of = [&](int j) { return kSigmoid ? L::fma(token<K>(w, j), minus, one) : token<K>(w, j); };

@@ -25,9 +25,9 @@
 #pragma once
 #include <algorithm>
 
+#include "sc_bulk.cuh"
 #include "sc_seq.cuh"
 #include "sc_seq_launch.h"
-#include "sc_tma.cuh"
 
 namespace scg {
 
@@ -190,18 +190,6 @@ template <class T, Way kWay, int kLanes, int NV> struct Team {
     static constexpr int kGroups = NT / kLanes;
 };
 
-// A wait for bulk copies: they end by themselves; one that should run out all the same
-// (a second or so) gives up, and the rows count as NaN.
-__device__ __forceinline__ bool arrived(uint32_t bar, uint32_t parity) {
-    for (int i = 0; i < (1 << 20); ++i)
-        if (mbar_try_wait_sleep(bar, parity, 1000)) return true;
-    return false;
-}
-__device__ __forceinline__ void bulk_load(uint32_t to, const void* from, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(to), "l"(from), "r"(bytes), "r"(bar) : "memory");
-}
-
 // A team's ring: stages of kTensors x kRows rows.
 template <class T, int kTensors, int kRows>
 struct RowRing {
@@ -340,7 +328,6 @@ struct Turns {
         }
     }
 };
-__device__ __forceinline__ float not_a_number() { return __int_as_float(0x7fffffff); }
 
 // ---------------------------------------------------------------- forward
 // CTAs that an SM holds: 65536 registers by 80 a thread, 128 with rows in registers.

@@ -95,6 +95,31 @@ def test_rows_there_and_back(tokens, choices, experts, dim, dropped, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,choices,experts,dim", [
+    (9001, 2, 40, 64), (12001, 1, 5, 8), (3001, 8, 16, 200), (2501, 3, 9, 1000), (1501, 32, 40, 72), (1301, 2, 4, 4096)])
+def test_more_tokens_than_the_machine_holds(tokens, choices, experts, dim, dtype):
+    """Several tokens for every team of threads, their rows through the ring; the same bits again."""
+    ids = _ids(tokens, choices, experts, 0.1)
+    order = sc.expert_sort(ids.cuda(), experts)
+    place, kept = order.place.flatten().tolist(), int(order.offsets[-1])
+    y, dout = _normal(tokens * choices, dim, dtype=dtype), _normal(tokens, dim, seed=2, dtype=dtype)
+    y[kept:] = float("nan")
+    w = torch.rand(tokens, choices)
+    r = ref.expert_combine(y, place, kept, tokens, choices, w, dout)
+    plain = ref.expert_combine(y, place, kept, tokens, choices, None, dout)
+    y, dout, w = y.cuda(), dout.cuda(), w.cuda()
+    out, dx = sc.expert_combine(y, order, w), sc.expert_gather_grad(y, order)
+    ref.check("out", out, r["out"])
+    ref.check("dx", dx, plain["out"])
+    g, g1 = sc.expert_combine_grad(dout, y, order, w), sc.expert_combine_grad(dout, y, order)
+    ref.check("dy", g["y"], r["dy"])
+    ref.check("dweights", g["weights"], r["dweights"])
+    ref.check("dy, no weights", g1["y"], plain["dy"])
+    again = sc.expert_combine_grad(dout, y, order, w)
+    assert torch.equal(sc.expert_combine(y, order, w), out) and all(torch.equal(g[k], again[k]) for k in g)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("offset,dim", [(0, 64), (1, 64), (8, 72), (3, 37)])
 def test_slices(offset, dim, dtype):
     """Columns of wider rows, aligned or not; what lies beside them stays."""
