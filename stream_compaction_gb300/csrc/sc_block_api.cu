@@ -145,8 +145,9 @@ Tensor expert_rows(const sc_expert_desc* d, const void* p, int64_t rows, int64_t
     return {p, 1, rows, d->dim, 0, ld, bytes_of(d->dtype)};
 }
 Tensor expert_weights(const sc_expert_desc* d, const void* p) { return flat(p, d->tokens * d->choices, bytes_of(d->wtype)); }
-bool expert_vec(const sc_expert_desc* d, std::initializer_list<Tensor> rows) {
-    const int e = 16 / bytes_of(d->dtype);
+// Whether rows begin and end at multiples of `bytes`.
+bool expert_rows_at(const sc_expert_desc* d, int bytes, std::initializer_list<Tensor> rows) {
+    const int e = bytes / bytes_of(d->dtype);
     if (d->dim % e != 0) return false;
     for (const Tensor& t : rows)
         if (t.p && !t.vec(e)) return false;
@@ -165,7 +166,8 @@ sc_status expert_move(const sc_expert_desc* d, ExpertParams* p, const Tensor& in
     p->ld_in = in.st;
     p->out = const_cast<void*>(out.p);
     p->ld_out = out.st;
-    p->vec = expert_vec(d, {in, out});
+    p->vec = expert_rows_at(d, 16, {in, out});
+    p->pairs = expert_rows_at(d, 4, {in, out});
     return status_of(launch());
 }
 
@@ -403,7 +405,8 @@ sc_status sc_expert_combine_grad(const sc_expert_desc* d, const void* d_dout, in
     p.out = d_drows;
     p.ld_out = ldd;
     p.dweights = d_dweights;
-    p.vec = expert_vec(d, {g, o, r});
+    p.vec = expert_rows_at(d, 16, {g, o, r});
+    p.pairs = expert_rows_at(d, 4, {g, o, r});
     return status_of(launch_expert_combine_grad(d->dtype, p, cu(stream)));
 }
 

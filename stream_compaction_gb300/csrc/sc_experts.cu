@@ -151,41 +151,41 @@ __global__ void __launch_bounds__(32 * kSortMaxWarps) expert_sort_kernel(SortPar
 // ------------------------------------------------------------------ rows
 constexpr int kNT = 256, kAhead = 4;
 
-// A lane's elements of a row: 16 bytes, or one element where rows are not aligned.
-template <class T, bool kVec>
+// A lane's elements of a row in one access: the widest of 16, 4 and (16-bit elements) 2
+// bytes that every row is aligned to.
+template <class T, int kBytes>
 struct Part {
-    static constexpr int W = kVec ? 16 / (int)sizeof(T) : 1;
-    uint4 v;
-    T e;
-    __device__ __forceinline__ void load(const T* p) {
-        if constexpr (kVec) v = __ldg(reinterpret_cast<const uint4*>(p));
-        else e = __ldg(p);
-    }
-    __device__ __forceinline__ void store(T* p) const {
-        if constexpr (kVec) *reinterpret_cast<uint4*>(p) = v;
-        else *p = e;
-    }
-    __device__ __forceinline__ void zero() {
-        v = make_uint4(0u, 0u, 0u, 0u);
-        e = from_f32<T>(0.0f);
-    }
+    static constexpr int W = kBytes / (int)sizeof(T);
+    // Of them, side by side in a lane's loop; narrow ones need more for as much under way.
+    static constexpr int kColumns = kBytes == 16 ? 1 : 4;
+    using U = typename std::conditional<kBytes == 16, uint4, typename std::conditional<kBytes == 4, uint32_t, unsigned short>::type>::type;
+    U v;
+    __device__ __forceinline__ void load(const T* p) { v = __ldg(reinterpret_cast<const U*>(p)); }
+    __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<U*>(p) = v; }
+    __device__ __forceinline__ void zero() { memset(&v, 0, sizeof(v)); }
     __device__ __forceinline__ void get(float (&f)[W]) const {
-        if constexpr (kVec) {
+        if constexpr (kBytes == 16) {
             Vec<T, W> r;
             memcpy(r.w, &v, 16);
 #pragma unroll
             for (int i = 0; i < W; ++i) f[i] = r.get(i);
         } else {
-            f[0] = to_f32(e);
+            T e[W];
+            memcpy(e, &v, sizeof(v));
+#pragma unroll
+            for (int i = 0; i < W; ++i) f[i] = to_f32(e[i]);
         }
     }
     __device__ __forceinline__ void set(const float (&f)[W]) {
-        if constexpr (kVec) {
+        if constexpr (kBytes == 16) {
             Vec<T, W> r;
             r.set(f);
             memcpy(&v, r.w, 16);
         } else {
-            e = from_f32<T>(f[0]);
+            T e[W];
+#pragma unroll
+            for (int i = 0; i < W; ++i) e[i] = from_f32<T>(f[i]);
+            memcpy(&v, e, sizeof(v));
         }
     }
 };
@@ -208,110 +208,142 @@ __device__ __forceinline__ float weight_of(const ExpertParams& p, long long entr
     if (!p.weights) return 1.0f;
     return p.weights_f32 ? __ldg(static_cast<const float*>(p.weights) + entry) : to_f32(__ldg(static_cast<const T*>(p.weights) + entry));
 }
+// The row of an entry; -1: passed over.
+__device__ __forceinline__ long long row_of(const ExpertParams& p, long long entry) {
+    const long long row = __ldg(p.place + entry);
+    return row < p.entries ? row : -1;
+}
 
-template <class T, bool kVec>
+template <class T, int kBytes>
 __global__ void __launch_bounds__(kNT) expert_gather_kernel(ExpertParams p, int lanes) {
+    using P = Part<T, kBytes>;
     const Where at = where(lanes);
     if (at.token >= p.tokens) return;
     const long long kept = kept_of(p);
     const T* x = static_cast<const T*>(p.in) + at.token * p.ld_in;
-    const int32_t* place = p.place + at.token * p.choices;
-    constexpr int W = Part<T, kVec>::W;
-    for (long long c = (long long)at.lane * W; c < p.dim; c += lanes * W) {
-        Part<T, kVec> v, none;
-        v.load(x + c);
+    const int step = lanes * P::W;
+    for (long long c0 = (long long)at.lane * P::W; c0 < p.dim; c0 += step * P::kColumns) {
+        P v[P::kColumns], none;
         none.zero();
+#pragma unroll
+        for (int k = 0; k < P::kColumns; ++k)
+            if (c0 + k * step < p.dim) v[k].load(x + c0 + k * step);
         for (long long j = 0; j < p.choices; ++j) {
-            const long long row = __ldg(place + j);
-            if (row < 0 || row >= p.entries) continue;
-            (row < kept ? v : none).store(static_cast<T*>(p.out) + row * p.ld_out + c);
+            const long long row = row_of(p, at.token * p.choices + j);
+            if (row < 0) continue;
+            T* to = static_cast<T*>(p.out) + row * p.ld_out + c0;
+#pragma unroll
+            for (int k = 0; k < P::kColumns; ++k)
+                if (c0 + k * step < p.dim) (row < kept ? v[k] : none).store(to + k * step);
         }
     }
 }
 
 // out[t] = sum over j of weights[t,j] rows[place[t,j]]
-template <class T, bool kVec>
+template <class T, int kBytes>
 __global__ void __launch_bounds__(kNT) expert_combine_kernel(ExpertParams p, int lanes) {
+    using P = Part<T, kBytes>;
+    constexpr int W = P::W, C = P::kColumns;
     const Where at = where(lanes);
     if (at.token >= p.tokens) return;
     const long long kept = kept_of(p);
     const long long entry = at.token * p.choices;
-    const T* rows = static_cast<const T*>(p.in);
-    constexpr int W = Part<T, kVec>::W;
-    for (long long c = (long long)at.lane * W; c < p.dim; c += lanes * W) {
-        float sum[W];
+    const int step = lanes * W;
+    for (long long c0 = (long long)at.lane * W; c0 < p.dim; c0 += step * C) {
+        float sum[C][W];
 #pragma unroll
-        for (int i = 0; i < W; ++i) sum[i] = 0.0f;
+        for (int k = 0; k < C; ++k)
+#pragma unroll
+            for (int i = 0; i < W; ++i) sum[k][i] = 0.0f;
         for (long long j0 = 0; j0 < p.choices; j0 += kAhead) {
-            Part<T, kVec> v[kAhead];
+            P v[kAhead][C];
             bool live[kAhead];
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
-                const long long row = j0 + a < p.choices ? __ldg(p.place + entry + j0 + a) : -1;
+                const long long row = j0 + a < p.choices ? row_of(p, entry + j0 + a) : -1;
                 live[a] = row >= 0 && row < kept;
-                if (live[a]) v[a].load(rows + row * p.ld_in + c);
+                const T* from = static_cast<const T*>(p.in) + row * p.ld_in + c0;
+#pragma unroll
+                for (int k = 0; k < C; ++k)
+                    if (live[a] && c0 + k * step < p.dim) v[a][k].load(from + k * step);
             }
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
                 if (!live[a]) continue;
                 const float w = weight_of<T>(p, entry + j0 + a);
-                float f[W];
-                v[a].get(f);
 #pragma unroll
-                for (int i = 0; i < W; ++i) sum[i] = fmaf(w, f[i], sum[i]);
+                for (int k = 0; k < C; ++k) {
+                    float f[W];
+                    v[a][k].get(f);
+#pragma unroll
+                    for (int i = 0; i < W; ++i) sum[k][i] = fmaf(w, f[i], sum[k][i]);
+                }
             }
         }
-        Part<T, kVec> o;
-        o.set(sum);
-        o.store(static_cast<T*>(p.out) + at.token * p.ld_out + c);
+        T* to = static_cast<T*>(p.out) + at.token * p.ld_out + c0;
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+            P o;
+            o.set(sum[k]);
+            if (c0 + k * step < p.dim) o.store(to + k * step);
+        }
     }
 }
 
 // drows[place[t,j]] = weights[t,j] dout[t];  dweights[t,j] = dout[t] . rows[place[t,j]]
-template <class T, bool kVec>
+template <class T, int kBytes>
 __global__ void __launch_bounds__(kNT) expert_combine_grad_kernel(ExpertParams p, int lanes) {
+    using P = Part<T, kBytes>;
+    constexpr int W = P::W, C = P::kColumns;
     __shared__ float s_dot[kNT / 32][kAhead];
     const Where at = where(lanes);
     const bool here = at.token < p.tokens;  // all stay for the sums over threads
     const long long kept = kept_of(p), entry = (here ? at.token : 0) * p.choices;
     const T* dout = static_cast<const T*>(p.in) + (here ? at.token : 0) * p.ld_in;
     const T* rows = static_cast<const T*>(p.rows);
-    T* drows = static_cast<T*>(p.out);
-    constexpr int W = Part<T, kVec>::W;
+    const int step = lanes * W;
     for (long long j0 = 0; j0 < p.choices; j0 += kAhead) {
         long long row[kAhead];
         float w[kAhead], dot[kAhead];
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
-            row[a] = here && j0 + a < p.choices ? __ldg(p.place + entry + j0 + a) : -1;
-            if (row[a] >= p.entries) row[a] = -1;
-            w[a] = row[a] >= 0 && row[a] < kept ? weight_of<T>(p, entry + j0 + a) : 0.0f;
+            row[a] = here && j0 + a < p.choices ? row_of(p, entry + j0 + a) : -1;
             dot[a] = 0.0f;
         }
-        for (long long c = (long long)at.lane * W; here && c < p.dim; c += lanes * W) {
-            Part<T, kVec> g, v[kAhead];
-            g.load(dout + c);
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a)
-                if (rows && row[a] >= 0 && row[a] < kept) v[a].load(rows + row[a] * p.ld_rows + c);
-            float d[W];
-            g.get(d);
+        for (int a = 0; a < kAhead; ++a) w[a] = row[a] >= 0 && row[a] < kept ? weight_of<T>(p, entry + j0 + a) : 0.0f;
+        for (long long c0 = (long long)at.lane * W; here && c0 < p.dim; c0 += step * C) {
+            P g[C], v[kAhead][C];
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                if (row[a] < 0) continue;
-                const bool live = row[a] < kept;
-                float f[W];
-                if (rows && live) {
-                    v[a].get(f);
+            for (int k = 0; k < C; ++k) {
+                if (c0 + k * step >= p.dim) break;
+                g[k].load(dout + c0 + k * step);
 #pragma unroll
-                    for (int i = 0; i < W; ++i) dot[a] = fmaf(d[i], f[i], dot[a]);
+                for (int a = 0; a < kAhead; ++a)
+                    if (rows && row[a] >= 0 && row[a] < kept) v[a][k].load(rows + row[a] * p.ld_rows + c0 + k * step);
+            }
+#pragma unroll
+            for (int k = 0; k < C; ++k) {
+                if (c0 + k * step >= p.dim) break;
+                float d[W];
+                g[k].get(d);
+#pragma unroll
+                for (int a = 0; a < kAhead; ++a) {
+                    if (row[a] < 0) continue;
+                    const bool live = row[a] < kept;
+                    float f[W];
+                    if (rows && live) {
+                        v[a][k].get(f);
+#pragma unroll
+                        for (int i = 0; i < W; ++i) dot[a] = fmaf(d[i], f[i], dot[a]);
+                    }
+                    P o;
+#pragma unroll
+                    for (int i = 0; i < W; ++i) f[i] = w[a] * d[i];
+                    o.set(f);
+                    if (!live) o.zero();
+                    o.store(static_cast<T*>(p.out) + row[a] * p.ld_out + c0 + k * step);
                 }
-                Part<T, kVec> o;
-#pragma unroll
-                for (int i = 0; i < W; ++i) f[i] = w[a] * d[i];
-                o.set(f);
-                if (!live) o.zero();
-                o.store(drows + row[a] * p.ld_out + c);
             }
         }
         if (!p.dweights) continue;
@@ -413,7 +445,7 @@ __global__ void __launch_bounds__(kNT) expert_ring_kernel(ExpertParams p, int si
     extern __shared__ __align__(128) unsigned char s_mem[];
     __shared__ float s_dot[kNT / 32][kMaxChoices];
     constexpr int W = 16 / (int)sizeof(T);
-    using P = Part<T, true>;
+    using P = Part<T, 16>;
     const int teams = kNT / size, team = threadIdx.x / size, thread = threadIdx.x - team * size, lane = threadIdx.x % 32;
     const int choices = (int)p.choices;
     const long long step = (long long)gridDim.x * teams;
@@ -510,15 +542,16 @@ __global__ void __launch_bounds__(kNT) expert_ring_kernel(ExpertParams p, int si
     }
 }
 
-// Threads a token: one or two vectors each, up to a whole CTA.
-template <class T, bool kVec>
+// Threads a token: a Part's columns each, up to a whole CTA.
+template <class P>
 int lanes_of(long long dim) {
-    const long long n = (dim + Part<T, kVec>::W - 1) / Part<T, kVec>::W;
+    const long long n = (dim + P::W * P::kColumns - 1) / (P::W * P::kColumns);
     int lanes = 8;
     while (lanes < kNT && lanes < n) lanes *= 2;
     return lanes;
 }
 enum { kGather, kCombine, kCombineGrad };
+
 // Through a ring where two stages fit a team's share of the shared memory and CTAs have
 // several turns.
 template <class T, bool kGrad>
@@ -546,23 +579,27 @@ bool ring_as(const ExpertParams& p, cudaStream_t s, cudaError_t* e) {
     return true;
 }
 
-template <class T, bool kVec>
+template <class T, int kBytes>
 cudaError_t rows_as(int what, const ExpertParams& p, cudaStream_t s) {
-    if constexpr (kVec) {
-        cudaError_t e;
-        if ((what == kCombine && ring_as<T, false>(p, s, &e)) || (what == kCombineGrad && ring_as<T, true>(p, s, &e))) return e;
-    }
-    const int lanes = lanes_of<T, kVec>(p.dim);
+    const int lanes = lanes_of<Part<T, kBytes>>(p.dim);
     const unsigned grid = (unsigned)((p.tokens + kNT / lanes - 1) / (kNT / lanes));
-    if (what == kGather) expert_gather_kernel<T, kVec><<<grid, kNT, 0, s>>>(p, lanes);
-    else if (what == kCombine) expert_combine_kernel<T, kVec><<<grid, kNT, 0, s>>>(p, lanes);
-    else expert_combine_grad_kernel<T, kVec><<<grid, kNT, 0, s>>>(p, lanes);
+    if (what == kGather) expert_gather_kernel<T, kBytes><<<grid, kNT, 0, s>>>(p, lanes);
+    else if (what == kCombine) expert_combine_kernel<T, kBytes><<<grid, kNT, 0, s>>>(p, lanes);
+    else expert_combine_grad_kernel<T, kBytes><<<grid, kNT, 0, s>>>(p, lanes);
     count_launches(1);
     return cudaGetLastError();
 }
 template <class T>
 cudaError_t rows_of(int what, const ExpertParams& p, cudaStream_t s) {
-    return p.vec ? rows_as<T, true>(what, p, s) : rows_as<T, false>(what, p, s);
+    if (p.vec) {
+        cudaError_t e;
+        if ((what == kCombine && ring_as<T, false>(p, s, &e)) || (what == kCombineGrad && ring_as<T, true>(p, s, &e))) return e;
+        return rows_as<T, 16>(what, p, s);
+    }
+    if constexpr (sizeof(T) == 2) {
+        if (!p.pairs) return rows_as<T, 2>(what, p, s);
+    }
+    return rows_as<T, 4>(what, p, s);
 }
 cudaError_t rows(int dtype, int what, const ExpertParams& p, cudaStream_t s) {
     return dtype == SC_F32 ? rows_of<float>(what, p, s) : dtype == SC_F16 ? rows_of<f16>(what, p, s) : rows_of<bf16>(what, p, s);

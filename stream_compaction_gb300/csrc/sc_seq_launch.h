@@ -184,7 +184,7 @@ struct ExpertParams {
     const int32_t* place;
     const int64_t* kept;  // offsets + experts
     const void* weights;
-    int weights_f32, vec;
+    int weights_f32, vec, pairs;  // rows aligned to 16 bytes; to 4
     const void* in;  // rows of tokens, or of entries
     long long ld_in;
     void* out;
