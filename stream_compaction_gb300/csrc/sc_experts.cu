@@ -2,7 +2,7 @@
 // expert, rows moved into that order and summed back with weights, and the gradients.
 //
 // The sort is one counting pass, since there is one digit: the expert.  One cluster of
-// up to 8 CTAs, without scratch memory:
+// up to 16 CTAs, without scratch memory:
 //   count   a warp counts its run of consecutive entries by expert (shared memory);
 //   scan    per expert over the CTA's warps, over the CTAs (distributed shared
 //           memory), then over the experts;
@@ -31,17 +31,29 @@ namespace {
 namespace cg = cooperative_groups;
 
 // ------------------------------------------------------------------ sort
-constexpr int kSortMaxWarps = 32, kSortMaxCtas = 8;
+constexpr int kSortMaxWarps = 32, kSortMaxCtas = 16;
 constexpr int kRounds = 4;  // of 32 entries, loaded together
 constexpr int kMaxBins = SC_EXPERT_MAX + 1;
 
 struct SortParams {
     const void* ids;
-    int ids64, experts;
-    long long entries, run;  // of a warp, a multiple of 32
+    int ids64, experts, bits;  // bits: of a bin, and of the number behind the last
+    long long entries, run;    // of a warp, a multiple of 32
     int32_t *order, *place;
     int64_t* offsets;
 };
+
+// The lanes whose bin equals this one's, by one ballot a bit: a match instruction takes
+// about 60 cycles of a unit that the SM has once, whatever the number of bins (262144
+// entries of 512 experts: 65 us with it).
+__device__ __forceinline__ uint32_t same_bin(int bin, int bits) {
+    uint32_t same = 0xffffffffu;
+    for (int b = 0; b < bits; ++b) {
+        const uint32_t bit = (uint32_t)bin >> b & 1u, on = __ballot_sync(0xffffffffu, bit);
+        same &= on ^ (bit - 1u);
+    }
+    return same;
+}
 
 __device__ __forceinline__ int bin_of(const SortParams& p, long long i) {
     const long long id = p.ids64 ? __ldg(static_cast<const long long*>(p.ids) + i)
@@ -128,12 +140,15 @@ __global__ void __launch_bounds__(32 * kSortMaxWarps) expert_sort_kernel(SortPar
 #pragma unroll
         for (int r = 0; r < kRounds; ++r) {
             const long long i = i0 + r * 32 + lane;
-            d[r] = i < last ? bin_of(p, i) : -1;
+            d[r] = i < last ? bin_of(p, i) : bins;
         }
+        uint32_t same_[kRounds];
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) same_[r] = same_bin(d[r], p.bits);
 #pragma unroll
         for (int r = 0; r < kRounds; ++r) {
-            const uint32_t same = __match_any_sync(0xffffffffu, d[r]);
-            const bool live = d[r] >= 0;
+            const uint32_t same = same_[r];
+            const bool live = d[r] < bins;
             const uint32_t begin = live ? mine[d[r]] : 0u;
             __syncwarp();
             if (live) {
@@ -149,15 +164,15 @@ __global__ void __launch_bounds__(32 * kSortMaxWarps) expert_sort_kernel(SortPar
 }
 
 // ------------------------------------------------------------------ rows
-constexpr int kNT = 256, kAhead = 4;
+constexpr int kNT = 256;
 
 // A lane's elements of a row in one access: the widest of 16, 4 and (16-bit elements) 2
-// bytes that every row is aligned to.
-template <class T, int kBytes>
+// bytes that every row is aligned to.  kAhead: the entries of a token that are loaded
+// together, 2 or 4; kColumns: the accesses of a row that are, more where they are narrow.
+template <class T, int kBytes, int kAhead_>
 struct Part {
-    static constexpr int W = kBytes / (int)sizeof(T);
-    // Of them, side by side in a lane's loop; narrow ones need more for as much under way.
-    static constexpr int kColumns = kBytes == 16 ? 1 : 4;
+    static constexpr int W = kBytes / (int)sizeof(T), kAhead = kAhead_;
+    static constexpr int kColumns = (kBytes == 16 ? 4 : 16) / kAhead;
     using U = typename std::conditional<kBytes == 16, uint4, typename std::conditional<kBytes == 4, uint32_t, unsigned short>::type>::type;
     U v;
     __device__ __forceinline__ void load(const T* p) { v = __ldg(reinterpret_cast<const U*>(p)); }
@@ -214,9 +229,8 @@ __device__ __forceinline__ long long row_of(const ExpertParams& p, long long ent
     return row < p.entries ? row : -1;
 }
 
-template <class T, int kBytes>
+template <class T, class P>
 __global__ void __launch_bounds__(kNT) expert_gather_kernel(ExpertParams p, int lanes) {
-    using P = Part<T, kBytes>;
     const Where at = where(lanes);
     if (at.token >= p.tokens) return;
     const long long kept = kept_of(p);
@@ -240,10 +254,9 @@ __global__ void __launch_bounds__(kNT) expert_gather_kernel(ExpertParams p, int 
 }
 
 // out[t] = sum over j of weights[t,j] rows[place[t,j]]
-template <class T, int kBytes>
+template <class T, class P>
 __global__ void __launch_bounds__(kNT) expert_combine_kernel(ExpertParams p, int lanes) {
-    using P = Part<T, kBytes>;
-    constexpr int W = P::W, C = P::kColumns;
+    constexpr int W = P::W, C = P::kColumns, kAhead = P::kAhead;
     const Where at = where(lanes);
     if (at.token >= p.tokens) return;
     const long long kept = kept_of(p);
@@ -291,10 +304,9 @@ __global__ void __launch_bounds__(kNT) expert_combine_kernel(ExpertParams p, int
 }
 
 // drows[place[t,j]] = weights[t,j] dout[t];  dweights[t,j] = dout[t] . rows[place[t,j]]
-template <class T, int kBytes>
+template <class T, class P>
 __global__ void __launch_bounds__(kNT) expert_combine_grad_kernel(ExpertParams p, int lanes) {
-    using P = Part<T, kBytes>;
-    constexpr int W = P::W, C = P::kColumns;
+    constexpr int W = P::W, C = P::kColumns, kAhead = P::kAhead;
     __shared__ float s_dot[kNT / 32][kAhead];
     const Where at = where(lanes);
     const bool here = at.token < p.tokens;  // all stay for the sums over threads
@@ -445,7 +457,7 @@ __global__ void __launch_bounds__(kNT) expert_ring_kernel(ExpertParams p, int si
     extern __shared__ __align__(128) unsigned char s_mem[];
     __shared__ float s_dot[kNT / 32][kMaxChoices];
     constexpr int W = 16 / (int)sizeof(T);
-    using P = Part<T, 16>;
+    using P = Part<T, 16, 4>;
     const int teams = kNT / size, team = threadIdx.x / size, thread = threadIdx.x - team * size, lane = threadIdx.x % 32;
     const int choices = (int)p.choices;
     const long long step = (long long)gridDim.x * teams;
@@ -552,13 +564,17 @@ int lanes_of(long long dim) {
 }
 enum { kGather, kCombine, kCombineGrad };
 
-// Through a ring where two stages fit a team's share of the shared memory and CTAs have
-// several turns.
+// Through a ring where CTAs have several turns and two stages fit a team's share of the
+// shared memory; and where a token has few entries: with four or more a lane's direct
+// loads are as much under way, without a stage of that many rows (16384 tokens with 8
+// entries of 4096 bfloat16: gradient 608 us through the ring, 348 directly, sum 275 and
+// 211; 32768 with 8 of 512: gradient 152 and 111, sum 59 and 68).
 template <class T, bool kGrad>
 bool ring_as(const ExpertParams& p, cudaStream_t s, cudaError_t* e) {
     constexpr int kShared = 200 * 1024;
     const long long vectors = p.dim * (long long)sizeof(T) / 16, row = p.dim * (long long)sizeof(T);
     if (p.choices < 1 || p.choices > kMaxChoices || row > kShared) return false;
+    if (p.choices > 3 && (kGrad || vectors >= kNT)) return false;
     int size = 32;
     while (size < kNT && size < vectors) size *= 2;
     const int teams = kNT / size;
@@ -579,15 +595,19 @@ bool ring_as(const ExpertParams& p, cudaStream_t s, cudaError_t* e) {
     return true;
 }
 
-template <class T, int kBytes>
-cudaError_t rows_as(int what, const ExpertParams& p, cudaStream_t s) {
-    const int lanes = lanes_of<Part<T, kBytes>>(p.dim);
+template <class T, class P>
+cudaError_t launch_rows(int what, const ExpertParams& p, cudaStream_t s) {
+    const int lanes = lanes_of<P>(p.dim);
     const unsigned grid = (unsigned)((p.tokens + kNT / lanes - 1) / (kNT / lanes));
-    if (what == kGather) expert_gather_kernel<T, kBytes><<<grid, kNT, 0, s>>>(p, lanes);
-    else if (what == kCombine) expert_combine_kernel<T, kBytes><<<grid, kNT, 0, s>>>(p, lanes);
-    else expert_combine_grad_kernel<T, kBytes><<<grid, kNT, 0, s>>>(p, lanes);
+    if (what == kGather) expert_gather_kernel<T, P><<<grid, kNT, 0, s>>>(p, lanes);
+    else if (what == kCombine) expert_combine_kernel<T, P><<<grid, kNT, 0, s>>>(p, lanes);
+    else expert_combine_grad_kernel<T, P><<<grid, kNT, 0, s>>>(p, lanes);
     count_launches(1);
     return cudaGetLastError();
+}
+template <class T, int kBytes>
+cudaError_t rows_as(int what, const ExpertParams& p, cudaStream_t s) {
+    return p.choices <= 2 ? launch_rows<T, Part<T, kBytes, 2>>(what, p, s) : launch_rows<T, Part<T, kBytes, 4>>(what, p, s);
 }
 template <class T>
 cudaError_t rows_of(int what, const ExpertParams& p, cudaStream_t s) {
@@ -609,18 +629,20 @@ cudaError_t rows(int dtype, int what, const ExpertParams& p, cudaStream_t s) {
 
 cudaError_t launch_expert_sort(const void* ids, int ids64, long long entries, int experts, int32_t* order, int32_t* place,
                                int64_t* offsets, cudaStream_t s) {
-    // a warp per 32 entries up to 8 CTAs of 32 warps, then longer runs
+    // a warp per 32 entries up to 16 CTAs of 32 warps, then longer runs
     const long long least = (entries + 31) / 32;
     int ctas = 1;
     while (ctas < kSortMaxCtas && (long long)ctas * kSortMaxWarps < least) ctas *= 2;
     // (a thread has two bins at most where a CTA can have as many threads)
     const int warps = (int)std::clamp<long long>(std::max<long long>((least + ctas - 1) / ctas, experts / 64 + 1), 1, kSortMaxWarps);
-    SortParams p{ids, ids64, experts, entries, 0, order, place, offsets};
+    SortParams p{ids, ids64, experts, 0, entries, 0, order, place, offsets};
+    while (experts + 1 >> p.bits) ++p.bits;
     p.run = ((entries + (long long)ctas * warps - 1) / ((long long)ctas * warps) + 31) / 32 * 32;
     const size_t bytes = (size_t)warps * (experts + 1) * sizeof(uint32_t);
     // the limit is one per device: always the whole, whatever this call needs
     cudaError_t e = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kSortMaxWarps * kMaxBins * (int)sizeof(uint32_t));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)ctas);

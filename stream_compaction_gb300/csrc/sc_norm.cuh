@@ -331,10 +331,10 @@ struct Turns {
 
 // ---------------------------------------------------------------- forward
 // CTAs that an SM holds: 65536 registers by 80 a thread, 128 with rows in registers.
-template <Way kWay, int kLanes> constexpr int kResident = kThreads<kLanes> == 256 ? (kWay == kRing ? 3 : 2) : 1;
+template <class T, Way kWay, int kLanes> constexpr int kResident = kThreads<kLanes> == 256 ? (kWay == kRing || sizeof(T) == 4 ? 3 : 2) : 1;
 
 template <class T, Way kWay, int kLanes, int NV>
-__global__ void __launch_bounds__(kThreads<kLanes>, kResident<kWay, kLanes>) norm_kernel(NormParams p) {
+__global__ void __launch_bounds__(kThreads<kLanes>, kResident<T, kWay, kLanes>) norm_kernel(NormParams p) {
     using G = Team<T, kWay, kLanes, NV>;
     using R = Row<T, kWay != kElements, kLanes, NV>;
     constexpr int W = G::W, N = G::N, D = G::kDeep;
@@ -750,7 +750,7 @@ template <class T, Way kWay, int kLanes, int NV, bool kGrad>
 cudaError_t launch_as(NormParams& p, cudaStream_t s) {
     using G = Team<T, kWay, kLanes, NV>;
     const long long turns = (p.rows + (long long)G::kTeams * G::kRows - 1) / (G::kTeams * G::kRows);
-    const int resident = kGrad ? kGradResident<kLanes> : kResident<kWay, kLanes>;
+    const int resident = kGrad ? kGradResident<kLanes> : kResident<T, kWay, kLanes>;
     const int tensors = kGrad ? (p.dsum ? 3 : 2) : p.residual ? 2 : 1;
     int bytes = kGrad && G::kGroups > 1 ? (int)sizeof(float) * G::NT * G::N : 0;  // the columns' sums
     if (kWay == kRing) {
@@ -777,7 +777,7 @@ cudaError_t go(NormParams& p, bool grad, cudaStream_t s) {
 template <class T, int kLanes, int NV>
 cudaError_t vectors(NormParams& p, bool grad, cudaStream_t s) {
     using G = Team<T, kVectors, kLanes, NV>;
-    const long long held = seq_sms() * (grad ? kGradResident<kLanes> : kResident<kVectors, kLanes>) * G::kTeams * G::kRows;
+    const long long held = seq_sms() * (grad ? kGradResident<kLanes> : kResident<T, kVectors, kLanes>) * G::kTeams * G::kRows;
     if (p.rows <= held) return go<T, kVectors, kLanes, NV>(p, grad, s);
     return go<T, kRing, kLanes, NV>(p, grad, s);
 }
