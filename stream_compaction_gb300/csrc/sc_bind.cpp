@@ -6,6 +6,7 @@
 // Names, arguments and meanings: seq.py, whose functions these are.
 #include <ATen/Functions.h>
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
@@ -102,6 +103,18 @@ void written(const Tensor& t) {
 }
 void written(const Maybe& t) {
     if (t) written(*t);
+}
+
+// Whether torch records a gradient by one of the tensors: the call is then made through
+// an autograd function, and the direct one returns None to say so (cheaper than to ask
+// first, from the interpreter).
+bool records(std::initializer_list<const Maybe*> some, std::initializer_list<const Tensor*> given) {
+    if (!at::GradMode::is_enabled()) return false;
+    for (const Maybe* t : some)
+        if (*t && (*t)->requires_grad()) return true;
+    for (const Tensor* t : given)
+        if (t->requires_grad()) return true;
+    return false;
 }
 
 Tensor make(at::IntArrayRef shape, const Tensor& like_this) { return at::empty(shape, like_this.options()); }
@@ -411,9 +424,10 @@ Tensor gated_scan_saved(const Tensor& x) {
     return make_f32(gated_saved_shape(x), x);
 }
 
-Tensor gated_scan(const Tensor& x, const Tensor& gate, const std::optional<std::string>& activation,
-                  const Maybe& heads, const Maybe& state, const Maybe& final_state, const Maybe& saved,
-                  const Maybe& out) {
+py::object gated_scan(const Tensor& x, const Tensor& gate, const std::optional<std::string>& activation,
+                      const Maybe& heads, const Maybe& state, const Maybe& final_state, const Maybe& saved,
+                      const Maybe& out) {
+    if (records({&state}, {&x, &gate})) return py::none();
     sc_gated_desc d = gated_desc(x, gate, activation, false);
     d.heads = heads_of(heads, x);
     d.state = gated_state(state, "state", x);
@@ -424,7 +438,7 @@ Tensor gated_scan(const Tensor& x, const Tensor& gate, const std::optional<std::
     written(final_state);
     written(saved);
     written(out);
-    return y;
+    return py::cast(y);
 }
 
 py::dict gated_scan_grad(const Tensor& dy, const Tensor& x, const Tensor& gate,
@@ -449,8 +463,9 @@ py::dict gated_scan_grad(const Tensor& dy, const Tensor& x, const Tensor& gate,
     return g;
 }
 
-Tensor gated_scan_step(const Tensor& x, const Tensor& gate, const Tensor& state,
-                       const std::optional<std::string>& activation, const Maybe& slots, const Maybe& out) {
+py::object gated_scan_step(const Tensor& x, const Tensor& gate, const Tensor& state,
+                           const std::optional<std::string>& activation, const Maybe& slots, const Maybe& out) {
+    if (records({}, {&x, &gate, &state})) return py::none();
     const sc_gated_desc d = gated_desc(x, gate, activation, true);
     need(state.dim() == 2, "state must have shape (rows, channels)");
     void* pool = whole(state, "state", {state.size(0), d.channels}, at::kFloat, x.device());
@@ -460,7 +475,7 @@ Tensor gated_scan_step(const Tensor& x, const Tensor& gate, const Tensor& state,
           "sc_gated_scan_step");
     written(state);
     written(out);
-    return y;
+    return py::cast(y);
 }
 
 // ------------------------------------------------------------------ norm
@@ -529,6 +544,7 @@ Tensor layer_norm_saved(const Tensor& x) {
 
 py::object layer_norm(const Tensor& x, const Maybe& weight, const Maybe& bias, double eps, bool rms,
                       const Maybe& residual, const Maybe& saved, const Maybe& out) {
+    if (records({&weight, &bias, &residual}, {&x})) return py::none();
     sc_norm_desc d = norm_desc(x, weight, bias, rms);
     need(eps >= 0, "eps must not be negative");
     d.eps = (float)eps;
@@ -640,13 +656,14 @@ Tensor rows_out(const Maybe& out, int64_t rows, const Tensor& like_this) {
     return like(*out, "out", shape, like_this.scalar_type(), like_this.device());
 }
 
-Tensor expert_gather(const Tensor& x, const Tensor& offsets, const Tensor& place, const Maybe& out) {
+py::object expert_gather(const Tensor& x, const Tensor& offsets, const Tensor& place, const Maybe& out) {
+    if (records({}, {&x})) return py::none();
     const sc_expert_desc d = expert_desc(offsets, place, x, "x");
     need(x.size(0) == d.tokens, "x must have a row for each token");
     Tensor rows = rows_out(out, d.tokens * d.choices, x);
     check(sc_expert_gather(&d, x.data_ptr(), ld(x), rows.data_ptr(), ld(rows), stream()), "sc_expert_gather");
     written(out);
-    return rows;
+    return py::cast(rows);
 }
 Tensor expert_gather_grad(const Tensor& drows, const Tensor& offsets, const Tensor& place, const Maybe& out) {
     const sc_expert_desc d = expert_desc(offsets, place, drows, "drows");
@@ -656,15 +673,16 @@ Tensor expert_gather_grad(const Tensor& drows, const Tensor& offsets, const Tens
     written(out);
     return dx;
 }
-Tensor expert_combine(const Tensor& rows, const Tensor& offsets, const Tensor& place, const Maybe& weights,
-                      const Maybe& out) {
+py::object expert_combine(const Tensor& rows, const Tensor& offsets, const Tensor& place, const Maybe& weights,
+                          const Maybe& out) {
+    if (records({&weights}, {&rows})) return py::none();
     sc_expert_desc d = expert_desc(offsets, place, rows, "rows");
     need(rows.size(0) == d.tokens * d.choices, "rows must have a row for each entry");
     expert_weights(d, weights, rows);
     Tensor y = rows_out(out, d.tokens, rows);
     check(sc_expert_combine(&d, rows.data_ptr(), ld(rows), y.data_ptr(), ld(y), stream()), "sc_expert_combine");
     written(out);
-    return y;
+    return py::cast(y);
 }
 py::dict expert_combine_grad(const Tensor& dout, const Tensor& rows, const Tensor& offsets, const Tensor& place,
                              const Maybe& weights) {

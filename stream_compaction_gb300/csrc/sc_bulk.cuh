@@ -4,6 +4,10 @@
 
 namespace scg {
 
+// Shared memory that a launch may ask for without a limit set for its kernel (with room
+// for what the kernels have by themselves).
+constexpr int kDefaultShared = 40 * 1024;
+
 // `bytes` (a multiple of 16, both addresses aligned so) into shared memory, counted on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t to, const void* from, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"

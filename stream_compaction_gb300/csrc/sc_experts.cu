@@ -640,9 +640,11 @@ cudaError_t launch_expert_sort(const void* ids, int ids64, long long entries, in
     p.run = ((entries + (long long)ctas * warps - 1) / ((long long)ctas * warps) + 31) / 32 * 32;
     const size_t bytes = (size_t)warps * (experts + 1) * sizeof(uint32_t);
     // the limit is one per device: always the whole, whatever this call needs
-    cudaError_t e = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSortMaxWarps * kMaxBins * (int)sizeof(uint32_t));
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaError_t e = cudaSuccess;
+    if (bytes > kDefaultShared - 8 * 1024)
+        e = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kSortMaxWarps * kMaxBins * (int)sizeof(uint32_t));
+    if (e == cudaSuccess && ctas > 8) e = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)ctas);

@@ -791,7 +791,8 @@ cudaError_t go(const GatedParams& p, const GatedMaps& maps, bool grad, long long
         return (int)(grad ? Shared<K, kWarps, BackwardRing<T, K>, kTma>::bytes(n) : Shared<K, kWarps, ForwardRing<T, K>, kTma>::bytes(n));
     };
     // the limit is one per device: always the largest, whatever this call needs
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(kMaxCluster));
+    cudaError_t e = cudaSuccess;
+    if (bytes(ctas) > kDefaultShared) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(kMaxCluster));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(groups * ctas));

@@ -763,8 +763,10 @@ cudaError_t launch_as(NormParams& p, cudaStream_t s) {
     if constexpr (kGrad) kernel = (const void*)norm_grad_kernel<T, kWay, kLanes, NV>;
     else kernel = (const void*)norm_kernel<T, kWay, kLanes, NV>;
     // the limit is one per device: always the largest, whatever this call needs
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes + 8192);
-    if (e != cudaSuccess) return e;
+    if (bytes > kDefaultShared) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes + 8192);
+        if (e != cudaSuccess) return e;
+    }
     void* args[] = {&p};
     return cudaLaunchKernel(kernel, dim3((unsigned)p.parts), dim3(G::NT), args, (size_t)bytes, s);
 }

@@ -122,7 +122,8 @@ SIGNATURES = {
 
 # ------------------------------------------------------------ tensor layer
 # The functions are compiled (csrc/sc_bind.cpp); here are their arguments and
-# what they mean.
+# what they mean.  Those of the block's operators return None where a gradient is to be
+# recorded, and the call goes through its autograd function instead.
 _bind = None
 
 
@@ -263,9 +264,10 @@ def gated_scan(x, gate, activation="sigmoid", heads=None, state=None, final_stat
     with f = sigmoid(gate), or with activation None h = gate * h + x.  heads as in
     causal_conv; state / final_state: (batch, channels) float32.  saved: from
     gated_scan_saved, for gated_scan_grad."""
-    if _requires_grad(x, gate, state):
+    y = _call("gated_scan", stream, x, gate, activation, heads, state, final_state, saved, out)
+    if y is None:
         return _record("GatedScan", stream, out, x, gate, activation, heads, state, final_state, saved)
-    return _call("gated_scan", stream, x, gate, activation, heads, state, final_state, saved, out)
+    return y
 
 
 def gated_scan_grad(dy, x, gate, activation="sigmoid", heads=None, state=None, saved=None, dfinal_state=None,
@@ -278,7 +280,10 @@ def gated_scan_grad(dy, x, gate, activation="sigmoid", heads=None, state=None, s
 def gated_scan_step(x, gate, state, activation="sigmoid", slots=None, out=None, stream=None):
     """One token for each row of x (batch, channels); state (rows, channels) float32 is
     moved on in place.  slots as in causal_conv_step."""
-    return _step("gated_scan_step", stream, (x, gate, state), x, gate, state, activation, slots, out)
+    y = _call("gated_scan_step", stream, x, gate, state, activation, slots, out)
+    if y is None:
+        return _step("gated_scan_step", stream, (x, gate, state), x, gate, state, activation, slots, out)
+    return y
 
 
 def layer_norm_saved(x, stream=None):
@@ -293,9 +298,10 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, rms: bool = False, 
     (channels), of x's type or float32); rms: without the mean.  residual (like x): the
     norm of x + residual, and the result is the pair (y, x + residual), the sum rounded
     to x's type.  saved: from layer_norm_saved, for layer_norm_grad."""
-    if _requires_grad(x, weight, bias, residual):
+    y = _call("layer_norm", stream, x, weight, bias, eps, rms, residual, saved, out)
+    if y is None:
         return _record("LayerNorm", stream, out, x, weight, bias, eps, rms, residual, saved)
-    return _call("layer_norm", stream, x, weight, bias, eps, rms, residual, saved, out)
+    return y
 
 
 def layer_norm_grad(dy, x, weight=None, bias=None, rms: bool = False, saved=None, dsum=None, stream=None):
@@ -326,9 +332,10 @@ def expert_sort(experts, n_experts: int, stream=None):
 def expert_gather(x, order, out=None, stream=None):
     """A row of x (tokens, dim) for each entry, in the order of the experts (tokens *
     choices, dim); zeros for entries of no expert."""
-    if _requires_grad(x):
+    y = _call("expert_gather", stream, x, order.offsets, order.place, out)
+    if y is None:
         return _record("ExpertGather", stream, out, x, order.offsets, order.place)
-    return _call("expert_gather", stream, x, order.offsets, order.place, out)
+    return y
 
 
 def expert_gather_grad(drows, order, out=None, stream=None):
@@ -340,9 +347,10 @@ def expert_combine(y, order, weights=None, out=None, stream=None):
     """The way back: the sum of a token's rows of y (tokens * choices, dim, in the order
     of the experts), times weights (tokens, choices; of y's type or float32) where they
     are given; entries of no expert add nothing."""
-    if _requires_grad(y, weights):
+    z = _call("expert_combine", stream, y, order.offsets, order.place, weights, out)
+    if z is None:
         return _record("ExpertCombine", stream, out, y, order.offsets, order.place, weights)
-    return _call("expert_combine", stream, y, order.offsets, order.place, weights, out)
+    return z
 
 
 def expert_combine_grad(dout, y, order, weights=None, stream=None):
