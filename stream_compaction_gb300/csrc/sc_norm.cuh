@@ -242,9 +242,8 @@ struct RowRing {
 };
 
 // The rows of a team's turns, of 1 or 2 tensors forward, 2 or 3 backward.
-template <class T, Way kWay, int kLanes, int NV, bool kGrad>
+template <class T, Way kWay, int kLanes, int NV, int kTensors>
 struct Turns {
-    static constexpr int kTensors = kGrad ? 3 : 2;
     using G = Team<T, kWay, kLanes, NV>;
     using R = Row<T, kWay != kElements, kLanes, NV>;
     RowRing<T, kTensors, G::kRows> ring;
@@ -252,8 +251,8 @@ struct Turns {
     uint32_t rows, step, ahead;  // below 2^31; a turn behind the last stays below 2^32
     int thread, lane, side, channels;  // thread: of the team
 
-    __device__ __forceinline__ void begin(const NormParams& p, unsigned char* mem, const void* const (&from)[kTensors],
-                                          const long long (&sb)[kTensors], const long long (&st)[kTensors], int tensors) {
+    __device__ __forceinline__ void begin(const NormParams& p, unsigned char* mem, const void* const* from,
+                                          const long long* sb, const long long* st, int tensors) {
         const int team = threadIdx.x / G::kSize;
         thread = threadIdx.x % G::kSize;
         lane = threadIdx.x % kLanes;
@@ -342,7 +341,7 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kResident<T, kWay, kLanes>) 
     __shared__ __align__(16) float s_sum[G::kGroups][2][2][kLanes > 32 ? kLanes / 32 : 1];
     extern __shared__ __align__(128) unsigned char s_mem[];
     const int group = threadIdx.x / kLanes, channels = (int)p.channels;
-    Turns<T, kWay, kLanes, NV, false> turns;
+    Turns<T, kWay, kLanes, NV, 2> turns;
     {
         const void* const from[2] = {p.x, p.residual};
         const long long sb[2] = {p.x_batch, p.residual_batch}, st[2] = {p.x_token, p.residual_token};
@@ -450,11 +449,14 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kResident<T, kWay, kLanes>) 
 }
 
 // --------------------------------------------------------------- gradient
-// 128 registers a thread (64 of 1024 threads).
-template <int kLanes> constexpr int kGradResident = kThreads<kLanes> == 256 ? 2 : 1;
+// 128 registers a thread (64 of 1024 threads); 80 where a thread has 8 elements of one row
+// and two tensors (3003 rows of 2047 float32: 27 us with two CTAs an SM, 25 with three; two
+// 16-bit rows a thread spill so, and take 55 us in place of 49).  kSum: dsum is there.
+template <class T, Way kWay, int kLanes, int NV, bool kSum>
+constexpr int kGradResident = kThreads<kLanes> > 256 ? 1 : kWidth<T> * NV == 8 && !kSum && (kWay != kRing || sizeof(T) == 4) ? 3 : 2;
 
-template <class T, Way kWay, int kLanes, int NV>
-__global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<kLanes>) norm_grad_kernel(NormParams p) {
+template <class T, Way kWay, int kLanes, int NV, bool kSum>
+__global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<T, kWay, kLanes, NV, kSum>) norm_grad_kernel(NormParams p) {
     using G = Team<T, kWay, kLanes, NV>;
     using R = Row<T, kWay != kElements, kLanes, NV>;
     constexpr int W = G::W, N = G::N, D = G::kDeep, NT = G::NT, kGroups = G::kGroups;
@@ -462,11 +464,17 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<kLanes>) norm_
     __shared__ __align__(16) float s_sum[kGroups][2][2 * D * (kLanes > 32 ? kLanes / 32 : 1)];
     extern __shared__ __align__(128) unsigned char s_mem[];
     const int group = threadIdx.x / kLanes, channels = (int)p.channels;
-    Turns<T, kWay, kLanes, NV, true> turns;
+    constexpr int kTensors = kSum ? 3 : 2;
+    Turns<T, kWay, kLanes, NV, kTensors> turns;
     {
-        const void* const from[3] = {p.x, p.dy, p.dsum};
-        const long long sb[3] = {p.x_batch, p.dy_batch, p.dsum_batch}, st[3] = {p.x_token, p.dy_token, p.dsum_token};
-        turns.begin(p, s_mem, from, sb, st, p.dsum ? 3 : 2);
+        const void* from[kTensors] = {p.x, p.dy};
+        long long sb[kTensors] = {p.x_batch, p.dy_batch}, st[kTensors] = {p.x_token, p.dy_token};
+        if constexpr (kSum) {
+            from[2] = p.dsum;
+            sb[2] = p.dsum_batch;
+            st[2] = p.dsum_token;
+        }
+        turns.begin(p, s_mem, from, sb, st, kTensors);
     }
     const int lane = turns.lane;
     f2 w[N / 2], dw[N / 2], db[N / 2];
@@ -496,10 +504,10 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<kLanes>) norm_
     fetch_stat(turns.first());
     for (uint32_t base = turns.first(); base < turns.rows; base += turns.step) {
         const bool ok = turns.wait();
-        R x[D], dy[D], ds[D];
+        R x[D], dy[D], ds[kSum ? D : 1];
         turns.take(0, base, x);
         turns.take(1, base, dy);
-        if (p.dsum) turns.take(2, base, ds);
+        if constexpr (kSum) turns.take(2, base, ds);
         float mean[D], rstd[D], s[2 * D];
 #pragma unroll
         for (int d = 0; d < D; ++d) {
@@ -540,7 +548,7 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<kLanes>) norm_
                     const f2 n = mul2(add2(x[d].pair(i, j), both(-mean[d])), both(rstd[d]));
                     o[k] = fma2(n, b, fma2(dy[d].pair(i, j), w[k], a));
                 }
-            if (p.dsum) {
+            if constexpr (kSum) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -746,12 +754,12 @@ __global__ void __launch_bounds__(kColumnNT) norm_columns_kernel(NormParams p) {
 // Shared memory of an SM that its rings share, and of a CTA's ring at most.
 constexpr int kRingBytes = 200 * 1024;
 
-template <class T, Way kWay, int kLanes, int NV, bool kGrad>
+template <class T, Way kWay, int kLanes, int NV, bool kGrad, bool kSum>
 cudaError_t launch_as(NormParams& p, cudaStream_t s) {
     using G = Team<T, kWay, kLanes, NV>;
     const long long turns = (p.rows + (long long)G::kTeams * G::kRows - 1) / (G::kTeams * G::kRows);
-    const int resident = kGrad ? kGradResident<kLanes> : kResident<T, kWay, kLanes>;
-    const int tensors = kGrad ? (p.dsum ? 3 : 2) : p.residual ? 2 : 1;
+    const int resident = kGrad ? kGradResident<T, kWay, kLanes, NV, kSum> : kResident<T, kWay, kLanes>;
+    const int tensors = kGrad ? (kSum ? 3 : 2) : p.residual ? 2 : 1;
     int bytes = kGrad && G::kGroups > 1 ? (int)sizeof(float) * G::NT * G::N : 0;  // the columns' sums
     if (kWay == kRing) {
         const int stage = G::kTeams * tensors * G::kRows * (int)(p.channels * sizeof(T));
@@ -760,7 +768,7 @@ cudaError_t launch_as(NormParams& p, cudaStream_t s) {
     }
     p.parts = std::min(turns, seq_sms() * resident);
     const void* kernel;
-    if constexpr (kGrad) kernel = (const void*)norm_grad_kernel<T, kWay, kLanes, NV>;
+    if constexpr (kGrad) kernel = (const void*)norm_grad_kernel<T, kWay, kLanes, NV, kSum>;
     else kernel = (const void*)norm_kernel<T, kWay, kLanes, NV>;
     // the limit is one per device: always the largest, whatever this call needs
     if (bytes > kDefaultShared) {
@@ -772,14 +780,17 @@ cudaError_t launch_as(NormParams& p, cudaStream_t s) {
 }
 template <class T, Way kWay, int kLanes, int NV>
 cudaError_t go(NormParams& p, bool grad, cudaStream_t s) {
-    return grad ? launch_as<T, kWay, kLanes, NV, true>(p, s) : launch_as<T, kWay, kLanes, NV, false>(p, s);
+    if (!grad) return launch_as<T, kWay, kLanes, NV, false, false>(p, s);
+    return p.dsum ? launch_as<T, kWay, kLanes, NV, true, true>(p, s) : launch_as<T, kWay, kLanes, NV, true, false>(p, s);
 }
 
 // Through the ring where CTAs have several turns to take.
 template <class T, int kLanes, int NV>
 cudaError_t vectors(NormParams& p, bool grad, cudaStream_t s) {
     using G = Team<T, kVectors, kLanes, NV>;
-    const long long held = seq_sms() * (grad ? kGradResident<kLanes> : kResident<T, kVectors, kLanes>) * G::kTeams * G::kRows;
+    const int resident = !grad ? kResident<T, kVectors, kLanes>
+                         : p.dsum ? kGradResident<T, kVectors, kLanes, NV, true> : kGradResident<T, kVectors, kLanes, NV, false>;
+    const long long held = seq_sms() * resident * G::kTeams * G::kRows;
     if (p.rows <= held) return go<T, kVectors, kLanes, NV>(p, grad, s);
     return go<T, kRing, kLanes, NV>(p, grad, s);
 }
