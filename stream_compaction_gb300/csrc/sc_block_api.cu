@@ -26,7 +26,7 @@ sc_status gated_args(const sc_gated_desc* d, bool step, GatedParams* p) {
         return SC_ERR_INVALID;
     if (product(d->batch, std::max<int64_t>(d->length, 1), d->channels, 64) < 0) return SC_ERR_INVALID;
     // the smallest channel block, the largest cluster
-    const int64_t grid = product(d->batch, (d->channels + 31) / 32, 8);
+    const int64_t grid = product(d->batch, (d->channels + 31) / 32, 16);
     if (grid < 0 || grid > kMaxGrid) return SC_ERR_INVALID;
     if (d->batch > 0 && d->length > 0 && d->channels > 0) {
         const int64_t f = step ? 0 : 1;

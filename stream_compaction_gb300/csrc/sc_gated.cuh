@@ -42,7 +42,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kTokens = SC_GATED_SAVE;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;  // beyond 8 a launch has to ask for it
 
 // Tensor maps of a call: forward x, gate and y; backward x, gate, dy, dx and dgate.
 struct GatedMaps {
@@ -529,9 +529,11 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
 // --------------------------------------------------------------- gradient
 template <class T, int K> using BackwardRing = Ring<T, K, 3, 2>;
 
-// Warps, CTAs and rounds count from the end of the row.
+// Warps, CTAs and rounds count from the end of the row.  Three tensors in registers, two
+// channels a lane: 12 warps an SM (4 x 4096 tokens of 4094 bfloat16: 178 us; with one
+// channel a lane 221).
 template <class T, int K, bool kTma, bool kSigmoid, int kWarps, bool kCuts>
-__global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
+__global__ void __launch_bounds__(32 * kWarps, (kTma || K == 1 ? 16 : 12) / kWarps)
     gated_grad_kernel(GatedParams p, const __grid_constant__ GatedMaps maps) {
     using L = Lane<K>;
     using V = typename L::V;
@@ -775,24 +777,17 @@ bool maps_of(GatedMaps* m, const GatedParams& p, bool grad) {
            map_of<T, K>(&m->map[4], p.dgate, p, row, p.channels);
 }
 
-// The kernel of a call (forward with K = 2 in registers has no gradient beside it).
-template <class T, int K, bool kTma, bool kSigmoid, int kWarps, bool kCuts>
-const void* kernel_of(bool grad) {
-    if constexpr (kTma || K == 1) {
-        if (grad) return (const void*)gated_grad_kernel<T, K, kTma, kSigmoid, kWarps, kCuts>;
-    }
-    return (const void*)gated_kernel<T, K, kTma, kSigmoid, kWarps, kCuts>;
-}
-
 template <class T, int K, bool kTma, bool kSigmoid, int kWarps, bool kCuts>
 cudaError_t go(const GatedParams& p, const GatedMaps& maps, bool grad, long long groups, int ctas, cudaStream_t s) {
-    const void* kernel = kernel_of<T, K, kTma, kSigmoid, kWarps, kCuts>(grad);
+    const void* kernel = grad ? (const void*)gated_grad_kernel<T, K, kTma, kSigmoid, kWarps, kCuts>
+                              : (const void*)gated_kernel<T, K, kTma, kSigmoid, kWarps, kCuts>;
     auto bytes = [&](int n) {
         return (int)(grad ? Shared<K, kWarps, BackwardRing<T, K>, kTma>::bytes(n) : Shared<K, kWarps, ForwardRing<T, K>, kTma>::bytes(n));
     };
     // the limit is one per device: always the largest, whatever this call needs
     cudaError_t e = cudaSuccess;
     if (bytes(ctas) > kDefaultShared) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(kMaxCluster));
+    if (e == cudaSuccess && ctas > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(groups * ctas));
@@ -834,8 +829,7 @@ cudaError_t launch_gated_as(const GatedParams& p, bool grad, cudaStream_t s) {
     constexpr int K = 4 / (int)sizeof(T);  // 4 bytes a lane
     if (p.wide) return by_gate<T, K, true>(p, grad, s);
     if constexpr (K == 2) {
-        // (the gradient's three tensors in registers, with two channels a lane: 12 warps an SM)
-        if (p.pairs && !grad) return by_gate<T, 2, false>(p, grad, s);
+        if (p.pairs) return by_gate<T, 2, false>(p, grad, s);
     }
     return by_gate<T, 1, false>(p, grad, s);
 }
