@@ -733,8 +733,10 @@ __global__ void __launch_bounds__(kStepNT) gated_step_kernel(GatedParams p) {
 // The machine holds 16 warps an SM (128 registers a thread).  CTAs of 4 warps where the
 // rows and channels alone make enough of them (a round's fold is half as long, and they
 // fill the SMs more evenly), else of 8.  CTAs in a cluster: until there are 12 warps an
-// SM or the length has no more tiles; and while the last wave of CTAs is mostly empty,
-// up to 4.
+// SM or the length has no more tiles (16 of them only where all clusters are resident at
+// once, which takes as many SMs of one part of the chip each: 8192 tokens of 384 bfloat16
+// channels, 6 clusters, 20 us with 8 CTAs and 16 with 16; of 512, 8 clusters, 20 and 27);
+// and while the last wave of CTAs is mostly empty, up to 4.
 struct Split {
     int warps, ctas;
 };
@@ -745,7 +747,7 @@ inline Split split_of(long long groups, long long tiles) {
     auto more = [&] {
         if ((long long)s.ctas * s.warps >= tiles) return false;
         const long long n = groups * s.ctas;
-        if (n * s.warps < 12 * sms) return s.ctas < kMaxCluster;
+        if (n * s.warps < 12 * sms) return s.ctas < 8 || (s.ctas == 8 && groups * kMaxCluster * 3 <= sms * 2);
         return n > slots && s.ctas < 4 && n * 5 < (n + slots - 1) / slots * slots * 4;
     };
     while (more()) s.ctas *= 2;
@@ -807,9 +809,7 @@ cudaError_t go(const GatedParams& p, const GatedMaps& maps, bool grad, long long
 }
 
 template <class T, int K, bool kTma, bool kSigmoid>
-cudaError_t by_length(const GatedParams& p, bool grad, cudaStream_t s) {
-    GatedMaps maps{};
-    if (kTma && !maps_of<T, K>(&maps, p, grad)) return cudaErrorInvalidValue;
+cudaError_t by_length(const GatedParams& p, const GatedMaps& maps, bool grad, cudaStream_t s) {
     const long long tiles = (p.length + kTokens - 1) / kTokens, groups = p.batch * ((p.channels + 32 * K - 1) / (32 * K));
     const Split split = split_of(groups, tiles);
     if (split.warps == 4)
@@ -820,18 +820,19 @@ cudaError_t by_length(const GatedParams& p, bool grad, cudaStream_t s) {
 }
 
 template <class T, int K, bool kTma>
-cudaError_t by_gate(const GatedParams& p, bool grad, cudaStream_t s) {
-    return p.sigmoid ? by_length<T, K, kTma, true>(p, grad, s) : by_length<T, K, kTma, false>(p, grad, s);
+cudaError_t by_gate(const GatedParams& p, const GatedMaps& maps, bool grad, cudaStream_t s) {
+    return p.sigmoid ? by_length<T, K, kTma, true>(p, maps, grad, s) : by_length<T, K, kTma, false>(p, maps, grad, s);
 }
 
 template <class T>
 cudaError_t launch_gated_as(const GatedParams& p, bool grad, cudaStream_t s) {
     constexpr int K = 4 / (int)sizeof(T);  // 4 bytes a lane
-    if (p.wide) return by_gate<T, K, true>(p, grad, s);
+    GatedMaps maps{};
+    if (p.wide && maps_of<T, K>(&maps, p, grad)) return by_gate<T, K, true>(p, maps, grad, s);
     if constexpr (K == 2) {
-        if (p.pairs) return by_gate<T, 2, false>(p, grad, s);
+        if (p.pairs) return by_gate<T, 2, false>(p, maps, grad, s);
     }
-    return by_gate<T, 1, false>(p, grad, s);
+    return by_gate<T, 1, false>(p, maps, grad, s);
 }
 
 template <class T, int K>

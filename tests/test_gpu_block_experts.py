@@ -145,6 +145,29 @@ def test_slices(offset, dim, dtype):
     ref.check("dweights", a["weights"], r["dweights"])
 
 
+def test_more_than_2_31_elements():
+    """Offsets beyond 32 bits: the last tokens and rows."""
+    ids = _ids(70000, 8, 64, 0.1)[:, :8].cuda()
+    order = sc.expert_sort(ids, 64)
+    x = torch.randn(70000, 4096, dtype=torch.bfloat16, device="cuda")
+    rows = sc.expert_gather(x, order)
+    kept = int(order.offsets[-1])
+    at = torch.arange(kept - 500, kept, device="cuda")
+    assert torch.equal(rows[at], x[order.order[at].long() // 8]) and (rows[kept:] == 0).all()
+    w = torch.rand(70000, 8, device="cuda")
+    out, g = sc.expert_combine(rows, order, w), sc.expert_combine_grad(x, rows, order, w)
+    live = order.place[-500:] < kept
+    share = torch.where(live, w[-500:], 0.0)
+    # every row of a token is the token itself
+    r = x[-500:].double() * share.double().sum(1, keepdim=True)
+    assert ((out[-500:].double() - r).abs() <= (2 ** -8 + 16 * ref.EPS) * r.abs() + ref.TINY[x.dtype]).all()
+    entry = order.order[at].long()
+    want = (x[entry // 8].float() * w.flatten()[entry][:, None]).to(x.dtype)
+    assert torch.equal(g["y"][at], want)
+    square = (x[-500:].double() ** 2).sum(1, keepdim=True)
+    assert ((g["weights"][-500:] - torch.where(live, square, 0.0)).abs() <= 4098 * ref.EPS * square).all()
+
+
 def test_places_outside_are_passed_over():
     ids = _ids(20, 2, 5, 0)
     order, offsets, rows, place = _sorted(ids, 5)

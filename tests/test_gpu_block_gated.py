@@ -59,7 +59,7 @@ def _check(case, activation, got, dfinal=None):
 @pytest.mark.parametrize("packed", [False, True])
 @pytest.mark.parametrize("batch,length,channels", [
     (1, 1, 1), (2, 2, 64), (3, 15, 33), (1, 16, 32), (2, 17, 65), (1, 64, 31), (2, 65, 130), (1, 128, 2), (3, 129, 66),
-    (1, 300, 100), (2, 1025, 40), (1, 2500, 70)])
+    (1, 300, 100), (2, 1025, 40), (1, 2500, 70), (12, 1100, 40)])
 def test_forward_and_gradient(batch, length, channels, packed, activation, dtype):
     case = _case(batch, length, channels, dtype, activation, packed)
     dfinal = _normal(batch, channels, seed=9) if packed else None
@@ -94,6 +94,52 @@ def test_slices_of_a_joint_buffer(offset, channels, dtype):
     grads = sc.gated_scan_grad(dy, x, g, saved=saved)
     ref.check("dx", grads["x"], r["dx"])
     ref.check("dgate", grads["gate"], r["dgate"])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_layouts(dtype):
+    """Tokens before rows, rows with gaps between them, one row for all."""
+    case = _case(3, 70, 64, dtype)
+    r = ref.gated(case[0], case[1], dy=case[4])
+    gap = torch.zeros(3, 70 * 64 + 24, dtype=dtype, device="cuda")
+
+    def turned(t):
+        return t.transpose(0, 1).contiguous().transpose(0, 1)
+
+    def apart(t):
+        v = gap.clone()[:, :70 * 64].view(3, 70, 64)
+        v.copy_(t)
+        return v
+
+    for lay in (turned, apart):
+        x, g, dy = (lay(case[i].cuda()) for i in (0, 1, 4))
+        assert not x.is_contiguous()
+        out, saved = lay(torch.zeros_like(x)), sc.gated_scan_saved(x)
+        ref.check("y", sc.gated_scan(x, g, saved=saved, out=out), r["y"])
+        grads = sc.gated_scan_grad(dy, x, g, saved=saved)
+        ref.check("dx", grads["x"], r["dx"])
+        ref.check("dgate", grads["gate"], r["dgate"])
+    x, g = case[0][:1].cuda().expand(3, 70, 64), case[1][:1].cuda().expand(3, 70, 64)
+    ref.check("one row", sc.gated_scan(x, g), [v[:1].expand(3, 70, 64) for v in r["y"]])
+
+
+def test_more_than_2_31_elements():
+    """Offsets beyond 32 bits: the last channels of the last row as a call of their own has them."""
+    shape, dtype = (2, 270000, 4096), torch.bfloat16
+    x = torch.randn(shape, dtype=dtype, device="cuda")
+    g = torch.randn(shape, dtype=dtype, device="cuda")
+    saved = sc.gated_scan_saved(x)
+    y = sc.gated_scan(x, g, saved=saved)
+    part = [t[1:, :, -64:].contiguous() for t in (x, g, y)]
+    small = sc.gated_scan_saved(part[0])
+    want = sc.gated_scan(part[0], part[1], saved=small)
+    # other splits of the length: float32 differences far below bfloat16's steps, so neighbours at most
+    assert (part[2].float() - want.float()).abs().max() <= 2 ** -7 * want.abs().max()
+    grads = sc.gated_scan_grad(y, x, g, saved=saved)
+    want = sc.gated_scan_grad(part[2], part[0], part[1], saved=small)
+    for k in ("x", "gate"):
+        got = grads[k][1:, :, -64:].float()
+        assert (got - want[k].float()).abs().max() <= 2 ** -7 * want[k].abs().max(), k
 
 
 @pytest.mark.parametrize("activation", ["sigmoid", None])

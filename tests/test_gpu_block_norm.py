@@ -127,6 +127,19 @@ def test_slices_and_strides(offset, channels, dtype):
     assert all(torch.equal(a.reshape(3, 20, channels), b) for a, b in zip(got, flat))
 
 
+def test_more_than_2_31_elements():
+    """Offsets beyond 32 bits: the last rows as a call of their own has them, bit by bit."""
+    x = torch.randn(540000, 4096, dtype=torch.bfloat16, device="cuda")
+    w = torch.randn(4096, device="cuda")
+    saved, few = sc.layer_norm_saved(x), sc.layer_norm_saved(x[-1000:])
+    y, s = sc.layer_norm(x, w, residual=x, saved=saved)
+    y2, s2 = sc.layer_norm(x[-1000:], w, residual=x[-1000:], saved=few)
+    assert torch.equal(y[-1000:], y2) and torch.equal(s[-1000:], s2) and torch.equal(saved[-1000:], few)
+    del y
+    dx = sc.layer_norm_grad(x, s, w, saved=saved, dsum=x)["x"]
+    assert torch.equal(dx[-1000:], sc.layer_norm_grad(x[-1000:], s2, w, saved=few, dsum=x[-1000:])["x"])
+
+
 def test_strides_that_two_cannot_tell():
     x = torch.zeros(4, 5, 6, 8, device="cuda").transpose(0, 1).transpose(1, 2)
     with pytest.raises(ValueError, match="strides"):
