@@ -191,7 +191,10 @@ size_t sc_selective_scan_grad_workspace_bytes(int64_t batch, int64_t length, int
 sc_status sc_selective_scan_step(const sc_ssm_desc *p, float *pool, int64_t pool_rows, const int32_t *slots, void *y,
                                  int64_t y_batch, sc_stream_t stream);
 
-/* ---- gated recurrence: one gate and one state per channel ---- */
+/* ---- gated recurrence: one gate and one state per channel ----
+ * length < 2^30.  Decays of a run of tokens are multiplied before they meet a state, so
+ * with sigmoid == 0 they should be at most 1 in size: where a product of larger ones
+ * passes float32's range, the states behind it are infinite or NaN. */
 typedef struct {
     int32_t dtype;             /* sc_dtype of x, gate, y and their gradients */
     int32_t sigmoid;           /* 0: the gate is the decay itself and x enters as it is */

@@ -5,26 +5,30 @@
 //   dh[t] = dy[t] + f[t+1] dh[t+1];  dx = dh (1 - f);  dgate = dh (h[t-1] - x) f (1 - f)
 //
 // Three elements moved forward and five backward for some ten operations each: bytes
-// bound it, if the length is split.  A tile of kTokens tokens by 32 or 64 channels
-// lies in a warp's registers, a lane's channels side by side with all their tokens, so
-// the recurrence needs no exchange inside a tile.  The warps of a CTA take consecutive
-// tiles of the same channels, and the CTAs of a cluster consecutive runs of them; a
-// round of kWarps x cluster tiles goes like a scan:
+// bound it, if the length is split.  A warp takes a tile of kTokens tokens by 32 or 64
+// channels, a lane's channels side by side with all their tokens, so the recurrence
+// needs no exchange inside a tile.  The warps of a CTA take consecutive tiles of the same
+// channels, and the CTAs of a cluster consecutive runs of them; a round of kWarps x
+// cluster tiles goes like a scan:
 //
 //   each warp   its tile's map h -> A h + B (A the product of f, B the recurrence from 0);
 //   the CTA     the maps meet in shared memory; the CTA's own map goes to every CTA of
-//               the cluster (distributed shared memory, one cluster barrier a round);
+//               the cluster (distributed shared memory, writes that are counted there);
 //   each warp   the state before its tile: the carry, through the maps before it in order;
 //               then the recurrence again, on registers, and the results.
 //
 // So every element is read once and written once, no scratch memory is needed, and the
-// order of all roundings is fixed.  The next round's elements are loaded into registers
-// before the exchange and arrive during it.
+// order of all roundings is fixed.  Tiles come and results go by the copy engine, one
+// instruction each, one or two rounds ahead in shared memory; rows that are not aligned
+// to 16 bytes are loaded a round ahead into registers.
 //
 // The gradient runs the same rounds backwards on q[t] = f[t] dh[t], with the states
 // recomputed from those that the forward pass saved (one in kTokens: 1/16 of an
 // element's place in float32, where keeping h itself would cost an element read and
 // rounding errors of 16 bits in dgate).
+//
+// 8 x 4096 tokens of 4096 bfloat16: forward 137 to 147 us (5.5 to 5.9 TB/s, a copy 6.5),
+// gradient 229 to 245 (5.5 to 5.9); rows that are not aligned 3.0 to 5.3 TB/s.
 #pragma once
 #include <algorithm>
 
@@ -59,6 +63,7 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int c, int 
                  ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(t), "r"(b), "r"(src)
                  : "memory");
 }
+
 // A lane's K channels of a token: as they lie in memory, and as one operand.
 template <class T, int K> struct Raw { using type = unsigned short; };
 template <> struct Raw<float, 1> { using type = float; };
