@@ -104,12 +104,14 @@ Tensor norm_parameter(const sc_norm_desc* d, const void* p) { return flat(p, d->
 // Rows by vectors where every tensor has aligned rows; one index where all have one stride.
 template <int N>
 void norm_rows(const sc_norm_desc* d, const Tensor (&t)[N], NormParams* p) {
-    const int e = 16 / bytes_of(d->dtype);
+    const int e = 16 / bytes_of(d->dtype), pair = 4 / bytes_of(d->dtype);
     bool one = true, dense = true;
     p->vec = d->channels % e == 0;
+    p->pairs = d->channels % pair == 0;
     for (const Tensor& v : t) {
         if (!v.p) continue;
         p->vec = p->vec && v.vec(e);
+        p->pairs = p->pairs && v.vec(pair);
         one = one && one_stride(v);
         dense = dense && (v.tokens > 1 ? v.st : v.sb) == v.channels;
     }

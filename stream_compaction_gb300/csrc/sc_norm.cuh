@@ -17,7 +17,8 @@
 // tokens) in registers.  A team, the threads of a wide row or a warp with several
 // narrow ones, has a ring of rows in shared memory that bulk copies fill some turns
 // ahead; rows that are not aligned to 16 bytes, and calls of one turn, are loaded into
-// registers, the next row's while this one is worked on.
+// registers, the next row's while this one is worked on.  (Unaligned rows through the
+// ring, their ends by themselves: 17367 rows of 636 bfloat16 43 us forward, 23 so.)
 //
 // The gradient's sums over tokens: a CTA's columns' sums over all its rows become one row
 // of partial sums, and a second kernel adds those in the order of the CTAs: the same bits
@@ -44,28 +45,41 @@ __device__ __forceinline__ long long at(uint32_t row, uint32_t length, long long
     return (long long)b * sb + (long long)(row - b * length) * st;
 }
 
-// Element j of vector i of a lane: aligned rows by vectors, others by elements.
-template <class T, bool kVec, int kLanes>
+// How rows come: by the widest accesses that all of them are aligned to, single 16-bit
+// elements, 4 bytes, or vectors of 16; or by vectors through the ring.
+enum Way { kElements, kUnits, kVectors, kRing };
+template <Way kWay> constexpr bool kByVectors = kWay == kVectors || kWay == kRing;
+template <class T, Way kWay> constexpr int kAccess = kByVectors<kWay> ? kWidth<T> : kWay == kUnits ? 4 / (int)sizeof(T) : 1;  // elements
+
+// Element j of vector i of a lane: the lanes' accesses lie side by side.
+template <class T, Way kWay, int kLanes>
 __device__ __forceinline__ int column(int i, int j, int lane) {
-    return kVec ? (i * kLanes + lane) * kWidth<T> + j : (i * kWidth<T> + j) * kLanes + lane;
+    constexpr int A = kAccess<T, kWay>;
+    return ((i * (kWidth<T> / A) + j / A) * kLanes + lane) * A + j % A;
 }
 
-template <class T, bool kVec, int kLanes, int NV>
+template <class T, Way kWay, int kLanes, int NV>
 struct Row {
-    static constexpr int W = kWidth<T>;
+    static constexpr int W = kWidth<T>, A = kAccess<T, kWay>;
     Vec<T, W> v[NV];
     __device__ __forceinline__ void load(const T* p, int lane, int channels) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if constexpr (kVec) {
-                const int c = column<T, kVec, kLanes>(i, 0, lane);
+            if constexpr (kByVectors<kWay>) {
+                const int c = column<T, kWay, kLanes>(i, 0, lane);
                 if (c < channels) v[i].load(p + c);
                 else v[i].zero();
+            } else if constexpr (kWay == kUnits) {
+#pragma unroll
+                for (int j = 0; j < W; j += A) {
+                    const int c = column<T, kWay, kLanes>(i, j, lane);
+                    v[i].w[j / A] = c < channels ? __ldg(reinterpret_cast<const uint32_t*>(p + c)) : 0u;
+                }
             } else {
                 T e[W];
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
-                    const int c = column<T, kVec, kLanes>(i, j, lane);
+                    const int c = column<T, kWay, kLanes>(i, j, lane);
                     e[j] = c < channels ? __ldg(p + c) : from_f32<T>(0.0f);
                 }
                 memcpy(v[i].w, e, 16);
@@ -75,7 +89,7 @@ struct Row {
     __device__ __forceinline__ void load_shared(const unsigned char* row, int lane, int channels) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = column<T, true, kLanes>(i, 0, lane);
+            const int c = column<T, kRing, kLanes>(i, 0, lane);
             if (c < channels) v[i].load_rw(reinterpret_cast<const T*>(row) + c);
             else v[i].zero();
         }
@@ -87,23 +101,24 @@ struct Row {
     __device__ __forceinline__ static void store(T* p, int lane, int channels, f2 (&f)[NV * W / 2]) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if constexpr (kVec) {
-                const int c = column<T, kVec, kLanes>(i, 0, lane);
-                Vec<T, W> o;
+            Vec<T, W> o;
 #pragma unroll
-                for (int j = 0; j < W / 2; ++j) set_pair(o, j, f[i * W / 2 + j]);
-                if (kRounded)
+            for (int j = 0; j < W / 2; ++j) set_pair(o, j, f[i * W / 2 + j]);
+            if (kRounded)
 #pragma unroll
-                    for (int j = 0; j < W / 2; ++j) f[i * W / 2 + j] = o.pair(j);
+                for (int j = 0; j < W / 2; ++j) f[i * W / 2 + j] = o.pair(j);
+            if constexpr (kByVectors<kWay>) {
+                const int c = column<T, kWay, kLanes>(i, 0, lane);
                 if (c < channels) o.store(p + c);
             } else {
+                T e[W];
+                memcpy(e, o.w, 16);
 #pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    const int c = column<T, kVec, kLanes>(i, j, lane);
-                    f2& v = f[(i * W + j) / 2];
-                    const T e = from_f32<T>(j % 2 ? hi2(v) : lo2(v));
-                    if (kRounded) v = j % 2 ? pack2(lo2(v), to_f32(e)) : pack2(to_f32(e), hi2(v));
-                    if (c < channels) p[c] = e;
+                for (int j = 0; j < W; j += A) {
+                    const int c = column<T, kWay, kLanes>(i, j, lane);
+                    if (c >= channels) continue;
+                    if constexpr (kWay == kUnits) *reinterpret_cast<uint32_t*>(p + c) = o.w[j / A];
+                    else p[c] = e[j];
                 }
             }
         }
@@ -176,9 +191,6 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* slot, int lane, in
 
 template <int kLanes> constexpr int kThreads = kLanes < 256 ? 256 : kLanes;
 
-// How rows come: element by element, by vectors, or by vectors through the ring.
-enum Way { kElements, kVectors, kRing };
-
 // A team: the threads of a row, or a warp with kSide rows side by side, and two of them
 // one behind the other where they are short (four: 262144 rows of 128 16-bit channels 31 us
 // forward, 29 so, and the gradient spills).
@@ -245,7 +257,7 @@ struct RowRing {
 template <class T, Way kWay, int kLanes, int NV, int kTensors>
 struct Turns {
     using G = Team<T, kWay, kLanes, NV>;
-    using R = Row<T, kWay != kElements, kLanes, NV>;
+    using R = Row<T, kWay, kLanes, NV>;
     RowRing<T, kTensors, G::kRows> ring;
     R next[kWay == kRing ? 1 : kTensors][kWay == kRing ? 1 : G::kDeep];
     uint32_t rows, step, ahead;  // below 2^31; a turn behind the last stays below 2^32
@@ -329,15 +341,17 @@ struct Turns {
 };
 
 // ---------------------------------------------------------------- forward
-// CTAs that an SM holds: 65536 registers by 80 a thread, 128 with rows in registers.
-template <class T, Way kWay, int kLanes> constexpr int kResident = kThreads<kLanes> == 256 ? (kWay == kRing || sizeof(T) == 4 ? 3 : 2) : 1;
+// Threads that an SM's 65536 registers hold, 80 a thread through the ring, 128 with 16
+// elements of a row and of the next, 64 with 8; and CTAs of them.
+template <class T, Way kWay> constexpr int kHeld = kWay == kRing ? 768 : kWay == kVectors && sizeof(T) == 2 ? 512 : 1024;
+template <class T, Way kWay, int kLanes>
+constexpr int kResident = kHeld<T, kWay> > kThreads<kLanes> ? kHeld<T, kWay> / kThreads<kLanes> : 1;
 
 template <class T, Way kWay, int kLanes, int NV>
 __global__ void __launch_bounds__(kThreads<kLanes>, kResident<T, kWay, kLanes>) norm_kernel(NormParams p) {
     using G = Team<T, kWay, kLanes, NV>;
-    using R = Row<T, kWay != kElements, kLanes, NV>;
+    using R = Row<T, kWay, kLanes, NV>;
     constexpr int W = G::W, N = G::N, D = G::kDeep;
-    constexpr bool kVec = kWay != kElements;
     __shared__ __align__(16) float s_sum[G::kGroups][2][2][kLanes > 32 ? kLanes / 32 : 1];
     extern __shared__ __align__(128) unsigned char s_mem[];
     const int group = threadIdx.x / kLanes, channels = (int)p.channels;
@@ -356,7 +370,7 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kResident<T, kWay, kLanes>) 
             float v[2][2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int c = column<T, kVec, kLanes>(i, j + h, lane);
+                const int c = column<T, kWay, kLanes>(i, j + h, lane);
                 v[0][h] = c < channels && p.weight ? parameter<T>(p.weight, p.params_f32, c) : 1.0f;
                 v[1][h] = c < channels && p.bias ? parameter<T>(p.bias, p.params_f32, c) : 0.0f;
             }
@@ -418,9 +432,9 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kResident<T, kWay, kLanes>) 
 #pragma unroll
                         for (int j = 0; j < W / 2; ++j) {
                             f2& v = f[d][i * W / 2 + j];
-                            if (kVec) v = column<T, kVec, kLanes>(i, 0, lane) < channels ? v : 0ull;
-                            else v = pack2(column<T, kVec, kLanes>(i, 2 * j, lane) < channels ? lo2(v) : 0.0f,
-                                           column<T, kVec, kLanes>(i, 2 * j + 1, lane) < channels ? hi2(v) : 0.0f);
+                            if (kAccess<T, kWay> > 1) v = column<T, kWay, kLanes>(i, 2 * j, lane) < channels ? v : 0ull;
+                            else v = pack2(column<T, kWay, kLanes>(i, 2 * j, lane) < channels ? lo2(v) : 0.0f,
+                                           column<T, kWay, kLanes>(i, 2 * j + 1, lane) < channels ? hi2(v) : 0.0f);
                         }
             }
         }
@@ -458,9 +472,8 @@ constexpr int kGradResident = kThreads<kLanes> > 256 ? 1 : kWidth<T> * NV == 8 &
 template <class T, Way kWay, int kLanes, int NV, bool kSum>
 __global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<T, kWay, kLanes, NV, kSum>) norm_grad_kernel(NormParams p) {
     using G = Team<T, kWay, kLanes, NV>;
-    using R = Row<T, kWay != kElements, kLanes, NV>;
+    using R = Row<T, kWay, kLanes, NV>;
     constexpr int W = G::W, N = G::N, D = G::kDeep, NT = G::NT, kGroups = G::kGroups;
-    constexpr bool kVec = kWay != kElements;
     __shared__ __align__(16) float s_sum[kGroups][2][2 * D * (kLanes > 32 ? kLanes / 32 : 1)];
     extern __shared__ __align__(128) unsigned char s_mem[];
     const int group = threadIdx.x / kLanes, channels = (int)p.channels;
@@ -485,7 +498,7 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<T, kWay, kLane
             float v[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int c = column<T, kVec, kLanes>(i, j + h, lane);
+                const int c = column<T, kWay, kLanes>(i, j + h, lane);
                 v[h] = c >= channels ? 0.0f : p.weight ? parameter<T>(p.weight, p.params_f32, c) : 1.0f;
             }
             w[(i * W + j) / 2] = pack2(v[0], v[1]);
@@ -574,7 +587,7 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<T, kWay, kLane
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
-                    const int c = column<T, kVec, kLanes>(i, j, lane);
+                    const int c = column<T, kWay, kLanes>(i, j, lane);
                     if (c < channels) to[c] = element(i * W + j);
                 }
         } else {
@@ -582,7 +595,7 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<T, kWay, kLane
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < W; ++j) s_col[group * (kLanes * N) + column<T, kVec, kLanes>(i, j, lane)] = element(i * W + j);
+                for (int j = 0; j < W; ++j) s_col[group * (kLanes * N) + column<T, kWay, kLanes>(i, j, lane)] = element(i * W + j);
             __syncthreads();
             for (int c = threadIdx.x; c < channels; c += NT) {
                 float sum = 0.0f;
@@ -795,22 +808,30 @@ cudaError_t vectors(NormParams& p, bool grad, cudaStream_t s) {
     return go<T, kRing, kLanes, NV>(p, grad, s);
 }
 
+// Rows that are not aligned to 16 bytes; 16-bit elements 8 a thread (with 16 the gradient's
+// rows do not fit the registers).
+template <class T, Way kWay>
+cudaError_t narrow(NormParams& p, long long n, bool grad, cudaStream_t s) {
+    if constexpr (sizeof(T) == 4 && kWay == kElements) {
+        return cudaErrorInvalidValue;
+    } else {
+        constexpr int NV = sizeof(T) == 4 ? 2 : 1;
+        if (n <= 8) return go<T, kWay, 8, 1>(p, grad, s);
+        if (n <= 16) return go<T, kWay, 16, 1>(p, grad, s);
+        if (n <= 32) return go<T, kWay, 32, 1>(p, grad, s);
+        if (n <= 32 * NV) return go<T, kWay, 32, NV>(p, grad, s);
+        if (n <= 64 * NV) return go<T, kWay, 64, NV>(p, grad, s);
+        if (n <= 128 * NV) return go<T, kWay, 128, NV>(p, grad, s);
+        if (n <= 256 * NV) return go<T, kWay, 256, NV>(p, grad, s);
+        if (n <= 512 * NV) return go<T, kWay, 512, NV>(p, grad, s);
+        return go<T, kWay, 1024, NV>(p, grad, s);
+    }
+}
+
 template <class T>
 cudaError_t by_width(NormParams& p, bool grad, cudaStream_t s) {
     const long long n = (p.channels + kWidth<T> - 1) / kWidth<T>;
-    if (!p.vec) {
-        // 16-bit elements one by one: 8 a thread (with 16 the gradient's rows do not fit the registers)
-        constexpr int NV = sizeof(T) == 4 ? 2 : 1;
-        if (n <= 8) return go<T, kElements, 8, 1>(p, grad, s);
-        if (n <= 16) return go<T, kElements, 16, 1>(p, grad, s);
-        if (n <= 32) return go<T, kElements, 32, 1>(p, grad, s);
-        if (n <= 32 * NV) return go<T, kElements, 32, NV>(p, grad, s);
-        if (n <= 64 * NV) return go<T, kElements, 64, NV>(p, grad, s);
-        if (n <= 128 * NV) return go<T, kElements, 128, NV>(p, grad, s);
-        if (n <= 256 * NV) return go<T, kElements, 256, NV>(p, grad, s);
-        if (n <= 512 * NV) return go<T, kElements, 512, NV>(p, grad, s);
-        return go<T, kElements, 1024, NV>(p, grad, s);
-    }
+    if (!p.vec) return sizeof(T) == 4 || p.pairs ? narrow<T, kUnits>(p, n, grad, s) : narrow<T, kElements>(p, n, grad, s);
     if (n <= 8) return vectors<T, 8, 1>(p, grad, s);
     if (n <= 16) return vectors<T, 16, 1>(p, grad, s);
     if (n <= 32) return vectors<T, 32, 1>(p, grad, s);

@@ -155,7 +155,7 @@ cudaError_t launch_gated_step(int dtype, const GatedParams& p, cudaStream_t s);
 
 // ---------------------------------------------------------------- norm
 struct NormParams {
-    int rms, params_f32, vec, dense, stages;  // dense: all rows follow one another
+    int rms, params_f32, vec, pairs, dense, stages;  // rows aligned to 16 bytes, to 4; dense: all follow one another
     float eps;
     uint32_t rows, length;  // rows = batch * length
     long long channels;
