@@ -65,8 +65,10 @@
  * *_workspace_bytes are for the current device); such a call
  * on a capturing stream returns SC_ERR_UNSUPPORTED.  The others may be
  * captured: sc_embed, sc_causal_conv, the steps, sc_layer_norm, sc_gated_scan and
- * its gradient, every sc_expert_* call, and any call whose *_workspace_bytes is 0.  Empty problems (no tokens, no rows, no channels)
- * succeed; sums over no tokens are zeros.
+ * its gradient, every sc_expert_* call, and any call whose *_workspace_bytes is 0.
+ * Empty problems (no tokens, no rows, no channels) succeed; sums over no tokens are
+ * zeros.  Waits inside kernels are bounded: one that should run out makes NaN of the
+ * rows that it was for.
  */
 #ifndef SC_SEQ_H
 #define SC_SEQ_H
@@ -254,7 +256,7 @@ sc_status sc_layer_norm(const sc_norm_desc *p, void *y, int64_t y_batch, int64_t
 sc_status sc_layer_norm_grad(const sc_norm_desc *p, const void *dy, int64_t dy_batch, int64_t dy_token,
                              const void *dsum, int64_t dsum_batch, int64_t dsum_token, const float *saved, void *dx,
                              float *dweight, float *dbias, sc_stream_t stream);
-/* Without dweight and dbias the call needs none. */
+/* Without dweight and dbias the call needs none, and may be captured. */
 size_t sc_layer_norm_grad_workspace_bytes(int64_t batch, int64_t length, int64_t channels, sc_dtype dtype);
 
 /* ---- tokens to their experts and back ---- */

@@ -8,7 +8,10 @@ namespace {
 
 using namespace scg;
 
-sc_status types(int dtype) { return dtype < 0 || dtype > SC_BF16 ? SC_ERR_INVALID : bytes_of(dtype) ? SC_OK : SC_ERR_UNSUPPORTED; }
+sc_status types(int dtype) {
+    if (dtype < 0 || dtype > SC_BF16) return SC_ERR_INVALID;
+    return bytes_of(dtype) ? SC_OK : SC_ERR_UNSUPPORTED;
+}
 sc_status types(int dtype, int wtype) {
     const sc_status st = types(dtype);
     if (st != SC_OK) return st;
@@ -64,7 +67,8 @@ bool gated_wide(const sc_gated_desc* d, std::initializer_list<Tensor> all) {
     if (d->channels % e != 0 || d->channels > kMaxGrid || d->batch > kMaxGrid) return false;
     for (const Tensor& t : all) {
         const int64_t most = (((int64_t)1 << 40) - 1) / eb;
-        if (!t.vec(e) || (t.tokens > 1 && (t.st == 0 || t.st > most)) || (t.batch > 1 && (t.sb == 0 || t.sb > most))) return false;
+        if (!t.vec(e)) return false;
+        if ((t.tokens > 1 && (t.st == 0 || t.st > most)) || (t.batch > 1 && (t.sb == 0 || t.sb > most))) return false;
     }
     return true;
 }

@@ -173,7 +173,8 @@ template <class T, int kBytes, int kAhead_>
 struct Part {
     static constexpr int W = kBytes / (int)sizeof(T), kAhead = kAhead_;
     static constexpr int kColumns = (kBytes == 16 ? 4 : 16) / kAhead;
-    using U = typename std::conditional<kBytes == 16, uint4, typename std::conditional<kBytes == 4, uint32_t, unsigned short>::type>::type;
+    using Narrow = typename std::conditional<kBytes == 4, uint32_t, unsigned short>::type;
+    using U = typename std::conditional<kBytes == 16, uint4, Narrow>::type;
     U v;
     __device__ __forceinline__ void load(const T* p) { v = __ldg(reinterpret_cast<const U*>(p)); }
     __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<U*>(p) = v; }
@@ -221,7 +222,8 @@ __device__ __forceinline__ long long kept_of(const ExpertParams& p) {
 template <class T>
 __device__ __forceinline__ float weight_of(const ExpertParams& p, long long entry) {
     if (!p.weights) return 1.0f;
-    return p.weights_f32 ? __ldg(static_cast<const float*>(p.weights) + entry) : to_f32(__ldg(static_cast<const T*>(p.weights) + entry));
+    return p.weights_f32 ? __ldg(static_cast<const float*>(p.weights) + entry)
+                         : to_f32(__ldg(static_cast<const T*>(p.weights) + entry));
 }
 // The row of an entry; -1: passed over.
 __device__ __forceinline__ long long row_of(const ExpertParams& p, long long entry) {
@@ -434,7 +436,8 @@ struct TeamRing {
         if (lane == 0) mbar_arrive_expect_tx(full, copies * row_bytes);
         const uint32_t to = smem_u32(rows(fill));
         const T* from = static_cast<const T*>(kGrad ? p.rows : p.in);
-        if (live) bulk_load(to + (lane + (kGrad ? 1 : 0)) * row_bytes, from + row * (kGrad ? p.ld_rows : p.ld_in), row_bytes, full);
+        if (live)
+            bulk_load(to + (lane + (kGrad ? 1 : 0)) * row_bytes, from + row * (kGrad ? p.ld_rows : p.ld_in), row_bytes, full);
         if (kGrad && lane == 0) bulk_load(to, static_cast<const T*>(p.in) + token * p.ld_in, row_bytes, full);
         if (++fill == stages) fill = 0;
     }
@@ -622,7 +625,8 @@ cudaError_t rows_of(int what, const ExpertParams& p, cudaStream_t s) {
     return rows_as<T, 4>(what, p, s);
 }
 cudaError_t rows(int dtype, int what, const ExpertParams& p, cudaStream_t s) {
-    return dtype == SC_F32 ? rows_of<float>(what, p, s) : dtype == SC_F16 ? rows_of<f16>(what, p, s) : rows_of<bf16>(what, p, s);
+    return dtype == SC_F32 ? rows_of<float>(what, p, s) : dtype == SC_F16 ? rows_of<f16>(what, p, s)
+                                                                         : rows_of<bf16>(what, p, s);
 }
 
 }  // namespace
@@ -634,7 +638,8 @@ cudaError_t launch_expert_sort(const void* ids, int ids64, long long entries, in
     int ctas = 1;
     while (ctas < kSortMaxCtas && (long long)ctas * kSortMaxWarps < least) ctas *= 2;
     // (a thread has two bins at most where a CTA can have as many threads)
-    const int warps = (int)std::clamp<long long>(std::max<long long>((least + ctas - 1) / ctas, experts / 64 + 1), 1, kSortMaxWarps);
+    const long long wanted = std::max<long long>((least + ctas - 1) / ctas, experts / 64 + 1);
+    const int warps = (int)std::min<long long>(wanted, kSortMaxWarps);
     SortParams p{ids, ids64, experts, 0, entries, 0, order, place, offsets};
     while (experts + 1 >> p.bits) ++p.bits;
     p.run = ((entries + (long long)ctas * warps - 1) / ((long long)ctas * warps) + 31) / 32 * 32;
@@ -644,7 +649,8 @@ cudaError_t launch_expert_sort(const void* ids, int ids64, long long entries, in
     if (bytes > kDefaultShared - 8 * 1024)
         e = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kSortMaxWarps * kMaxBins * (int)sizeof(uint32_t));
-    if (e == cudaSuccess && ctas > 8) e = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && ctas > 8)
+        e = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)ctas);

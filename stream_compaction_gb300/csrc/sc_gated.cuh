@@ -183,7 +183,8 @@ struct Held : Elements<T, K> {
             for (int j = 0; j < kTokens; ++j) r[j] = __ldg(reinterpret_cast<const R*>(p + j * stride));
         } else {
 #pragma unroll
-            for (int j = 0; j < kTokens; ++j) r[j] = live && j < left ? __ldg(reinterpret_cast<const R*>(p + j * stride)) : R(0);
+            for (int j = 0; j < kTokens; ++j)
+                r[j] = live && j < left ? __ldg(reinterpret_cast<const R*>(p + j * stride)) : R(0);
         }
         p += advance;
     }
@@ -258,7 +259,8 @@ __device__ __forceinline__ void send(uint32_t to, uint32_t bar, const Map<2>& m)
                  ::"r"(to), "l"(m.A), "l"(m.B), "r"(bar) : "memory");
 }
 __device__ __forceinline__ void send(uint32_t to, uint32_t bar, int v) {
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(to), "r"(v), "r"(bar) : "memory");
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];"
+                 ::"r"(to), "r"(v), "r"(bar) : "memory");
 }
 __device__ __forceinline__ bool arrived_from_cluster(uint32_t bar, uint32_t parity) {
     for (int i = 0; i < (1 << 20); ++i) {
@@ -377,7 +379,8 @@ struct Ring {
     static constexpr int kRound = kTensors * Tl::kBytes, kBytes = kStages * kRound;
     unsigned char *base, *fill, *take;
     uint32_t bar, phase = 0;  // the stages' barriers, the parity of the round to take
-    __device__ __forceinline__ Ring(unsigned char* mem, uint64_t* bars, int lane) : base(mem), fill(mem), take(mem), bar(smem_u32(bars)) {
+    __device__ __forceinline__ Ring(unsigned char* mem, uint64_t* bars, int lane)
+        : base(mem), fill(mem), take(mem), bar(smem_u32(bars)) {
         if (bars && lane == 0) {
 #pragma unroll
             for (int i = 0; i < kStages; ++i) mbar_init(bar + 8 * i, 1);
@@ -438,7 +441,8 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
     const int step = c.ranks * kWarps;
     int tile = c.rank * kWarps + c.warp;
     ForwardRing<T, K> ring(s.ring[kTma ? c.warp : 0], kTma ? s.bars[c.warp] : nullptr, c.lane);
-    Held<T, K> x(p.x, c.b * p.x_batch, p.x_token, tile, step, c.ch), g(p.gate, c.b * p.gate_batch, p.gate_token, tile, step, c.ch);
+    Held<T, K> x(p.x, c.b * p.x_batch, p.x_token, tile, step, c.ch);
+    Held<T, K> g(p.gate, c.b * p.gate_batch, p.gate_token, tile, step, c.ch);
     T* y = static_cast<T*>(p.y) + c.b * p.y_batch + (long long)tile * kTokens * p.y_token + c.ch;
     float* saved = p.saved ? p.saved + (c.b * c.tiles + tile) * p.channels + c.ch : nullptr;
     int left = (int)p.length - tile * kTokens, left_ahead = left;  // tokens from a tile's start to the row's end
@@ -549,8 +553,9 @@ __global__ void __launch_bounds__(32 * kWarps, (kTma || K == 1 ? 16 : 12) / kWar
     const int step = c.ranks * kWarps;
     int tile = c.tiles - 1 - (c.rank * kWarps + c.warp);
     BackwardRing<T, K> ring(s.ring[kTma ? c.warp : 0], kTma ? s.bars[c.warp] : nullptr, c.lane);
-    Held<T, K> x(p.x, c.b * p.x_batch, p.x_token, tile, -step, c.ch), g(p.gate, c.b * p.gate_batch, p.gate_token, tile, -step, c.ch),
-        dy(p.dy, c.b * p.dy_batch, p.dy_token, tile, -step, c.ch);
+    Held<T, K> x(p.x, c.b * p.x_batch, p.x_token, tile, -step, c.ch);
+    Held<T, K> g(p.gate, c.b * p.gate_batch, p.gate_token, tile, -step, c.ch);
+    Held<T, K> dy(p.dy, c.b * p.dy_batch, p.dy_token, tile, -step, c.ch);
     const long long to = (c.b * p.length + (long long)tile * kTokens) * p.channels + c.ch;
     T *dx = static_cast<T*>(p.dx) + to, *dg = static_cast<T*>(p.dgate) + to;
     // a warp's first tile ends with the row, those before the row's first are none
@@ -584,7 +589,8 @@ __global__ void __launch_bounds__(32 * kWarps, (kTma || K == 1 ? 16 : 12) / kWar
     for (int round = 0; round < c.rounds; ++round) {
         if (kTma) fetch();
         const bool ok = !kTma || tile < 0 || ring.wait();
-        const auto xr = tile_of<kTma>(ring, x, 0, c.lane), gr = tile_of<kTma>(ring, g, 1, c.lane), d = tile_of<kTma>(ring, dy, 2, c.lane);
+        const auto xr = tile_of<kTma>(ring, x, 0, c.lane), gr = tile_of<kTma>(ring, g, 1, c.lane);
+        const auto d = tile_of<kTma>(ring, dy, 2, c.lane);
         // u: what dh is multiplied with for dgate; w: for dx (sigmoid), or f itself
         f2 u[kPairs<K>], w[kPairs<K>];
         const uint32_t cut = kCuts ? cuts_of(head) : 0u;
@@ -772,11 +778,13 @@ bool map_of(CUtensorMap* m, const void* base, const GatedParams& p, long long ba
     const cuuint32_t box[3] = {32 * K, kTokens, 1}, each[3] = {1, 1, 1};
     const CUtensorMapDataType type = sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
     return enc(m, type, 3, const_cast<void*>(base), dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 template <class T, int K>
 bool maps_of(GatedMaps* m, const GatedParams& p, bool grad) {
-    if (!map_of<T, K>(&m->map[0], p.x, p, p.x_batch, p.x_token) || !map_of<T, K>(&m->map[1], p.gate, p, p.gate_batch, p.gate_token))
+    if (!map_of<T, K>(&m->map[0], p.x, p, p.x_batch, p.x_token) ||
+        !map_of<T, K>(&m->map[1], p.gate, p, p.gate_batch, p.gate_token))
         return false;
     if (!grad) return map_of<T, K>(&m->map[2], p.y, p, p.y_batch, p.y_token);
     const long long row = p.length * p.channels;
@@ -789,12 +797,15 @@ cudaError_t go(const GatedParams& p, const GatedMaps& maps, bool grad, long long
     const void* kernel = grad ? (const void*)gated_grad_kernel<T, K, kTma, kSigmoid, kWarps, kCuts>
                               : (const void*)gated_kernel<T, K, kTma, kSigmoid, kWarps, kCuts>;
     auto bytes = [&](int n) {
-        return (int)(grad ? Shared<K, kWarps, BackwardRing<T, K>, kTma>::bytes(n) : Shared<K, kWarps, ForwardRing<T, K>, kTma>::bytes(n));
+        return (int)(grad ? Shared<K, kWarps, BackwardRing<T, K>, kTma>::bytes(n)
+                          : Shared<K, kWarps, ForwardRing<T, K>, kTma>::bytes(n));
     };
     // the limit is one per device: always the largest, whatever this call needs
     cudaError_t e = cudaSuccess;
-    if (bytes(ctas) > kDefaultShared) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(kMaxCluster));
-    if (e == cudaSuccess && ctas > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (bytes(ctas) > kDefaultShared)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(kMaxCluster));
+    if (e == cudaSuccess && ctas > 8)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(groups * ctas));

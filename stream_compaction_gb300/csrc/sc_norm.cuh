@@ -49,7 +49,8 @@ __device__ __forceinline__ long long at(uint32_t row, uint32_t length, long long
 // elements, 4 bytes, or vectors of 16; or by vectors through the ring.
 enum Way { kElements, kUnits, kVectors, kRing };
 template <Way kWay> constexpr bool kByVectors = kWay == kVectors || kWay == kRing;
-template <class T, Way kWay> constexpr int kAccess = kByVectors<kWay> ? kWidth<T> : kWay == kUnits ? 4 / (int)sizeof(T) : 1;  // elements
+template <class T, Way kWay>  // elements of an access
+constexpr int kAccess = kByVectors<kWay> ? kWidth<T> : kWay == kUnits ? 4 / (int)sizeof(T) : 1;
 
 // Element j of vector i of a lane: the lanes' accesses lie side by side.
 template <class T, Way kWay, int kLanes>
@@ -325,8 +326,10 @@ struct Turns {
     __device__ __forceinline__ void take(int i, uint32_t base, R (&to)[G::kDeep]) const {
 #pragma unroll
         for (int d = 0; d < G::kDeep; ++d) {
-            if constexpr (kWay == kRing) to[d].load_shared(ring.row(i, d * G::kSide + side), lane, row(base, d) < rows ? channels : 0);
-            else to[d] = next[i][d];
+            if constexpr (kWay == kRing)
+                to[d].load_shared(ring.row(i, d * G::kSide + side), lane, row(base, d) < rows ? channels : 0);
+            else
+                to[d] = next[i][d];
         }
     }
     // Every thread of the team has taken its rows (a barrier lies between): the next turn's
@@ -467,7 +470,9 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kResident<T, kWay, kLanes>) 
 // and two tensors (3003 rows of 2047 float32: 27 us with two CTAs an SM, 25 with three; two
 // 16-bit rows a thread spill so, and take 55 us in place of 49).  kSum: dsum is there.
 template <class T, Way kWay, int kLanes, int NV, bool kSum>
-constexpr int kGradResident = kThreads<kLanes> > 256 ? 1 : kWidth<T> * NV == 8 && !kSum && (kWay != kRing || sizeof(T) == 4) ? 3 : 2;
+constexpr int kGradResident = kThreads<kLanes> > 256                                                        ? 1
+                              : kWidth<T> * NV == 8 && !kSum && (kWay != kRing || sizeof(T) == 4) ? 3
+                                                                                                   : 2;
 
 template <class T, Way kWay, int kLanes, int NV, bool kSum>
 __global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<T, kWay, kLanes, NV, kSum>) norm_grad_kernel(NormParams p) {
@@ -537,7 +542,8 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<T, kWay, kLane
 #pragma unroll
                 for (int j = 0; j < W / 2; ++j) {
                     const int k = i * W / 2 + j;
-                    const f2 g = dy[d].pair(i, j), n = mul2(add2(x[d].pair(i, j), both(-mean[d])), both(rstd[d])), dn = mul2(g, w[k]);
+                    const f2 n = mul2(add2(x[d].pair(i, j), both(-mean[d])), both(rstd[d]));
+                    const f2 g = dy[d].pair(i, j), dn = mul2(g, w[k]);
                     a = add2(a, dn);
                     b = fma2(dn, n, b);  // w = 0 behind the row's end, where n is not 0
                     db[k] = add2(db[k], g);
@@ -595,7 +601,8 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<T, kWay, kLane
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < W; ++j) s_col[group * (kLanes * N) + column<T, kWay, kLanes>(i, j, lane)] = element(i * W + j);
+                for (int j = 0; j < W; ++j)
+                    s_col[group * (kLanes * N) + column<T, kWay, kLanes>(i, j, lane)] = element(i * W + j);
             __syncthreads();
             for (int c = threadIdx.x; c < channels; c += NT) {
                 float sum = 0.0f;
@@ -801,8 +808,9 @@ cudaError_t go(NormParams& p, bool grad, cudaStream_t s) {
 template <class T, int kLanes, int NV>
 cudaError_t vectors(NormParams& p, bool grad, cudaStream_t s) {
     using G = Team<T, kVectors, kLanes, NV>;
-    const int resident = !grad ? kResident<T, kVectors, kLanes>
-                         : p.dsum ? kGradResident<T, kVectors, kLanes, NV, true> : kGradResident<T, kVectors, kLanes, NV, false>;
+    const int resident = !grad    ? kResident<T, kVectors, kLanes>
+                         : p.dsum ? kGradResident<T, kVectors, kLanes, NV, true>
+                                  : kGradResident<T, kVectors, kLanes, NV, false>;
     const long long held = seq_sms() * resident * G::kTeams * G::kRows;
     if (p.rows <= held) return go<T, kVectors, kLanes, NV>(p, grad, s);
     return go<T, kRing, kLanes, NV>(p, grad, s);
