@@ -85,7 +85,7 @@ def _bind_commands(cc: str, torch_dir: str):
         compile_ += ["-isystem", d]
     lib = os.path.join(torch_dir, "lib")
     tmp = BIND + ".tmp.%d" % os.getpid()
-    link = [gxx, "-shared", "-o", tmp, obj, LIB, "-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda",
+    link = [gxx, "-shared", "-o", tmp, obj, LIB, "-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda",
             "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
     return compile_, link, tmp
 

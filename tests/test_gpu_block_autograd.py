@@ -112,6 +112,34 @@ def test_experts(weighted, dtype):
             assert torch.equal(w.grad, want["weights"])
 
 
+def test_a_captured_step():
+    """Forward and backward in one graph, replayed on other inputs (without a norm's
+    parameters, whose gradients need scratch memory)."""
+    x, g = _leaf(_normal(2, 40, 64)), _leaf(_normal(2, 40, 64, seed=1))
+    ids = torch.randint(0, 5, (80, 2), generator=torch.Generator().manual_seed(1)).cuda()
+    share, dy = _leaf(_normal(80, 2, seed=2)), _normal(80, 64, seed=3)
+
+    def step():
+        y = sc.layer_norm(sc.gated_scan(x, g), residual=x)[0].flatten(0, 1)
+        order = sc.expert_sort(ids, 5)
+        out = sc.expert_combine(sc.expert_gather(y, order), order, share)
+        return out, *torch.autograd.grad(out, (x, g, share), dy)
+
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        step()
+    torch.cuda.current_stream().wait_stream(stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        made = step()
+    with torch.no_grad():
+        x.copy_(x.flip(1))
+        ids.copy_(ids.flip(0))
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(made, step()))
+
+
 def _block(p, x, ids, heads, library):
     """Norm, gated recurrence, its way back to the stream, norm, experts (a matrix each),
     and back: by the library, or from the definitions in float64."""
