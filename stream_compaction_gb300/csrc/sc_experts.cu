@@ -206,7 +206,8 @@ struct Part {
     }
 };
 
-// `lanes` threads a token, the token's group within the CTA.
+// `lanes` threads a token, the token's group within the CTA; the CTAs of a column of the
+// grid share a token's row.
 struct Where {
     long long token;
     int lane;
@@ -238,7 +239,8 @@ __global__ void __launch_bounds__(kNT) expert_gather_kernel(ExpertParams p, int 
     const long long kept = kept_of(p);
     const T* x = static_cast<const T*>(p.in) + at.token * p.ld_in;
     const int step = lanes * P::W;
-    for (long long c0 = (long long)at.lane * P::W; c0 < p.dim; c0 += step * P::kColumns) {
+    const long long stride = (long long)step * P::kColumns;
+    for (long long c0 = blockIdx.y * stride + at.lane * P::W; c0 < p.dim; c0 += gridDim.y * stride) {
         P v[P::kColumns], none;
         none.zero();
 #pragma unroll
@@ -264,7 +266,8 @@ __global__ void __launch_bounds__(kNT) expert_combine_kernel(ExpertParams p, int
     const long long kept = kept_of(p);
     const long long entry = at.token * p.choices;
     const int step = lanes * W;
-    for (long long c0 = (long long)at.lane * W; c0 < p.dim; c0 += step * C) {
+    const long long stride = (long long)step * C;
+    for (long long c0 = blockIdx.y * stride + at.lane * W; c0 < p.dim; c0 += gridDim.y * stride) {
         float sum[C][W];
 #pragma unroll
         for (int k = 0; k < C; ++k)
@@ -602,8 +605,11 @@ template <class T, class P>
 cudaError_t launch_rows(int what, const ExpertParams& p, cudaStream_t s) {
     const int lanes = lanes_of<P>(p.dim);
     const unsigned grid = (unsigned)((p.tokens + kNT / lanes - 1) / (kNT / lanes));
-    if (what == kGather) expert_gather_kernel<T, P><<<grid, kNT, 0, s>>>(p, lanes);
-    else if (what == kCombine) expert_combine_kernel<T, P><<<grid, kNT, 0, s>>>(p, lanes);
+    // rows of more than one turn are shared where there are few tokens for the machine
+    const long long turns = (p.dim + (long long)lanes * P::W * P::kColumns - 1) / ((long long)lanes * P::W * P::kColumns);
+    const dim3 shared(grid, (unsigned)std::min<long long>(turns, 1 + 4 * seq_sms() / grid));
+    if (what == kGather) expert_gather_kernel<T, P><<<shared, kNT, 0, s>>>(p, lanes);
+    else if (what == kCombine) expert_combine_kernel<T, P><<<shared, kNT, 0, s>>>(p, lanes);
     else expert_combine_grad_kernel<T, P><<<grid, kNT, 0, s>>>(p, lanes);
     count_launches(1);
     return cudaGetLastError();
