@@ -12,10 +12,10 @@
 // Entries of no expert are one more bin behind the others, so order and place are
 // permutations and every row of an output has exactly one writer.
 //
-// The rows: bytes alone.  All four kernels go by tokens, through place: a token's row
-// is read (or written) once, and its entries' rows wherever they lie; 16 bytes a lane,
-// up to kAhead entries under way.  No atomics; a token's sum goes in the order of its
-// choices.
+// The rows: bytes alone.  All kernels go by tokens, through place: a token's row is read
+// (or written) once, and its entries' rows wherever they lie.  No atomics; a token's sum
+// goes in the order of its choices.  16384 tokens, 2 of 64 experts, rows of 4096 bfloat16:
+// sort 11 us, rows there 57, back 62, their gradients 61 and 100 (6.5 to 7 TB/s).
 #include <algorithm>
 
 #include <cooperative_groups.h>
@@ -257,9 +257,10 @@ __global__ void __launch_bounds__(kNT) expert_gather_kernel(ExpertParams p, int 
     }
 }
 
-// out[t] = sum over j of weights[t,j] rows[place[t,j]]
+// out[t] = sum over j of weights[t,j] rows[place[t,j]].  64 registers a thread, for four CTAs
+// an SM (8000 tokens, 2 of 2047 float32: 59 us with three, 51 so).
 template <class T, class P>
-__global__ void __launch_bounds__(kNT) expert_combine_kernel(ExpertParams p, int lanes) {
+__global__ void __launch_bounds__(kNT, 4) expert_combine_kernel(ExpertParams p, int lanes) {
     constexpr int W = P::W, C = P::kColumns, kAhead = P::kAhead;
     const Where at = where(lanes);
     if (at.token >= p.tokens) return;

@@ -20,6 +20,9 @@
 // registers, the next row's while this one is worked on.  (Unaligned rows through the
 // ring, their ends by themselves: 17367 rows of 636 bfloat16 43 us forward, 23 so.)
 //
+// 4 x 4096 rows of 4096 bfloat16 with a residual: forward 85 us, gradient 87 and its sums
+// 8 (6.2 TB/s; a copy 6.5).
+//
 // The gradient's sums over tokens: a CTA's columns' sums over all its rows become one row
 // of partial sums, and a second kernel adds those in the order of the CTAs: the same bits
 // on every run.
