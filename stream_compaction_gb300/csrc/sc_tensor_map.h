@@ -1,4 +1,4 @@
-// The driver's tensor-map encoder, found at run time (the library links the CUDA
+// CUDA's tensor-map encoder, found at run time (the library links the CUDA
 // runtime alone).
 #pragma once
 #include <cuda.h>
