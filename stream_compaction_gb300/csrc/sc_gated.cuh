@@ -504,27 +504,31 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
                 map.B = cut >> j & 1u ? token<K>(b, j) : L::fma(token<K>(f, j), map.B, token<K>(b, j));
         }
         V h = exchange<K, kWarps, kCuts>(s.ex, round, c.warp, c.lane, c.rank, c.ranks, map, cut != 0, carry);
-        if (saved && c.live && valid > 0) L::store(saved, h);
-        T* to = y;
+        // A warp without a tile leaves its stage as it is: the copy of earlier results out of
+        // it is waited for only where the stage is filled again (Ring::load).
+        if (valid > 0) {
+            if (saved && c.live) L::store(saved, h);
+            T* to = y;
 #pragma unroll
-        for (int j = 0; j < kTokens; ++j) {
-            h = kCuts && (cut >> j & 1u) ? token<K>(b, j) : L::fma(token<K>(f, j), h, token<K>(b, j));
+            for (int j = 0; j < kTokens; ++j) {
+                h = kCuts && (cut >> j & 1u) ? token<K>(b, j) : L::fma(token<K>(f, j), h, token<K>(b, j));
+                if constexpr (kTma) {
+                    xr.put(j, h);
+                } else {
+                    if (c.live && j < valid) Elements<T, K>::store(to, h);
+                    to += p.y_token;
+                }
+            }
             if constexpr (kTma) {
-                xr.put(j, h);
-            } else {
-                if (c.live && j < valid) Elements<T, K>::store(to, h);
-                to += p.y_token;
+                fence_proxy_async();
+                __syncwarp();
+                if (c.lane == 0) {
+                    tma_store_3d(&maps.map[2], (int)c.ch0, tile * kTokens, (int)c.b, smem_u32(ring.take));
+                    bulk_commit();
+                }
             }
         }
-        if constexpr (kTma) {
-            fence_proxy_async();
-            __syncwarp();
-            if (c.lane == 0 && valid > 0) {
-                tma_store_3d(&maps.map[2], (int)c.ch0, tile * kTokens, (int)c.b, smem_u32(ring.take));
-                bulk_commit();
-            }
-            ring.next(ring.take);
-        }
+        if constexpr (kTma) ring.next(ring.take);
         if (saved) saved += step * p.channels;
         y += (long long)step * kTokens * p.y_token;
         tile += step;
@@ -640,39 +644,42 @@ __global__ void __launch_bounds__(32 * kWarps, (kTma || K == 1 ? 16 : 12) / kWar
             }
         }
         V q = exchange<K, kWarps, kCuts>(s.ex, round, c.warp, c.lane, c.rank, c.ranks, map, cut != 0, carry);
-        T *tx = dx + (kTokens - 1) * p.channels, *tg = dg + (kTokens - 1) * p.channels;
+        if (valid > 0) {  // as in the forward kernel
+            T *tx = dx + (kTokens - 1) * p.channels, *tg = dg + (kTokens - 1) * p.channels;
 #pragma unroll
-        for (int j = kTokens - 1; j >= 0; --j) {
-            const V dh = L::add(d.get(j), q);
-            V og = L::mul(dh, token<K>(u, j));
-            const V ox = kSigmoid ? L::mul(dh, token<K>(w, j)) : dh;
-            q = L::mul(decay_of(j), dh);
-            if (kCuts && (cut >> j & 1u)) {
-                q = none;
-                if (!kSigmoid) og = none;
+            for (int j = kTokens - 1; j >= 0; --j) {
+                const V dh = L::add(d.get(j), q);
+                V og = L::mul(dh, token<K>(u, j));
+                const V ox = kSigmoid ? L::mul(dh, token<K>(w, j)) : dh;
+                q = L::mul(decay_of(j), dh);
+                if (kCuts && (cut >> j & 1u)) {
+                    q = none;
+                    if (!kSigmoid) og = none;
+                }
+                if constexpr (kTma) {
+                    xr.put(j, ox);
+                    gr.put(j, og);
+                } else {
+                    if (c.live && j < valid) {
+                        Elements<T, K>::store(tx, ox);
+                        Elements<T, K>::store(tg, og);
+                    }
+                    tx -= p.channels;
+                    tg -= p.channels;
+                }
             }
             if constexpr (kTma) {
-                xr.put(j, ox);
-                gr.put(j, og);
-            } else {
-                if (c.live && j < valid) {
-                    Elements<T, K>::store(tx, ox);
-                    Elements<T, K>::store(tg, og);
+                fence_proxy_async();
+                __syncwarp();
+                if (c.lane == 0) {
+                    const uint32_t from = smem_u32(ring.take);
+                    tma_store_3d(&maps.map[3], (int)c.ch0, tile * kTokens, (int)c.b, from);
+                    tma_store_3d(&maps.map[4], (int)c.ch0, tile * kTokens, (int)c.b, from + Tile<T, K>::kBytes);
+                    bulk_commit();
                 }
-                tx -= p.channels;
-                tg -= p.channels;
             }
         }
-        if constexpr (kTma) {
-            fence_proxy_async();
-            __syncwarp();
-            if (c.lane == 0 && valid > 0) {
-                tma_store_3d(&maps.map[3], (int)c.ch0, tile * kTokens, (int)c.b, smem_u32(ring.take));
-                tma_store_3d(&maps.map[4], (int)c.ch0, tile * kTokens, (int)c.b, smem_u32(ring.take + Tile<T, K>::kBytes));
-                bulk_commit();
-            }
-            ring.next(ring.take);
-        }
+        if constexpr (kTma) ring.next(ring.take);
         tile -= step;
         dx -= (long long)step * kTokens * p.channels;
         dg -= (long long)step * kTokens * p.channels;
