@@ -28,7 +28,7 @@
 // rounding errors of 16 bits in dgate).
 //
 // 8 x 4096 tokens of 4096 bfloat16: forward 137 to 147 us (5.5 to 5.9 TB/s, a copy 6.5),
-// gradient 229 to 245 (5.5 to 5.9); rows that are not aligned 3.0 to 5.3 TB/s.
+// gradient 246 (5.5); rows that are not aligned 3.0 to 5.3 TB/s.
 #pragma once
 #include <algorithm>
 
@@ -105,6 +105,13 @@ template <int K>
 __device__ __forceinline__ void set_token(f2 (&v)[kPairs<K>], int j, typename Lane<K>::V t) {
     if constexpr (K == 2) v[j] = t;
     else v[j / 2] = j % 2 ? pack2(lo2(v[j / 2]), t) : pack2(t, hi2(v[j / 2]));
+}
+
+// Token j's part of the pair that it is in.
+template <int K>
+__device__ __forceinline__ typename Lane<K>::V half(f2 v, int j) {
+    if constexpr (K == 2) return v;
+    else return j % 2 ? hi2(v) : lo2(v);
 }
 
 // A lane's elements as they lie in memory, as an operand.
@@ -196,22 +203,46 @@ struct Held : Elements<T, K> {
     __device__ __forceinline__ void put(int, typename E::V) const {}
 };
 
-// rest = 1 - f = e / (1 + e), e = exp(-g), and f = 1 - rest, for a pair.  rest has its
-// relative error (4 + |g| units of 2^-24 in 16 bits, 8 in float32) however small it
-// is, and so has what x enters with; f is off by as much absolutely, times rest: decays
-// close to 1 are as good as rounded ones, however many are multiplied.  e ends at 2^126
-// (its reciprocal is a normal number; f is 0 to float32 then).
+// The smaller of f and 1 - f, e / (1 + e) with e = exp(-|g|), and the larger, for a pair.
+// The smaller one has its relative error ((4 + |g|) 2^-24 in 16 bits, 9 x 2^-24 in
+// float32; 0 where e is below 2^-126) however small it is: so has a closed gate's f, which
+// dgate is proportional to, and an open gate's 1 - f, which x enters with.  The larger is
+// off by as much absolutely, times the smaller: decays close to 1 are as good as rounded
+// ones, however many are multiplied.  (f = 1 - e / (1 + e) with e = exp(-g) for all gates
+// saves a selection, but keeps of a gate of -12 one digit, of one below -17 none.)
+template <class T>
+__device__ __forceinline__ void gate_parts(f2 g, f2& small, f2& large) {
+    f2 e;
+    if constexpr (kFine<T>) e = exp_minus_2<true>(g & 0x7fffffff7fffffffull);
+    else e = pack2(ex2(fabsf(lo2(g)) * -kLog2e), ex2(fabsf(hi2(g)) * -kLog2e));
+    small = mul2(e, rcp_2(add2(e, both(1.0f))));
+    large = fma2(small, both(-1.0f), both(1.0f));
+}
+// By a gate's sign bit.
+__device__ __forceinline__ bool closed(float g) { return __float_as_int(g) < 0; }
+__device__ __forceinline__ f2 select2(f2 by, f2 shut, f2 open) {
+    return pack2(closed(lo2(by)) ? lo2(shut) : lo2(open), closed(hi2(by)) ? hi2(shut) : hi2(open));
+}
+// f and 1 - f.
 template <class T>
 __device__ __forceinline__ void gates(f2 g, f2& f, f2& rest) {
-    f2 e;
-    if constexpr (kFine<T>) {
-        e = exp_minus_2<true>(pack2(at_least(lo2(g), -87.0f), at_least(hi2(g), -87.0f)));
-    } else {
-        const f2 t = mul2(g, both(kLog2e));
-        e = pack2(ex2(-at_least(lo2(t), -126.0f)), ex2(-at_least(hi2(t), -126.0f)));
-    }
-    rest = mul2(e, rcp_2(add2(e, both(1.0f))));
-    f = fma2(rest, both(-1.0f), both(1.0f));
+    f2 small, large;
+    gate_parts<T>(g, small, large);
+    f = select2(g, small, large);
+    rest = select2(g, large, small);
+}
+// f dh and (1 - f) dh from the smaller of f and 1 - f with the gate's sign.
+__device__ __forceinline__ void shares(float part, float dh, float& f, float& rest) {
+    const float a = fabsf(part), less = a * dh, more = fmaf(-a, dh, dh);
+    f = closed(part) ? less : more;
+    rest = closed(part) ? more : less;
+}
+__device__ __forceinline__ void shares(f2 part, f2 dh, f2& f, f2& rest) {
+    float v[2][2];
+    shares(lo2(part), lo2(dh), v[0][0], v[1][0]);
+    shares(hi2(part), hi2(dh), v[0][1], v[1][1]);
+    f = pack2(v[0][0], v[0][1]);
+    rest = pack2(v[1][0], v[1][1]);
 }
 
 // A lane's flag of a tile's tokens, and the tokens where a segment starts, one bit each.
@@ -595,63 +626,79 @@ __global__ void __launch_bounds__(32 * kWarps, (kTma || K == 1 ? 16 : 12) / kWar
         const bool ok = !kTma || tile < 0 || ring.wait();
         const auto xr = tile_of<kTma>(ring, x, 0, c.lane), gr = tile_of<kTma>(ring, g, 1, c.lane);
         const auto d = tile_of<kTma>(ring, dy, 2, c.lane);
-        // u: what dh is multiplied with for dgate; w: for dx (sigmoid), or f itself
+        // u: what dh is multiplied with for dgate; w: the smaller of f and 1 - f with the
+        // gate's sign (sigmoid), or f itself.  map: q behind the tile -> q before it, as the
+        // sum over its tokens of dy times the product of f from the tile's start up to there.
         f2 u[kPairs<K>], w[kPairs<K>];
         const uint32_t cut = kCuts ? cuts_of(head) : 0u;
-        const int valid = tokens_of(tile);
+        const int valid = tokens_of(tile), until = kCuts && cut ? __ffs(cut) - 1 : kTokens;
         V h = start;
         fetch_small(tile - step);
+        Map<K> map{one, none};
         if constexpr (kSigmoid) {
 #pragma unroll
             for (int i = 0; i < kPairs<K>; ++i) {
-                f2 f;
-                gates<T>(gr.pair(i), f, w[i]);
-                u[i] = f;
-            }
-        }
+                f2 small, large;
+                const f2 g2 = gr.pair(i);
+                gate_parts<T>(g2, small, large);
+                const f2 fs = select2(g2, small, large), rests = select2(g2, large, small), product = mul2(small, large);
+                w[i] = small | (g2 & 0x8000000080000000ull);
 #pragma unroll
-        for (int j = 0; j < kTokens; ++j) {
-            const V xv = xr.get(j);
-            if (kCuts && (cut >> j & 1u)) h = none;
-            if constexpr (kSigmoid) {
-                const V f = token<K>(u, j), r = token<K>(w, j);
-                set_token<K>(u, j, L::mul(L::fma(xv, minus, h), L::mul(f, r)));
-                h = L::fma(f, h, L::mul(r, xv));
-            } else {
-                const V f = gr.get(j);
+                for (int j = i * 2 / K; j < (i + 1) * 2 / K; ++j) {
+                    const V f = half<K>(fs, j), xv = xr.get(j);
+                    if (kCuts && (cut >> j & 1u)) h = none;
+                    set_token<K>(u, j, L::mul(L::fma(xv, minus, h), half<K>(product, j)));
+                    h = L::fma(f, h, L::mul(half<K>(rests, j), xv));
+                    map.A = L::mul(map.A, f);
+                    if (!kCuts || j < until) map.B = L::fma(map.A, d.get(j), map.B);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kTokens; ++j) {
+                const V f = gr.get(j), xv = xr.get(j);
+                if (kCuts && (cut >> j & 1u)) h = none;
                 set_token<K>(w, j, f);
                 set_token<K>(u, j, h);
                 h = kCuts && (cut >> j & 1u) ? xv : L::fma(f, h, xv);
             }
         }
         if (valid < kTokens) {  // behind the row's end: q stays
+            map.A = one;
 #pragma unroll
-            for (int j = 0; j < kTokens; ++j)
+            for (int j = 0; j < kTokens; ++j) {
+                V more = map.A, unused;
                 if (j >= valid) set_token<K>(w, j, kSigmoid ? none : one);
+                else if constexpr (kSigmoid) shares(token<K>(w, j), map.A, more, unused);
+                map.A = more;
+            }
+            if (valid <= 0) map.B = none;
         }
-        if (!ok) set_token<K>(w, 0, L::all(not_a_number()));
-        if (!kTma) fetch();
-        // f from 1 - f: it enters with its absolute error
-        auto decay_of = [&](int j) { return kSigmoid ? L::fma(token<K>(w, j), minus, one) : token<K>(w, j); };
-        Map<K> map{one, none};
-        if (valid > 0) {
+        if constexpr (!kSigmoid) {
+            if (valid > 0) {
 #pragma unroll
-            for (int j = kTokens - 1; j >= 0; --j) {
-                const V f = decay_of(j);
-                map.A = L::mul(map.A, f);
-                map.B = L::mul(f, L::add(d.get(j), map.B));
-                if (kCuts && (cut >> j & 1u)) map.B = none;
+                for (int j = kTokens - 1; j >= 0; --j) {
+                    const V f = token<K>(w, j);
+                    map.A = L::mul(map.A, f);
+                    map.B = L::mul(f, L::add(d.get(j), map.B));
+                    if (kCuts && (cut >> j & 1u)) map.B = none;
+                }
             }
         }
+        if (!ok) {
+            set_token<K>(w, 0, L::all(not_a_number()));
+            map.A = map.B = L::all(not_a_number());
+        }
+        if (!kTma) fetch();
         V q = exchange<K, kWarps, kCuts>(s.ex, round, c.warp, c.lane, c.rank, c.ranks, map, cut != 0, carry);
         if (valid > 0) {  // as in the forward kernel
             T *tx = dx + (kTokens - 1) * p.channels, *tg = dg + (kTokens - 1) * p.channels;
 #pragma unroll
             for (int j = kTokens - 1; j >= 0; --j) {
                 const V dh = L::add(d.get(j), q);
-                V og = L::mul(dh, token<K>(u, j));
-                const V ox = kSigmoid ? L::mul(dh, token<K>(w, j)) : dh;
-                q = L::mul(decay_of(j), dh);
+                V og = L::mul(dh, token<K>(u, j)), ox = dh;
+                if constexpr (kSigmoid) shares(token<K>(w, j), dh, q, ox);
+                else q = L::mul(token<K>(w, j), dh);
                 if (kCuts && (cut >> j & 1u)) {
                     q = none;
                     if (!kSigmoid) og = none;
