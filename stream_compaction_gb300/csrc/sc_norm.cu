@@ -51,10 +51,11 @@ cudaError_t by_type(int dtype, NormParams& p, bool grad, cudaStream_t s) {
 
 cudaError_t launch_norm(int dtype, NormParams p, cudaStream_t s) { return by_type(dtype, p, false, s); }
 
-// One row of partial sums for each CTA of the gradient's kernel: at most three an SM,
-// and a row each.
+// One row of partial sums for each CTA of the gradient's kernel, at most three an SM and a
+// row each; of wide rows, one for each part of the columns' sums.
 size_t norm_grad_scratch(long long rows, long long channels) {
-    return (size_t)std::min(rows, std::max<long long>(3 * seq_sms(), kColumnParts)) * 2 * channels * sizeof(float);
+    const long long parts = channels > kRowMax ? kColumnParts : 3 * seq_sms();
+    return (size_t)std::min(rows, parts) * 2 * channels * sizeof(float);
 }
 
 cudaError_t launch_norm_grad(int dtype, NormParams p, cudaStream_t s) {
