@@ -630,7 +630,10 @@ sc_status launch_embed_grad(int dtype, int wtype, const EmbedParams& p, const Em
     const long long each = ceil_div(p.tokens, (long long)kClusterNT * kClusterCtas);
     const long long k = each <= 2 ? std::max(each, 1ll) : each <= 4 ? 4 : 8, ctas = ceil_div(p.tokens, kClusterNT * k);
     const bool in_cluster = p.tokens > 0 && p.tokens <= kClusterKeys, zero_last = in_cluster && p.vocab <= 16 * kClusterNT * ctas;
-    if (!zero_last && cudaMemsetAsync(runs.last, 0, (size_t)p.vocab * 4, s) != cudaSuccess) return SC_ERR_CUDA;
+    if (!zero_last) {
+        const sc_status st = status_of(cudaMemsetAsync(runs.last, 0, (size_t)p.vocab * 4, s));
+        if (st != SC_OK) return st;
+    }
     if (in_cluster) {
         auto go = [&](auto kernel) {
             const int bytes = kClusterWarps * (1 << g.digit_bits) * 2;
@@ -653,7 +656,7 @@ sc_status launch_embed_grad(int dtype, int wtype, const EmbedParams& p, const Em
                               : k == 2 ? go(sort_cluster_kernel<2>)
                               : k == 4 ? go(sort_cluster_kernel<4>)
                                        : go(sort_cluster_kernel<8>);
-        if (e != cudaSuccess) return SC_ERR_CUDA;
+        if (e != cudaSuccess) return status_of(e);
         count_launches(1);
         kin = keys[(g.passes - 1) & 1];
         vin = vals[(g.passes - 1) & 1];
@@ -679,7 +682,7 @@ sc_status launch_embed_grad(int dtype, int wtype, const EmbedParams& p, const Em
                                                   : sums_of<f16, f16>(p, kin, vin, runs, partials, s);
     else if (dtype == SC_BF16) e = wtype == SC_F32 ? sums_of<bf16, float>(p, kin, vin, runs, partials, s)
                                                    : sums_of<bf16, bf16>(p, kin, vin, runs, partials, s);
-    return e == cudaSuccess ? SC_OK : SC_ERR_CUDA;
+    return status_of(e);
 }
 
 }  // namespace scg

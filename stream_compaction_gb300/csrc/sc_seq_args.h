@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/sc_seq.h"
+#include "sc_seq_launch.h"
 
 namespace scg {
 
@@ -98,14 +99,13 @@ inline bool vec_row(int64_t dim, int64_t ld, const void* p, int elems, int64_t r
 
 inline sc_status zero(void* p, size_t bytes, cudaStream_t s) {
     if (!p || !bytes) return SC_OK;
-    return cudaMemsetAsync(p, 0, bytes, s) == cudaSuccess ? SC_OK : SC_ERR_CUDA;
+    return status_of(cudaMemsetAsync(p, 0, bytes, s));
 }
 // dst = src, or zeros without one
 inline sc_status copy_or_zero(void* dst, const void* src, size_t bytes, cudaStream_t s) {
     if (!dst || !bytes || dst == src) return SC_OK;
     if (!src) return zero(dst, bytes, s);
-    return cudaMemcpyAsync(dst, src, bytes, cudaMemcpyDeviceToDevice, s) == cudaSuccess ? SC_OK : SC_ERR_CUDA;
+    return status_of(cudaMemcpyAsync(dst, src, bytes, cudaMemcpyDeviceToDevice, s));
 }
-inline sc_status status_of(cudaError_t e) { return e == cudaSuccess ? SC_OK : SC_ERR_CUDA; }
 
 }  // namespace scg

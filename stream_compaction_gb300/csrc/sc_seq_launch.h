@@ -15,6 +15,14 @@ size_t seq_scratch_total(size_t bytes);  // workspace bytes that hold it
 void count_launches(int n);
 long long seq_sms();  // multiprocessors of the current device
 
+// A failed call is reported once: its error does not stay behind for the next call, which
+// asks for the last error after its launches.
+inline sc_status status_of(cudaError_t e) {
+    if (e == cudaSuccess) return SC_OK;
+    cudaGetLastError();
+    return SC_ERR_CUDA;
+}
+
 // ------------------------------------------------------------- embedding
 struct EmbedParams {
     const void* ids;
