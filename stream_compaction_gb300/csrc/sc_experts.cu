@@ -21,6 +21,7 @@
 #include <cooperative_groups.h>
 
 #include "sc_bulk.cuh"
+#include "sc_cluster.h"
 #include "sc_seq.cuh"
 #include "sc_seq_launch.h"
 
@@ -644,6 +645,28 @@ cudaError_t launch_expert_sort(const void* ids, int ids64, long long entries, in
     const long long least = (entries + 31) / 32;
     int ctas = 1;
     while (ctas < kSortMaxCtas && (long long)ctas * kSortMaxWarps < least) ctas *= 2;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute a{};
+    a.id = cudaLaunchAttributeClusterDimension;
+    a.val.clusterDim.y = a.val.clusterDim.z = 1;
+    cfg.attrs = &a;
+    cfg.numAttrs = 1;
+    cfg.stream = s;
+    // the limit is one per device: always the whole, whatever this call needs
+    constexpr int kShared = kSortMaxWarps * kMaxBins * (int)sizeof(uint32_t);
+    cudaError_t e = cudaSuccess;
+    auto allow = [&] { return cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared); };
+    if (ctas > 8) {
+        e = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess) e = allow();
+        if (e != cudaSuccess) return e;
+        static LargeClusters large;
+        a.val.clusterDim.x = (unsigned)ctas;
+        cfg.gridDim = dim3((unsigned)ctas);
+        cfg.blockDim = dim3(32 * kSortMaxWarps);
+        cfg.dynamicSmemBytes = kShared;
+        if (!large.fit((const void*)expert_sort_kernel, cfg)) ctas = 8;
+    }
     // (a thread has two bins at most where a CTA can have as many threads)
     const long long wanted = std::max<long long>((least + ctas - 1) / ctas, experts / 64 + 1);
     const int warps = (int)std::min<long long>(wanted, kSortMaxWarps);
@@ -651,25 +674,14 @@ cudaError_t launch_expert_sort(const void* ids, int ids64, long long entries, in
     while (experts + 1 >> p.bits) ++p.bits;
     p.run = ((entries + (long long)ctas * warps - 1) / ((long long)ctas * warps) + 31) / 32 * 32;
     const size_t bytes = (size_t)warps * (experts + 1) * sizeof(uint32_t);
-    // the limit is one per device: always the whole, whatever this call needs
-    cudaError_t e = cudaSuccess;
-    if (bytes > kDefaultShared - 8 * 1024)
-        e = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kSortMaxWarps * kMaxBins * (int)sizeof(uint32_t));
-    if (e == cudaSuccess && ctas > 8)
-        e = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
+    if (ctas <= 8 && bytes > kDefaultShared - 8 * 1024) {
+        e = allow();
+        if (e != cudaSuccess) return e;
+    }
+    a.val.clusterDim.x = (unsigned)ctas;
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(32 * warps);
     cfg.dynamicSmemBytes = bytes;
-    cfg.stream = s;
-    cudaLaunchAttribute a{};
-    a.id = cudaLaunchAttributeClusterDimension;
-    a.val.clusterDim.x = (unsigned)ctas;
-    a.val.clusterDim.y = a.val.clusterDim.z = 1;
-    cfg.attrs = &a;
-    cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, expert_sort_kernel, p);
     count_launches(1);
     return e;

@@ -35,6 +35,7 @@
 #include <cooperative_groups.h>
 
 #include "sc_bulk.cuh"
+#include "sc_cluster.h"
 #include "sc_seq.cuh"
 #include "sc_seq_launch.h"
 #include "sc_tensor_map.h"
@@ -862,16 +863,21 @@ cudaError_t go(const GatedParams& p, const GatedMaps& maps, bool grad, long long
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(groups * ctas));
-    cfg.blockDim = dim3(32 * kWarps);
-    cfg.dynamicSmemBytes = (size_t)bytes(ctas);
-    cfg.stream = s;
     cudaLaunchAttribute a{};
     a.id = cudaLaunchAttributeClusterDimension;
-    a.val.clusterDim.x = (unsigned)ctas;
     a.val.clusterDim.y = a.val.clusterDim.z = 1;
+    cfg.blockDim = dim3(32 * kWarps);
+    cfg.stream = s;
     cfg.attrs = &a;
     cfg.numAttrs = 1;
+    auto size = [&](int n) {
+        a.val.clusterDim.x = (unsigned)n;
+        cfg.gridDim = dim3((unsigned)(groups * n));
+        cfg.dynamicSmemBytes = (size_t)bytes(n);
+    };
+    size(ctas);
+    static LargeClusters large[2];
+    if (ctas > 8 && !large[grad].fit(kernel, cfg)) size(8);
     void* args[] = {const_cast<GatedParams*>(&p), const_cast<GatedMaps*>(&maps)};
     e = cudaLaunchKernelExC(&cfg, kernel, args);
     count_launches(1);
