@@ -10,6 +10,7 @@
 #include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/record_function.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -67,6 +68,14 @@ std::string text(at::IntArrayRef s) {
     return r + ")";
 }
 
+// No operator carries tangents (forward-mode derivatives) on; a result without them would
+// say that they are zero.
+void no_tangent(const Tensor& t, const char* what) {
+    if (!c10::AutogradState::get_tls_state().get_fw_grad_mode() || !t._fw_grad(0).defined()) return;
+    PyErr_Format(PyExc_NotImplementedError, "%s has a tangent: forward-mode derivatives are not recorded", what);
+    throw py::error_already_set();
+}
+
 // Shape, type and device as given, the last dimension contiguous.
 const Tensor& like(const Tensor& t, const char* what, at::IntArrayRef shape, at::ScalarType type,
                    const at::Device& device) {
@@ -78,6 +87,7 @@ const Tensor& like(const Tensor& t, const char* what, at::IntArrayRef shape, at:
     need(t.device() == device, what, ": expected a tensor on the device of the others");
     need(t.dim() == 0 || t.size(-1) <= 1 || t.stride(-1) == 1, what,
          ": elements of the last dimension must be contiguous");
+    no_tangent(t, what);
     return t;
 }
 void* whole(const Tensor& t, const char* what, at::IntArrayRef shape, at::ScalarType type, const at::Device& device) {

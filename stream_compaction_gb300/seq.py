@@ -11,8 +11,9 @@ embed, causal_conv, selective_scan, gated_scan, layer_norm, expert_gather and
 expert_combine are differentiable: where torch records gradients and an input requires
 one, their results carry it (seq_autograd.py), by the `_grad` functions below, which may
 also be called by themselves.  `out` cannot be given then, and nothing goes back through
-`final_state`.  The `_step` forms have no gradient;
-asking for one raises.
+`final_state`.  The `_step` forms have no gradient; asking for one raises.  Forward-mode
+derivatives are not recorded either: a tensor with a tangent is refused
+(NotImplementedError).
 
     ids, weight                 y = embed(ids, weight, scale)
                                 dweight = embed_grad(ids, dy, vocab, scale)
