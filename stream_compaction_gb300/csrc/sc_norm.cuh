@@ -98,6 +98,13 @@ struct Row {
             else v[i].zero();
         }
     }
+    // NaN in every element, of whichever type.
+    __device__ __forceinline__ void spoil() {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < Vec<T, W>::kWords; ++j) v[i].w[j] = 0x7fff7fffu;
+    }
     // Elements 2 j and 2 j + 1 of vector i.
     __device__ __forceinline__ f2 pair(int i, int j) const { return v[i].pair(j); }
     // The elements of f (as pairs, vector by vector) to a row, rounded; `rounded`: and back in f.
@@ -386,10 +393,15 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kResident<T, kWay, kLanes>) 
     const float per = 1.0f / (float)channels;
     const bool full = channels == kLanes * N;
     int turn = 0;
+    bool good = true;  // all rows up to here came
     for (uint32_t base = turns.first(); base < turns.rows; base += turns.step) {
-        const bool ok = turns.wait();
+        good = turns.wait() && good;
         R x[D];
         turns.take(0, base, x);
+        if (!good) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) x[d].spoil();
+        }
         f2 f[D][N / 2];
 #pragma unroll
         for (int d = 0; d < D; ++d)
@@ -458,7 +470,7 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kResident<T, kWay, kLanes>) 
         for (int d = 0; d < D; ++d) {
             const uint32_t r = turns.row(base, d);
             const bool live = r < turns.rows;
-            const float rstd = ok ? inverse_root(fmaf(q[d], per, p.eps)) : not_a_number();
+            const float rstd = inverse_root(fmaf(q[d], per, p.eps));
             if (p.saved && lane == 0 && live) reinterpret_cast<float2*>(p.saved)[r] = make_float2(mean[d], rstd);
 #pragma unroll
             for (int i = 0; i < N / 2; ++i) f[d][i] = fma2(mul2(f[d][i], both(rstd)), w[i], b[i]);
@@ -522,9 +534,10 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<T, kWay, kLane
         }
     };
     int turn = 0;
+    bool good = true;  // all rows up to here came
     fetch_stat(turns.first());
     for (uint32_t base = turns.first(); base < turns.rows; base += turns.step) {
-        const bool ok = turns.wait();
+        good = turns.wait() && good;
         R x[D], dy[D], ds[kSum ? D : 1];
         turns.take(0, base, x);
         turns.take(1, base, dy);
@@ -533,7 +546,7 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<T, kWay, kLane
 #pragma unroll
         for (int d = 0; d < D; ++d) {
             mean[d] = stat[d].x;
-            rstd[d] = ok ? stat[d].y : not_a_number();
+            rstd[d] = good ? stat[d].y : not_a_number();
         }
         fetch_stat(base + turns.step);
         if constexpr (kWay != kRing) turns.fetch();
@@ -585,6 +598,10 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kGradResident<T, kWay, kLane
         }
     }
     if (!p.partials) return;
+    if (!good) {  // dy of rows that did not come
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) db[k] = both(not_a_number());
+    }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the kernel that adds the partial sums may get ready
     // one row of partial sums a CTA: over its groups, in their order
     float* s_col = reinterpret_cast<float*>(s_mem);
