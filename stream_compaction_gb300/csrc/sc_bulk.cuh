@@ -15,9 +15,7 @@ __device__ __forceinline__ void bulk_load(uint32_t to, const void* from, uint32_
 }
 
 // Copies end by themselves; a wait that should run out all the same (a second or so) gives
-// up, and the caller makes NaN of what was to come of them, and of what comes behind in the
-// same ring (one flag for all turns costs nothing; leaving the later waits out, or the loads,
-// 10 us of the 45 of 262144 rows' gradient of a norm: a ring's state is the same in all lanes).
+// up, and the caller makes NaN of what was to come of them.
 __device__ __forceinline__ bool arrived(uint32_t bar, uint32_t parity) {
     for (int i = 0; i < (1 << 20); ++i)
         if (mbar_try_wait_sleep(bar, parity, 1000)) return true;

@@ -251,7 +251,12 @@ __device__ __forceinline__ uint8_t head_of(const uint8_t* heads, long long row, 
     const long long t = t0 + lane;
     return lane < kTokens && t >= 0 && t < length ? __ldg(heads + row * length + t) : 0;
 }
-__device__ __forceinline__ uint32_t cuts_of(uint8_t head) { return __ballot_sync(0xffffffffu, head != 0); }
+// (A tile that did not come is NaN from one end to the other, whatever starts in it.)
+template <bool kTma>
+__device__ __forceinline__ uint32_t cuts_of(uint8_t head, bool ok) {
+    const uint32_t cuts = __ballot_sync(0xffffffffu, head != 0);
+    return !kTma || __all_sync(0xffffffffu, ok) ? cuts : 0u;
+}
 
 // The map of a run of tokens on the value before it: h -> A h + B, or B alone where a
 // segment starts inside (whatever h is, infinities too).
@@ -355,12 +360,13 @@ __device__ __forceinline__ typename Lane<K>::V exchange(Exchange<K, kWarps>& x, 
         send(at_rank(to, r), at_rank(bar, r), all);
         if (kCuts && lane == 0) send(at_rank(smem_u32(&x.rank_cut[turn][rank]), r), at_rank(bar, r), (int)all_cut);
     }
-    if (!arrived_from_cluster(bar, (uint32_t)(round >> 1) & 1u)) carry = Lane<K>::all(not_a_number());
+    const bool here = arrived_from_cluster(bar, (uint32_t)(round >> 1) & 1u);
+    if (!here) carry = Lane<K>::all(not_a_number());
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r) {
         if (r >= ranks) break;
         if (r == rank) in = carry;
-        carry = x.rank[turn * ranks + r][lane].of(carry, kCuts && x.rank_cut[turn][r] != 0);
+        carry = x.rank[turn * ranks + r][lane].of(carry, kCuts && here && x.rank_cut[turn][r] != 0);
     }
     return before.of(in, kCuts && before_cut);
 }
@@ -498,7 +504,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
         const bool ok = !kTma || left <= 0 || ring.wait();
         const auto xr = tile_of<kTma>(ring, x, 0, c.lane), gr = tile_of<kTma>(ring, g, 1, c.lane);
         f2 f[kPairs<K>], b[kPairs<K>];
-        const uint32_t cut = kCuts ? cuts_of(head) : 0u;
+        const uint32_t cut = kCuts ? cuts_of<kTma>(head, ok) : 0u;
         if (kCuts) head = head_of(p.heads, c.b, (long long)(tile + step) * kTokens, p.length, c.lane);
         const int valid = min(left, kTokens);
 #pragma unroll
@@ -631,7 +637,7 @@ __global__ void __launch_bounds__(32 * kWarps, (kTma || K == 1 ? 16 : 12) / kWar
         // gate's sign (sigmoid), or f itself.  map: q behind the tile -> q before it, as the
         // sum over its tokens of dy times the product of f from the tile's start up to there.
         f2 u[kPairs<K>], w[kPairs<K>];
-        const uint32_t cut = kCuts ? cuts_of(head) : 0u;
+        const uint32_t cut = kCuts ? cuts_of<kTma>(head, ok) : 0u;
         const int valid = tokens_of(tile), until = kCuts && cut ? __ffs(cut) - 1 : kTokens;
         V h = start;
         fetch_small(tile - step);
@@ -686,12 +692,14 @@ __global__ void __launch_bounds__(32 * kWarps, (kTma || K == 1 ? 16 : 12) / kWar
                 }
             }
         }
-        if (!ok) {
-            set_token<K>(w, 0, L::all(not_a_number()));
+        if (!ok) {  // q and all that is made of it
             map.A = map.B = L::all(not_a_number());
+            set_token<K>(w, kTokens - 1, map.A);
+            set_token<K>(u, kTokens - 1, map.A);
         }
         if (!kTma) fetch();
         V q = exchange<K, kWarps, kCuts>(s.ex, round, c.warp, c.lane, c.rank, c.ranks, map, cut != 0, carry);
+        if (!kSigmoid && !ok) q = L::all(not_a_number());  // (dx is dh itself)
         if (valid > 0) {  // as in the forward kernel
             T *tx = dx + (kTokens - 1) * p.channels, *tg = dg + (kTokens - 1) * p.channels;
 #pragma unroll

@@ -76,3 +76,62 @@ def test_norm(tmp_path):
                 assert (mine.all(1) == mine.any(1)).all()
                 bad = mine.any(1).nonzero().flatten().tolist()
                 assert 1 < bad[0] <= 8 and bad == list(range(bad[0], len(mine)))
+
+
+GATED = r"""
+extern "C" int late_gated(int grad, long long batch, long long length, long long channels, const void* x, const void* gate,
+                          const uint8_t* heads, void* y, float* final_state, float* saved, const void* dy, void* dx, void* dgate) {
+    scg::GatedParams p{};
+    p.sigmoid = 1, p.batch = batch, p.length = length, p.channels = channels;
+    p.x = x, p.gate = gate, p.heads = heads, p.y = y, p.final_state = final_state, p.saved = saved;
+    p.dy = dy, p.dx = dx, p.dgate = dgate;
+    p.x_token = p.gate_token = p.y_token = p.dy_token = channels;
+    p.x_batch = p.gate_batch = p.y_batch = p.dy_batch = length * channels;
+    scg::GatedMaps maps{};
+    if (!scg::maps_of<float, 1>(&maps, p, grad != 0)) return -1;
+    const cudaError_t e = scg::go<float, 1, true, true, 4, true>(p, maps, grad != 0, batch * (channels / 32), 1, nullptr);
+    return e != cudaSuccess ? (int)e : (int)cudaDeviceSynchronize();
+}
+"""
+
+
+def test_gated(tmp_path):
+    """Four warps a CTA, a tile of 16 tokens each, 32 channels; NaN goes on, and back, until a
+    segment starts in a tile that came.  Forward three stages, gradient two, from the end."""
+    lib = late_copies.build(str(tmp_path), "sc_gated.cuh", GATED, 32)
+    batch, tiles, channels = 2, 43, 128
+    length = 16 * tiles - 7
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x, g, dy = (torch.randn(batch, length, channels, generator=gen, device="cuda") for _ in range(3))
+    heads = torch.rand(batch, length, generator=gen, device="cuda") < 0.05
+    saved, final = sc.gated_scan_saved(x), torch.empty(batch, channels, device="cuda")
+    want = sc.gated_scan(x, g, heads=heads, saved=saved, final_state=final)
+    grads = sc.gated_scan_grad(dy, x, g, heads=heads, saved=saved)
+    y, dx, dg, end, kept = (torch.zeros_like(t) for t in (x, x, x, final, saved))
+    torch.cuda.synchronize()
+    n = [ctypes.c_longlong(v) for v in (batch, length, channels)]
+    assert lib.late_gated(0, *n, _p(x), _p(g), _p(heads), _p(y), _p(end), _p(kept), None, None, None) == 0
+    assert lib.late_gated(1, *n, _p(x), _p(g), _p(heads), None, None, _p(saved), _p(dy), _p(dx), _p(dg)) == 0
+    cut = heads.cpu().tolist()
+    for b in range(batch):
+        for block in range(channels // 32):
+            cta, cols = b * (channels // 32) + block, slice(32 * block, 32 * block + 32)
+            lost = lambda i, ring: (cta == 1 and i % 4 == 2) or (cta == 3 and i // 4 // ring % 2 == 1)  # noqa: E731
+            gone, state = [], False
+            for t in range(length):
+                bad = lost(t // 16, 3)
+                state = bad or (state and not cut[b][t])
+                gone.append(state)
+            gone = torch.tensor(gone, device="cuda")
+            assert gone.any() == (cta in (1, 3))
+            assert torch.equal(y[b, ~gone, cols], want[b, ~gone, cols]) and y[b, gone, cols].isnan().all()
+            if gone[-1]:
+                assert end[b, cols].isnan().all()
+            back, state = [], False
+            for t in reversed(range(length)):
+                bad = lost(tiles - 1 - t // 16, 2)
+                back.append(bad or state)
+                state = bad or (state and not cut[b][t])
+            back = torch.tensor(back[::-1], device="cuda")
+            for got, name in ((dx, "x"), (dg, "gate")):
+                assert torch.equal(got[b, ~back, cols], grads[name][b, ~back, cols]) and got[b, back, cols].isnan().all(), name
