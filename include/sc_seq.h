@@ -194,9 +194,9 @@ sc_status sc_selective_scan_step(const sc_ssm_desc *p, float *pool, int64_t pool
                                  int64_t y_batch, sc_stream_t stream);
 
 /* ---- gated recurrence: one gate and one state per channel ----
- * length < 2^30.  Decays of a run of tokens are multiplied before they meet a state, so
- * with sigmoid == 0 they should be at most 1 in size: where a product of larger ones
- * passes float32's range, the states behind it are infinite or NaN. */
+ * length < 2^30.  With sigmoid == 0 the decays may have any size (they multiply rounding
+ * errors, too); where the product of a run of them passes float32's range, its tokens are
+ * gone through one after the other, which takes longer. */
 typedef struct {
     int32_t dtype;             /* sc_dtype of x, gate, y and their gradients */
     int32_t sigmoid;           /* 0: the gate is the decay itself and x enters as it is */

@@ -80,6 +80,9 @@ template <> struct Lane<1> {
     static __device__ __forceinline__ V fma(V a, V b, V c) { return fmaf(a, b, c); }
     static __device__ __forceinline__ V load(const float* p) { return __ldg(p); }
     static __device__ __forceinline__ void store(float* p, V v) { *p = v; }
+    static __device__ __forceinline__ bool nan(V v) { return v != v; }
+    // `a` where `by` is NaN, else b
+    static __device__ __forceinline__ V pick(V by, V a, V b) { return nan(by) ? a : b; }
 };
 template <> struct Lane<2> {
     using V = f2;
@@ -91,6 +94,10 @@ template <> struct Lane<2> {
     static __device__ __forceinline__ void store(float* p, V v) {
         p[0] = lo2(v);
         p[1] = hi2(v);
+    }
+    static __device__ __forceinline__ bool nan(V v) { return lo2(v) != lo2(v) || hi2(v) != hi2(v); }
+    static __device__ __forceinline__ V pick(V by, V a, V b) {
+        return pack2(Lane<1>::pick(lo2(by), lo2(a), lo2(b)), Lane<1>::pick(hi2(by), hi2(a), hi2(b)));
     }
 };
 
@@ -312,18 +319,50 @@ __device__ __forceinline__ bool arrived_from_cluster(uint32_t bar, uint32_t pari
     return false;
 }
 
+// The round's tiles one by one, from `value` before it, for the channels where `odd` is NaN.
+template <int K, int kWarps, class Walk>
+__device__ __forceinline__ void one_by_one(Exchange<K, kWarps>& x, int turn, int warp, int lane, int rank, int ranks,
+                                           typename Lane<K>::V odd, typename Lane<K>::V value, typename Lane<K>::V& in,
+                                           typename Lane<K>::V& carry, Walk walk) {
+    const cg::cluster_group cluster = cg::this_cluster();
+    if (ranks > 1) cluster.sync();  // the maps are read
+    else __syncthreads();
+    for (int r = 0; r < ranks; ++r) {
+        if (r == rank) {
+            for (int w = 0; w < kWarps; ++w) {
+                if (w == warp) {
+                    in = Lane<K>::pick(odd, value, in);
+                    x.warp[turn][w][lane].B = walk(value);
+                }
+                __syncthreads();
+                value = x.warp[turn][w][lane].B;
+            }
+            if (ranks > 1 && warp == 0)
+                for (int to = 0; to < ranks; ++to) *cluster.map_shared_rank(&x.rank[turn * ranks + r][lane].B, to) = value;
+        }
+        if (ranks > 1) {
+            cluster.sync();
+            value = x.rank[turn * ranks + r][lane].B;
+        }
+    }
+    carry = Lane<K>::pick(odd, value, carry);
+}
+
 // One round: takes this warp's map, returns the value before its tile and moves
 // `carry`, the value before the round, to behind it (the same in all warps).  Warps and
 // CTAs count in the direction of the recurrence.  Buffers alternate: a warp writes for
 // the next round while others still read this one's, and two rounds on a barrier lies
 // between (in a cluster: a CTA sends for a round when all its warps are through with
 // the one before, and gets no further until every other has).
-// kCuts: segments may start anywhere.
-template <int K, int kWarps, bool kCuts>
+// kCuts: segments may start anywhere.  kAny: decays of any size; where the product of some
+// passes float32's range (or is NaN), its channel goes through the round's tiles one by one
+// (walk: a value through this warp's), since infinity times a state of 0 is not 0.
+template <int K, int kWarps, bool kCuts, bool kAny, class Walk>
 __device__ __forceinline__ typename Lane<K>::V exchange(Exchange<K, kWarps>& x, int round, int warp, int lane, int rank,
                                                         int ranks, const Map<K>& map, bool cut,
-                                                        typename Lane<K>::V& carry) {
+                                                        typename Lane<K>::V& carry, Walk walk) {
     using V = typename Lane<K>::V;
+    [[maybe_unused]] V before_all = carry, odd = Lane<K>::all(0.0f);  // odd: 0, or NaN where a product is not finite
     const int turn = round & 1;
     x.warp[turn][warp][lane] = map;
     if (kCuts && lane == 0) x.cut[turn][warp] = cut;
@@ -336,7 +375,9 @@ __device__ __forceinline__ typename Lane<K>::V exchange(Exchange<K, kWarps>& x, 
             const bool c = kCuts && x.cut[turn][w] != 0;
             if (w < warp) in = m.of(in, c);
             carry = m.of(carry, c);
+            if (kAny) odd = Lane<K>::fma(m.A, Lane<K>::all(0.0f), odd);
         }
+        if (kAny && __any_sync(0xffffffffu, Lane<K>::nan(odd))) one_by_one(x, turn, warp, lane, rank, ranks, odd, before_all, in, carry, walk);
         return in;
     }
     // the maps of the warps before this one, and of the CTA
@@ -367,8 +408,13 @@ __device__ __forceinline__ typename Lane<K>::V exchange(Exchange<K, kWarps>& x, 
         if (r >= ranks) break;
         if (r == rank) in = carry;
         carry = x.rank[turn * ranks + r][lane].of(carry, kCuts && here && x.rank_cut[turn][r] != 0);
+        if (kAny) odd = Lane<K>::fma(x.rank[turn * ranks + r][lane].A, Lane<K>::all(0.0f), odd);
     }
-    return before.of(in, kCuts && before_cut);
+    in = before.of(in, kCuts && before_cut);
+    // (a wait that ran out: the CTAs may not have seen the same maps, and must not wait for one another)
+    if (kAny && here && __any_sync(0xffffffffu, Lane<K>::nan(odd)))
+        one_by_one(x, turn, warp, lane, rank, ranks, odd, before_all, in, carry, walk);
+    return in;
 }
 // Before the first round: every CTA's barriers stand before another writes to it.
 template <class E>
@@ -541,7 +587,15 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
             for (int j = 1; j < kTokens; ++j)
                 map.B = cut >> j & 1u ? token<K>(b, j) : L::fma(token<K>(f, j), map.B, token<K>(b, j));
         }
-        V h = exchange<K, kWarps, kCuts>(s.ex, round, c.warp, c.lane, c.rank, c.ranks, map, cut != 0, carry);
+        auto through = [&](int j, V v) {
+            return kCuts && (cut >> j & 1u) ? token<K>(b, j) : L::fma(token<K>(f, j), v, token<K>(b, j));
+        };
+        auto walk = [&](V v) {
+#pragma unroll
+            for (int j = 0; j < kTokens; ++j) v = through(j, v);
+            return v;
+        };
+        V h = exchange<K, kWarps, kCuts, !kSigmoid>(s.ex, round, c.warp, c.lane, c.rank, c.ranks, map, cut != 0, carry, walk);
         // A warp without a tile leaves its stage as it is: the copy of earlier results out of
         // it is waited for only where the stage is filled again (Ring::load).
         if (valid > 0) {
@@ -549,7 +603,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
             T* to = y;
 #pragma unroll
             for (int j = 0; j < kTokens; ++j) {
-                h = kCuts && (cut >> j & 1u) ? token<K>(b, j) : L::fma(token<K>(f, j), h, token<K>(b, j));
+                h = through(j, h);
                 if constexpr (kTma) {
                     xr.put(j, h);
                 } else {
@@ -698,7 +752,17 @@ __global__ void __launch_bounds__(32 * kWarps, (kTma || K == 1 ? 16 : 12) / kWar
             set_token<K>(u, kTokens - 1, map.A);
         }
         if (!kTma) fetch();
-        V q = exchange<K, kWarps, kCuts>(s.ex, round, c.warp, c.lane, c.rank, c.ranks, map, cut != 0, carry);
+        auto walk = [&](V v) {
+            if (valid > 0) {
+#pragma unroll
+                for (int j = kTokens - 1; j >= 0; --j) {
+                    v = L::mul(token<K>(w, j), L::add(d.get(j), v));
+                    if (kCuts && (cut >> j & 1u)) v = none;
+                }
+            }
+            return v;
+        };
+        V q = exchange<K, kWarps, kCuts, !kSigmoid>(s.ex, round, c.warp, c.lane, c.rank, c.ranks, map, cut != 0, carry, walk);
         if (!kSigmoid && !ok) q = L::all(not_a_number());  // (dx is dh itself)
         if (valid > 0) {  // as in the forward kernel
             T *tx = dx + (kTokens - 1) * p.channels, *tg = dg + (kTokens - 1) * p.channels;

@@ -262,8 +262,8 @@ def gated_scan_saved(x, stream=None):
 def gated_scan(x, gate, activation="sigmoid", heads=None, state=None, final_state=None, saved=None, out=None,
                stream=None):
     """Gated recurrence of x (batch, length, channels), gate like x: h = f * h + (1 - f) * x
-    with f = sigmoid(gate), or with activation None h = gate * h + x (gates at most 1 in
-    size: their products over runs of tokens must not overflow).  heads as in causal_conv; state / final_state: (batch, channels) float32.  saved: from
+    with f = sigmoid(gate), or with activation None h = gate * h + x (gates of any size).
+    heads as in causal_conv; state / final_state: (batch, channels) float32.  saved: from
     gated_scan_saved, for gated_scan_grad."""
     y = _call("gated_scan", stream, x, gate, activation, heads, state, final_state, saved, out)
     if y is None:
