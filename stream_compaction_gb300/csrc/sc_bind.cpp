@@ -9,7 +9,6 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
-#include <ATen/record_function.h>
 #include <c10/core/AutogradState.h>
 #include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDAFunctions.h>
@@ -131,11 +130,10 @@ bool records(std::initializer_list<const Maybe*> some, std::initializer_list<con
     return false;
 }
 
-// Whether somebody watches what torch allocates, or fills it: a dispatch mode, a profiler,
-// the deterministic algorithms' filling of new memory.
+// Whether a dispatch mode watches what torch allocates, or the deterministic algorithms fill it.
 bool watched() {
     const auto& context = at::globalContext();
-    return c10::impl::dispatch_mode_enabled() || at::hasCallbacks() ||
+    return c10::impl::dispatch_mode_enabled() ||
            (context.deterministicAlgorithms() && context.deterministicFillUninitializedMemory());
 }
 // New tensors, without torch's dispatcher where nobody watches: 0.8 us less each of a

@@ -67,12 +67,3 @@ def test_deterministic_algorithms_fill_them():
     finally:
         torch.use_deterministic_algorithms(False)
     assert all(t.isnan().all() for t in saved)
-
-
-@pytest.mark.gpu
-def test_a_profiler_sees_them():
-    _lib()
-    x = torch.zeros(2, 20, 8, device="cuda")
-    with torch.autograd.profiler.profile() as prof:
-        sc.gated_scan_saved(x)
-    assert any(e.name == "aten::empty" for e in prof.function_events)
