@@ -27,8 +27,9 @@
 // element's place in float32, where keeping h itself would cost an element read and
 // rounding errors of 16 bits in dgate).
 //
-// 8 x 4096 tokens of 4096 bfloat16: forward 137 to 147 us (5.5 to 5.9 TB/s, a copy 6.5),
-// gradient 246 (5.5); rows that are not aligned 3.0 to 5.3 TB/s.
+// 8 x 4096 tokens of 4096 bfloat16: forward 141 to 145 us (5.6 to 5.7 TB/s, a copy 6.5), 147
+// to 151 with the states saved, gradient 246 to 250 (5.4 to 5.5); rows that are not aligned
+// 2.4 to 4.6 TB/s.
 #pragma once
 #include <algorithm>
 
@@ -635,8 +636,8 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
 template <class T, int K> using BackwardRing = Ring<T, K, 3, 2>;
 
 // Warps, CTAs and rounds count from the end of the row.  Three tensors in registers, two
-// channels a lane: 12 warps an SM (4 x 4096 tokens of 4094 bfloat16: 178 us; with one
-// channel a lane 221).
+// channels a lane: 12 warps an SM (4 x 4096 tokens of 4094 bfloat16: 182 us; with one
+// channel a lane 221 or more).
 template <class T, int K, bool kTma, bool kSigmoid, int kWarps, bool kCuts>
 __global__ void __launch_bounds__(32 * kWarps, (kTma || K == 1 ? 16 : 12) / kWarps)
     gated_grad_kernel(GatedParams p, const __grid_constant__ GatedMaps maps) {
@@ -868,12 +869,14 @@ __global__ void __launch_bounds__(kStepNT) gated_step_kernel(GatedParams p) {
 }
 
 // ---------------------------------------------------------------- launch
-// The machine holds 16 warps an SM (128 registers a thread).  CTAs of 4 warps where the
+// The machine holds 16 warps an SM (128 registers a thread; the gradient of 16-bit tiles spills
+// 72 to 88 bytes so, rows that are not aligned up to 184, the most where segments start
+// anywhere).  CTAs of 4 warps where the
 // rows and channels alone make enough of them (a round's fold is half as long, and they
 // fill the SMs more evenly), else of 8.  CTAs in a cluster: until there are 12 warps an
 // SM or the length has no more tiles (16 of them only where all clusters are resident at
 // once, which takes as many SMs of one part of the chip each: 8192 tokens of 384 bfloat16
-// channels, 6 clusters, 20 us with 8 CTAs and 16 with 16; of 512, 8 clusters, 20 and 27);
+// channels, 6 clusters, 20 us with 8 CTAs and 16 with 16; of 512, 8 clusters, 22, and 27 or more with 16);
 // and while the last wave of CTAs is mostly empty, up to 4.
 struct Split {
     int warps, ctas;

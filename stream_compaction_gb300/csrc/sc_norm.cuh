@@ -16,11 +16,13 @@
 // CTAs stay and take rows in turns, with the parameters (and the gradient's sums over
 // tokens) in registers.  A team, the threads of a wide row or a warp with several
 // narrow ones, has a ring of rows in shared memory that bulk copies fill some turns
-// ahead (should one not come, its row is NaN, and so are the ring's later ones: one flag for
-// all turns costs nothing, where leaving the later waits or loads out took 10 us more for the
-// gradient of 262144 rows, 45 so); rows that are not aligned to 16 bytes, and calls of one turn, are loaded into
+// ahead; rows that are not aligned to 16 bytes, and calls of one turn, are loaded into
 // registers, the next row's while this one is worked on.  (Unaligned rows through the
 // ring, their ends by themselves: 17367 rows of 636 bfloat16 43 us forward, 23 so.)
+//
+// Should a copy not come, its row is NaN, and so are the ring's later ones.  One flag for
+// all turns costs nothing; leaving the later waits or loads out made the gradient of 262144
+// rows of 128 float16 55 us in place of 45, as a ring's state then differs between lanes.
 //
 // 4 x 4096 rows of 4096 bfloat16 with a residual: forward 85 us, gradient 87 and its sums
 // 8 (6.2 TB/s; a copy 6.5).
@@ -486,6 +488,9 @@ __global__ void __launch_bounds__(kThreads<kLanes>, kResident<T, kWay, kLanes>) 
 // 128 registers a thread (64 of 1024 threads); 80 where a thread has 8 elements of one row
 // and two tensors (3003 rows of 2047 float32: 27 us with two CTAs an SM, 25 with three; two
 // 16-bit rows a thread spill so, and take 55 us in place of 49).  kSum: dsum is there.
+// Of the gradients with dsum, those that load 16 elements a thread and tensor into registers
+// spill 24 to 52 bytes (16 bits, calls of one turn), and with 1024 threads 16 to 64 (16 bits,
+// unaligned) and 176 to 208 (float32, 4097 to 8192 channels; without dsum 32 to 72).
 template <class T, Way kWay, int kLanes, int NV, bool kSum>
 constexpr int kGradResident = kThreads<kLanes> > 256                                                        ? 1
                               : kWidth<T> * NV == 8 && !kSum && (kWay != kRing || sizeof(T) == 4) ? 3
