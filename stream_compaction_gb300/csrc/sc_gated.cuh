@@ -218,7 +218,7 @@ struct Held : Elements<T, K> {
 // dgate is proportional to, and an open gate's 1 - f, which x enters with.  The larger is
 // off by as much absolutely, times the smaller: decays close to 1 are as good as rounded
 // ones, however many are multiplied.  (f = 1 - e / (1 + e) with e = exp(-g) for all gates
-// saves a selection, but keeps of a gate of -12 one digit, of one below -17 none.)
+// saves a selection, but keeps one or two digits of a gate of -12, none of one below -17.)
 template <class T>
 __device__ __forceinline__ void gate_parts(f2 g, f2& small, f2& large) {
     f2 e;
@@ -363,7 +363,8 @@ __device__ __forceinline__ typename Lane<K>::V exchange(Exchange<K, kWarps>& x, 
                                                         int ranks, const Map<K>& map, bool cut,
                                                         typename Lane<K>::V& carry, Walk walk) {
     using V = typename Lane<K>::V;
-    [[maybe_unused]] V before_all = carry, odd = Lane<K>::all(0.0f);  // odd: 0, or NaN where a product is not finite
+    // odd: 0, or NaN where a product is not finite
+    [[maybe_unused]] V before_all = carry, odd = Lane<K>::all(0.0f);
     const int turn = round & 1;
     x.warp[turn][warp][lane] = map;
     if (kCuts && lane == 0) x.cut[turn][warp] = cut;
@@ -378,7 +379,8 @@ __device__ __forceinline__ typename Lane<K>::V exchange(Exchange<K, kWarps>& x, 
             carry = m.of(carry, c);
             if (kAny) odd = Lane<K>::fma(m.A, Lane<K>::all(0.0f), odd);
         }
-        if (kAny && __any_sync(0xffffffffu, Lane<K>::nan(odd))) one_by_one(x, turn, warp, lane, rank, ranks, odd, before_all, in, carry, walk);
+        if (kAny && __any_sync(0xffffffffu, Lane<K>::nan(odd)))
+            one_by_one(x, turn, warp, lane, rank, ranks, odd, before_all, in, carry, walk);
         return in;
     }
     // the maps of the warps before this one, and of the CTA
@@ -703,7 +705,8 @@ __global__ void __launch_bounds__(32 * kWarps, (kTma || K == 1 ? 16 : 12) / kWar
                 f2 small, large;
                 const f2 g2 = gr.pair(i);
                 gate_parts<T>(g2, small, large);
-                const f2 fs = select2(g2, small, large), rests = select2(g2, large, small), product = mul2(small, large);
+                const f2 fs = select2(g2, small, large), rests = select2(g2, large, small);
+                const f2 product = mul2(small, large);
                 w[i] = small | (g2 & 0x8000000080000000ull);
 #pragma unroll
                 for (int j = i * 2 / K; j < (i + 1) * 2 / K; ++j) {
